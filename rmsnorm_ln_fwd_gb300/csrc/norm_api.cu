@@ -11,18 +11,20 @@
 #include <cstdint>
 #include <mutex>
 
+#include "api_common.h"
 #include "common.cuh"
 #include "launch.h"
 #include "norm.h"
-#include <nvtx3/nvToolsExt.h>
 
+using namespace normapi;
 using normk::BwdArgs;
+using normk::current_device_info;
 using normk::DeviceInfo;
 using normk::FwdArgs;
+using normk::launch_result;
 
 namespace {
 
-constexpr int64_t kMaxH = int64_t(1) << 24;  // counts stay exact in fp32
 constexpr int kMaxDevices = 64;
 
 std::mutex g_mu;
@@ -87,6 +89,11 @@ bool device_info(int dev, DeviceInfo* out) {
   return true;
 }
 
+}  // namespace
+
+namespace normk {
+bool device_info_for(int dev, DeviceInfo* out) { return device_info(dev, out); }
+
 bool current_device_info(DeviceInfo* out) {
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
@@ -115,77 +122,14 @@ bool current_device_info(DeviceInfo* out) {
   return true;
 }
 
-size_t elem_size(norm_dtype d) { return d == NORM_F32 ? 4 : 2; }
-
-norm_status check_dtypes(norm_dtype x, norm_dtype w) {
-  const bool xv = x == NORM_F32 || x == NORM_BF16 || x == NORM_F16;
-  const bool wv = w == NORM_F32 || w == NORM_BF16 || w == NORM_F16;
-  if (!xv || !wv) return NORM_ERR_UNSUPPORTED;
-  if (w != x && w != NORM_F32) return NORM_ERR_UNSUPPORTED;
-  return NORM_OK;
-}
-
-bool shape_ok(int64_t N, int64_t H) { return N >= 0 && H >= 1 && H <= kMaxH; }
-
-bool eps_ok(float eps) { return std::isfinite(eps) && eps > 0.f; }
-
-// The byte range [lo, hi) touched by N rows of H elements, `ld` apart.
-struct Span {
-  uintptr_t lo, hi;
-};
-
-// ld >= H and the extent (N-1)*ld + H elements fits comfortably in 63 bits.
-bool ld_ok(int64_t ld, int64_t N, int64_t H, size_t es) {
-  if (ld < H) return false;
-  if (N <= 1) return true;
-  const int64_t limit = (INT64_MAX / 8) / (int64_t)es;
-  return (N - 1) <= (limit - H) / ld;
-}
-
-Span rows_span(const void* p, int64_t N, int64_t ld, int64_t H, size_t es) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  const uint64_t n = N == 0 ? 0 : (uint64_t)((N - 1) * ld + H) * es;
-  return Span{lo, lo + n};
-}
-
-Span vec_span(const void* p, int64_t n, size_t es) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return Span{lo, lo + (uint64_t)n * es};
-}
-
-bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo; }
-
-// Whether any span of `a` overlaps any span of `b` (empty spans never do).
-template <size_t NA, size_t NB>
-bool any_overlap(const Span (&a)[NA], const Span (&b)[NB]) {
-  for (const Span& p : a)
-    for (const Span& q : b)
-      if (overlap(p, q)) return true;
-  return false;
-}
-
-constexpr Span kNoSpan{0, 0};
-
-// Two row tensors may be the same buffer (same pointer and stride) or
-// disjoint; anything in between is a partial overlap.
-bool same_or_disjoint(const void* p, int64_t ldp, const void* q, int64_t ldq, int64_t N, int64_t H, size_t es) {
-  if (p == q && ldp == ldq) return true;
-  return !overlap(rows_span(p, N, ldp, H, es), rows_span(q, N, ldq, H, es));
-}
-
-bool disjoint_rows(const void* p, int64_t ldp, const void* q, int64_t ldq, int64_t N, int64_t H, size_t es) {
-  return !overlap(rows_span(p, N, ldp, H, es), rows_span(q, N, ldq, H, es));
-}
-
 norm_status launch_result(const char* where, cudaError_t e) {
   if (e == cudaSuccess) return NORM_OK;
   note_error(where, e);
   return NORM_ERR_CUDA;
 }
+}  // namespace normk
 
-normk::Dtype to_dt(norm_dtype d) {
-  return d == NORM_BF16 ? normk::DT_BF16 : (d == NORM_F16 ? normk::DT_F16 : normk::DT_F32);
-}
+namespace {
 
 norm_status forward_common(int kind, const void* x, int64_t ldx, const void* res, int64_t ldr,
                            const void* gamma, const void* beta, void* y, int64_t ldy, void* h,
@@ -356,16 +300,6 @@ norm_status backward_common(int kind, const void* dy, int64_t lddy, const void* 
 }
 
 }  // namespace
-
-// Each compute entry point is an NVTX range named after it, so a profiler
-// (ncu --nvtx, nsys) can attribute kernels to the call that launched them; with
-// no tool attached a range costs a few nanoseconds.
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
 
 extern "C" {
 
