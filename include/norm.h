@@ -262,6 +262,127 @@ norm_status fused_add_rms_backward(const void* dy, int64_t lddy, const void* h, 
                                    void* workspace, size_t workspace_bytes, int64_t N, int64_t H,
                                    norm_dtype x_dtype, norm_dtype w_dtype, norm_stream_t stream);
 
+/*
+ * Block join forward: the RMSNorm after a block, its gate, the scaled residual
+ * add and the RMSNorm before the next block, in one pass.  (An extension of
+ * fused_add_rms_forward; the pages have no counterpart.)
+ *   p = x * rstd_post * gamma_post   (NORM_SANDWICH_POST; else p = x),
+ *   h = residual_scale * residual + gate * p   formed in fp32; h_out = h
+ *       rounded to x_dtype,
+ *   y = h * rstd_pre * gamma_pre     (NORM_SANDWICH_PRE), from the fp32 h,
+ *   rstd = 1/sqrt(sum_j v_j^2 / H + eps) of x's and of h's rows.
+ * x [N x ldx], residual [N x ldr]: inputs.
+ * gamma_post, gamma_pre [H] or NULL (ones).
+ * gate [gate_rows x ldgate] in gate_dtype (x_dtype or NORM_F32) or NULL (ones):
+ *   gate_rows divides N, and gate row k serves rows k*N/gate_rows up to
+ *   (k+1)*N/gate_rows (1: one vector for all rows; B: one for each sequence of
+ *   a (B, T, H) tensor).
+ * h_out [N x ldh]: may be exactly x or exactly residual; any other overlap is
+ *   rejected.  y [N x ldy]: must not overlap x, residual or h_out.
+ * rstd_post, rstd_pre [N] fp32 or NULL (saved for sandwich_rms_grad).
+ * norms: NORM_SANDWICH_POST, NORM_SANDWICH_PRE or both.  The gamma, statistic
+ *   and output of a norm that is not taken must be NULL.
+ * residual_scale must be finite.
+ */
+#define NORM_SANDWICH_POST 1u
+#define NORM_SANDWICH_PRE 2u
+#define NORM_SANDWICH_BOTH 3u
+norm_status sandwich_rms(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                         const void* gamma_post, const void* gate, int64_t ldgate, int64_t gate_rows,
+                         const void* gamma_pre, void* y, int64_t ldy, void* h_out, int64_t ldh,
+                         float* rstd_post, float* rstd_pre, int64_t N, int64_t H, float eps,
+                         float residual_scale, unsigned norms, norm_dtype x_dtype, norm_dtype w_dtype,
+                         norm_dtype gate_dtype, norm_stream_t stream);
+
+/*
+ * Bytes of device workspace sandwich_rms_grad needs for a row width H and a
+ * number of gate rows (0 without a gate) on CUDA device `device`; independent
+ * of N and, past one, of the number of gate rows.  Returns 0 if an argument is
+ * out of range or the device cannot be queried.
+ */
+size_t sandwich_rms_workspace_bytes(int64_t H, int64_t gate_rows, int device);
+
+/*
+ * Gradient of sandwich_rms, from the stored h and the saved statistics.  With
+ * h_hat = h * rstd_pre, o_hat = x * rstd_post (x without the norm after the
+ * block), g = dy * gamma_pre:
+ *   dh   = dh_in + rstd_pre * (g - h_hat * sum(g * h_hat) / H),
+ *   dres = residual_scale * dh,
+ *   dp   = gate * dh,  q = dp * gamma_post,
+ *   dx   = rstd_post * (q - o_hat * sum(q * o_hat) / H)   (dx = dp without it),
+ *   dgamma_pre  = sum over rows of dy * h_hat,
+ *   dgamma_post = sum over rows of dp * o_hat,
+ *   dgate[k]    = sum over gate row k's rows of dh * o_hat * gamma_post.
+ * dy [N x lddy] (NULL without NORM_SANDWICH_PRE, as h, gamma_pre, rstd_pre and
+ *   dgamma_pre), dh_in [N x lddh_in] or NULL (zeros; required when dy is NULL):
+ *   the gradient that arrives through the stored h.
+ * dx [N x lddx]: may be exactly dy.  dres [N x lddres]: may be exactly dh_in.
+ *   Otherwise neither overlaps an input or the other.
+ * dgamma_post, dgamma_pre [H] in w_dtype, dgate [gate_rows x lddgate] in
+ *   gate_dtype, or NULL to skip.  Overwritten, not accumulated into; zero with
+ *   N == 0.
+ * workspace: sandwich_rms_workspace_bytes(H, gate_rows, device) bytes, 16-byte
+ *   aligned; needed only when a parameter gradient is.  As in ln_backward, calls
+ *   that share it must be ordered.
+ * Sums have a fixed order: the same inputs give the same bits.
+ */
+norm_status sandwich_rms_grad(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* h, int64_t ldh,
+                              const float* rstd_post, const float* rstd_pre, const void* gamma_post,
+                              const void* gate, int64_t ldgate, int64_t gate_rows, const void* gamma_pre,
+                              const void* dh_in, int64_t lddh_in, void* dx, int64_t lddx, void* dres,
+                              int64_t lddres, void* dgamma_post, void* dgate, int64_t lddgate, void* dgamma_pre,
+                              void* workspace, size_t workspace_bytes, int64_t N, int64_t H, float residual_scale,
+                              unsigned norms, norm_dtype x_dtype, norm_dtype w_dtype, norm_dtype gate_dtype,
+                              norm_stream_t stream);
+
+/* Type of token ids. */
+typedef enum { NORM_I32 = 0, NORM_I64 = 1 } norm_itype;
+
+/*
+ * Token lookup: the rows that start a residual stream.  (No counterpart on the
+ * pages; embedding_rms is to the first block what fused_add_rms_forward is to
+ * the others.)
+ *   h_i = scale * table[tokens_i], formed in fp32, rounded to the row dtype;
+ *   embedding_rms also y_i = h_i * rstd_i * gamma from the fp32 h_i, with
+ *   rstd_i = 1/sqrt(sum_j h_ij^2 / H + eps).
+ * table [V x ldt] in the row dtype.  tokens [N], contiguous, of token_type.
+ * h [N x ldh], y [N x ldy]: outputs, clear of the inputs and of each other.
+ * gamma [H] or NULL (ones).  rstd [N] fp32 or NULL.
+ * A token outside [0, V) gives a row of zeros and raises
+ * NORM_DEVICE_ERR_BAD_TOKEN.  V and N are at most 2^31 - 2; scale is finite.
+ */
+norm_status embedding_lookup(const void* table, int64_t ldt, int64_t V, const void* tokens, norm_itype token_type,
+                             void* h, int64_t ldh, int64_t N, int64_t H, float scale, norm_dtype dtype,
+                             norm_stream_t stream);
+norm_status embedding_rms(const void* table, int64_t ldt, int64_t V, const void* tokens, norm_itype token_type,
+                          const void* gamma, void* y, int64_t ldy, void* h, int64_t ldh, float* rstd, int64_t N,
+                          int64_t H, float eps, float scale, norm_dtype x_dtype, norm_dtype w_dtype,
+                          norm_stream_t stream);
+
+/*
+ * Bytes of device workspace embedding_grad needs for N tokens of H columns.
+ * Returns 0 if an argument is out of range.
+ */
+size_t embedding_grad_workspace_bytes(int64_t N, int64_t H);
+
+/*
+ * Gradient of the table: dtable[v] = scale * sum of dh_i over the tokens equal
+ * to v, in fp32, rounded once; with accumulate != 0 it is added to what dtable
+ * holds (only the rows of tokens that occur are then touched), else rows no
+ * token names are set to zero.  The tokens are sorted by id (stably, on the
+ * GPU), so the sums have a fixed order: the same inputs give the same bits.
+ * dh [N x lddh]: the gradient of h.  dtable [V x lddt] in w_dtype (the row
+ *   dtype or NORM_F32), clear of the inputs.
+ * padding_idx: a token that has no gradient, or -1.  Tokens outside [0, V) are
+ *   left out and raise NORM_DEVICE_ERR_BAD_TOKEN.
+ * workspace: embedding_grad_workspace_bytes(N, H) bytes, 16-byte aligned;
+ *   calls that share it must be ordered.
+ */
+norm_status embedding_grad(const void* dh, int64_t lddh, const void* tokens, norm_itype token_type, void* dtable,
+                           int64_t lddt, int64_t V, void* workspace, size_t workspace_bytes, int64_t N, int64_t H,
+                           float scale, int64_t padding_idx, int accumulate, norm_dtype x_dtype, norm_dtype w_dtype,
+                           norm_stream_t stream);
+
 /* A static, human-readable name for a status code (never NULL). */
 const char* norm_status_str(norm_status status);
 
@@ -281,6 +402,7 @@ const char* norm_last_error(void);
  */
 #define NORM_DEVICE_ERR_WAIT_TIMEOUT 1u
 #define NORM_DEVICE_ERR_BAD_COPY 2u /* a bulk copy failed its bounds check and was skipped */
+#define NORM_DEVICE_ERR_BAD_TOKEN 4u /* a token id outside its table was met (and left out) */
 norm_status norm_device_errors(int device, unsigned int* flags, int clear);
 
 /*

@@ -22,6 +22,14 @@ NORM_F32 = 0
 NORM_BF16 = 1
 NORM_F16 = 2
 
+NORM_I32 = 0
+NORM_I64 = 1
+
+NORM_SANDWICH_POST = 1
+NORM_SANDWICH_PRE = 2
+
+NORM_DEVICE_ERR_BAD_TOKEN = 4
+
 # name -> (restype, argtypes), one entry per function declared in include/norm.h
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -43,6 +51,17 @@ SIGNATURES = {
                                     ctypes.c_size_t, _I64, _I64, _I, _I, _P]),
     "ln_backward_static_workspace": (_I, [_P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _P, _I64, _I64, _I, _I,
                                          _P]),
+    "sandwich_rms": (_I, [_P, _I64, _P, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _F, _F,
+                          ctypes.c_uint, _I, _I, _I, _P]),
+    "sandwich_rms_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I]),
+    "sandwich_rms_grad": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P, _I64, _P, _I64, _P,
+                               _I64, _P, _P, _I64, _P, _P, ctypes.c_size_t, _I64, _I64, _F, ctypes.c_uint, _I, _I,
+                               _I, _P]),
+    "embedding_lookup": (_I, [_P, _I64, _I64, _P, _I, _P, _I64, _I64, _I64, _F, _I, _P]),
+    "embedding_rms": (_I, [_P, _I64, _I64, _P, _I, _P, _P, _I64, _P, _I64, _P, _I64, _I64, _F, _F, _I, _I, _P]),
+    "embedding_grad_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "embedding_grad": (_I, [_P, _I64, _P, _I, _P, _I64, _I64, _P, ctypes.c_size_t, _I64, _I64, _F, _I64, _I, _I, _I,
+                            _P]),
     "norm_status_str": (ctypes.c_char_p, [_I]),
     "norm_abi_version": (_I, []),
     "norm_last_error": (ctypes.c_char_p, []),

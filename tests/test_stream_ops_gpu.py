@@ -1,0 +1,577 @@
+"""The residual-stream operators on the GPU against the fp64 oracle.
+
+Tolerances, from the arithmetic (U = 2^-24, half an fp32 step; S the sum of the
+magnitudes of the terms an element is formed from):
+
+* a row sum of H terms: at most 16 or H/256 serial additions in a thread (the
+  widest shape of each kernel family) and 20 tree levels, two roundings a term
+  before it: K = H/256 + 40 steps of U relative to the sum of magnitudes.  A
+  reciprocal norm halves that and adds rsqrtf's two steps.
+* an element of y: K*U on its terms and the norm's error.  dx combines two row
+  sums, the second formed from the first: 2K.
+* a sum over rows: each term's error, N/64 serial additions (units are never
+  fewer than 64 for these N; 32 in a tile) and 20 tree levels.
+* a value stored in fewer bits: half a step, finfo.eps/2 of the value (and half
+  the smallest subnormal), on top.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import rmsnorm_ln_fwd_gb300 as nl
+from normtest import Guarded
+from oracle import stream_oracle as S
+from rmsnorm_ln_fwd_gb300 import _lib, synth
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U = 2.0 ** -24
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from rmsnorm_ln_fwd_gb300 import _build
+    _build.build()
+    _lib.device_errors()
+
+
+def n64(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+def steps(H):
+    return H / 256 + 40
+
+
+def close(got, ref, slack, what):
+    """|got - ref| <= slack + half a step of got's type (fp32 itself: U)."""
+    dt = got.dtype
+    half = U if dt == torch.float32 else torch.finfo(dt).eps / 2
+    tiny = torch.finfo(dt).smallest_normal * torch.finfo(dt).eps / 2
+    g = n64(got).reshape(np.shape(ref))
+    err = np.abs(g - ref)
+    tol = slack + half * (np.abs(ref) + slack) + tiny
+    assert np.all(np.isfinite(g)), f"{what}: not finite"
+    if not np.all(err <= tol):
+        i = np.unravel_index(np.argmax(err - tol), err.shape)
+        raise AssertionError(f"{what}: {int((err > tol).sum())} of {err.size} beyond the bound; at {i} got {g[i]!r} "
+                             f"want {ref[i]!r} (bound {np.broadcast_to(tol, err.shape)[i]:.3g})")
+
+
+def rnd(shape, seed, dt, mean=0.0, std=1.0, roles=("x",)):
+    return synth.normal(shape, seed, roles[0], mean=mean, std=std, dtype=dt).to(DEV)
+
+
+def join_inputs(N, H, dt, wdt, gates, seed=0, gdt=None):
+    g = None
+    if gates:
+        g = rnd((H,) if gates == 1 else (gates, H), seed + 5, gdt or wdt, 0.5, 0.5)
+    return dict(x=rnd((N, H), seed, dt), res=rnd((N, H), seed + 1, dt, std=2.0), gpost=rnd((H,), seed + 2, wdt, 1.0, 0.1),
+                gpre=rnd((H,), seed + 3, wdt, 1.0, 0.1), gate=g, dy=rnd((N, H), seed + 6, dt),
+                dh=rnd((N, H), seed + 7, dt, std=0.5))
+
+
+def check_join(c, out, eps, alpha, post, pre):
+    y, h, rpost, rpre = out
+    x, res, gpost, gate, gpre = (n64(c[k]) for k in ("x", "res", "gpost", "gate", "gpre"))
+    N, H = x.shape
+    k = steps(H) * U
+    ry, rh, rrpost, rrpre = S.sandwich_forward(x, res, gpost if post else None, gate, gpre if pre else None, eps,
+                                               alpha, post, pre)
+    terms = np.abs(alpha * res) + np.abs(rh - alpha * res)
+    close(h, rh, k * terms, "h")
+    if post:
+        close(rpost, rrpost, k * rrpost, "rstd_post")
+    if pre:
+        # sum h^2 moves by at most 2 |h| . dh: relative to it, the rms of the terms over that of h
+        spread = np.sqrt((terms ** 2).mean(1)) * rrpre
+        close(rpre, rrpre, k * (1 + spread) * rrpre, "rstd_pre")
+        close(y, ry, k * (terms * rrpre[:, None] * np.abs(gpre) + np.abs(ry) * (1 + spread[:, None])), "y")
+    else:
+        assert y is None and rpre is None
+
+
+SHAPES = [(1, 1), (1, 4096), (2, 7), (5, 1000), (33, 1001), (64, 256), (18, 2056), (40, 5120), (6, 10240), (4, 16384),
+          (3, 16390), (2, 40008), (700, 512), (310, 48), (2500, 128), (9, 24)]
+
+
+@pytest.mark.parametrize("post,pre", [(True, True), (True, False), (False, True)])
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("N,H", SHAPES)
+def test_join(N, H, dt, post, pre):
+    eps, alpha = 1e-5, 0.75
+    gates = {0: 0, 1: 1}.get((N + H) % 3, 1 if N == 1 else next(b for b in (5, 3, 2, 11, 7, N) if N % b == 0))
+    wdt = DT["f32"] if H % 2 else DT[dt]
+    c = join_inputs(N, H, DT[dt], wdt, gates, seed=N + H)
+    out = nl.sandwich_rms(c["x"], c["res"], c["gpost"] if post else None, c["gate"], c["gpre"] if pre else None, eps,
+                          residual_scale=alpha, post_norm=post, pre_norm=pre)
+    torch.cuda.synchronize()
+    check_join(c, out, eps, alpha, post, pre)
+
+
+def check_join_grad(c, out, rpost, rpre, alpha, N_serial=None):
+    dx, dres, dgpost, dgate, dgpre = out
+    x, h, gpost, gate, gpre, dy, dh = (n64(c[k]) for k in ("x", "res", "gpost", "gate", "gpre", "dy", "dh"))
+    N, H = x.shape
+    post, pre = rpost is not None, rpre is not None
+    rpo, rpr = n64(rpost), n64(rpre)
+    ref = S.sandwich_backward(dy if pre else None, x, h if pre else None, rpo, rpr, gpost if post else None, gate,
+                              gpre if pre else None, dh, alpha)
+    k = steps(H) * U
+    # magnitudes of the terms
+    sdh = np.abs(dh)
+    hh = np.zeros_like(x)
+    if pre:
+        hh = np.abs(h * rpr[:, None])
+        g = np.abs(dy * gpre)
+        C = (g * hh).mean(1, keepdims=True)
+        sdh = sdh + rpr[:, None] * (g + hh * C)
+    rows = S._rows_of_gate(gate, N, H)
+    w, oh, ro = np.abs(rows), np.abs(x), 1.0
+    if post:
+        ro = rpo[:, None]
+        oh = oh * ro
+        w = w * np.abs(gpost)
+    sk = (w * oh * sdh).mean(1, keepdims=True) if post else 0.0
+    close(dres, ref[1], 2 * k * np.abs(alpha) * sdh, "dres")
+    close(dx, ref[0], 2 * k * ro * (w * sdh + oh * sk), "dx")
+    kr = 2 * k + (N / 64 + 20) * U
+    if post:
+        close(dgpost, ref[2], kr * (np.abs(rows) * sdh * oh).sum(0), "dgamma_post")
+    else:
+        assert dgpost is None
+    if gate is not None:
+        B = gate.reshape(-1, H).shape[0]
+        terms = (sdh * oh * (np.abs(gpost) if post else 1.0)).reshape(B, N // B, H).sum(1).reshape(gate.shape)
+        close(dgate, ref[3], kr * terms, "dgate")
+    else:
+        assert dgate is None
+    if pre:
+        close(dgpre, ref[4], kr * (np.abs(dy) * hh).sum(0), "dgamma_pre")
+    else:
+        assert dgpre is None
+
+
+def run_join_grad(c, post, pre, alpha=0.75, eps=1e-5, **kw):
+    """The gradient at the stream given by c["res"] (as the stored h)."""
+    rpost = torch.from_numpy(S._rstd(n64(c["x"]), eps)).float().to(DEV) if post else None
+    rpre = torch.from_numpy(S._rstd(n64(c["res"]), eps)).float().to(DEV) if pre else None
+    out = nl.sandwich_rms_grad(c["dy"] if pre else None, c["x"], c["res"] if pre else None, rpost, rpre,
+                               c["gpost"] if post else None, c["gate"], c["gpre"] if pre else None, c["dh"],
+                               residual_scale=alpha, **kw)
+    torch.cuda.synchronize()
+    return out, rpost, rpre
+
+
+@pytest.mark.parametrize("post,pre", [(True, True), (True, False), (False, True)])
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("N,H", SHAPES)
+def test_join_grad(N, H, dt, post, pre):
+    gates = {0: 0, 1: 1}.get((N + H) % 3, 1 if N == 1 else next(b for b in (5, 3, 2, 11, 7, N) if N % b == 0))
+    wdt = DT["f32"] if H % 2 else DT[dt]
+    c = join_inputs(N, H, DT[dt], wdt, gates, seed=N + H)
+    out, rpost, rpre = run_join_grad(c, post, pre)
+    check_join_grad(c, out, rpost, rpre, 0.75)
+
+
+@pytest.mark.parametrize("N,B", [(2000, 2), (2000, 8), (2000, 400), (2000, 1000), (2000, 2000), (1333, 43), (1333, 31),
+                                 (608, 304), (303, 3)])
+@pytest.mark.parametrize("H,dt", [(256, "bf16"), (1024, "f16"), (2048, "bf16"), (130, "f32"), (1024, "f32")])
+def test_join_gates_of_runs(N, B, H, dt):
+    """Runs that end inside a unit, cross units, are longer and shorter than a
+    unit, and of one row."""
+    c = join_inputs(N, H, DT[dt], torch.float32, B, seed=B)
+    out = nl.sandwich_rms(c["x"], c["res"], c["gpost"], c["gate"], c["gpre"], 1e-5, residual_scale=0.75)
+    check_join(c, out, 1e-5, 0.75, True, True)
+    out, rpost, rpre = run_join_grad(c, True, True)
+    check_join_grad(c, out, rpost, rpre, 0.75)
+
+
+def padded(t, ld, off=0):
+    """A copy of t in rows `ld` apart, `off` elements into a larger buffer whose
+    every other element is a sentinel; returns (view, buffer, mask of the rest)."""
+    N, H = t.shape
+    buf = torch.full((off + N * ld + 8,), -77.0, dtype=t.dtype, device=t.device)
+    view = buf[off:off + N * ld].view(N, ld)[:, :H]
+    view.copy_(t)
+    rest = torch.ones_like(buf, dtype=torch.bool)
+    rest[off:off + N * ld].view(N, ld)[:, :H] = False
+    return view, buf, rest
+
+
+@pytest.mark.parametrize("N,H,ld,off", [(37, 1024, 1032, 8), (37, 1024, 1024, 1), (21, 1000, 1003, 3), (5, 5120, 5136, 16),
+                                        (300, 64, 65, 0), (3, 16384, 16400, 0)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_join_strides_and_margins(N, H, ld, off, dt):
+    """Padded and shifted rows give the contiguous call's bits or stay within the
+    bound, and what lies between and behind the rows is left as it was."""
+    c = join_inputs(N, H, DT[dt], DT[dt], 1, seed=H)
+    p = {k: padded(c[k], ld, off)[0] for k in ("x", "res", "dy", "dh")}
+    bufs = {k: padded(torch.zeros_like(c["x"]), ld, off) for k in ("y", "h", "dx", "dr")}
+    # a gate that is a column slice of a wider tensor
+    wide = torch.full((1, 3 * H), 5.0, dtype=DT[dt], device=DEV)
+    wide[:, H:2 * H] = c["gate"]
+    gate = wide[:, H:2 * H]
+    y, h, rpost, rpre = nl.sandwich_rms(p["x"], p["res"], c["gpost"], gate, c["gpre"], 1e-5, residual_scale=0.75,
+                                        h_out=bufs["h"][0], out=bufs["y"][0])
+    check_join(c, (y, h, rpost, rpre), 1e-5, 0.75, True, True)
+    cc = {**c, "gate": gate}
+    rp = torch.from_numpy(S._rstd(n64(c["x"]), 1e-5)).float().to(DEV)
+    rq = torch.from_numpy(S._rstd(n64(c["res"]), 1e-5)).float().to(DEV)
+    out = nl.sandwich_rms_grad(p["dy"], p["x"], p["res"], rp, rq, c["gpost"], gate, c["gpre"], p["dh"],
+                               residual_scale=0.75, dx=bufs["dx"][0], dres=bufs["dr"][0])
+    torch.cuda.synchronize()
+    assert out[3].shape == gate.shape
+    check_join_grad(cc, out, rp, rq, 0.75)
+    for k, (view, buf, rest) in bufs.items():
+        assert torch.all(buf[rest] == -77.0), k
+
+
+@pytest.mark.parametrize("N,H,dt", [(50, 1024, "bf16"), (7, 1001, "f16"), (20, 5120, "bf16"), (4, 16384, "f32"),
+                                    (2, 70000, "bf16")])
+def test_join_in_place(N, H, dt):
+    c = join_inputs(N, H, DT[dt], DT[dt], 1, seed=1)
+    ref = nl.sandwich_rms(c["x"], c["res"], c["gpost"], c["gate"], c["gpre"], residual_scale=0.5)
+    for name in ("x", "res"):
+        d = {k: None if v is None else v.clone() for k, v in c.items()}
+        y, h, a, b = nl.sandwich_rms(d["x"], d["res"], d["gpost"], d["gate"], d["gpre"], residual_scale=0.5,
+                                     h_out=d[name])
+        assert h is d[name]
+        for got, want in zip((y, h, a, b), ref):
+            assert torch.equal(got, want)
+    want, rpost, rpre = run_join_grad(c, True, True)
+    d = {k: None if v is None else v.clone() for k, v in c.items()}
+    got = nl.sandwich_rms_grad(d["dy"], d["x"], d["res"], rpost, rpre, d["gpost"], d["gate"], d["gpre"], d["dh"],
+                               residual_scale=0.75, dx=d["dy"], dres=d["dh"])
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_join_guards_and_bits():
+    """Margins of every output survive, and a second call gives the same bits."""
+    N, H, B = 400, 1040, 5
+    c = join_inputs(N, H, torch.bfloat16, torch.bfloat16, B, seed=4)
+    rp = torch.from_numpy(S._rstd(n64(c["x"]), 1e-5)).float().to(DEV)
+    rq = torch.from_numpy(S._rstd(n64(c["res"]), 1e-5)).float().to(DEV)
+    first = None
+    for _ in range(3):
+        g = [Guarded((N, H), torch.bfloat16, DEV) for _ in range(4)]
+        y, h, a, b = nl.sandwich_rms(c["x"], c["res"], c["gpost"], c["gate"], c["gpre"], out=g[0].t, h_out=g[1].t)
+        out = nl.sandwich_rms_grad(c["dy"], c["x"], c["res"], rp, rq, c["gpost"], c["gate"], c["gpre"], c["dh"],
+                                   dx=g[2].t, dres=g[3].t)
+        torch.cuda.synchronize()
+        assert all(x.ok() for x in g)
+        now = [t.clone() for t in (y, h, a, b, *out)]
+        if first is None:
+            first = now
+        assert all(torch.equal(p, q) for p, q in zip(first, now))
+
+
+def test_join_skips_what_is_not_asked():
+    c = join_inputs(30, 256, torch.bfloat16, torch.bfloat16, 3, seed=4)
+    out, rp, rq = run_join_grad(c, True, True)
+    bare, _, _ = run_join_grad(c, True, True, need_param_grads=False)
+    assert torch.equal(out[0], bare[0]) and torch.equal(out[1], bare[1])
+    assert bare[2] is None and bare[3] is None and bare[4] is None
+    y, h, a, b = nl.sandwich_rms(c["x"], c["res"], c["gpost"], c["gate"], c["gpre"], save_stats=False)
+    assert a is None and b is None
+
+
+def test_join_no_rows():
+    x = torch.empty((0, 64), device=DEV, dtype=torch.bfloat16)
+    r = torch.empty(0, device=DEV)
+    gate = torch.ones((4, 64), device=DEV, dtype=torch.bfloat16)
+    y, h, a, b = nl.sandwich_rms(x, x, None, gate)
+    assert y.shape == h.shape == (0, 64)
+    dx, dr, dp, dg, dn = nl.sandwich_rms_grad(x, x, x, r, r, None, gate, None, None)
+    assert not dp.any() and not dg.any() and not dn.any() and dg.shape == (4, 64)
+
+
+@pytest.mark.parametrize("H", [64, 1001, 5120, 16384])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_join_bad_rows_stay_alone(H, bad):
+    """A row with a NaN or an infinity leaves the other rows' bits as they were."""
+    c = join_inputs(9, H, torch.bfloat16, torch.bfloat16, 1, seed=2)
+    want = nl.sandwich_rms(c["x"], c["res"], c["gpost"], c["gate"], c["gpre"])
+    x = c["x"].clone()
+    x[4, H // 2] = bad
+    got = nl.sandwich_rms(x, c["res"], c["gpost"], c["gate"], c["gpre"])
+    keep = [i for i in range(9) if i != 4]
+    for a, b in zip(got, want):
+        assert torch.equal(a[keep], b[keep])
+    assert not torch.isfinite(got[0][4]).all()
+
+
+def test_join_cancelling_stream():
+    """A block output that cancels the stream almost everywhere: the second
+    norm's sum is far smaller than its terms.  The rows are exact multiples, so
+    the bound is that of the terms."""
+    N, H = 16, 2048
+    x = rnd((N, H), 3, torch.float32)
+    x = torch.sign(x)  # rstd of x is 1 up to eps
+    res = -x.clone()
+    res[:, 5] += 0.01
+    c = dict(x=x, res=res, gpost=torch.ones(H, device=DEV), gate=None, gpre=torch.ones(H, device=DEV))
+    out = nl.sandwich_rms(x, res, c["gpost"], None, c["gpre"], 1e-6)
+    check_join(c, out, 1e-6, 1.0, True, True)
+
+
+def test_join_zero_rows():
+    """Rows of zeros: the norms give eps^-1/2 and zeros, no NaN."""
+    x = torch.zeros((4, 512), device=DEV, dtype=torch.bfloat16)
+    y, h, a, b = nl.sandwich_rms(x, x, eps=1e-4)
+    assert not y.any() and not h.any() and torch.allclose(a, torch.full_like(a, 100.0)) and torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ lookup
+
+@pytest.mark.parametrize("it", [torch.int32, torch.int64])
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("N,H,V", [(1, 1, 1), (1, 4096, 50), (8, 1000, 7), (33, 1001, 100), (700, 512, 2000), (18, 2056, 9),
+                                   (40, 5120, 30), (5, 16384, 6), (3, 16390, 4), (2, 40008, 3), (1000, 64, 500)])
+def test_lookup(N, H, V, dt, it):
+    table = rnd((V, H), H, DT[dt])
+    gamma = rnd((H,), 2, DT["f32"] if H % 2 else DT[dt], 1.0, 0.1)
+    tokens = torch.from_numpy(np.random.default_rng(N).integers(0, V, N)).to(DEV, it)
+    y, h, rstd = nl.embedding_rms(tokens, table, gamma, 1e-5, 1.5)
+    only = nl.embedding_lookup(tokens, table, 1.5)
+    torch.cuda.synchronize()
+    assert torch.equal(only, h) and _lib.device_errors() == 0
+    ry, rh, rr = S.lookup_forward(tokens.tolist(), n64(table), 1.5, n64(gamma), 1e-5)
+    k = steps(H) * U
+    close(h, rh, U * np.abs(rh), "h")
+    close(rstd, rr, k * rr, "rstd")
+    close(y, ry, 2 * k * np.abs(ry), "y")
+
+
+@pytest.mark.parametrize("H", [64, 1001, 2048])
+def test_lookup_bad_tokens(H):
+    table = rnd((10, H), 1, torch.bfloat16)
+    tokens = torch.tensor([3, 10, -1, 9, 2 ** 40, 0], device=DEV)
+    y, h, rstd = nl.embedding_rms(tokens, table, None, 1e-4)
+    torch.cuda.synchronize()
+    assert _lib.device_errors() == _lib.NORM_DEVICE_ERR_BAD_TOKEN
+    assert not h[[1, 2, 4]].any() and not y[[1, 2, 4]].any()
+    assert torch.equal(h[[0, 3, 5]], table[[3, 9, 0]])
+    dt = nl.embedding_grad(h, tokens, 10)
+    torch.cuda.synchronize()
+    assert _lib.device_errors() == _lib.NORM_DEVICE_ERR_BAD_TOKEN
+    assert torch.equal(dt[[3, 9, 0]], h[[0, 3, 5]]) and not dt[[1, 2, 4, 5, 6, 7, 8]].any()
+    nl.embedding_lookup(tokens[:1], table)
+    torch.cuda.synchronize()
+    assert _lib.device_errors() == 0
+
+
+def test_lookup_shapes_strides_margins():
+    big = rnd((20, 300), 1, torch.float16)
+    table = big[:, 3:260]  # padded, misaligned rows
+    tokens = torch.arange(12, device=DEV).view(3, 4)
+    g = Guarded((3, 4, 257), torch.float16, DEV)
+    h = nl.embedding_lookup(tokens, table, 0.5, out=g.t)
+    torch.cuda.synchronize()
+    assert h.shape == (3, 4, 257) and g.ok()
+    assert torch.equal(h.view(12, 257), (table[:12].float() * 0.5).half())
+    assert nl.embedding_lookup(tokens[:0], table).shape == (0, 4, 257)
+    with pytest.raises(ValueError, match="contiguous"):
+        nl.embedding_lookup(tokens.t(), table)
+    with pytest.raises(TypeError, match="int32 or int64"):
+        nl.embedding_lookup(tokens.float(), table)
+
+
+KINDS = ["uniform", "skewed", "one", "distinct", "padded", "two"]
+
+
+def make_tokens(kind, N, V):
+    r = np.random.default_rng(N + V)
+    if kind == "uniform":
+        t = r.integers(0, V, N)
+    elif kind == "skewed":
+        t = np.clip(np.floor(np.exp(r.random(N) * np.log(V + 1))) - 1, 0, V - 1).astype(np.int64)
+    elif kind == "one":
+        t = np.full(N, V // 2)
+    elif kind == "distinct":
+        t = r.permutation(max(N, V))[:N] % V
+    elif kind == "two":
+        t = np.where(r.random(N) < 0.5, 0, V - 1)
+    else:
+        t = np.where(r.random(N) < 0.4, V - 1, r.integers(0, V, N))
+    return t
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("N,H,V,dt,odt", [(1, 64, 5, "bf16", "bf16"), (31, 8, 1, "f32", "f32"), (32, 100, 40, "bf16", "f32"),
+                                          (33, 1001, 600, "f16", "f16"), (65, 256, 513, "bf16", "bf16"),
+                                          (2000, 48, 70000, "bf16", "f32"), (5000, 16, 300000, "f32", "f32"),
+                                          (3333, 520, 1000, "f16", "f32"), (300, 4104, 64, "bf16", "bf16"),
+                                          (9000, 24, 511, "f32", "f32")])
+def test_lookup_grad(kind, N, H, V, dt, odt):
+    tokens = make_tokens(kind, N, V)
+    pad = V - 1 if kind == "padded" else -1
+    dh = rnd((N, H), N, DT[dt])
+    tok = torch.from_numpy(tokens).to(DEV, torch.int32 if N % 2 else torch.int64)
+    g = Guarded((V, H), DT[odt], DEV)
+    out = nl.embedding_grad(dh, tok, V, 1.5, padding_idx=None if pad < 0 else pad, out=g.t)
+    torch.cuda.synchronize()
+    assert out is g.t and g.ok() and _lib.device_errors() == 0
+    d = n64(dh)
+    ref = S.lookup_backward(d, tokens, V, 1.5, pad)
+    terms = S.lookup_backward(np.abs(d), tokens, V, 1.5, pad)
+    # serial additions: 32 in a tile, the tiles of an id, and its scale
+    counts = np.bincount(tokens, minlength=V)[:, None]
+    close(out, ref, (40 + counts / 32) * U * terms, "dtable")
+    # absent rows are exact zeros, a second call gives the same bits
+    keep = out.clone()
+    assert not keep[torch.from_numpy((counts[:, 0] == 0) | (np.arange(V) == pad)).to(DEV)].any()
+    again = nl.embedding_grad(dh, tok, V, 1.5, padding_idx=None if pad < 0 else pad, param_dtype=DT[odt])
+    assert torch.equal(keep, again)
+    # accumulated into what is there: only the named rows change, by the same sums
+    base = rnd((V, H), 9, DT[odt])
+    acc = nl.embedding_grad(dh, tok, V, 1.5, padding_idx=None if pad < 0 else pad, out=base.clone(), accumulate=True)
+    torch.cuda.synchronize()
+    b = n64(base)
+    close(acc, ref + b, (42 + counts / 32) * U * (terms + np.abs(b)), "dtable accumulated")
+    absent = torch.from_numpy((counts[:, 0] == 0) | (np.arange(V) == pad)).to(DEV)
+    assert torch.equal(acc[absent], base[absent])
+
+
+def test_lookup_grad_strided_table_and_none():
+    N, H, V = 50, 96, 30
+    dh = rnd((N, H), 1, torch.bfloat16)
+    tok = torch.from_numpy(make_tokens("uniform", N, V)).to(DEV)
+    for ld, off in ((104, 8), (99, 1)):
+        view, buf, rest = padded(torch.ones((V, H), dtype=torch.bfloat16, device=DEV), ld, off)
+        out = nl.embedding_grad(dh, tok, V, out=view)
+        torch.cuda.synchronize()
+        assert torch.all(buf[rest] == -77.0)
+        assert torch.equal(out.contiguous(), nl.embedding_grad(dh, tok, V))
+    none = nl.embedding_grad(dh[:0], tok[:0], V)
+    assert none.shape == (V, H) and not none.any()
+    kept = torch.ones((V, H), device=DEV)
+    nl.embedding_grad(dh[:0], tok[:0], V, out=kept, accumulate=True)
+    assert torch.all(kept == 1)
+    with pytest.raises(ValueError, match="padding_idx"):
+        nl.embedding_grad(dh, tok, V, padding_idx=V)
+    with pytest.raises(ValueError, match="accumulate"):
+        nl.embedding_grad(dh, tok, V, accumulate=True)
+    with pytest.raises(ValueError, match="rows for"):
+        nl.embedding_grad(dh, tok[:-1], V)
+
+
+# ------------------------------------------------------------------ together
+
+def test_join_refusals_of_tensors():
+    x = torch.zeros((6, 64), device=DEV, dtype=torch.bfloat16)
+    r = torch.ones(6, device=DEV)
+    v = torch.ones(64, device=DEV)
+    with pytest.raises(ValueError, match="divide"):
+        nl.sandwich_rms(x, x.clone(), gate=torch.ones((4, 64), device=DEV))
+    with pytest.raises(ValueError, match="columns"):
+        nl.sandwich_rms(x, x.clone(), gate=torch.ones(63, device=DEV))
+    with pytest.raises(TypeError, match="gate"):
+        nl.sandwich_rms(x, x.clone(), gate=torch.ones(64, device=DEV, dtype=torch.float16))
+    with pytest.raises(ValueError, match="post_norm"):
+        nl.sandwich_rms(x, x.clone(), v, post_norm=False)
+    with pytest.raises(nl.NormError):
+        nl.sandwich_rms(x, x.clone(), post_norm=False, pre_norm=False)
+    with pytest.raises(nl.NormError):
+        nl.sandwich_rms(x, x.clone(), out=x)
+    with pytest.raises(ValueError, match="come together"):
+        nl.sandwich_rms_grad(x, x, None, r, r)
+    with pytest.raises(ValueError, match="no norm"):
+        nl.sandwich_rms_grad(None, x, None, None, None, dh_in=x)
+    with pytest.raises(ValueError, match="no gradient"):
+        nl.sandwich_rms_grad(None, x, None, r, None)
+    with pytest.raises(nl.NormError):
+        nl.sandwich_rms_grad(x, x.clone(), x.clone(), r, r.clone(), workspace=torch.empty(16, device=DEV))
+    with pytest.raises(ValueError, match="elements"):
+        nl.sandwich_rms_grad(x, x.clone(), x.clone(), r[:5], r)
+
+
+def _model(tokens, table, params, gates, steps_, dev):
+    """Tokens -> stream; blocks (a fixed elementwise map stands for each) joined
+    to it; gradients back to the table.  Returns every gradient."""
+    y, h, r = nl.embedding_rms(tokens, table, params[0], 1e-5, 1.5)
+    saved = []
+    for i in range(steps_):
+        x = y * (0.5 + i)
+        y2, h2, rpost, rpre = nl.sandwich_rms(x, h, params[1 + 2 * i], gates[i], params[2 + 2 * i], 1e-5,
+                                              residual_scale=0.9)
+        saved.append((x, h2, rpost, rpre))
+        y, h = y2, h2
+    dy, dh = torch.cos(h), torch.sin(h)
+    grads = []
+    for i in reversed(range(steps_)):
+        x, h2, rpost, rpre = saved[i]
+        dx, dh, dpost, dgate, dpre = nl.sandwich_rms_grad(dy, x, h2, rpost, rpre, params[1 + 2 * i], gates[i],
+                                                          params[2 + 2 * i], dh, residual_scale=0.9)
+        dy = dx * (0.5 + i)
+        grads += [dpost, dgate, dpre]
+    h0 = nl.embedding_lookup(tokens, table, 1.5)
+    dh0, _, dg = nl.fused_add_rms_backward(dy, h0, r, params[0], dh, residual_grad="none")
+    return [y, h, *grads, dg, nl.embedding_grad(dh0, tokens, table.shape[0], 1.5)]
+
+
+def _model_inputs(H=512, V=300, B=4, T=25, dt=torch.float32):
+    table = rnd((V, H), 1, dt)
+    params = [rnd((H,), 10 + i, dt, 1.0, 0.1) for i in range(5)]
+    gates = [rnd((B, 1, H), 20, dt, 0.5, 0.3), rnd((H,), 21, dt, 0.5, 0.3)]
+    tokens = torch.from_numpy(make_tokens("skewed", B * T, V)).view(B, T).to(DEV)
+    return tokens, table, params, gates
+
+
+def test_stream_end_to_end_is_autograd():
+    """Lookup, two joins and all their gradients in fp32 against torch autograd
+    in 64 bits.  Eight operators of at most 2K steps each in a row, each step
+    relative to terms a few times the values: 64 K U of the largest value."""
+    tokens, table, params, gates = _model_inputs()
+    got = _model(tokens, table, params, gates, 2, DEV)
+    leaf = [t.double().requires_grad_() for t in [table, *params, *gates]]
+    tab, ps, gs = leaf[0], leaf[1:6], leaf[6:]
+
+    def norm(v, g):
+        return v / torch.sqrt((v * v).mean(-1, keepdim=True) + 1e-5) * g
+
+    h = 1.5 * tab[tokens]
+    y = norm(h, ps[0])
+    for i in range(2):
+        h = 0.9 * h + gs[i] * norm(y * (0.5 + i), ps[1 + 2 * i])
+        y = norm(h, ps[2 + 2 * i])
+    torch.autograd.backward([y, h], [torch.cos(got[1]).double(), torch.sin(got[1]).double()])
+    want = [y, h, ps[3].grad, gs[1].grad, ps[4].grad, ps[1].grad, gs[0].grad, ps[2].grad, ps[0].grad, tab.grad]
+    for i, (a, b) in enumerate(zip(got, want)):
+        b = b.detach()
+        err = (a.double() - b.view(a.shape)).abs().max().item()
+        assert err <= 64 * steps(512) * U * b.abs().max().item(), (i, err)
+
+
+def test_stream_captured_and_on_other_streams():
+    """The whole run captured into two graphs, replayed in turn and on another
+    stream, gives the eager call's bits with new inputs too."""
+    tokens, table, params, gates = _model_inputs(dt=torch.bfloat16)
+    want = _model(tokens, table, params, gates, 2, DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = _model(tokens, table, params, gates, 2, DEV)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(want, other))
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs = _model(tokens, table, params, gates, 2, DEV)
+        graphs.append((g, outs))
+    for k in range(2):
+        if k:
+            tokens.copy_(torch.flip(tokens, [1]))
+            table.mul_(0.5)
+            want = _model(tokens, table, params, gates, 2, DEV)
+        for g, outs in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for g, outs in graphs:
+            assert all(torch.equal(a, b) for a, b in zip(want, outs))
