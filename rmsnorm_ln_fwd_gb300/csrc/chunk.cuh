@@ -1,0 +1,170 @@
+// A thread's share of a row: 32 bytes (E = 16 half-precision or 8 fp32
+// columns), as NG granules of GB bytes.  A warp owns 1024 contiguous bytes of
+// the row: granule g of lane l holds the GE columns from 32*GE*g + GE*l of the
+// warp's, so every access of a warp is contiguous and a thread reaches its
+// granules from one pointer at constant offsets.  GB is 32 where rows are
+// 32-byte aligned (one 256-bit access), 16 where they are 16-byte aligned, and
+// one element otherwise: odd widths and shifted rows run the same kernels, only
+// with narrower accesses.
+#pragma once
+
+#include "common.cuh"
+
+namespace normk {
+
+template <typename D, int GB>
+struct Chunk {
+  using T = typename D::T;
+  static constexpr int ES = (int)sizeof(T);
+  static constexpr int E = 32 / ES;        // columns a thread
+  static constexpr int NP = E / 2;         // fp32 pairs
+  static constexpr int NG = 32 / GB;       // granules
+  static constexpr int GE = GB / ES;       // columns a granule
+  static_assert(GB == 32 || GB == 16 || GB == ES, "granule");
+
+  // First column of thread t of a row group, and column of its e-th element
+  // from there.
+  __device__ static __forceinline__ int base(int t) { return (t >> 5) * (32 * E) + (t & 31) * GE; }
+  __device__ static __forceinline__ constexpr int col(int e) { return (e / GE) * (32 * GE) + e % GE; }
+
+  // Load the thread's columns from its first, `p` (those `lim` columns or more
+  // behind it lie past the row: zeros), as packed words.
+  __device__ static __forceinline__ void load(const T* p, int lim, uint32_t (&w)[8]) {
+    if constexpr (GB == 32) {
+      if (0 < lim) {
+        ld_stream32(p, w);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = 0u;
+      }
+    } else if constexpr (GB == 16) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const uint4 u = col(g * GE) < lim ? ld_stream(p + col(g * GE)) : make_uint4(0u, 0u, 0u, 0u);
+        w[4 * g] = u.x;
+        w[4 * g + 1] = u.y;
+        w[4 * g + 2] = u.z;
+        w[4 * g + 3] = u.w;
+      }
+    } else if constexpr (ES == 4) {
+#pragma unroll
+      for (int g = 0; g < 8; ++g) w[g] = col(g) < lim ? ldg32(p + col(g)) : 0u;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t lo = col(2 * k) < lim ? ldg16(p + col(2 * k)) : 0u;
+        const uint32_t hi = col(2 * k + 1) < lim ? ldg16(p + col(2 * k + 1)) : 0u;
+        w[k] = __byte_perm(lo, hi, 0x5410);
+      }
+    }
+  }
+
+  __device__ static __forceinline__ void store(T* p, int lim, const uint32_t (&w)[8]) {
+    if constexpr (GB == 32) {
+      if (0 < lim) st_vec32(p, w);
+    } else if constexpr (GB == 16) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        if (col(g * GE) < lim) st_vec(p + col(g * GE), make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]));
+    } else if constexpr (ES == 4) {
+#pragma unroll
+      for (int g = 0; g < 8; ++g)
+        if (col(g) < lim) reinterpret_cast<uint32_t*>(p)[col(g)] = w[g];
+    } else {
+#pragma unroll
+      for (int g = 0; g < 16; ++g)
+        if (col(g) < lim) reinterpret_cast<uint16_t*>(p)[col(g)] = (uint16_t)(w[g / 2] >> (16 * (g & 1)));
+    }
+  }
+
+  // Multiply f by the thread's parameters, p the row's (nullptr: ones); 0 past
+  // the row.
+  __device__ static __forceinline__ void scale_by_param(const void* p, bool f32, int b, int lim, float (&f)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float v = col(e) < lim ? (p ? load_param<D>(p, b + col(e), f32) : 1.f) : 0.f;
+      f[e] *= v;
+    }
+  }
+
+  __device__ static __forceinline__ uint32_t ldg32(const T* p) {
+    uint32_t v;
+    asm volatile("ld.global.L1::no_allocate.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+  }
+  __device__ static __forceinline__ uint32_t ldg16(const T* p) {
+    uint32_t v;
+    asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+  }
+};
+
+// fp32 parameters of a thread in shared memory: NV vectors of E floats, then 4
+// floats of padding, so that the 16-byte reads of eight consecutive threads
+// fall into distinct banks (the stride is 4 mod 32 words for E = 16 and even
+// NV, 20 for the others).
+template <int E, int NV>
+__host__ __device__ constexpr int param_slot() { return NV * E + 4; }
+
+template <int E>
+__device__ __forceinline__ void put_params(float* slot, const float (&f)[E]) {
+#pragma unroll
+  for (int q = 0; q < E / 4; ++q)
+    *reinterpret_cast<float4*>(slot + 4 * q) = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+}
+
+// Pairs 2q and 2q + 1 of a parameter vector.
+__device__ __forceinline__ void get_pairs(const float* slot, int q, float2 (&p)[2]) {
+  const float4 v = *reinterpret_cast<const float4*>(slot + 4 * q);
+  p[0] = make_float2(v.x, v.y);
+  p[1] = make_float2(v.z, v.w);
+}
+
+// Sum four values over a row group of nw <= 32 warps, as group_sum: the warp
+// stage is a reduce-scatter (six shuffles; value k ends in lanes 8k..8k+7).
+// `sh` holds 2*nw*4 floats; parity alternates per call.
+__device__ __forceinline__ void group_sum4(float (&v)[4], float* sh, int nw, int wig, int lane, int bar_id, int parity) {
+  const bool hi4 = (lane & 16) != 0;
+  float k0 = hi4 ? v[2] : v[0], k1 = hi4 ? v[3] : v[1];
+  k0 += __shfl_xor_sync(0xffffffffu, hi4 ? v[0] : v[2], 16);
+  k1 += __shfl_xor_sync(0xffffffffu, hi4 ? v[1] : v[3], 16);
+  const bool hi3 = (lane & 8) != 0;
+  float k = hi3 ? k1 : k0;
+  k += __shfl_xor_sync(0xffffffffu, hi3 ? k0 : k1, 8);
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) k += __shfl_xor_sync(0xffffffffu, k, off);
+  if (nw == 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, k, 8 * i);
+    return;
+  }
+  float* buf = sh + parity * nw * 4;
+  if ((lane & 7) == 0) buf[wig * 4 + (lane >> 3)] = k;
+  named_barrier(bar_id, nw * 32);
+  const int P = pow2_ceil(nw);
+  const int src = lane & (P - 1);
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (src < nw) s = *reinterpret_cast<const float4*>(buf + 4 * src);
+  v[0] = s.x;
+  v[1] = s.y;
+  v[2] = s.z;
+  v[3] = s.w;
+  warp_sum_pow2<4>(v, P);
+}
+
+// Granule that every given row tensor allows: 32, 16 or one element.
+struct GranuleRule {
+  unsigned long long bits = 0;
+  void add(const void* p, int64_t ld, size_t es) {
+    bits |= (unsigned long long)reinterpret_cast<uintptr_t>(p) | (unsigned long long)(ld * (int64_t)es);
+  }
+  int bytes(int H, size_t es) const {
+    const unsigned long long b = bits | (unsigned long long)H * es;
+    return (b & 31u) == 0 ? 32 : (b & 15u) == 0 ? 16 : (int)es;
+  }
+};
+
+// Threads a row: one 32-byte share each, whole warps.
+inline int chunk_threads(int64_t H, size_t es) { return (int)((H * (int64_t)es + 32 * 32 - 1) / (32 * 32) * 32); }
+
+}  // namespace normk

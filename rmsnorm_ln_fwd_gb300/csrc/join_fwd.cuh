@@ -13,6 +13,7 @@
 
 #include <algorithm>
 
+#include "chunk.cuh"
 #include "common.cuh"
 #include "stream.h"
 
@@ -78,9 +79,252 @@ __global__ void __launch_bounds__(kJoinLoopThreads) join_loop_kernel(const JoinA
   }
 }
 
+// Register rows.  A row group of tpr threads, 32 bytes of each tensor a thread
+// (chunk.cuh), walks its rows with the next row's x and residual already in
+// flight; gate*gamma_post and gamma_pre are products formed once (and again at
+// a new gate row) in the thread's own shared-memory slot, so no barrier guards
+// them.
+//
+// One reduction a row in place of two.  With w = gate*gamma_post and the
+// reciprocal norm r of x,
+//   sum(h^2) = sum((alpha*res)^2) + 2 r sum(alpha*res * w*x) + r^2 sum((w*x)^2),
+// so the three sums meet in the same exchange as sum(x^2).  Where the terms
+// cancel (sum(h^2) under a quarter of them) or overflow, the row takes a second
+// exchange over h itself; every thread holds the same sums, so the branch is
+// uniform.
+//
+// CL > 1: a cluster of CL CTAs shares each row, in parts of equal whole granules
+// (the last one or two may be shorter or empty).
+template <typename D, int GB, int MAXT, int MINB, int CL>
+__global__ void __launch_bounds__(MAXT, MINB) join_rows_kernel(const JoinArgs a, const int tpr) {
+  using C = Chunk<D, GB>;
+  using T = typename D::T;
+  constexpr int E = C::E, NP = C::NP;
+  constexpr int SLOT = param_slot<E, 2>();
+  extern __shared__ __align__(16) float sh_join[];
+  __shared__ float xch[2][CL * 4], xch2[2][CL * 4];
+  __shared__ uint64_t xbar[2], xbar2[2];
+  __shared__ int xabort;
+  const int rpc = blockDim.x / tpr;
+  const int group = threadIdx.x / tpr;
+  const int t = threadIdx.x - group * tpr;
+  const int nw = tpr >> 5, wig = t >> 5, lane = threadIdx.x & 31;
+  const int crank = CL > 1 ? (int)cluster_ctarank() : 0;
+  // this CTA's columns [c0, c0 + H), the thread's first one c0 + b, `lim` of the
+  // row's columns from there on
+  const int part = CL > 1 ? ((a.H + CL * C::GE - 1) / (CL * C::GE)) * C::GE : a.H;
+  const int c0 = crank * part;
+  const int H = min(part, a.H - c0);  // not positive: nothing is left for this CTA
+  const int b = C::base(t);
+  const int lim = H - b;
+  const float inv_h = 1.f / (float)a.H;
+  const bool w_f32 = a.w_f32 != 0, g_f32 = a.g_f32 != 0;
+  const size_t wes = w_f32 ? 4 : sizeof(T), ges = g_f32 ? 4 : sizeof(T);
+  float* sh = sh_join + group * (2 * nw * 4);
+  float* slot = sh_join + rpc * (2 * nw * 4) + threadIdx.x * SLOT;
+  const int bar_id = 1 + group;
+
+  // this group's rows: strided, or (several gate rows) one contiguous range
+  const int64_t units = (int64_t)(gridDim.x / CL) * rpc, unit = (int64_t)(blockIdx.x / CL) * rpc + group;
+  const bool runs = a.run < a.N;
+  int64_t row = unit, end = a.N, step = units;
+  if (runs) {
+    cta_rows(a.N, (int)unit, (int)units, row, end);
+    step = 1;
+  }
+  uint32_t nx[8], nr[8];
+  auto fetch = [&](int64_t r) {
+    C::load(reinterpret_cast<const T*>(a.x) + r * a.ldx + c0 + b, lim, nx);
+    C::load(reinterpret_cast<const T*>(a.res) + r * a.ldr + c0 + b, lim, nr);
+  };
+  if (row < end) fetch(row);
+
+  auto at = [](const void* p, int64_t i, size_t es) -> const void* {
+    return p ? reinterpret_cast<const unsigned char*>(p) + i * es : nullptr;
+  };
+  int64_t gate_end = a.N;  // first row past the gate row in use
+  auto stage_w = [&](int64_t r) {
+    float f[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = 1.f;
+    C::scale_by_param(at(a.gpost, c0, wes), w_f32, b, lim, f);
+    if (a.gate) {
+      const int64_t k = runs ? r / a.run : 0;
+      C::scale_by_param(at(a.gate, k * a.ldg + c0, ges), g_f32, b, lim, f);
+      gate_end = (k + 1) * a.run;
+    }
+    put_params<E>(slot, f);
+  };
+  if (row < end) {
+    stage_w(row);
+    float f[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = 1.f;
+    C::scale_by_param(at(a.gpre, c0, wes), w_f32, b, lim, f);
+    put_params<E>(slot + E, f);
+  }
+  if constexpr (CL > 1) {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&xbar[i], 1);
+        mbar_init(&xbar2[i], 1);
+      }
+      xabort = 0;
+      fence_barrier_init();
+    }
+    cluster_sync_all();  // every CTA's mbarriers exist before any CTA sends to them
+  }
+
+  const float2 alpha2 = splat2(a.alpha);
+  int parity = 0;
+  unsigned it = 0, it2 = 0;
+  for (; row < end; row += step) {
+    if (row >= gate_end) stage_w(row);
+    float2 f[NP];     // w * x, later h
+    uint32_t rw[8];   // residual
+#pragma unroll
+    for (int k = 0; k < 8; ++k) rw[k] = nr[k];
+    float2 sx = splat2(0.f), sa = splat2(0.f), sb = splat2(0.f), sc = splat2(0.f);
+#pragma unroll
+    for (int q = 0; q < NP / 2; ++q) {
+      float2 w[2];
+      get_pairs(slot, q, w);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int p = 2 * q + i;
+        const float2 x = word_pair<D>(nx, p);
+        const float2 r = mul2(word_pair<D>(rw, p), alpha2);
+        f[p] = mul2(x, w[i]);
+        sx = fma2(x, x, sx);
+        sa = fma2(r, r, sa);
+        sb = fma2(r, f[p], sb);
+        sc = fma2(f[p], f[p], sc);
+      }
+    }
+    if (row + step < end) fetch(row + step);
+    float s[4] = {sx.x + sx.y, sa.x + sa.y, sb.x + sb.y, sc.x + sc.y};
+    group_sum4(s, sh, nw, wig, lane, bar_id, parity);
+    parity ^= 1;
+    if constexpr (CL > 1) {
+      cluster_group_sum_async<4, CL>(s, xch[it & 1], &xbar[it & 1], (it >> 1) & 1u, crank, a.err, &xabort);
+      ++it;
+    }
+    const float rp = a.post ? rsqrtf(s[0] * inv_h + a.eps) : 1.f;
+    const float2 rp2 = splat2(rp);
+    T* hrow = reinterpret_cast<T*>(a.h) + row * a.ldh + c0 + b;
+    uint32_t out[8];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      f[p] = fma2(f[p], rp2, mul2(word_pair<D>(rw, p), alpha2));
+      pair_word<D>(out, p, f[p]);
+    }
+    C::store(hrow, lim, out);
+    const bool writer = t == 0 && crank == 0;
+    if (writer && a.rpost) a.rpost[row] = rp;
+    if (!a.pre) continue;
+    const float terms = fmaf(rp * rp, s[3], s[1]);
+    float ss = fmaf(2.f * rp, s[2], terms);
+    if (!(ss < __int_as_float(0x7f800000)) || 4.f * ss < terms) {
+      float2 h2 = splat2(0.f);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) h2 = fma2(f[p], f[p], h2);
+      float v[4] = {h2.x + h2.y, 0.f, 0.f, 0.f};
+      group_sum4(v, sh, nw, wig, lane, bar_id, parity);
+      parity ^= 1;
+      if constexpr (CL > 1) {
+        cluster_group_sum_async<1, CL>(reinterpret_cast<float(&)[1]>(v), xch2[it2 & 1], &xbar2[it2 & 1],
+                                       (it2 >> 1) & 1u, crank, a.err, &xabort);
+        ++it2;
+      }
+      ss = v[0];
+    }
+    const float rn = rsqrtf(ss * inv_h + a.eps);
+    if (writer && a.rpre) a.rpre[row] = rn;
+    const float2 rn2 = splat2(rn);
+#pragma unroll
+    for (int q = 0; q < NP / 2; ++q) {
+      float2 g[2];
+      get_pairs(slot + E, q, g);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) pair_word<D>(out, 2 * q + i, mul2(mul2(f[2 * q + i], rn2), g[i]));
+    }
+    C::store(reinterpret_cast<T*>(a.y) + row * a.ldy + c0 + b, lim, out);
+  }
+  if constexpr (CL > 1) cluster_sync_all();  // no CTA leaves while a partner may still write to it
+}
+
+template <typename D, int GB, int MAXT, int MINB, int CL>
+static cudaError_t run_join_rows(const JoinArgs& a, int tpr, int rpc, const DeviceInfo& dev, cudaStream_t s) {
+  auto kern = join_rows_kernel<D, GB, MAXT, MINB, CL>;
+  const int threads = rpc * tpr;
+  const size_t smem = sizeof(float) * ((size_t)rpc * 2 * (tpr / 32) * 4 + (size_t)threads * param_slot<Chunk<D, GB>::E, 2>());
+  if (smem > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t want = std::min<int64_t>((a.N + rpc - 1) / rpc, 1 << 20);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(CL * want));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  int resident = 0;
+  if (CL > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CL;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&resident, kern, &cfg) != cudaSuccess) resident = 1;
+  } else {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kern, threads, smem) != cudaSuccess) resident = 1;
+    resident *= dev.sm_count;
+  }
+  cfg.gridDim = dim3((unsigned)(CL * std::max<int64_t>(1, std::min<int64_t>(want, resident))));
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, tpr);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+template <typename D, int GB>
+static cudaError_t run_join(const JoinArgs& a, const DeviceInfo& dev, cudaStream_t s, bool* done) {
+  using T = typename D::T;
+  *done = true;
+  const int tpr = chunk_threads(a.H, sizeof(T));
+  if (tpr <= 256) return run_join_rows<D, GB, 256, (GB >= 16 ? 3 : 2), 1>(a, tpr, 256 / tpr, dev, s);
+  if (tpr <= kRowsAutoMaxThreads) return run_join_rows<D, GB, kRowsAutoMaxThreads, 1, 1>(a, tpr, 1, dev, s);
+  // wider rows: the smallest cluster with parts of at most 512 threads
+  auto threads = [&](int cl) {
+    constexpr int GE = Chunk<D, GB>::GE;
+    return chunk_threads((a.H + cl * GE - 1) / (cl * GE) * GE, sizeof(T));
+  };
+  if (threads(2) <= 512) return run_join_rows<D, GB, 512, 1, 2>(a, threads(2), 1, dev, s);
+  if (threads(4) <= 512) return run_join_rows<D, GB, 512, 1, 4>(a, threads(4), 1, dev, s);
+  if (threads(8) <= 512) return run_join_rows<D, GB, 512, 1, 8>(a, threads(8), 1, dev, s);
+  *done = false;
+  return cudaSuccess;
+}
+
 template <typename D>
 cudaError_t launch_join(JoinArgs a, const DeviceInfo& dev, cudaStream_t s) {
   (void)cudaGetLastError();  // drop a stale, non-sticky error left by an earlier call
+  using T = typename D::T;
+  a.err = dev.err;
+  if (dev.path != PATH_LOOP) {
+    GranuleRule rule;
+    rule.add(a.x, a.ldx, sizeof(T));
+    rule.add(a.res, a.ldr, sizeof(T));
+    rule.add(a.h, a.ldh, sizeof(T));
+    if (a.pre) rule.add(a.y, a.ldy, sizeof(T));
+    const int gb = rule.bytes(a.H, sizeof(T));
+    bool done = false;
+    cudaError_t e = gb == 32   ? run_join<D, 32>(a, dev, s, &done)
+                    : gb == 16 ? run_join<D, 16>(a, dev, s, &done)
+                               : run_join<D, (int)sizeof(T)>(a, dev, s, &done);
+    if (done) return e;
+  }
   const int64_t blocks = std::min<int64_t>(a.N, (int64_t)dev.sm_count * 8);
   join_loop_kernel<D><<<(unsigned)blocks, kJoinLoopThreads, 0, s>>>(a);
   return cudaGetLastError();

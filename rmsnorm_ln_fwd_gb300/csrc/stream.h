@@ -35,6 +35,7 @@ struct JoinArgs {
   float alpha;
   int post, pre;     // which norms are taken
   int w_f32, g_f32;  // gammas / gate are fp32 (else the row dtype)
+  unsigned* err;     // device error word (bounded waits; filled in by the launcher)
 };
 
 // Its gradient.  Partial rows (fp32, Hp apart): ws_pre[P] for dgamma_pre,
