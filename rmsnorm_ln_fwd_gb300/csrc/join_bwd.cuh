@@ -29,6 +29,7 @@
 
 #include <algorithm>
 
+#include "chunk.cuh"
 #include "common.cuh"
 #include "stream.h"
 
@@ -133,6 +134,431 @@ __global__ void __launch_bounds__(kJoinGradLoopThreads) join_grad_loop_kernel(co
       }
     }
   }
+}
+
+// Rows through shared memory.  A row group of tpr threads, 32 bytes of each
+// tensor a thread (chunk.cuh), takes its rows from a ring of NB row buffers of
+// its own: one thread bulk-copies the next rows of dy, dh_in, h and x, each
+// completing on the buffer's mbarrier, and refills a buffer when the row sums'
+// barrier has passed (every thread has then read it).  No registers hold a row
+// in flight, which leaves them to the two accumulators (dgamma_pre, and A for
+// gate and gamma_post) and to the row's own terms.  Shared memory is read 16
+// bytes a lane, a warp's reads contiguous, whatever the rows' alignment.
+//
+// Rows that are not 16-byte aligned (GB = one element): the copy takes the
+// whole 16-byte lines inside the row, and the up to 15 bytes at either end come
+// by ordinary loads of the group's first warp, issued with the copy and put
+// into the buffer a row later.
+//
+// CL > 1: a cluster of CL CTAs shares each row in parts of equal whole granules;
+// the row sums meet through distributed shared memory.
+constexpr int kJoinRowTensors = 4;  // dy, dh_in, h, x
+constexpr int kJoinMaxBuffers = 4;
+
+struct JoinRing {
+  int tpr, rpc, nb;
+  int part;        // columns a CTA of the cluster takes
+  int buf_bytes;   // of one tensor's part of a row
+  int red_off, par_off, buf_off, total;
+};
+
+template <int E>
+inline JoinRing join_ring(int H, int es, int ge, int cl, bool runs, int max_smem) {
+  JoinRing r{};
+  r.part = (H + cl * ge - 1) / (cl * ge) * ge;
+  r.tpr = chunk_threads(r.part, es);
+  r.rpc = cl == 1 && r.tpr <= 256 ? 256 / r.tpr : 1;
+  r.buf_bytes = (r.part * es + 16 + 127) & ~127;
+  r.red_off = (r.rpc * kJoinMaxBuffers * 8 + 16 + 15) & ~15;
+  r.par_off = r.red_off + r.rpc * 2 * (r.tpr / 32) * 3 * 4;
+  r.par_off = (r.par_off + 15) & ~15;
+  const int slot = runs ? param_slot<E, 3>() : param_slot<E, 2>();
+  r.buf_off = (r.par_off + r.rpc * r.tpr * slot * 4 + 127) & ~127;
+  const int stage = r.rpc * kJoinRowTensors * r.buf_bytes;
+  r.nb = std::min(kJoinMaxBuffers, (max_smem - r.buf_off) / stage);
+  const int fold = r.rpc > 1 ? r.rpc * r.tpr * E * 4 : 0;  // the groups' accumulators, after the rows
+  r.total = r.buf_off + std::max(r.nb * stage, fold);
+  return r;
+}
+
+template <typename D, int GB, bool RUNS, int MAXT, int MINB, int CL>
+__global__ void __launch_bounds__(MAXT, MINB) join_grad_rows_kernel(const JoinGradArgs a, const JoinRing ring) {
+  using C = Chunk<D, GB>;
+  using T = typename D::T;
+  constexpr int E = C::E, NP = C::NP, ES = C::ES;
+  constexpr bool EDGES = GB < 16;
+  constexpr int SLOT = param_slot<E, RUNS ? 3 : 2>();
+  extern __shared__ __align__(128) unsigned char sm_join[];
+  __shared__ float xch[2][CL * 4];
+  __shared__ uint64_t xbar[2];
+  const int tpr = ring.tpr;
+  const int group = threadIdx.x / tpr;
+  const int t = threadIdx.x - group * tpr;
+  const int nw = tpr >> 5, wig = t >> 5, lane = threadIdx.x & 31;
+  const int crank = CL > 1 ? (int)cluster_ctarank() : 0;
+  const int c0 = crank * ring.part;
+  const int H = min(ring.part, a.H - c0);  // this CTA's columns (not positive: none)
+  const int b0 = C::base(t);
+  const int lim = H - b0;
+  const float inv_h = 1.f / (float)a.H;
+  const bool w_f32 = a.w_f32 != 0, g_f32 = a.g_f32 != 0;
+  const size_t wes = w_f32 ? 4 : sizeof(T), ges = g_f32 ? 4 : sizeof(T);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm_join) + group * kJoinMaxBuffers;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm_join + ring.rpc * kJoinMaxBuffers * 8);
+  float* red = reinterpret_cast<float*>(sm_join + ring.red_off) + group * (2 * nw * 3);
+  float* slot = reinterpret_cast<float*>(sm_join + ring.par_off) + threadIdx.x * SLOT;
+  unsigned char* bufs = sm_join + ring.buf_off + (size_t)group * ring.nb * kJoinRowTensors * ring.buf_bytes;
+  const int bar_id = 1 + group;
+  const int NB = ring.nb;
+
+  const int unit = ((int)blockIdx.x / CL) * ring.rpc + group;
+  int64_t row = unit, end = a.N, step = (int64_t)(gridDim.x / CL) * ring.rpc;
+  if (RUNS) {
+    step = 1;
+    row = end = 0;
+    if (unit < a.U) cta_rows(a.N, unit, a.U, row, end);
+  }
+  const int64_t first_row = row;
+
+  if (t == 0) {
+    for (int i = 0; i < NB; ++i) mbar_init(&bars[i], 1);
+    if (threadIdx.x == 0) *abort_flag = 0;
+    if (CL > 1) {
+      mbar_init(&xbar[0], 1);
+      mbar_init(&xbar[1], 1);
+    }
+    fence_barrier_init();
+  }
+  __syncthreads();
+
+  // Copying a row: the bytes [start, start + H*ES) of each tensor land at
+  // (start mod 16) of its buffer.
+  struct Src {
+    const void* p;
+    int64_t ld;
+  };
+  const Src srcs[kJoinRowTensors] = {{a.dy, a.lddy}, {a.dh_in, a.lddh}, {a.dy ? a.h : nullptr, a.ldh}, {a.x, a.ldx}};
+  auto start_of = [&](int k, int64_t r) {
+    return reinterpret_cast<uintptr_t>(reinterpret_cast<const T*>(srcs[k].p) + r * srcs[k].ld + c0);
+  };
+  const bool copies = H > 0;
+  unsigned used = 0u, fills = 0u;  // per buffer: ever filled; fills issued, mod 2 (thread 0 of the group)
+  auto issue = [&](int64_t r, int buf) {  // by thread 0 of the group
+    uint32_t bytes[kJoinRowTensors], total = 0;
+    uintptr_t from[kJoinRowTensors];
+#pragma unroll
+    for (int k = 0; k < kJoinRowTensors; ++k) {
+      bytes[k] = 0;
+      if (srcs[k].p == nullptr) continue;
+      const uintptr_t s = start_of(k, r), e = s + (uintptr_t)H * ES;
+      from[k] = (s + 15) & ~(uintptr_t)15;
+      const uintptr_t to = e & ~(uintptr_t)15;
+      if (to > from[k]) bytes[k] = (uint32_t)(to - from[k]);
+      total += bytes[k];
+    }
+    mbar_arrive_expect_tx(&bars[buf], total);
+    used |= 1u << buf;
+    fills ^= 1u << buf;
+#pragma unroll
+    for (int k = 0; k < kJoinRowTensors; ++k)
+      if (bytes[k] != 0) {
+        unsigned char* dst = bufs + ((size_t)buf * kJoinRowTensors + k) * ring.buf_bytes;
+        bulk_g2s(dst + (from[k] - (start_of(k, r) & ~(uintptr_t)15)), reinterpret_cast<const void*>(from[k]), bytes[k],
+                 &bars[buf]);
+      }
+  };
+  // The ends of a row that no whole line holds: lane l of the group's first
+  // warp takes elements l and l + 32 of the 4 tensors x {front, back} x 8.
+  T edge[2];
+  int edge_at[2] = {-1, -1};  // byte offset in the row buffers, or none
+  auto edge_fetch = [&](int64_t r, int buf) {
+    if constexpr (EDGES) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        edge_at[j] = -1;
+        if (wig != 0) continue;
+        const int id = lane + 32 * j, k = id >> 4, back = (id >> 3) & 1, i = id & 7;
+        const T* base = nullptr;
+        int64_t ld = 0;
+#pragma unroll
+        for (int q = 0; q < kJoinRowTensors; ++q)
+          if (q == k) {
+            base = reinterpret_cast<const T*>(srcs[q].p);
+            ld = srcs[q].ld;
+          }
+        if (base == nullptr) continue;
+        const uintptr_t s = reinterpret_cast<uintptr_t>(base + r * ld + c0), e = s + (uintptr_t)H * ES;
+        const uintptr_t up = (s + 15) & ~(uintptr_t)15, down = e & ~(uintptr_t)15;
+        uintptr_t from = s, to = up < e ? up : e;  // front
+        if (back) {
+          from = down > up ? down : up;
+          to = e;
+        }
+        const uintptr_t p = from + (uintptr_t)i * ES;
+        if (from >= to || p >= to) continue;
+        edge[j] = *reinterpret_cast<const T*>(p);
+        edge_at[j] = (buf * kJoinRowTensors + k) * ring.buf_bytes + (int)(p - (s & ~(uintptr_t)15));
+      }
+    }
+  };
+  auto edge_store = [&]() {
+    if constexpr (EDGES) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (edge_at[j] >= 0) *reinterpret_cast<T*>(bufs + edge_at[j]) = edge[j];
+        edge_at[j] = -1;
+      }
+    }
+  };
+  if (copies) {
+    for (int i = 0; i < NB; ++i) {
+      if (row + i * step >= end) break;
+      if (t == 0) issue(row + i * step, i);
+      edge_fetch(row + i * step, i);
+      edge_store();
+    }
+  }
+
+  auto at = [](const void* p, int64_t i, size_t es) -> const void* {
+    return p ? reinterpret_cast<const unsigned char*>(p) + i * es : nullptr;
+  };
+  float nrn = 0.f, nro = 1.f;  // the next row's statistics
+  auto fetch_stats = [&](int64_t r) {
+    if (a.rpre) nrn = a.rpre[r];
+    if (a.rpost) nro = a.rpost[r];
+  };
+  if (row < end) fetch_stats(row);
+  int64_t gate_row = 0, gate_end = a.N;
+  auto stage_w = [&](int64_t r) {
+    float f[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = 1.f;
+    C::scale_by_param(a.rpost ? at(a.gpost, c0, wes) : nullptr, w_f32, b0, lim, f);
+    if (a.gate) {
+      gate_row = RUNS ? r / a.run : 0;
+      gate_end = (gate_row + 1) * a.run;
+      C::scale_by_param(at(a.gate, gate_row * a.ldg + c0, ges), g_f32, b0, lim, f);
+    }
+    put_params<E>(slot, f);
+  };
+  {
+    float f[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = 1.f;
+    C::scale_by_param(at(a.gpre, c0, wes), w_f32, b0, lim, f);
+    put_params<E>(slot + E, f);
+    if (row < end) stage_w(row);
+    if constexpr (RUNS) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = 0.f;
+      put_params<E>(slot + 2 * E, f);
+    }
+  }
+  if constexpr (EDGES) named_barrier(bar_id, tpr);  // the first rows' ends are in place
+  if constexpr (CL > 1) cluster_sync_all();         // every CTA's mbarriers exist before any CTA sends to them
+
+  float2 acc_pre[NP], acc[NP];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) acc_pre[p] = acc[p] = splat2(0.f);
+
+  // A run ends (RUNS): its share of dgamma_post, and dgate if it lies in this
+  // unit, else a partial row.
+  auto flush = [&](int64_t k) {
+    if constexpr (RUNS) {
+      const bool whole = k * a.run >= first_row && (k + 1) * a.run <= end;
+      const int64_t part_row = 2 * (int64_t)unit + (!whole && k == first_row / a.run ? 0 : 1);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int c = c0 + b0 + C::col(e);
+        if (C::col(e) < lim) {
+          const float v = (e & 1) ? acc[e / 2].y : acc[e / 2].x;
+          slot[2 * E + e] = fmaf(load_param<D>(at(a.gate, k * a.ldg, ges), c, g_f32), v, slot[2 * E + e]);
+          if (!whole) {
+            if (a.ws_seg) a.ws_seg[part_row * a.Hp + c] = v;
+          } else if (a.dgate) {
+            const float g = v * (a.rpost && a.gpost ? load_param<D>(a.gpost, c, w_f32) : 1.f);
+            if (g_f32)
+              reinterpret_cast<float*>(a.dgate)[k * a.lddg + c] = g;
+            else
+              store_elem<D>(a.dgate, k * a.lddg + c, g);
+          }
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < NP; ++p) acc[p] = splat2(0.f);
+    }
+  };
+
+  const float2 alpha2 = splat2(a.alpha);
+  int parity = 0, buf = 0;
+  unsigned phase = 0u, it = 0;
+  for (; row < end; row += step) {
+    if (RUNS && row >= gate_end) {
+      flush(gate_row);
+      stage_w(row);
+    }
+    const float rn = nrn, ro = nro;
+    if (row + step < end) fetch_stats(row + step);
+    edge_store();
+    bool ok = true;
+    if (copies) ok = mbar_wait(&bars[buf], phase, a.err, abort_flag);
+    auto read = [&](int k, uint32_t (&w)[8]) {
+      if (srcs[k].p == nullptr || !copies) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = 0u;
+        return;
+      }
+      const unsigned char* p = bufs + ((size_t)buf * kJoinRowTensors + k) * ring.buf_bytes;
+      if constexpr (GB >= 16) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          uint4 u = make_uint4(0u, 0u, 0u, 0u);
+          if (C::col(g * C::GE) < lim) u = lds16(p + (size_t)(b0 + C::col(g * C::GE)) * ES);
+          w[4 * g] = u.x;
+          w[4 * g + 1] = u.y;
+          w[4 * g + 2] = u.z;
+          w[4 * g + 3] = u.w;
+        }
+      } else {
+        const unsigned char* q = p + (start_of(k, row) & 15u) + (size_t)b0 * ES;
+        if constexpr (ES == 4) {
+#pragma unroll
+          for (int g = 0; g < 8; ++g)
+            w[g] = C::col(g) < lim ? *reinterpret_cast<const uint32_t*>(q + C::col(g) * 4) : 0u;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t lo = C::col(2 * i) < lim ? *reinterpret_cast<const uint16_t*>(q + C::col(2 * i) * 2) : 0u;
+            const uint32_t hi =
+                C::col(2 * i + 1) < lim ? *reinterpret_cast<const uint16_t*>(q + C::col(2 * i + 1) * 2) : 0u;
+            w[i] = __byte_perm(lo, hi, 0x5410);
+          }
+        }
+      }
+    };
+    uint32_t dyw[8], xw[8], iw[8], hw[8];
+    read(0, dyw);
+    read(1, iw);
+    read(2, hw);
+    read(3, xw);
+    // pass 1: t = dh_in + rstd_pre * g, h_hat, and the three row sums (those
+    // over o_hat = x * rstd_post with rstd_post taken out)
+    float2 tt[NP], hh[NP];
+    float2 s0 = splat2(0.f), s1 = splat2(0.f), s2 = splat2(0.f);
+    const float2 rn2 = splat2(rn);
+#pragma unroll
+    for (int q = 0; q < NP / 2; ++q) {
+      float2 w[2], gp[2];
+      get_pairs(slot, q, w);
+      get_pairs(slot + E, q, gp);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int p = 2 * q + i;
+        const float2 g = mul2(word_pair<D>(dyw, p), gp[i]);
+        const float2 wx = mul2(word_pair<D>(xw, p), w[i]);
+        hh[p] = mul2(word_pair<D>(hw, p), rn2);
+        tt[p] = fma2(g, rn2, word_pair<D>(iw, p));
+        s0 = fma2(g, hh[p], s0);
+        s1 = fma2(wx, tt[p], s1);
+        s2 = fma2(wx, hh[p], s2);
+      }
+    }
+    float s[3] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y};
+    group_sum<3>(s, red, nw, wig, lane, bar_id, parity);
+    parity ^= 1;
+    if (nw == 1) __syncwarp();
+    // every thread has read this buffer: refill it with the row NB ahead
+    const int64_t ahead = row + (int64_t)NB * step;
+    if (ahead < end && copies) {
+      if (t == 0 && !*abort_flag) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        issue(ahead, buf);
+      }
+      edge_fetch(ahead, buf);
+    }
+    if constexpr (CL > 1) {
+      ok &= cluster_group_sum_async<3, CL>(s, xch[it & 1], &xbar[it & 1], (it >> 1) & 1u, crank, a.err, abort_flag);
+      ++it;
+    }
+    const float c = s[0] * inv_h;
+    const float k = a.rpost ? ro * fmaf(-rn * c, s[2], s[1]) * inv_h : 0.f;  // mean(w dh o_hat)
+    const float2 nc2 = splat2(-c * rn), ro2 = splat2(ro), nk2 = splat2(-k * ro * ro);
+    if (ok) {
+      uint32_t od[8], ox[8];
+#pragma unroll
+      for (int q = 0; q < NP / 2; ++q) {
+        float2 w[2];
+        get_pairs(slot, q, w);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int p = 2 * q + i;
+          const float2 x = word_pair<D>(xw, p);
+          const float2 dh = fma2(hh[p], nc2, tt[p]);
+          pair_word<D>(od, p, mul2(dh, alpha2));
+          const float2 dr = mul2(dh, ro2);
+          pair_word<D>(ox, p, fma2(x, nk2, mul2(dr, w[i])));
+          acc_pre[p] = fma2(word_pair<D>(dyw, p), hh[p], acc_pre[p]);
+          acc[p] = fma2(dr, x, acc[p]);
+        }
+      }
+      C::store(reinterpret_cast<T*>(a.dres) + row * a.lddres + c0 + b0, lim, od);
+      C::store(reinterpret_cast<T*>(a.dx) + row * a.lddx + c0 + b0, lim, ox);
+    }
+    if (++buf == NB) {
+      buf = 0;
+      phase ^= 1u;
+    }
+  }
+  if (t == 0) {  // no copy outlives the CTA (they have all been waited for unless a wait ran out)
+    for (int q = 0; q < NB; ++q)  // the last fill of buffer q has parity (fills - 1) mod 2
+      if ((used >> q) & 1u) mbar_wait(&bars[q], ((fills >> q) & 1u) ^ 1u, a.err, nullptr);
+  }
+  if (RUNS && first_row < end) flush(gate_row);
+  if constexpr (CL > 1) cluster_sync_all();  // no CTA leaves while a partner may still write to it
+  if (a.ws_pre == nullptr) return;
+  if constexpr (RUNS) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p) acc[p] = make_float2(slot[2 * E + 2 * p], slot[2 * E + 2 * p + 1]);
+  }
+  // The CTA's partial rows: its groups' accumulators in group order.
+  const int prow = (int)blockIdx.x / CL;
+  auto partial = [&](float2 (&v)[NP], float* ws) {
+    if (ring.rpc > 1) {
+      float* fold = reinterpret_cast<float*>(sm_join + ring.buf_off);
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < NP / 2; ++q)
+        *reinterpret_cast<float4*>(fold + ((size_t)q * blockDim.x + threadIdx.x) * 4) =
+            make_float4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
+      __syncthreads();
+      if (group != 0) return;
+      for (int g = 1; g < ring.rpc; ++g) {
+#pragma unroll
+        for (int q = 0; q < NP / 2; ++q) {
+          const float4 o = *reinterpret_cast<const float4*>(fold + ((size_t)q * blockDim.x + g * tpr + t) * 4);
+          v[2 * q] = add2(v[2 * q], make_float2(o.x, o.y));
+          v[2 * q + 1] = add2(v[2 * q + 1], make_float2(o.z, o.w));
+        }
+      }
+    }
+    float* to = ws + (size_t)prow * a.Hp + c0 + b0;
+#pragma unroll
+    for (int q = 0; q < NP / 2; ++q) {
+      if constexpr (GB >= 16) {
+        if (C::col(4 * q) < lim)
+          *reinterpret_cast<float4*>(to + C::col(4 * q)) =
+              make_float4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = 4 * q + i;
+          if (C::col(e) < lim) to[C::col(e)] = (e & 1) ? v[e / 2].y : v[e / 2].x;
+        }
+      }
+    }
+  };
+  partial(acc_pre, a.ws_pre);
+  partial(acc, a.ws_post);
 }
 
 // The parameter gradients from the partial rows, columns over blockIdx.x.
@@ -290,6 +716,63 @@ __global__ void join_grad_zero_kernel(const JoinGradArgs a) {
     for (int64_t g = 0; g < a.gate_rows; ++g) zero(a.dgate, g * a.lddg + i, a.g_f32);
 }
 
+template <typename D, int GB, bool RUNS, int MAXT, int MINB, int CL>
+static cudaError_t run_join_grad_rows(JoinGradArgs& a, const JoinRing& ring, const DeviceInfo& dev, cudaStream_t s) {
+  auto kern = join_grad_rows_kernel<D, GB, RUNS, MAXT, MINB, CL>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ring.total);
+  if (e != cudaSuccess) return e;
+  const int threads = ring.rpc * ring.tpr;
+  const int64_t cap = std::min<int64_t>(kJoinMaxPartialsPerSm * dev.sm_count, (a.N + ring.rpc - 1) / ring.rpc);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(CL * cap));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = ring.total;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  int resident = 0;
+  if (CL > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CL;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&resident, kern, &cfg) != cudaSuccess) resident = 1;
+  } else {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kern, threads, ring.total) != cudaSuccess) resident = 1;
+    resident *= dev.sm_count;
+  }
+  a.P = (int)std::max<int64_t>(1, std::min<int64_t>(cap, resident));
+  a.U = (int)std::min<int64_t>(a.N, (int64_t)a.P * ring.rpc);
+  cfg.gridDim = dim3((unsigned)(CL * a.P));
+  e = cudaLaunchKernelEx(&cfg, kern, a, ring);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+// The fewest CTAs a row (1, 2, 4, 8) whose part fits 512 threads and at least
+// two row buffers; *done = false where none does.
+template <typename D, int GB, bool RUNS>
+static cudaError_t run_join_grad(JoinGradArgs& a, const DeviceInfo& dev, cudaStream_t s, bool* done) {
+  using C = Chunk<D, GB>;
+  *done = true;
+  for (int cl = 1; cl <= 8; cl *= 2) {
+    const JoinRing two = join_ring<C::E>(a.H, C::ES, C::GE, cl, RUNS, dev.max_smem_optin);
+    if (two.tpr > 512 || two.nb < 2) continue;
+    if (cl == 1 && two.tpr <= 256) {
+      // two CTAs an SM where each still has two buffers
+      const JoinRing half = join_ring<C::E>(a.H, C::ES, C::GE, 1, RUNS, (dev.max_smem_optin - 2048) / 2);
+      return run_join_grad_rows<D, GB, RUNS, 256, 2, 1>(a, half.nb >= 2 ? half : two, dev, s);
+    }
+    if (cl == 1) return run_join_grad_rows<D, GB, RUNS, 512, 1, 1>(a, two, dev, s);
+    if (cl == 2) return run_join_grad_rows<D, GB, RUNS, 512, 1, 2>(a, two, dev, s);
+    if (cl == 4) return run_join_grad_rows<D, GB, RUNS, 512, 1, 4>(a, two, dev, s);
+    return run_join_grad_rows<D, GB, RUNS, 512, 1, 8>(a, two, dev, s);
+  }
+  *done = false;
+  return cudaSuccess;
+}
+
 template <typename D>
 cudaError_t launch_join_grad(JoinGradArgs a, const DeviceInfo& dev, cudaStream_t s) {
   (void)cudaGetLastError();  // drop a stale, non-sticky error left by an earlier call
@@ -298,10 +781,31 @@ cudaError_t launch_join_grad(JoinGradArgs a, const DeviceInfo& dev, cudaStream_t
     join_grad_zero_kernel<D><<<(unsigned)((a.H + 255) / 256), 256, 0, s>>>(a);
     return cudaGetLastError();
   }
-  const int cap = kJoinMaxPartialsPerSm * dev.sm_count;
-  a.P = a.U = (int)std::min<int64_t>(a.N, cap);
-  join_grad_loop_kernel<D><<<(unsigned)a.P, kJoinGradLoopThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  using T = typename D::T;
+  bool done = false;
+  cudaError_t e = cudaSuccess;
+  if (dev.path != PATH_LOOP) {
+    GranuleRule rule;
+    rule.add(a.x, a.ldx, sizeof(T));
+    if (a.dy) {
+      rule.add(a.dy, a.lddy, sizeof(T));
+      rule.add(a.h, a.ldh, sizeof(T));
+    }
+    if (a.dh_in) rule.add(a.dh_in, a.lddh, sizeof(T));
+    rule.add(a.dx, a.lddx, sizeof(T));
+    rule.add(a.dres, a.lddres, sizeof(T));
+    const bool vec = rule.bytes(a.H, sizeof(T)) >= 16, runs = a.gate_rows > 1;
+    if (vec)
+      e = runs ? run_join_grad<D, 16, true>(a, dev, s, &done) : run_join_grad<D, 16, false>(a, dev, s, &done);
+    else
+      e = runs ? run_join_grad<D, (int)sizeof(T), true>(a, dev, s, &done)
+               : run_join_grad<D, (int)sizeof(T), false>(a, dev, s, &done);
+  }
+  if (!done) {
+    a.P = a.U = (int)std::min<int64_t>(a.N, kJoinMaxPartialsPerSm * dev.sm_count);
+    join_grad_loop_kernel<D><<<(unsigned)a.P, kJoinGradLoopThreads, 0, s>>>(a);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
   return launch_join_reduce<D>(a, dev, s);
 }
