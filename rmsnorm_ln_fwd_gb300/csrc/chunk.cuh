@@ -1,26 +1,27 @@
-// A thread's share of a row: 32 bytes (E = 16 half-precision or 8 fp32
-// columns), as NG granules of GB bytes.  A warp owns 1024 contiguous bytes of
-// the row: granule g of lane l holds the GE columns from 32*GE*g + GE*l of the
-// warp's, so every access of a warp is contiguous and a thread reaches its
-// granules from one pointer at constant offsets.  GB is 32 where rows are
-// 32-byte aligned (one 256-bit access), 16 where they are 16-byte aligned, and
-// one element otherwise: odd widths and shifted rows run the same kernels, only
-// with narrower accesses.
+// A thread's share of a row: E columns, as granules of GB bytes.  A warp owns
+// 32*E contiguous columns: granule g of lane l holds the GE columns from
+// 32*GE*g + GE*l of the warp's, so every access of a warp is contiguous and a
+// thread reaches its granules from one pointer at constant offsets.  GB is 32
+// where rows are 32-byte aligned (one 256-bit access), 16 where they are
+// 16-byte aligned, and one element otherwise: odd widths and shifted rows run
+// the same kernels, only with narrower accesses.
 #pragma once
 
 #include "common.cuh"
 
 namespace normk {
 
-template <typename D, int GB>
+template <typename D, int GB, int E_>
 struct Chunk {
   using T = typename D::T;
   static constexpr int ES = (int)sizeof(T);
-  static constexpr int E = 32 / ES;        // columns a thread
+  static constexpr int E = E_;             // columns a thread
   static constexpr int NP = E / 2;         // fp32 pairs
-  static constexpr int NG = 32 / GB;       // granules
+  static constexpr int NW = E * ES / 4;    // packed words
   static constexpr int GE = GB / ES;       // columns a granule
+  static constexpr int NG = E / GE;        // granules
   static_assert(GB == 32 || GB == 16 || GB == ES, "granule");
+  static_assert(E % GE == 0 && E % 4 == 0, "whole granules");
 
   // First column of thread t of a row group, and column of its e-th element
   // from there.
@@ -29,17 +30,18 @@ struct Chunk {
 
   // Load the thread's columns from its first, `p` (those `lim` columns or more
   // behind it lie past the row: zeros), as packed words.
-  __device__ static __forceinline__ void load(const T* p, int lim, uint32_t (&w)[8]) {
+  __device__ static __forceinline__ void load(const T* p, int lim, uint32_t (&w)[NW]) {
     if constexpr (GB == 32) {
+      static_assert(NG == 1, "one 256-bit access");
       if (0 < lim) {
         ld_stream32(p, w);
       } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = 0u;
+        for (int k = 0; k < NW; ++k) w[k] = 0u;
       }
     } else if constexpr (GB == 16) {
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
+      for (int g = 0; g < NG; ++g) {
         const uint4 u = col(g * GE) < lim ? ld_stream(p + col(g * GE)) : make_uint4(0u, 0u, 0u, 0u);
         w[4 * g] = u.x;
         w[4 * g + 1] = u.y;
@@ -48,10 +50,10 @@ struct Chunk {
       }
     } else if constexpr (ES == 4) {
 #pragma unroll
-      for (int g = 0; g < 8; ++g) w[g] = col(g) < lim ? ldg32(p + col(g)) : 0u;
+      for (int g = 0; g < NG; ++g) w[g] = col(g) < lim ? ldg32(p + col(g)) : 0u;
     } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < NW; ++k) {
         const uint32_t lo = col(2 * k) < lim ? ldg16(p + col(2 * k)) : 0u;
         const uint32_t hi = col(2 * k + 1) < lim ? ldg16(p + col(2 * k + 1)) : 0u;
         w[k] = __byte_perm(lo, hi, 0x5410);
@@ -59,20 +61,20 @@ struct Chunk {
     }
   }
 
-  __device__ static __forceinline__ void store(T* p, int lim, const uint32_t (&w)[8]) {
+  __device__ static __forceinline__ void store(T* p, int lim, const uint32_t (&w)[NW]) {
     if constexpr (GB == 32) {
       if (0 < lim) st_vec32(p, w);
     } else if constexpr (GB == 16) {
 #pragma unroll
-      for (int g = 0; g < 2; ++g)
+      for (int g = 0; g < NG; ++g)
         if (col(g * GE) < lim) st_vec(p + col(g * GE), make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]));
     } else if constexpr (ES == 4) {
 #pragma unroll
-      for (int g = 0; g < 8; ++g)
+      for (int g = 0; g < NG; ++g)
         if (col(g) < lim) reinterpret_cast<uint32_t*>(p)[col(g)] = w[g];
     } else {
 #pragma unroll
-      for (int g = 0; g < 16; ++g)
+      for (int g = 0; g < NG; ++g)
         if (col(g) < lim) reinterpret_cast<uint16_t*>(p)[col(g)] = (uint16_t)(w[g / 2] >> (16 * (g & 1)));
     }
   }
@@ -164,7 +166,7 @@ struct GranuleRule {
   }
 };
 
-// Threads a row: one 32-byte share each, whole warps.
-inline int chunk_threads(int64_t H, size_t es) { return (int)((H * (int64_t)es + 32 * 32 - 1) / (32 * 32) * 32); }
+// Threads a row of H columns at E columns a thread: whole warps.
+inline int chunk_threads(int64_t H, int E) { return (int)((H + 32 * E - 1) / (32 * E) * 32); }
 
 }  // namespace normk

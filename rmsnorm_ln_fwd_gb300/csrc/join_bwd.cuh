@@ -136,14 +136,14 @@ __global__ void __launch_bounds__(kJoinGradLoopThreads) join_grad_loop_kernel(co
   }
 }
 
-// Rows through shared memory.  A row group of tpr threads, 32 bytes of each
-// tensor a thread (chunk.cuh), takes its rows from a ring of NB row buffers of
-// its own: one thread bulk-copies the next rows of dy, dh_in, h and x, each
-// completing on the buffer's mbarrier, and refills a buffer when the row sums'
-// barrier has passed (every thread has then read it).  No registers hold a row
-// in flight, which leaves them to the two accumulators (dgamma_pre, and A for
-// gate and gamma_post) and to the row's own terms.  Shared memory is read 16
-// bytes a lane, a warp's reads contiguous, whatever the rows' alignment.
+// Rows through shared memory.  A row group of tpr threads, E columns a
+// thread (chunk.cuh), takes its rows from a ring of NB row buffers of its own:
+// one thread bulk-copies the next rows of dy, dh_in, h and x, each completing
+// on the buffer's mbarrier, and refills a buffer when the row sums' barrier has
+// passed (every thread has then read it).  No registers hold a row in flight,
+// which leaves them to the two accumulators (dgamma_pre, and A for gate and
+// gamma_post) and to the row's own terms.  Shared memory is read 16 bytes a
+// lane, a warp's reads contiguous, whatever the rows' alignment.
 //
 // Rows that are not 16-byte aligned (GB = one element): the copy takes the
 // whole 16-byte lines inside the row, and the up to 15 bytes at either end come
@@ -153,23 +153,36 @@ __global__ void __launch_bounds__(kJoinGradLoopThreads) join_grad_loop_kernel(co
 // CL > 1: a cluster of CL CTAs shares each row in parts of equal whole granules;
 // the row sums meet through distributed shared memory.
 constexpr int kJoinRowTensors = 4;  // dy, dh_in, h, x
-constexpr int kJoinMaxBuffers = 4;
+constexpr int kJoinMaxBuffers = 4;  // row buffers a group
+constexpr int kJoinMinBuffers = 2;
+// Columns a thread.
+template <typename D>
+constexpr int kJoinGradCols = D::VEC == 8 ? 16 : 8;
+
+// What a group's copies need, in shared memory rather than in every thread's
+// registers: the next row's address and the step of each tensor (0: absent),
+// and where in its 16-byte line each tensor's row of each buffer starts.
+struct __align__(16) JoinSources {
+  unsigned long long next[kJoinRowTensors], step[kJoinRowTensors];
+  int off[kJoinMaxBuffers][kJoinRowTensors];
+};
 
 struct JoinRing {
   int tpr, rpc, nb;
   int part;        // columns a CTA of the cluster takes
   int buf_bytes;   // of one tensor's part of a row
-  int red_off, par_off, buf_off, total;
+  int src_off, red_off, par_off, buf_off, total;
 };
 
 template <int E>
 inline JoinRing join_ring(int H, int es, int ge, int cl, bool runs, int max_smem) {
   JoinRing r{};
   r.part = (H + cl * ge - 1) / (cl * ge) * ge;
-  r.tpr = chunk_threads(r.part, es);
+  r.tpr = chunk_threads(r.part, E);
   r.rpc = cl == 1 && r.tpr <= 256 ? 256 / r.tpr : 1;
   r.buf_bytes = (r.part * es + 16 + 127) & ~127;
-  r.red_off = (r.rpc * kJoinMaxBuffers * 8 + 16 + 15) & ~15;
+  r.src_off = (r.rpc * kJoinMaxBuffers * 8 + 16 + 15) & ~15;
+  r.red_off = r.src_off + r.rpc * (int)sizeof(JoinSources);
   r.par_off = r.red_off + r.rpc * 2 * (r.tpr / 32) * 3 * 4;
   r.par_off = (r.par_off + 15) & ~15;
   const int slot = runs ? param_slot<E, 3>() : param_slot<E, 2>();
@@ -183,13 +196,13 @@ inline JoinRing join_ring(int H, int es, int ge, int cl, bool runs, int max_smem
 
 template <typename D, int GB, bool RUNS, int MAXT, int MINB, int CL>
 __global__ void __launch_bounds__(MAXT, MINB) join_grad_rows_kernel(const JoinGradArgs a, const JoinRing ring) {
-  using C = Chunk<D, GB>;
+  using C = Chunk<D, GB, kJoinGradCols<D>>;
   using T = typename D::T;
-  constexpr int E = C::E, NP = C::NP, ES = C::ES;
+  constexpr int E = C::E, NP = C::NP, NW = C::NW, ES = C::ES;
   constexpr bool EDGES = GB < 16;
   constexpr int SLOT = param_slot<E, RUNS ? 3 : 2>();
   extern __shared__ __align__(128) unsigned char sm_join[];
-  __shared__ float xch[2][CL * 4];
+  __shared__ __align__(16) float xch[2][CL * 4];
   __shared__ uint64_t xbar[2];
   const int tpr = ring.tpr;
   const int group = threadIdx.x / tpr;
@@ -207,7 +220,8 @@ __global__ void __launch_bounds__(MAXT, MINB) join_grad_rows_kernel(const JoinGr
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm_join + ring.rpc * kJoinMaxBuffers * 8);
   float* red = reinterpret_cast<float*>(sm_join + ring.red_off) + group * (2 * nw * 3);
   float* slot = reinterpret_cast<float*>(sm_join + ring.par_off) + threadIdx.x * SLOT;
-  unsigned char* bufs = sm_join + ring.buf_off + (size_t)group * ring.nb * kJoinRowTensors * ring.buf_bytes;
+  const int row_bytes = kJoinRowTensors * ring.buf_bytes;  // a row's four buffers
+  unsigned char* bufs = sm_join + ring.buf_off + (size_t)group * ring.nb * row_bytes;
   const int bar_id = 1 + group;
   const int NB = ring.nb;
 
@@ -233,101 +247,93 @@ __global__ void __launch_bounds__(MAXT, MINB) join_grad_rows_kernel(const JoinGr
 
   // Copying a row: the bytes [start, start + H*ES) of each tensor land at
   // (start mod 16) of its buffer.
-  struct Src {
-    const void* p;
-    int64_t ld;
-  };
-  const Src srcs[kJoinRowTensors] = {{a.dy, a.lddy}, {a.dh_in, a.lddh}, {a.dy ? a.h : nullptr, a.ldh}, {a.x, a.ldx}};
-  auto start_of = [&](int k, int64_t r) {
-    return reinterpret_cast<uintptr_t>(reinterpret_cast<const T*>(srcs[k].p) + r * srcs[k].ld + c0);
-  };
+  const bool has_dy = a.dy != nullptr, has_in = a.dh_in != nullptr;
   const bool copies = H > 0;
+  volatile JoinSources* src = reinterpret_cast<volatile JoinSources*>(sm_join + ring.src_off) + group;
+  if (t < kJoinRowTensors) {
+    const void* q = t == 0 ? a.dy : t == 1 ? a.dh_in : t == 2 ? (has_dy ? a.h : nullptr) : a.x;
+    const int64_t ld = t == 0 ? a.lddy : t == 1 ? a.lddh : t == 2 ? a.ldh : a.ldx;
+    src->next[t] = q ? (unsigned long long)reinterpret_cast<uintptr_t>(reinterpret_cast<const T*>(q) + row * ld + c0) : 0ull;
+    src->step[t] = (unsigned long long)(step * ld * ES);
+  }
+  __syncthreads();
   unsigned used = 0u, fills = 0u;  // per buffer: ever filled; fills issued, mod 2 (thread 0 of the group)
-  auto issue = [&](int64_t r, int buf) {  // by thread 0 of the group
-    uint32_t bytes[kJoinRowTensors], total = 0;
-    uintptr_t from[kJoinRowTensors];
-#pragma unroll
-    for (int k = 0; k < kJoinRowTensors; ++k) {
-      bytes[k] = 0;
-      if (srcs[k].p == nullptr) continue;
-      const uintptr_t s = start_of(k, r), e = s + (uintptr_t)H * ES;
-      from[k] = (s + 15) & ~(uintptr_t)15;
-      const uintptr_t to = e & ~(uintptr_t)15;
-      if (to > from[k]) bytes[k] = (uint32_t)(to - from[k]);
-      total += bytes[k];
-    }
-    mbar_arrive_expect_tx(&bars[buf], total);
-    used |= 1u << buf;
-    fills ^= 1u << buf;
-#pragma unroll
-    for (int k = 0; k < kJoinRowTensors; ++k)
-      if (bytes[k] != 0) {
-        unsigned char* dst = bufs + ((size_t)buf * kJoinRowTensors + k) * ring.buf_bytes;
-        bulk_g2s(dst + (from[k] - (start_of(k, r) & ~(uintptr_t)15)), reinterpret_cast<const void*>(from[k]), bytes[k],
-                 &bars[buf]);
-      }
-  };
   // The ends of a row that no whole line holds: lane l of the group's first
   // warp takes elements l and l + 32 of the 4 tensors x {front, back} x 8.
-  T edge[2];
-  int edge_at[2] = {-1, -1};  // byte offset in the row buffers, or none
-  auto edge_fetch = [&](int64_t r, int buf) {
+  struct Edge {
+    T v[2];
+    int at[2];  // byte offset in the row buffers, or -1
+  };
+  // Ask for the next row, into buffer `buf`: by the group's first warp.
+  auto issue = [&](int buf, Edge& ed) {
     if constexpr (EDGES) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        edge_at[j] = -1;
-        if (wig != 0) continue;
+        ed.at[j] = -1;
         const int id = lane + 32 * j, k = id >> 4, back = (id >> 3) & 1, i = id & 7;
-        const T* base = nullptr;
-        int64_t ld = 0;
-#pragma unroll
-        for (int q = 0; q < kJoinRowTensors; ++q)
-          if (q == k) {
-            base = reinterpret_cast<const T*>(srcs[q].p);
-            ld = srcs[q].ld;
-          }
-        if (base == nullptr) continue;
-        const uintptr_t s = reinterpret_cast<uintptr_t>(base + r * ld + c0), e = s + (uintptr_t)H * ES;
-        const uintptr_t up = (s + 15) & ~(uintptr_t)15, down = e & ~(uintptr_t)15;
-        uintptr_t from = s, to = up < e ? up : e;  // front
-        if (back) {
-          from = down > up ? down : up;
-          to = e;
-        }
-        const uintptr_t p = from + (uintptr_t)i * ES;
+        const unsigned long long s = src->next[k];
+        if (s == 0) continue;
+        const unsigned long long e = s + (unsigned long long)H * ES, up = (s + 15) & ~15ull, down = e & ~15ull;
+        const unsigned long long from = back ? (down > up ? down : up) : s, to = back ? e : (up < e ? up : e);
+        const unsigned long long p = from + (unsigned long long)(i * ES);
         if (from >= to || p >= to) continue;
-        edge[j] = *reinterpret_cast<const T*>(p);
-        edge_at[j] = (buf * kJoinRowTensors + k) * ring.buf_bytes + (int)(p - (s & ~(uintptr_t)15));
+        ed.v[j] = *reinterpret_cast<const T*>(p);
+        ed.at[j] = buf * row_bytes + k * ring.buf_bytes + (int)(p - (s & ~15ull));
       }
+      __syncwarp();  // read before thread 0 moves on
     }
+    if (lane == 0) {
+      uint32_t total = 0;
+#pragma unroll 1
+      for (int k = 0; k < kJoinRowTensors; ++k) {
+        const unsigned long long s = src->next[k];
+        if (s == 0) continue;
+        const unsigned long long from = (s + 15) & ~15ull, to = (s + (unsigned long long)H * ES) & ~15ull;
+        if (to > from) total += (uint32_t)(to - from);
+      }
+      if constexpr (EDGES) {
+        for (int k = 0; k < kJoinRowTensors; ++k) src->off[buf][k] = (int)(src->next[k] & 15ull);
+      }
+      mbar_arrive_expect_tx(&bars[buf], total);
+#pragma unroll 1
+      for (int k = 0; k < kJoinRowTensors; ++k) {
+        const unsigned long long s = src->next[k];
+        if (s == 0) continue;
+        const unsigned long long from = (s + 15) & ~15ull, to = (s + (unsigned long long)H * ES) & ~15ull;
+        if (to > from)
+          bulk_g2s(bufs + buf * row_bytes + k * ring.buf_bytes + (from - (s & ~15ull)), reinterpret_cast<const void*>(from),
+                   (uint32_t)(to - from), &bars[buf]);
+        src->next[k] = s + src->step[k];
+      }
+      used |= 1u << buf;
+      fills ^= 1u << buf;
+    }
+    if constexpr (EDGES) __syncwarp();
   };
-  auto edge_store = [&]() {
+  auto edge_store = [&](Edge& ed) {
     if constexpr (EDGES) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        if (edge_at[j] >= 0) *reinterpret_cast<T*>(bufs + edge_at[j]) = edge[j];
-        edge_at[j] = -1;
+        if (ed.at[j] >= 0) *reinterpret_cast<T*>(bufs + ed.at[j]) = ed.v[j];
+        ed.at[j] = -1;
       }
     }
   };
+  Edge edge;
   if (copies) {
     for (int i = 0; i < NB; ++i) {
       if (row + i * step >= end) break;
-      if (t == 0) issue(row + i * step, i);
-      edge_fetch(row + i * step, i);
-      edge_store();
+      if (wig == 0) {
+        issue(i, edge);
+        edge_store(edge);
+      }
     }
   }
+  if constexpr (EDGES) edge.at[0] = edge.at[1] = -1;
 
   auto at = [](const void* p, int64_t i, size_t es) -> const void* {
     return p ? reinterpret_cast<const unsigned char*>(p) + i * es : nullptr;
   };
-  float nrn = 0.f, nro = 1.f;  // the next row's statistics
-  auto fetch_stats = [&](int64_t r) {
-    if (a.rpre) nrn = a.rpre[r];
-    if (a.rpost) nro = a.rpost[r];
-  };
-  if (row < end) fetch_stats(row);
   int64_t gate_row = 0, gate_end = a.N;
   auto stage_w = [&](int64_t r) {
     float f[E];
@@ -389,9 +395,18 @@ __global__ void __launch_bounds__(MAXT, MINB) join_grad_rows_kernel(const JoinGr
     }
   };
 
+  T* dxp = reinterpret_cast<T*>(a.dx) + row * a.lddx + c0 + b0;
+  T* drp = reinterpret_cast<T*>(a.dres) + row * a.lddres + c0 + b0;
+  const int64_t dx_step = step * a.lddx, dr_step = step * a.lddres;
   const float2 alpha2 = splat2(a.alpha);
   int parity = 0, buf = 0;
-  unsigned phase = 0u, it = 0;
+  unsigned phase = 0u, it = 0;  // phase: parity of the ring's current turn
+  float nrn = 0.f, nro = 1.f;   // the next row's statistics
+  auto fetch_stats = [&](int64_t r) {
+    if (a.rpre) nrn = a.rpre[r];
+    if (a.rpost) nro = a.rpost[r];
+  };
+  if (row < end) fetch_stats(row);
   for (; row < end; row += step) {
     if (RUNS && row >= gate_end) {
       flush(gate_row);
@@ -399,92 +414,99 @@ __global__ void __launch_bounds__(MAXT, MINB) join_grad_rows_kernel(const JoinGr
     }
     const float rn = nrn, ro = nro;
     if (row + step < end) fetch_stats(row + step);
-    edge_store();
+    edge_store(edge);
     bool ok = true;
     if (copies) ok = mbar_wait(&bars[buf], phase, a.err, abort_flag);
-    auto read = [&](int k, uint32_t (&w)[8]) {
-      if (srcs[k].p == nullptr || !copies) {
+    const unsigned char* base = bufs + buf * row_bytes;
+    auto read = [&](int k, bool there, uint32_t (&w)[NW]) {
+      if (!there || !copies) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = 0u;
+        for (int i = 0; i < NW; ++i) w[i] = 0u;
         return;
       }
-      const unsigned char* p = bufs + ((size_t)buf * kJoinRowTensors + k) * ring.buf_bytes;
+      const unsigned char* p = base + k * ring.buf_bytes + b0 * ES;
       if constexpr (GB >= 16) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < C::NG; ++g) {
           uint4 u = make_uint4(0u, 0u, 0u, 0u);
-          if (C::col(g * C::GE) < lim) u = lds16(p + (size_t)(b0 + C::col(g * C::GE)) * ES);
+          if (C::col(g * C::GE) < lim) u = lds16(p + C::col(g * C::GE) * ES);
           w[4 * g] = u.x;
           w[4 * g + 1] = u.y;
           w[4 * g + 2] = u.z;
           w[4 * g + 3] = u.w;
         }
       } else {
-        const unsigned char* q = p + (start_of(k, row) & 15u) + (size_t)b0 * ES;
+        p += src->off[buf][k];
         if constexpr (ES == 4) {
 #pragma unroll
-          for (int g = 0; g < 8; ++g)
-            w[g] = C::col(g) < lim ? *reinterpret_cast<const uint32_t*>(q + C::col(g) * 4) : 0u;
+          for (int g = 0; g < C::NG; ++g)
+            w[g] = C::col(g) < lim ? *reinterpret_cast<const uint32_t*>(p + C::col(g) * 4) : 0u;
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t lo = C::col(2 * i) < lim ? *reinterpret_cast<const uint16_t*>(q + C::col(2 * i) * 2) : 0u;
+          for (int i = 0; i < NW; ++i) {
+            const uint32_t lo = C::col(2 * i) < lim ? *reinterpret_cast<const uint16_t*>(p + C::col(2 * i) * 2) : 0u;
             const uint32_t hi =
-                C::col(2 * i + 1) < lim ? *reinterpret_cast<const uint16_t*>(q + C::col(2 * i + 1) * 2) : 0u;
+                C::col(2 * i + 1) < lim ? *reinterpret_cast<const uint16_t*>(p + C::col(2 * i + 1) * 2) : 0u;
             w[i] = __byte_perm(lo, hi, 0x5410);
           }
         }
       }
     };
-    uint32_t dyw[8], xw[8], iw[8], hw[8];
-    read(0, dyw);
-    read(1, iw);
-    read(2, hw);
-    read(3, xw);
-    // pass 1: t = dh_in + rstd_pre * g, h_hat, and the three row sums (those
-    // over o_hat = x * rstd_post with rstd_post taken out)
-    float2 tt[NP], hh[NP];
-    float2 s0 = splat2(0.f), s1 = splat2(0.f), s2 = splat2(0.f);
-    const float2 rn2 = splat2(rn);
+    // pass 1: t = dh_in + rstd_pre * g, and the row's three sums over h and x
+    // (the statistics that turn them into h_hat and o_hat come in behind)
+    uint32_t dyw[NW], xw[NW], hw[NW];
+    float2 tt[NP];
+    read(0, has_dy, dyw);
+    read(2, has_dy, hw);
+    read(3, true, xw);
+    float s[3];
+    {
+      uint32_t iw[NW];
+      read(1, has_in, iw);
+      float2 s0 = splat2(0.f), s1 = splat2(0.f), s2 = splat2(0.f);
+      const float2 rn2 = splat2(rn);
 #pragma unroll
-    for (int q = 0; q < NP / 2; ++q) {
-      float2 w[2], gp[2];
-      get_pairs(slot, q, w);
-      get_pairs(slot + E, q, gp);
+      for (int q = 0; q < NP / 2; ++q) {
+        float2 w[2], gp[2];
+        get_pairs(slot, q, w);
+        get_pairs(slot + E, q, gp);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int p = 2 * q + i;
-        const float2 g = mul2(word_pair<D>(dyw, p), gp[i]);
-        const float2 wx = mul2(word_pair<D>(xw, p), w[i]);
-        hh[p] = mul2(word_pair<D>(hw, p), rn2);
-        tt[p] = fma2(g, rn2, word_pair<D>(iw, p));
-        s0 = fma2(g, hh[p], s0);
-        s1 = fma2(wx, tt[p], s1);
-        s2 = fma2(wx, hh[p], s2);
+        for (int i = 0; i < 2; ++i) {
+          const int p = 2 * q + i;
+          const float2 g = mul2(word_pair<D>(dyw, p), gp[i]);
+          const float2 wx = mul2(word_pair<D>(xw, p), w[i]);
+          const float2 h = word_pair<D>(hw, p);
+          tt[p] = fma2(g, rn2, word_pair<D>(iw, p));
+          s0 = fma2(g, h, s0);
+          s1 = fma2(wx, tt[p], s1);
+          s2 = fma2(wx, h, s2);
+        }
       }
+      s[0] = s0.x + s0.y;
+      s[1] = s1.x + s1.y;
+      s[2] = s2.x + s2.y;
     }
-    float s[3] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y};
     group_sum<3>(s, red, nw, wig, lane, bar_id, parity);
     parity ^= 1;
     if (nw == 1) __syncwarp();
     // every thread has read this buffer: refill it with the row NB ahead
-    const int64_t ahead = row + (int64_t)NB * step;
-    if (ahead < end && copies) {
-      if (t == 0 && !*abort_flag) {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        issue(ahead, buf);
-      }
-      edge_fetch(ahead, buf);
+    if (wig == 0 && copies && row + NB * step < end && !*abort_flag) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      issue(buf, edge);
     }
     if constexpr (CL > 1) {
       ok &= cluster_group_sum_async<3, CL>(s, xch[it & 1], &xbar[it & 1], (it >> 1) & 1u, crank, a.err, abort_flag);
       ++it;
     }
-    const float c = s[0] * inv_h;
-    const float k = a.rpost ? ro * fmaf(-rn * c, s[2], s[1]) * inv_h : 0.f;  // mean(w dh o_hat)
-    const float2 nc2 = splat2(-c * rn), ro2 = splat2(ro), nk2 = splat2(-k * ro * ro);
+    // c = mean(g h_hat), dh = t - rstd_pre c h_hat, k = mean(w dh o_hat)
+    const float crr = s[0] * inv_h * rn * rn * rn;
+    const float k = a.rpost ? ro * fmaf(-crr, s[2], s[1]) * inv_h : 0.f;
+    // unpack again rather than hold the fp32 values over the barrier
+#pragma unroll
+    for (int i = 0; i < NW; ++i) asm volatile("" : "+r"(dyw[i]), "+r"(hw[i]), "+r"(xw[i]));
+    const float2 nc2 = splat2(-crr), rn2 = splat2(rn), ro2 = splat2(ro), nk2 = splat2(-k * ro * ro);
     if (ok) {
-      uint32_t od[8], ox[8];
+      uint32_t od[NW], ox[NW];
 #pragma unroll
       for (int q = 0; q < NP / 2; ++q) {
         float2 w[2];
@@ -492,18 +514,20 @@ __global__ void __launch_bounds__(MAXT, MINB) join_grad_rows_kernel(const JoinGr
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int p = 2 * q + i;
-          const float2 x = word_pair<D>(xw, p);
-          const float2 dh = fma2(hh[p], nc2, tt[p]);
+          const float2 x = word_pair<D>(xw, p), h = word_pair<D>(hw, p);
+          const float2 dh = fma2(h, nc2, tt[p]);
           pair_word<D>(od, p, mul2(dh, alpha2));
           const float2 dr = mul2(dh, ro2);
           pair_word<D>(ox, p, fma2(x, nk2, mul2(dr, w[i])));
-          acc_pre[p] = fma2(word_pair<D>(dyw, p), hh[p], acc_pre[p]);
+          acc_pre[p] = fma2(word_pair<D>(dyw, p), mul2(h, rn2), acc_pre[p]);
           acc[p] = fma2(dr, x, acc[p]);
         }
       }
-      C::store(reinterpret_cast<T*>(a.dres) + row * a.lddres + c0 + b0, lim, od);
-      C::store(reinterpret_cast<T*>(a.dx) + row * a.lddx + c0 + b0, lim, ox);
+      C::store(drp, lim, od);
+      C::store(dxp, lim, ox);
     }
+    drp += dr_step;
+    dxp += dx_step;
     if (++buf == NB) {
       buf = 0;
       phase ^= 1u;
@@ -751,18 +775,18 @@ static cudaError_t run_join_grad_rows(JoinGradArgs& a, const JoinRing& ring, con
 }
 
 // The fewest CTAs a row (1, 2, 4, 8) whose part fits 512 threads and at least
-// two row buffers; *done = false where none does.
+// four row buffers; *done = false where none does.
 template <typename D, int GB, bool RUNS>
 static cudaError_t run_join_grad(JoinGradArgs& a, const DeviceInfo& dev, cudaStream_t s, bool* done) {
-  using C = Chunk<D, GB>;
+  using C = Chunk<D, GB, kJoinGradCols<D>>;
   *done = true;
   for (int cl = 1; cl <= 8; cl *= 2) {
     const JoinRing two = join_ring<C::E>(a.H, C::ES, C::GE, cl, RUNS, dev.max_smem_optin);
-    if (two.tpr > 512 || two.nb < 2) continue;
+    if (two.tpr > 512 || two.nb < kJoinMinBuffers) continue;
     if (cl == 1 && two.tpr <= 256) {
-      // two CTAs an SM where each still has two buffers
+      // two CTAs an SM where each still has its buffers
       const JoinRing half = join_ring<C::E>(a.H, C::ES, C::GE, 1, RUNS, (dev.max_smem_optin - 2048) / 2);
-      return run_join_grad_rows<D, GB, RUNS, 256, 2, 1>(a, half.nb >= 2 ? half : two, dev, s);
+      return run_join_grad_rows<D, GB, RUNS, 256, 2, 1>(a, half.nb >= kJoinMinBuffers ? half : two, dev, s);
     }
     if (cl == 1) return run_join_grad_rows<D, GB, RUNS, 512, 1, 1>(a, two, dev, s);
     if (cl == 2) return run_join_grad_rows<D, GB, RUNS, 512, 1, 2>(a, two, dev, s);

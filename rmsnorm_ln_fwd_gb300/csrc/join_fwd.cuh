@@ -20,6 +20,9 @@
 namespace normk {
 
 constexpr int kJoinLoopThreads = 256;
+// Columns a thread of the register rows: 32 bytes.
+template <typename D>
+constexpr int kJoinCols = 32 / (int)sizeof(typename D::T);
 
 // Any width, stride and alignment: one CTA a row at a time, a strided loop over
 // the row for each of its passes (the second and third reads mostly hit L2).
@@ -97,7 +100,7 @@ __global__ void __launch_bounds__(kJoinLoopThreads) join_loop_kernel(const JoinA
 // (the last one or two may be shorter or empty).
 template <typename D, int GB, int MAXT, int MINB, int CL>
 __global__ void __launch_bounds__(MAXT, MINB) join_rows_kernel(const JoinArgs a, const int tpr) {
-  using C = Chunk<D, GB>;
+  using C = Chunk<D, GB, kJoinCols<D>>;
   using T = typename D::T;
   constexpr int E = C::E, NP = C::NP;
   constexpr int SLOT = param_slot<E, 2>();
@@ -132,7 +135,7 @@ __global__ void __launch_bounds__(MAXT, MINB) join_rows_kernel(const JoinArgs a,
     cta_rows(a.N, (int)unit, (int)units, row, end);
     step = 1;
   }
-  uint32_t nx[8], nr[8];
+  uint32_t nx[C::NW], nr[C::NW];
   auto fetch = [&](int64_t r) {
     C::load(reinterpret_cast<const T*>(a.x) + r * a.ldx + c0 + b, lim, nx);
     C::load(reinterpret_cast<const T*>(a.res) + r * a.ldr + c0 + b, lim, nr);
@@ -181,9 +184,9 @@ __global__ void __launch_bounds__(MAXT, MINB) join_rows_kernel(const JoinArgs a,
   for (; row < end; row += step) {
     if (row >= gate_end) stage_w(row);
     float2 f[NP];     // w * x, later h
-    uint32_t rw[8];   // residual
+    uint32_t rw[C::NW];   // residual
 #pragma unroll
-    for (int k = 0; k < 8; ++k) rw[k] = nr[k];
+    for (int k = 0; k < C::NW; ++k) rw[k] = nr[k];
     float2 sx = splat2(0.f), sa = splat2(0.f), sb = splat2(0.f), sc = splat2(0.f);
 #pragma unroll
     for (int q = 0; q < NP / 2; ++q) {
@@ -212,7 +215,7 @@ __global__ void __launch_bounds__(MAXT, MINB) join_rows_kernel(const JoinArgs a,
     const float rp = a.post ? rsqrtf(s[0] * inv_h + a.eps) : 1.f;
     const float2 rp2 = splat2(rp);
     T* hrow = reinterpret_cast<T*>(a.h) + row * a.ldh + c0 + b;
-    uint32_t out[8];
+    uint32_t out[C::NW];
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
       f[p] = fma2(f[p], rp2, mul2(word_pair<D>(rw, p), alpha2));
@@ -257,7 +260,7 @@ template <typename D, int GB, int MAXT, int MINB, int CL>
 static cudaError_t run_join_rows(const JoinArgs& a, int tpr, int rpc, const DeviceInfo& dev, cudaStream_t s) {
   auto kern = join_rows_kernel<D, GB, MAXT, MINB, CL>;
   const int threads = rpc * tpr;
-  const size_t smem = sizeof(float) * ((size_t)rpc * 2 * (tpr / 32) * 4 + (size_t)threads * param_slot<Chunk<D, GB>::E, 2>());
+  const size_t smem = sizeof(float) * ((size_t)rpc * 2 * (tpr / 32) * 4 + (size_t)threads * param_slot<Chunk<D, GB, kJoinCols<D>>::E, 2>());
   if (smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -290,15 +293,14 @@ static cudaError_t run_join_rows(const JoinArgs& a, int tpr, int rpc, const Devi
 
 template <typename D, int GB>
 static cudaError_t run_join(const JoinArgs& a, const DeviceInfo& dev, cudaStream_t s, bool* done) {
-  using T = typename D::T;
   *done = true;
-  const int tpr = chunk_threads(a.H, sizeof(T));
+  const int tpr = chunk_threads(a.H, kJoinCols<D>);
   if (tpr <= 256) return run_join_rows<D, GB, 256, (GB >= 16 ? 3 : 2), 1>(a, tpr, 256 / tpr, dev, s);
   if (tpr <= kRowsAutoMaxThreads) return run_join_rows<D, GB, kRowsAutoMaxThreads, 1, 1>(a, tpr, 1, dev, s);
   // wider rows: the smallest cluster with parts of at most 512 threads
   auto threads = [&](int cl) {
-    constexpr int GE = Chunk<D, GB>::GE;
-    return chunk_threads((a.H + cl * GE - 1) / (cl * GE) * GE, sizeof(T));
+    constexpr int GE = Chunk<D, GB, kJoinCols<D>>::GE;
+    return chunk_threads((a.H + cl * GE - 1) / (cl * GE) * GE, kJoinCols<D>);
   };
   if (threads(2) <= 512) return run_join_rows<D, GB, 512, 1, 2>(a, threads(2), 1, dev, s);
   if (threads(4) <= 512) return run_join_rows<D, GB, 512, 1, 4>(a, threads(4), 1, dev, s);
