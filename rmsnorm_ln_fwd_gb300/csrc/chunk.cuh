@@ -122,6 +122,29 @@ __device__ __forceinline__ void get_pairs(const float* slot, int q, float2 (&p)[
   p[1] = make_float2(v.z, v.w);
 }
 
+// Shared memory by 32-bit address.
+template <int W>
+__device__ __forceinline__ void lds_words(uint32_t p, uint32_t* w) {
+  static_assert(W == 2 || W == 4, "8 or 16 bytes");
+  if constexpr (W == 2)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(p));
+  else
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(p));
+}
+__device__ __forceinline__ uint32_t lds_u32(uint32_t p) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t p) {
+  uint32_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(p));
+  return v;
+}
+__device__ __forceinline__ void lds_pairs(uint32_t p, float2 (&v)[2]) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0].x), "=f"(v[0].y), "=f"(v[1].x), "=f"(v[1].y) : "r"(p));
+}
+
 // Sum four values over a row group of nw <= 32 warps, as group_sum: the warp
 // stage is a reduce-scatter (six shuffles; value k ends in lanes 8k..8k+7).
 // `sh` holds 2*nw*4 floats; parity alternates per call.

@@ -136,62 +136,87 @@ __global__ void __launch_bounds__(kJoinGradLoopThreads) join_grad_loop_kernel(co
   }
 }
 
-// Rows through shared memory.  A row group of tpr threads, E columns a
-// thread (chunk.cuh), takes its rows from a ring of NB row buffers of its own:
-// one thread bulk-copies the next rows of dy, dh_in, h and x, each completing
-// on the buffer's mbarrier, and refills a buffer when the row sums' barrier has
-// passed (every thread has then read it).  No registers hold a row in flight,
-// which leaves them to the two accumulators (dgamma_pre, and A for gate and
-// gamma_post) and to the row's own terms.  Shared memory is read 16 bytes a
-// lane, a warp's reads contiguous, whatever the rows' alignment.
+// Rows through shared memory.  A row group of tpr threads, E columns a thread
+// (chunk.cuh), takes its rows from a ring of NB row buffers of its own: lanes
+// 8k (k = 0..3) of its first warp bulk-copy the next row of dy, dh_in, h and x
+// into a buffer, completing on its mbarrier, when the row sums' barrier has
+// passed (every thread has then read the buffer).  The four lanes issue
+// together: one thread issuing all four kept its warp, and with it the row
+// sums' barrier, behind (barrier stalls 2.8 a cycle issued).  No registers hold
+// a row in flight, and between its two passes a row waits in them as it was
+// read, packed.  That leaves room for the two accumulators (dgamma_pre, and A
+// for gate and gamma_post) of sixteen columns a thread, over which the work a
+// row costs whatever its width (waits, row sums, addresses: half the
+// instructions at eight columns) is spread.  Shared memory is read 16
+// bytes a lane, a warp's reads contiguous, whatever the rows' alignment.
 //
 // Rows that are not 16-byte aligned (GB = one element): the copy takes the
-// whole 16-byte lines inside the row, and the up to 15 bytes at either end come
-// by ordinary loads of the group's first warp, issued with the copy and put
-// into the buffer a row later.
+// whole 16-byte lines inside the row; the up to 15 bytes at either end come by
+// ordinary loads of the group's first warp, issued with the copy (lane 8k + i
+// takes element i of both ends of tensor k) and put into the buffer a row later.
 //
 // CL > 1: a cluster of CL CTAs shares each row in parts of equal whole granules;
 // the row sums meet through distributed shared memory.
 constexpr int kJoinRowTensors = 4;  // dy, dh_in, h, x
 constexpr int kJoinMaxBuffers = 4;  // row buffers a group
 constexpr int kJoinMinBuffers = 2;
+constexpr int kJoinMaxGroups = 8;
 // Columns a thread.
 template <typename D>
 constexpr int kJoinGradCols = D::VEC == 8 ? 16 : 8;
-
-// What a group's copies need, in shared memory rather than in every thread's
-// registers: the next row's address and the step of each tensor (0: absent),
-// and where in its 16-byte line each tensor's row of each buffer starts.
-struct __align__(16) JoinSources {
-  unsigned long long next[kJoinRowTensors], step[kJoinRowTensors];
-  int off[kJoinMaxBuffers][kJoinRowTensors];
-};
+constexpr int kJoinRedStride = 24;  // warps of a group, at most
+constexpr int kJoinRedFloats = 2 * 3 * kJoinRedStride;
 
 struct JoinRing {
   int tpr, rpc, nb;
   int part;        // columns a CTA of the cluster takes
   int buf_bytes;   // of one tensor's part of a row
-  int src_off, red_off, par_off, buf_off, total;
+  int red_off, par_off, buf_off, total;
 };
 
+// Shared memory: [mbarriers][abort flag][where in its 16-byte line each
+// tensor's row of each buffer starts][row sums][parameters][rows].
+constexpr int kJoinBarBytes = kJoinMaxGroups * kJoinMaxBuffers * 8;
+constexpr int kJoinAbortOff = kJoinBarBytes;
+constexpr int kJoinShiftOff = kJoinAbortOff + 16;
+constexpr int kJoinRedOff = kJoinShiftOff + kJoinMaxGroups * kJoinMaxBuffers * kJoinRowTensors * 4;
+
+constexpr int kJoinStaticSmem = 512;  // of the kernel's own, at most
+
+// The ring of a CTA of at most `threads` threads, `ctas` of them an SM.
 template <int E>
-inline JoinRing join_ring(int H, int es, int ge, int cl, bool runs, int max_smem) {
+inline JoinRing join_ring(int H, int es, int ge, int cl, bool runs, int threads, int ctas, int max_smem) {
   JoinRing r{};
   r.part = (H + cl * ge - 1) / (cl * ge) * ge;
   r.tpr = chunk_threads(r.part, E);
-  r.rpc = cl == 1 && r.tpr <= 256 ? 256 / r.tpr : 1;
-  r.buf_bytes = (r.part * es + 16 + 127) & ~127;
-  r.src_off = (r.rpc * kJoinMaxBuffers * 8 + 16 + 15) & ~15;
-  r.red_off = r.src_off + r.rpc * (int)sizeof(JoinSources);
-  r.par_off = r.red_off + r.rpc * 2 * (r.tpr / 32) * 3 * 4;
-  r.par_off = (r.par_off + 15) & ~15;
+  r.rpc = cl == 1 && r.tpr <= threads ? std::min(threads / r.tpr, kJoinMaxGroups) : 1;
+  r.buf_bytes = (r.part * es + (ge * es < 16 ? 16 : 0) + 15) & ~15;
+  r.red_off = kJoinRedOff;
+  r.par_off = r.red_off + r.rpc * kJoinRedFloats * 4;
   const int slot = runs ? param_slot<E, 3>() : param_slot<E, 2>();
   r.buf_off = (r.par_off + r.rpc * r.tpr * slot * 4 + 127) & ~127;
   const int stage = r.rpc * kJoinRowTensors * r.buf_bytes;
-  r.nb = std::min(kJoinMaxBuffers, (max_smem - r.buf_off) / stage);
+  r.nb = std::min(kJoinMaxBuffers, ((max_smem + 1024) / ctas - 1024 - kJoinStaticSmem - r.buf_off) / stage);
   const int fold = r.rpc > 1 ? r.rpc * r.tpr * E * 4 : 0;  // the groups' accumulators, after the rows
   r.total = r.buf_off + std::max(r.nb * stage, fold);
   return r;
+}
+
+// The rows of unit u: the first, how many, and the distance between them.
+template <bool RUNS>
+__device__ __forceinline__ void join_unit_rows(const JoinGradArgs& a, int u, int64_t units, int64_t& first, int64_t& n,
+                                               int64_t& step) {
+  if (RUNS) {
+    int64_t hi = 0;
+    first = 0;
+    if (u < a.U) cta_rows(a.N, u, a.U, first, hi);
+    n = hi - first;
+    step = 1;
+  } else {
+    first = u;
+    step = units;
+    n = u < a.N ? (a.N - u + units - 1) / units : 0;
+  }
 }
 
 template <typename D, int GB, bool RUNS, int MAXT, int MINB, int CL>
@@ -202,42 +227,20 @@ __global__ void __launch_bounds__(MAXT, MINB) join_grad_rows_kernel(const JoinGr
   constexpr bool EDGES = GB < 16;
   constexpr int SLOT = param_slot<E, RUNS ? 3 : 2>();
   extern __shared__ __align__(128) unsigned char sm_join[];
-  __shared__ __align__(16) float xch[2][CL * 4];
+  __shared__ float xch[2][CL * 4];
   __shared__ uint64_t xbar[2];
   const int tpr = ring.tpr;
-  const int group = threadIdx.x / tpr;
-  const int t = threadIdx.x - group * tpr;
-  const int nw = tpr >> 5, wig = t >> 5, lane = threadIdx.x & 31;
   const int crank = CL > 1 ? (int)cluster_ctarank() : 0;
   const int c0 = crank * ring.part;
   const int H = min(ring.part, a.H - c0);  // this CTA's columns (not positive: none)
-  const int b0 = C::base(t);
-  const int lim = H - b0;
-  const float inv_h = 1.f / (float)a.H;
-  const bool w_f32 = a.w_f32 != 0, g_f32 = a.g_f32 != 0;
-  const size_t wes = w_f32 ? 4 : sizeof(T), ges = g_f32 ? 4 : sizeof(T);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm_join) + group * kJoinMaxBuffers;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm_join + ring.rpc * kJoinMaxBuffers * 8);
-  float* red = reinterpret_cast<float*>(sm_join + ring.red_off) + group * (2 * nw * 3);
-  float* slot = reinterpret_cast<float*>(sm_join + ring.par_off) + threadIdx.x * SLOT;
-  const int row_bytes = kJoinRowTensors * ring.buf_bytes;  // a row's four buffers
-  unsigned char* bufs = sm_join + ring.buf_off + (size_t)group * ring.nb * row_bytes;
-  const int bar_id = 1 + group;
-  const int NB = ring.nb;
+  const int64_t units = (int64_t)(gridDim.x / CL) * ring.rpc;
+  const int unit0 = ((int)blockIdx.x / CL) * ring.rpc;
+  const bool copies = H > 0;
 
-  const int unit = ((int)blockIdx.x / CL) * ring.rpc + group;
-  int64_t row = unit, end = a.N, step = (int64_t)(gridDim.x / CL) * ring.rpc;
-  if (RUNS) {
-    step = 1;
-    row = end = 0;
-    if (unit < a.U) cta_rows(a.N, unit, a.U, row, end);
-  }
-  const int64_t first_row = row;
-
-  if (t == 0) {
-    for (int i = 0; i < NB; ++i) mbar_init(&bars[i], 1);
-    if (threadIdx.x == 0) *abort_flag = 0;
-    if (CL > 1) {
+  if (threadIdx.x < kJoinMaxGroups * kJoinMaxBuffers) {
+    mbar_init(reinterpret_cast<uint64_t*>(sm_join) + threadIdx.x, kJoinRowTensors);
+    if (threadIdx.x == 0) {
+      *reinterpret_cast<volatile int*>(sm_join + kJoinAbortOff) = 0;
       mbar_init(&xbar[0], 1);
       mbar_init(&xbar[1], 1);
     }
@@ -245,91 +248,83 @@ __global__ void __launch_bounds__(MAXT, MINB) join_grad_rows_kernel(const JoinGr
   }
   __syncthreads();
 
-  // Copying a row: the bytes [start, start + H*ES) of each tensor land at
-  // (start mod 16) of its buffer.
-  const bool has_dy = a.dy != nullptr, has_in = a.dh_in != nullptr;
-  const bool copies = H > 0;
-  volatile JoinSources* src = reinterpret_cast<volatile JoinSources*>(sm_join + ring.src_off) + group;
-  if (t < kJoinRowTensors) {
-    const void* q = t == 0 ? a.dy : t == 1 ? a.dh_in : t == 2 ? (has_dy ? a.h : nullptr) : a.x;
-    const int64_t ld = t == 0 ? a.lddy : t == 1 ? a.lddh : t == 2 ? a.ldh : a.ldx;
-    src->next[t] = q ? (unsigned long long)reinterpret_cast<uintptr_t>(reinterpret_cast<const T*>(q) + row * ld + c0) : 0ull;
-    src->step[t] = (unsigned long long)(step * ld * ES);
+  const int group = threadIdx.x / tpr;
+  const int t = threadIdx.x - group * tpr;
+  const int nw = tpr >> 5, wig = t >> 5, lane = threadIdx.x & 31;
+  const int b0 = C::base(t);
+  const int lim = H - b0;
+  const float inv_h = 1.f / (float)a.H;
+  const bool w_f32 = a.w_f32 != 0, g_f32 = a.g_f32 != 0;
+  const size_t wes = w_f32 ? 4 : sizeof(T), ges = g_f32 ? 4 : sizeof(T);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm_join) + group * kJoinMaxBuffers;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm_join + kJoinAbortOff);
+  float* red = reinterpret_cast<float*>(sm_join + ring.red_off) + group * kJoinRedFloats;
+  float* slot = reinterpret_cast<float*>(sm_join + ring.par_off) + threadIdx.x * SLOT;
+  const int row_bytes = kJoinRowTensors * ring.buf_bytes;  // a row's four buffers
+  unsigned char* bufs = sm_join + ring.buf_off + (size_t)group * ring.nb * row_bytes;
+  const int bar_id = 1 + group;
+  const int NB = ring.nb;
+  const bool has_dy = a.dy != nullptr && copies, has_in = a.dh_in != nullptr && copies;
+  int* shift = reinterpret_cast<int*>(sm_join + kJoinShiftOff) + group * kJoinMaxBuffers * kJoinRowTensors;
+
+  const int unit = unit0 + group;
+  int64_t row, step, left;
+  join_unit_rows<RUNS>(a, unit, units, row, left, step);
+  const int64_t first_row = row, end = row + left * step;  // (RUNS: step is 1)
+
+  // Copies: lane 8k + i of the group's first warp serves tensor k.
+  const int ck = lane >> 3, ci = lane & 7;
+  const T* next = nullptr;  // the tensor's next row to ask for
+  int64_t next_step = 0;
+  if (wig == 0 && copies) {
+    next = reinterpret_cast<const T*>(ck == 0 ? a.dy : ck == 1 ? a.dh_in : ck == 2 ? (has_dy ? a.h : nullptr) : a.x);
+    next_step = step * (ck == 0 ? a.lddy : ck == 1 ? a.lddh : ck == 2 ? a.ldh : a.ldx);
+    if (next) next += row * (ck == 0 ? a.lddy : ck == 1 ? a.lddh : ck == 2 ? a.ldh : a.ldx) + c0;
   }
-  __syncthreads();
-  unsigned used = 0u, fills = 0u;  // per buffer: ever filled; fills issued, mod 2 (thread 0 of the group)
-  // The ends of a row that no whole line holds: lane l of the group's first
-  // warp takes elements l and l + 32 of the 4 tensors x {front, back} x 8.
-  struct Edge {
-    T v[2];
-    int at[2];  // byte offset in the row buffers, or -1
-  };
-  // Ask for the next row, into buffer `buf`: by the group's first warp.
-  auto issue = [&](int buf, Edge& ed) {
+  int issued = 0;  // rows asked for
+  T edge0 = T(0.f), edge1 = T(0.f);
+  int edge_at0 = -1, edge_at1 = -1;  // byte offsets in the row buffers, or none
+  auto issue = [&](int buf) {  // by the group's first warp
+    const uintptr_t s = reinterpret_cast<uintptr_t>(next), e = s + (uintptr_t)H * ES, line = s & ~(uintptr_t)15;
+    const uintptr_t up = (s + 15) & ~(uintptr_t)15, down = e & ~(uintptr_t)15;
+    const int dst = buf * row_bytes + ck * ring.buf_bytes;
     if constexpr (EDGES) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        ed.at[j] = -1;
-        const int id = lane + 32 * j, k = id >> 4, back = (id >> 3) & 1, i = id & 7;
-        const unsigned long long s = src->next[k];
-        if (s == 0) continue;
-        const unsigned long long e = s + (unsigned long long)H * ES, up = (s + 15) & ~15ull, down = e & ~15ull;
-        const unsigned long long from = back ? (down > up ? down : up) : s, to = back ? e : (up < e ? up : e);
-        const unsigned long long p = from + (unsigned long long)(i * ES);
-        if (from >= to || p >= to) continue;
-        ed.v[j] = *reinterpret_cast<const T*>(p);
-        ed.at[j] = buf * row_bytes + k * ring.buf_bytes + (int)(p - (s & ~15ull));
+      edge_at0 = edge_at1 = -1;
+      if (next) {
+        // front [s, min(up, e)), back [max(up, down), e): at most 8 elements each
+        const uintptr_t p0 = s + (uintptr_t)ci * ES, p1 = (down > up ? down : up) + (uintptr_t)ci * ES;
+        if (p0 < (up < e ? up : e)) {
+          edge0 = *reinterpret_cast<const T*>(p0);
+          edge_at0 = dst + (int)(p0 - line);
+        }
+        if (p1 < e) {
+          edge1 = *reinterpret_cast<const T*>(p1);
+          edge_at1 = dst + (int)(p1 - line);
+        }
       }
-      __syncwarp();  // read before thread 0 moves on
     }
-    if (lane == 0) {
-      uint32_t total = 0;
-#pragma unroll 1
-      for (int k = 0; k < kJoinRowTensors; ++k) {
-        const unsigned long long s = src->next[k];
-        if (s == 0) continue;
-        const unsigned long long from = (s + 15) & ~15ull, to = (s + (unsigned long long)H * ES) & ~15ull;
-        if (to > from) total += (uint32_t)(to - from);
-      }
-      if constexpr (EDGES) {
-        for (int k = 0; k < kJoinRowTensors; ++k) src->off[buf][k] = (int)(src->next[k] & 15ull);
-      }
-      mbar_arrive_expect_tx(&bars[buf], total);
-#pragma unroll 1
-      for (int k = 0; k < kJoinRowTensors; ++k) {
-        const unsigned long long s = src->next[k];
-        if (s == 0) continue;
-        const unsigned long long from = (s + 15) & ~15ull, to = (s + (unsigned long long)H * ES) & ~15ull;
-        if (to > from)
-          bulk_g2s(bufs + buf * row_bytes + k * ring.buf_bytes + (from - (s & ~15ull)), reinterpret_cast<const void*>(from),
-                   (uint32_t)(to - from), &bars[buf]);
-        src->next[k] = s + src->step[k];
-      }
-      used |= 1u << buf;
-      fills ^= 1u << buf;
+    if (ci == 0) {
+      const uint32_t n = next && down > up ? (uint32_t)(down - up) : 0u;
+      if constexpr (EDGES) shift[buf * kJoinRowTensors + ck] = (int)(s - line);
+      mbar_arrive_expect_tx(&full[buf], n);
+      if (n != 0) bulk_g2s(bufs + dst + (up - line), reinterpret_cast<const void*>(up), n, &full[buf]);
     }
-    if constexpr (EDGES) __syncwarp();
+    if (next) next += next_step;
+    ++issued;
   };
-  auto edge_store = [&](Edge& ed) {
+  auto edge_store = [&]() {
     if constexpr (EDGES) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (ed.at[j] >= 0) *reinterpret_cast<T*>(bufs + ed.at[j]) = ed.v[j];
-        ed.at[j] = -1;
-      }
+      if (edge_at0 >= 0) *reinterpret_cast<T*>(bufs + edge_at0) = edge0;
+      if (edge_at1 >= 0) *reinterpret_cast<T*>(bufs + edge_at1) = edge1;
+      edge_at0 = edge_at1 = -1;
     }
   };
-  Edge edge;
-  if (copies) {
-    for (int i = 0; i < NB; ++i) {
-      if (row + i * step >= end) break;
-      if (wig == 0) {
-        issue(i, edge);
-        edge_store(edge);
-      }
+  if (wig == 0 && copies) {
+    for (int i = 0; i < NB && i < left; ++i) {
+      issue(i);
+      edge_store();
     }
   }
-  if constexpr (EDGES) edge.at[0] = edge.at[1] = -1;
 
   auto at = [](const void* p, int64_t i, size_t es) -> const void* {
     return p ? reinterpret_cast<const unsigned char*>(p) + i * es : nullptr;
@@ -353,7 +348,7 @@ __global__ void __launch_bounds__(MAXT, MINB) join_grad_rows_kernel(const JoinGr
     for (int e = 0; e < E; ++e) f[e] = 1.f;
     C::scale_by_param(at(a.gpre, c0, wes), w_f32, b0, lim, f);
     put_params<E>(slot + E, f);
-    if (row < end) stage_w(row);
+    if (left > 0) stage_w(row);
     if constexpr (RUNS) {
 #pragma unroll
       for (int e = 0; e < E; ++e) f[e] = 0.f;
@@ -398,6 +393,29 @@ __global__ void __launch_bounds__(MAXT, MINB) join_grad_rows_kernel(const JoinGr
   T* dxp = reinterpret_cast<T*>(a.dx) + row * a.lddx + c0 + b0;
   T* drp = reinterpret_cast<T*>(a.dres) + row * a.lddres + c0 + b0;
   const int64_t dx_step = step * a.lddx, dr_step = step * a.lddres;
+  // The thread's columns of tensor k, from a row buffer.
+  const uint32_t bufs32 = smem_u32(bufs) + b0 * ES, slot32 = smem_u32(slot);
+  auto read = [&](uint32_t p, bool there, uint32_t (&w)[NW]) {
+#pragma unroll
+    for (int i = 0; i < NW; ++i) w[i] = 0u;
+    if (!there) return;
+    if constexpr (GB >= 16) {
+#pragma unroll
+      for (int g = 0; g < C::NG; ++g)
+        if (C::col(g * C::GE) < lim) lds_words<4>(p + C::col(g * C::GE) * ES, w + 4 * g);
+    } else if constexpr (ES == 4) {
+#pragma unroll
+      for (int g = 0; g < C::NG; ++g)
+        if (C::col(g) < lim) w[g] = lds_u32(p + C::col(g) * 4);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        const uint32_t lo = C::col(2 * i) < lim ? lds_u16(p + C::col(2 * i) * 2) : 0u;
+        const uint32_t hi = C::col(2 * i + 1) < lim ? lds_u16(p + C::col(2 * i + 1) * 2) : 0u;
+        w[i] = __byte_perm(lo, hi, 0x5410);
+      }
+    }
+  };
   const float2 alpha2 = splat2(a.alpha);
   int parity = 0, buf = 0;
   unsigned phase = 0u, it = 0;  // phase: parity of the ring's current turn
@@ -406,79 +424,46 @@ __global__ void __launch_bounds__(MAXT, MINB) join_grad_rows_kernel(const JoinGr
     if (a.rpre) nrn = a.rpre[r];
     if (a.rpost) nro = a.rpost[r];
   };
-  if (row < end) fetch_stats(row);
-  for (; row < end; row += step) {
+  if (left > 0) fetch_stats(row);
+  for (; left > 0; --left, row += step) {
     if (RUNS && row >= gate_end) {
       flush(gate_row);
       stage_w(row);
     }
     const float rn = nrn, ro = nro;
-    if (row + step < end) fetch_stats(row + step);
-    edge_store(edge);
-    bool ok = true;
-    if (copies) ok = mbar_wait(&bars[buf], phase, a.err, abort_flag);
-    const unsigned char* base = bufs + buf * row_bytes;
-    auto read = [&](int k, bool there, uint32_t (&w)[NW]) {
-      if (!there || !copies) {
-#pragma unroll
-        for (int i = 0; i < NW; ++i) w[i] = 0u;
-        return;
-      }
-      const unsigned char* p = base + k * ring.buf_bytes + b0 * ES;
-      if constexpr (GB >= 16) {
-#pragma unroll
-        for (int g = 0; g < C::NG; ++g) {
-          uint4 u = make_uint4(0u, 0u, 0u, 0u);
-          if (C::col(g * C::GE) < lim) u = lds16(p + C::col(g * C::GE) * ES);
-          w[4 * g] = u.x;
-          w[4 * g + 1] = u.y;
-          w[4 * g + 2] = u.z;
-          w[4 * g + 3] = u.w;
-        }
-      } else {
-        p += src->off[buf][k];
-        if constexpr (ES == 4) {
-#pragma unroll
-          for (int g = 0; g < C::NG; ++g)
-            w[g] = C::col(g) < lim ? *reinterpret_cast<const uint32_t*>(p + C::col(g) * 4) : 0u;
-        } else {
-#pragma unroll
-          for (int i = 0; i < NW; ++i) {
-            const uint32_t lo = C::col(2 * i) < lim ? *reinterpret_cast<const uint16_t*>(p + C::col(2 * i) * 2) : 0u;
-            const uint32_t hi =
-                C::col(2 * i + 1) < lim ? *reinterpret_cast<const uint16_t*>(p + C::col(2 * i + 1) * 2) : 0u;
-            w[i] = __byte_perm(lo, hi, 0x5410);
-          }
-        }
-      }
-    };
-    // pass 1: t = dh_in + rstd_pre * g, and the row's three sums over h and x
-    // (the statistics that turn them into h_hat and o_hat come in behind)
-    uint32_t dyw[NW], xw[NW], hw[NW];
-    float2 tt[NP];
-    read(0, has_dy, dyw);
-    read(2, has_dy, hw);
-    read(3, true, xw);
+    if (left > 1) fetch_stats(row + step);
+    edge_store();
+    int ok = 1;
+    if (copies) ok = mbar_wait(&full[buf], phase, a.err, abort_flag);
+    asm volatile("" : "+r"(ok));  // one body for both outcomes
+    uint32_t dyw[NW], iw[NW], hw[NW], xw[NW];
+    {
+      const uint32_t base = bufs32 + buf * row_bytes;
+      const int* sft = shift + buf * kJoinRowTensors;
+      read(base + (EDGES ? sft[0] : 0), has_dy, dyw);
+      read(base + ring.buf_bytes + (EDGES ? sft[1] : 0), has_in, iw);
+      read(base + 2 * ring.buf_bytes + (EDGES ? sft[2] : 0), has_dy, hw);
+      read(base + 3 * ring.buf_bytes + (EDGES ? sft[3] : 0), copies, xw);
+    }
+    // pass 1: the row's three sums over t = dh_in + rstd_pre * g, h and x (the
+    // statistics that turn h and x into h_hat and o_hat come in behind)
     float s[3];
     {
-      uint32_t iw[NW];
-      read(1, has_in, iw);
       float2 s0 = splat2(0.f), s1 = splat2(0.f), s2 = splat2(0.f);
       const float2 rn2 = splat2(rn);
 #pragma unroll
       for (int q = 0; q < NP / 2; ++q) {
         float2 w[2], gp[2];
-        get_pairs(slot, q, w);
-        get_pairs(slot + E, q, gp);
+        lds_pairs(slot32 + 16 * q, w);
+        lds_pairs(slot32 + 4 * E + 16 * q, gp);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int p = 2 * q + i;
           const float2 g = mul2(word_pair<D>(dyw, p), gp[i]);
           const float2 wx = mul2(word_pair<D>(xw, p), w[i]);
           const float2 h = word_pair<D>(hw, p);
-          tt[p] = fma2(g, rn2, word_pair<D>(iw, p));
           s0 = fma2(g, h, s0);
-          s1 = fma2(wx, tt[p], s1);
+          s1 = fma2(wx, fma2(g, rn2, word_pair<D>(iw, p)), s1);
           s2 = fma2(wx, h, s2);
         }
       }
@@ -486,43 +471,65 @@ __global__ void __launch_bounds__(MAXT, MINB) join_grad_rows_kernel(const JoinGr
       s[1] = s1.x + s1.y;
       s[2] = s2.x + s2.y;
     }
-    group_sum<3>(s, red, nw, wig, lane, bar_id, parity);
+    {
+      // value k in lanes 8k..8k+7 of each warp, then eight lanes a value over the group's warps
+      float part = warp_sum_scatter<3>(s, lane);
+      if (nw > 1) {
+        const int v = min(lane >> 3, 2);
+        if ((lane & 7) == 0 && lane < 24) red[(parity * 3 + v) * kJoinRedStride + wig] = part;
+        named_barrier(bar_id, tpr);
+        const float* from = red + (parity * 3 + v) * kJoinRedStride;
+        part = 0.f;
+#pragma unroll
+        for (int i = 0; i < kJoinRedStride / 8; ++i)
+          if ((lane & 7) + 8 * i < nw) part += from[(lane & 7) + 8 * i];
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+      }
+#pragma unroll
+      for (int k = 0; k < 3; ++k) s[k] = __shfl_sync(0xffffffffu, part, 8 * k);
+    }
     parity ^= 1;
-    if (nw == 1) __syncwarp();
     // every thread has read this buffer: refill it with the row NB ahead
-    if (wig == 0 && copies && row + NB * step < end && !*abort_flag) {
+    if (wig == 0 && copies && left > NB && !*abort_flag) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      issue(buf, edge);
+      issue(buf);
     }
     if constexpr (CL > 1) {
-      ok &= cluster_group_sum_async<3, CL>(s, xch[it & 1], &xbar[it & 1], (it >> 1) & 1u, crank, a.err, abort_flag);
+      ok &= (int)cluster_group_sum_async<3, CL>(s, xch[it & 1], &xbar[it & 1], (it >> 1) & 1u, crank, a.err, abort_flag);
       ++it;
     }
     // c = mean(g h_hat), dh = t - rstd_pre c h_hat, k = mean(w dh o_hat)
     const float crr = s[0] * inv_h * rn * rn * rn;
     const float k = a.rpost ? ro * fmaf(-crr, s[2], s[1]) * inv_h : 0.f;
-    // unpack again rather than hold the fp32 values over the barrier
-#pragma unroll
-    for (int i = 0; i < NW; ++i) asm volatile("" : "+r"(dyw[i]), "+r"(hw[i]), "+r"(xw[i]));
     const float2 nc2 = splat2(-crr), rn2 = splat2(rn), ro2 = splat2(ro), nk2 = splat2(-k * ro * ro);
-    if (ok) {
-      uint32_t od[NW], ox[NW];
+    uint32_t od[NW], ox[NW];
+    // Unpack again rather than hold the fp32 values over the barrier.  The wait
+    // (for the phase before a barrier's first: over before it begins) is there
+    // for the compiler, which otherwise moves the outputs' unpacking up among
+    // the row sums and spills 184 bytes a thread; a cluster has one of its own.
+    if constexpr (CL == 1) mbar_wait(&xbar[0], 1u, a.err, nullptr);
 #pragma unroll
-      for (int q = 0; q < NP / 2; ++q) {
-        float2 w[2];
-        get_pairs(slot, q, w);
+    for (int i = 0; i < NW; ++i) asm volatile("" : "+r"(dyw[i]), "+r"(iw[i]), "+r"(hw[i]), "+r"(xw[i]));
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int p = 2 * q + i;
-          const float2 x = word_pair<D>(xw, p), h = word_pair<D>(hw, p);
-          const float2 dh = fma2(h, nc2, tt[p]);
-          pair_word<D>(od, p, mul2(dh, alpha2));
-          const float2 dr = mul2(dh, ro2);
-          pair_word<D>(ox, p, fma2(x, nk2, mul2(dr, w[i])));
-          acc_pre[p] = fma2(word_pair<D>(dyw, p), mul2(h, rn2), acc_pre[p]);
-          acc[p] = fma2(dr, x, acc[p]);
-        }
+    for (int q = 0; q < NP / 2; ++q) {
+      float2 w[2], gp[2];
+      lds_pairs(slot32 + 16 * q, w);
+      lds_pairs(slot32 + 4 * E + 16 * q, gp);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int p = 2 * q + i;
+        const float2 x = word_pair<D>(xw, p), h = word_pair<D>(hw, p);
+        const float2 dyr = mul2(word_pair<D>(dyw, p), rn2);
+        const float2 dh = fma2(h, nc2, fma2(dyr, gp[i], word_pair<D>(iw, p)));
+        pair_word<D>(od, p, mul2(dh, alpha2));
+        const float2 dr = mul2(dh, ro2);
+        pair_word<D>(ox, p, fma2(x, nk2, mul2(dr, w[i])));
+        acc_pre[p] = fma2(dyr, h, acc_pre[p]);
+        acc[p] = fma2(dr, x, acc[p]);
       }
+    }
+    if (ok) {
       C::store(drp, lim, od);
       C::store(dxp, lim, ox);
     }
@@ -533,10 +540,8 @@ __global__ void __launch_bounds__(MAXT, MINB) join_grad_rows_kernel(const JoinGr
       phase ^= 1u;
     }
   }
-  if (t == 0) {  // no copy outlives the CTA (they have all been waited for unless a wait ran out)
-    for (int q = 0; q < NB; ++q)  // the last fill of buffer q has parity (fills - 1) mod 2
-      if ((used >> q) & 1u) mbar_wait(&bars[q], ((fills >> q) & 1u) ^ 1u, a.err, nullptr);
-  }
+  if (t == 0)  // no copy outlives the CTA (they have all been waited for unless a wait ran out)
+    for (int q = 0; q < NB && q < issued; ++q) mbar_wait(&full[q], (unsigned)((issued - 1 - q) / NB) & 1u, a.err, nullptr);
   if (RUNS && first_row < end) flush(gate_row);
   if constexpr (CL > 1) cluster_sync_all();  // no CTA leaves while a partner may still write to it
   if (a.ws_pre == nullptr) return;
@@ -774,27 +779,53 @@ static cudaError_t run_join_grad_rows(JoinGradArgs& a, const JoinRing& ring, con
   return cudaGetLastError();
 }
 
-// The fewest CTAs a row (1, 2, 4, 8) whose part fits 512 threads and at least
-// four row buffers; *done = false where none does.
-template <typename D, int GB, bool RUNS>
-static cudaError_t run_join_grad(JoinGradArgs& a, const DeviceInfo& dev, cudaStream_t s, bool* done) {
+// CTAs of at most MAXT threads, MINB an SM, in clusters of the fewest CTAs a row
+// (1, 2, 4, 8) whose part of it fits the threads and at least two row buffers;
+// *done = false where none does.
+template <typename D, int GB, bool RUNS, int MAXT, int MINB>
+static cudaError_t run_join_grad_shape(JoinGradArgs& a, const DeviceInfo& dev, cudaStream_t s, bool* done) {
   using C = Chunk<D, GB, kJoinGradCols<D>>;
   *done = true;
   for (int cl = 1; cl <= 8; cl *= 2) {
-    const JoinRing two = join_ring<C::E>(a.H, C::ES, C::GE, cl, RUNS, dev.max_smem_optin);
-    if (two.tpr > 512 || two.nb < kJoinMinBuffers) continue;
-    if (cl == 1 && two.tpr <= 256) {
-      // two CTAs an SM where each still has its buffers
-      const JoinRing half = join_ring<C::E>(a.H, C::ES, C::GE, 1, RUNS, (dev.max_smem_optin - 2048) / 2);
-      return run_join_grad_rows<D, GB, RUNS, 256, 2, 1>(a, half.nb >= kJoinMinBuffers ? half : two, dev, s);
-    }
-    if (cl == 1) return run_join_grad_rows<D, GB, RUNS, 512, 1, 1>(a, two, dev, s);
-    if (cl == 2) return run_join_grad_rows<D, GB, RUNS, 512, 1, 2>(a, two, dev, s);
-    if (cl == 4) return run_join_grad_rows<D, GB, RUNS, 512, 1, 4>(a, two, dev, s);
-    return run_join_grad_rows<D, GB, RUNS, 512, 1, 8>(a, two, dev, s);
+    const JoinRing r = join_ring<C::E>(a.H, C::ES, C::GE, cl, RUNS, MAXT, MINB, dev.max_smem_optin);
+    if (r.tpr > MAXT || r.nb < kJoinMinBuffers) continue;
+    if (cl == 1) return run_join_grad_rows<D, GB, RUNS, MAXT, MINB, 1>(a, r, dev, s);
+    if (cl == 2) return run_join_grad_rows<D, GB, RUNS, MAXT, MINB, 2>(a, r, dev, s);
+    if (cl == 4) return run_join_grad_rows<D, GB, RUNS, MAXT, MINB, 4>(a, r, dev, s);
+    return run_join_grad_rows<D, GB, RUNS, MAXT, MINB, 8>(a, r, dev, s);
   }
   *done = false;
   return cudaSuccess;
+}
+
+template <typename D, int GB, bool RUNS>
+static cudaError_t run_join_grad(JoinGradArgs& a, const DeviceInfo& dev, cudaStream_t s, bool* done) {
+  // Measured (us, bf16 unless said; in brackets the CTAs a row of each shape):
+  //   threads x CTAs an SM      160x3    256x2    512x1
+  //   16384x2048                 75.3     71.6       -
+  //   8192x4096 (cluster of 2)   76.2     73.5*    84.4*   (* one CTA a row)
+  //   8192x5120 (2)              86.4    112.7    103.3*
+  //   4096x8192 (4; 2)           91.0     80.8     79.0*
+  //   2048x16384 (8; 4; 2)      102.0     85.6     89.7
+  //   8197x2056 fp16, 7 gates    58.8*    69.9*       -
+  //   fp32 4096x4096 (4; 2)      67.6     71.1     65.7*
+  //   fp32 2048x8192 (8; 4; 2)   69.0     70.6     69.0
+  // Half precision takes 256x2, or 160x3 where the part of a row that fits 256
+  // threads has 129 to 160; fp32, eight columns a thread and half the
+  // instructions a byte, one large CTA.
+  const int whole = chunk_threads(a.H, kJoinGradCols<D>);
+  if constexpr (D::VEC == 4) {
+    if (whole <= 256) return run_join_grad_shape<D, GB, RUNS, 256, 2>(a, dev, s, done);
+    return run_join_grad_shape<D, GB, RUNS, 512, 1>(a, dev, s, done);
+  } else {
+    int part = whole;
+    while (part > 256) part = (part / 2 + 31) / 32 * 32;
+    if (part > 128 && part <= 160) {
+      cudaError_t e = run_join_grad_shape<D, GB, RUNS, 160, 3>(a, dev, s, done);
+      if (*done) return e;
+    }
+    return run_join_grad_shape<D, GB, RUNS, 256, 2>(a, dev, s, done);
+  }
 }
 
 template <typename D>

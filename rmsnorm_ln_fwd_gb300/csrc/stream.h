@@ -122,7 +122,7 @@ struct LookupGradArgs {
   unsigned* err;
 };
 
-constexpr int kJoinMaxPartialsPerSm = 2;
+constexpr int kJoinMaxPartialsPerSm = 3;
 // Row groups a CTA of the gradient may have: an upper bound by the width, for
 // the workspace.
 inline int join_max_groups(int64_t H) { return H <= 512 ? 8 : H <= 1024 ? 4 : H <= 2048 ? 2 : 1; }
