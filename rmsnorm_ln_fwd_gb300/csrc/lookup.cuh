@@ -12,6 +12,7 @@
 
 #include <algorithm>
 
+#include "chunk.cuh"
 #include "common.cuh"
 #include "stream.h"
 
@@ -62,10 +63,140 @@ __global__ void __launch_bounds__(kLookupLoopThreads) lookup_loop_kernel(const L
   }
 }
 
+// Register rows.  A row group of tpr threads, E columns a thread (chunk.cuh),
+// walks rows row, row + stride, ...: the next row's columns are in flight while
+// this one is scaled, reduced and written, and the token of the row after that,
+// whose address they would otherwise wait for.
+// Floats of the row sums' scratch in front of the parameter slots, which need
+// 16-byte alignment.
+__host__ __device__ inline int lookup_red_floats(int rpc, int tpr) { return (rpc * 2 * (tpr / 32) + 3) & ~3; }
+
+template <typename D, int GB, int E_, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) lookup_rows_kernel(const LookupArgs a, const int tpr) {
+  using C = Chunk<D, GB, E_>;
+  using T = typename D::T;
+  constexpr int E = C::E, NP = C::NP, NW = C::NW;
+  constexpr int SLOT = param_slot<E, 1>();
+  extern __shared__ __align__(16) float sh_look[];
+  const int rpc = blockDim.x / tpr;
+  const int group = threadIdx.x / tpr;
+  const int t = threadIdx.x - group * tpr;
+  const int nw = tpr >> 5, wig = t >> 5, lane = threadIdx.x & 31;
+  const int b = C::base(t), lim = a.H - b;
+  const bool norm = a.y != nullptr;
+  float* sh = sh_look + group * (2 * nw);
+  float* slot = sh_look + lookup_red_floats(rpc, tpr) + t * SLOT;  // gamma, shared by the groups
+  const uint32_t slot32 = smem_u32(slot);
+  const int64_t step = (int64_t)gridDim.x * rpc;
+  int64_t row = (int64_t)blockIdx.x * rpc + group;
+  unsigned* err = t == 0 ? a.err : nullptr;
+  auto token = [&](int64_t r) { return load_token(a.tokens, a.tok64, r, a.V, err); };
+  uint32_t nx[NW];
+  auto fetch = [&](int64_t tok) {
+    C::load(reinterpret_cast<const T*>(a.table) + (tok < 0 ? 0 : tok) * a.ldt + b, tok < 0 ? 0 : lim, nx);
+  };
+  int64_t tok2 = -1;  // the next row's
+  if (row < a.N) {
+    fetch(token(row));
+    if (row + step < a.N) tok2 = token(row + step);
+  }
+  if (norm && group == 0) {
+    float f[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = 1.f;
+    C::scale_by_param(a.gamma, a.w_f32 != 0, b, lim, f);
+    put_params<E>(slot, f);
+  }
+  __syncthreads();
+  T* hp = reinterpret_cast<T*>(a.h) + row * a.ldh + b;
+  T* yp = norm ? reinterpret_cast<T*>(a.y) + row * a.ldy + b : nullptr;
+  const int64_t hstep = step * a.ldh, ystep = step * a.ldy;
+  const float2 scale2 = splat2(a.scale);
+  const float inv_h = 1.f / (float)a.H;
+  int parity = 0;
+  for (; row < a.N; row += step, hp += hstep) {
+    float2 f[NP], s2 = splat2(0.f);
+    uint32_t out[NW];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      f[p] = mul2(word_pair<D>(nx, p), scale2);
+      s2 = fma2(f[p], f[p], s2);
+      pair_word<D>(out, p, f[p]);
+    }
+    if (row + step < a.N) {
+      fetch(tok2);
+      if (row + 2 * step < a.N) tok2 = token(row + 2 * step);
+    }
+    C::store(hp, lim, out);
+    if (!norm) continue;
+    float s[1] = {s2.x + s2.y};
+    group_sum<1>(s, sh, nw, wig, lane, 1 + group, parity);
+    parity ^= 1;
+    const float rstd = rsqrtf(s[0] * inv_h + a.eps);
+    if (t == 0 && a.rstd) a.rstd[row] = rstd;
+    const float2 r2 = splat2(rstd);
+#pragma unroll
+    for (int q = 0; q < NP / 2; ++q) {
+      float2 g[2];
+      lds_pairs(slot32 + 16 * q, g);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) pair_word<D>(out, 2 * q + i, mul2(mul2(f[2 * q + i], r2), g[i]));
+    }
+    C::store(yp, lim, out);
+    yp += ystep;
+  }
+}
+
+template <typename D, int GB, int E, int MAXT, int MINB>
+static cudaError_t run_lookup_rows(const LookupArgs& a, const DeviceInfo& dev, cudaStream_t s) {
+  auto kern = lookup_rows_kernel<D, GB, E, MAXT, MINB>;
+  const int tpr = chunk_threads(a.H, E);
+  const int rpc = tpr <= 256 ? 256 / tpr : 1, threads = rpc * tpr;
+  const size_t smem = sizeof(float) * ((size_t)lookup_red_floats(rpc, tpr) + (size_t)tpr * param_slot<E, 1>());
+  if (smem > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  int per_sm = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem) != cudaSuccess || per_sm < 1) per_sm = 1;
+  const int64_t blocks = std::min<int64_t>((a.N + rpc - 1) / rpc, (int64_t)per_sm * dev.sm_count);
+  kern<<<(unsigned)blocks, threads, smem, s>>>(a, tpr);
+  return cudaGetLastError();
+}
+
+// 32 bytes a thread up to 1024 threads, in fp32 64 bytes beyond.
+template <typename D, int GB>
+static cudaError_t run_lookup(const LookupArgs& a, const DeviceInfo& dev, cudaStream_t s, bool* done) {
+  constexpr int E = 32 / (int)sizeof(typename D::T);
+  *done = true;
+  const int tpr = chunk_threads(a.H, E);
+  if (tpr <= 256) return run_lookup_rows<D, GB, E, 256, 3>(a, dev, s);
+  if (tpr <= 1024) return run_lookup_rows<D, GB, E, 1024, 1>(a, dev, s);
+  if constexpr (D::VEC == 4) {
+    constexpr int GB2 = GB == 32 ? 16 : GB;
+    if (chunk_threads(a.H, 16) <= 1024) return run_lookup_rows<D, GB2, 16, 1024, 1>(a, dev, s);
+  }
+  *done = false;
+  return cudaSuccess;
+}
+
 template <typename D>
 cudaError_t launch_lookup(LookupArgs a, const DeviceInfo& dev, cudaStream_t s) {
   (void)cudaGetLastError();  // drop a stale, non-sticky error left by an earlier call
+  using T = typename D::T;
   a.err = dev.err;
+  if (dev.path != PATH_LOOP) {
+    GranuleRule rule;
+    rule.add(a.table, a.ldt, sizeof(T));
+    rule.add(a.h, a.ldh, sizeof(T));
+    if (a.y) rule.add(a.y, a.ldy, sizeof(T));
+    const int gb = rule.bytes(a.H, sizeof(T));
+    bool done = false;
+    cudaError_t e = gb == 32   ? run_lookup<D, 32>(a, dev, s, &done)
+                    : gb == 16 ? run_lookup<D, 16>(a, dev, s, &done)
+                               : run_lookup<D, (int)sizeof(T)>(a, dev, s, &done);
+    if (done) return e;
+  }
   const int64_t blocks = std::min<int64_t>(a.N, (int64_t)dev.sm_count * 8);
   lookup_loop_kernel<D><<<(unsigned)blocks, kLookupLoopThreads, 0, s>>>(a);
   return cudaGetLastError();
@@ -74,14 +205,15 @@ cudaError_t launch_lookup(LookupArgs a, const DeviceInfo& dev, cudaStream_t s) {
 // ---------------------------------------------------------------------------
 // The table's gradient.
 //
-// Kernel 1 sorts the tokens by id, stably, on one cluster of eight CTAs, while
-// the grid's other clusters clear the table's gradient (not when it
-// accumulates).  Kernel 2 takes the sorted tokens in tiles of 32: a tile sums
-// the gradient rows of each id in it, in position order, and stores the ids
-// whose tokens all lie in the tile; the first and the last id of a tile may
-// have tokens in its neighbours, and leave one partial row each.  Kernel 3 sums
-// the partial rows of those ids in tile order.  Every sum therefore has one
-// order, whatever runs first: the gradient is the same bits at every call.
+// Kernel 1 sorts the tokens by id, stably, on one cluster of eight CTAs.
+// Kernel 2, launched alongside it, clears the rows that no token names (not
+// when the gradient accumulates); it ends after kernel 1, so that waiting for
+// it is waiting for both.  Kernel 3 takes the sorted tokens in tiles of 32: a
+// tile sums the gradient rows of each id in it, in position order, and stores
+// the ids whose tokens all lie in the tile; the first and the last id of a tile
+// may have tokens in its neighbours, and leave one partial row each.  Kernel 4
+// sums the partial rows of those ids in tile order.  Every sum therefore has
+// one order, whatever runs first: the gradient is the same bits at every call.
 // ---------------------------------------------------------------------------
 
 // Sort: a least-significant-digit radix sort of (id, position) pairs, ids
@@ -206,92 +338,247 @@ __device__ __forceinline__ void sort_tokens(const LookupGradArgs& a, SortPlan pl
   }
 }
 
-// Kernel 1: cluster 0 sorts, the others clear rows [0, V) of the gradient.
-template <typename D, bool F32OUT>
-__global__ void __launch_bounds__(kSortThreads) lookup_grad_sort_kernel(const LookupGradArgs a, const SortPlan plan) {
+// Kernel 1.
+static __global__ void __launch_bounds__(kSortThreads) lookup_grad_sort_kernel(const LookupGradArgs a, const SortPlan plan) {
   extern __shared__ __align__(16) int smem_sort[];
-  if (blockIdx.x < kSortCluster) {
-    sort_tokens(a, plan, smem_sort);
-    return;
-  }
-  using T = typename std::conditional<F32OUT, float, typename D::T>::type;
-  const int64_t cta = blockIdx.x - kSortCluster, n = gridDim.x - kSortCluster;
+  pdl_launch_dependents();
+  sort_tokens(a, plan, smem_sort);
+}
+
+// Kernel 2.  CTA c clears its range of the table's rows: from a bitmap of the
+// ids in the range that it draws from the tokens itself, or every row: reading
+// the tokens pays where the rows are long (kClearMarkBytes) and the tokens'
+// bytes at most a quarter of the range's.
+constexpr int kClearThreads = 512;
+constexpr int kClearMaxRange = 8192;  // rows a CTA marks at a time
+constexpr int kClearMarkBytes = 2048;
+
+template <typename O>
+__global__ void __launch_bounds__(kClearThreads) lookup_grad_clear_kernel(const LookupGradArgs a) {
+  using T = typename O::T;
+  __shared__ unsigned marks[kClearMaxRange / 32];
+  pdl_launch_dependents();
   T* out = reinterpret_cast<T*>(a.dtable);
   const size_t row_bytes = (size_t)a.H * sizeof(T);
-  const bool vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && (a.lddt * sizeof(T)) % 16 == 0 && row_bytes % 16 == 0;
-  if (vec && a.lddt == a.H) {
-    const int64_t words = a.V * (int64_t)(row_bytes / 16);
-    for (int64_t i = cta * kSortThreads + threadIdx.x; i < words; i += n * kSortThreads)
-      st_vec(reinterpret_cast<uint4*>(out) + i, make_uint4(0u, 0u, 0u, 0u));
-    return;
+  const size_t bits = reinterpret_cast<uintptr_t>(out) | (size_t)a.lddt * sizeof(T) | row_bytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t lo, hi;
+  cta_rows(a.V, blockIdx.x, gridDim.x, lo, hi);
+  const bool mark = row_bytes >= (size_t)kClearMarkBytes && a.N * (a.tok64 ? 8 : 4) <= (hi - lo) * (int64_t)row_bytes / 4;
+  if (!mark && (bits & 15u) == 0 && a.lddt == a.H) {
+    uint4* p = reinterpret_cast<uint4*>(out);
+    const int64_t per = (int64_t)(row_bytes / 16);
+    for (int64_t i = lo * per + threadIdx.x; i < hi * per; i += kClearThreads) st_vec(p + i, make_uint4(0u, 0u, 0u, 0u));
+    lo = hi;
   }
-  for (int64_t v = cta; v < a.V; v += n) {
-    T* row = out + v * a.lddt;
-    if (vec) {
-      for (int i = threadIdx.x; i < (int)(row_bytes / 16); i += kSortThreads)
-        st_vec(reinterpret_cast<uint4*>(row) + i, make_uint4(0u, 0u, 0u, 0u));
-    } else {
-      for (int j = threadIdx.x; j < a.H; j += kSortThreads) row[j] = T(0.f);
+  for (int64_t v0 = lo; v0 < hi; v0 += kClearMaxRange) {
+    const int n = (int)min(hi - v0, (int64_t)kClearMaxRange);
+    __syncthreads();
+    for (int i = threadIdx.x; i < (n + 31) / 32; i += kClearThreads) marks[i] = 0u;
+    __syncthreads();
+    if (mark) {
+#pragma unroll 4
+      for (int64_t i = threadIdx.x; i < a.N; i += kClearThreads) {
+        const int64_t t = load_token(a.tokens, a.tok64, i, a.V, nullptr);
+        const int64_t at = t - v0;
+        if (t != a.padding && at >= 0 && at < n) atomicOr(&marks[at >> 5], 1u << (at & 31));
+      }
+      __syncthreads();
     }
+    for (int r = warp; r < n; r += kClearThreads / 32) {
+      if ((marks[r >> 5] >> (r & 31)) & 1u) continue;
+      unsigned char* row = reinterpret_cast<unsigned char*>(out + (v0 + r) * a.lddt);
+      if ((bits & 31u) == 0) {
+        const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+        for (size_t i = (size_t)lane * 32; i < row_bytes; i += 1024) st_vec32(row + i, z);
+      } else if ((bits & 15u) == 0) {
+        for (size_t i = (size_t)lane * 16; i < row_bytes; i += 512) st_vec(row + i, make_uint4(0u, 0u, 0u, 0u));
+      } else {
+        for (int j = lane; j < a.H; j += 32) reinterpret_cast<T*>(row)[j] = T(0.f);
+      }
+    }
+  }
+  pdl_wait_primary();  // the sort
+}
+
+// Store `v`, the sums of the thread's columns from column c of row `id`, times
+// the scale, onto what the row holds when the gradient accumulates.  `vec`: the
+// table allows 16-byte access.
+template <typename O, typename C>
+__device__ __forceinline__ void store_grad(const LookupGradArgs& a, int64_t id, int c, int lim, bool vec,
+                                           const float (&v)[C::E]) {
+  using T = typename O::T;
+  T* row = reinterpret_cast<T*>(a.dtable) + id * a.lddt + c;
+  constexpr int VEC = O::VEC;
+  if constexpr (C::GE >= VEC) {
+    if (vec) {
+#pragma unroll
+      for (int e = 0; e < C::E; e += VEC) {
+        if (C::col(e) >= lim) continue;
+        float f[VEC];
+        if (a.accumulate) unpack<O>(ld_cached(row + C::col(e)), f);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) f[i] = fmaf(a.scale, v[e + i], a.accumulate ? f[i] : 0.f);
+        st_vec(row + C::col(e), pack<O>(f));
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < C::E; ++e) {
+    if (C::col(e) >= lim) continue;
+    store_elem<O>(row, C::col(e), fmaf(a.scale, v[e], a.accumulate ? load_elem<O>(row, C::col(e)) : 0.f));
   }
 }
 
-// Kernel 2: one tile of sorted tokens (blockIdx.x) and 256 columns (blockIdx.y).
-template <typename D, bool F32OUT>
-__global__ void __launch_bounds__(256) lookup_grad_tile_kernel(const LookupGradArgs a) {
+// Kernel 3: tiles of sorted tokens (blockIdx.x) by blocks of columns
+// (blockIdx.y), 32 bytes a thread.  The rows' addresses come from the sorted
+// pairs, so kBatch rows' loads are in flight at a time.
+constexpr int kTileThreads = 128;
+constexpr int kTileBatch = 8;
+
+template <typename D, typename O, int GB>
+__global__ void __launch_bounds__(kTileThreads) lookup_grad_tile_kernel(const LookupGradArgs a, int vec) {
+  using C = Chunk<D, GB, 32 / (int)sizeof(typename D::T)>;
   using T = typename D::T;
-  using O = typename std::conditional<F32OUT, F32, D>::type;
+  constexpr int E = C::E, NP = C::NP, NW = C::NW;
+  pdl_launch_dependents();
   pdl_wait_primary();
   __shared__ uint2 kv[kLookupTile + 2];  // with the neighbours' nearest ids
   const int64_t first = (int64_t)blockIdx.x * kLookupTile;
   const int n = (int)min((int64_t)kLookupTile, a.N - first);
   const unsigned none = 0xffffffffu;  // no id (ids are at most V < 2^31)
-  for (int i = threadIdx.x; i < n + 2; i += blockDim.x) {
+  for (int i = threadIdx.x; i < kLookupTile + 2; i += kTileThreads) {
     const int64_t at = first + i - 1;
     kv[i] = at >= 0 && at < a.N ? __ldcg(a.sorted + at) : make_uint2(none, 0u);
   }
   __syncthreads();
-  const int j = blockIdx.y * 256 + threadIdx.x;
-  if (j >= a.H) return;
-  float sum = 0.f;
-  for (int i = 0; i < n; ++i) {
-    const unsigned id = kv[i + 1].x;
-    if (id == (unsigned)a.V) break;  // ignored tokens sort last
-    sum += load_elem<D>(reinterpret_cast<const T*>(a.dh) + (int64_t)kv[i + 1].y * a.lddh, j);
-    if (i + 1 < n && kv[i + 2].x == id) continue;  // its last token in the tile
-    const bool open_front = kv[0].x == kv[1].x && id == kv[1].x;
-    const bool open_back = i + 1 == n && kv[n + 1].x == id;
-    if (open_front) {
-      a.partial[(size_t)2 * blockIdx.x * a.Hp + j] = sum;
-    } else if (open_back) {
-      a.partial[((size_t)2 * blockIdx.x + 1) * a.Hp + j] = sum;
-    } else {
-      const int64_t at = (int64_t)id * a.lddt + j;
-      const float old = a.accumulate ? load_elem<O>(a.dtable, at) : 0.f;
-      store_elem<O>(a.dtable, at, fmaf(a.scale, sum, old));
+  const unsigned ignored = (unsigned)a.V;
+  const bool open_front = kv[0].x == kv[1].x;
+  for (int c0 = blockIdx.y * (kTileThreads * E); c0 < a.H; c0 += gridDim.y * (kTileThreads * E)) {
+    const int c = c0 + C::base(threadIdx.x), lim = a.H - c;
+    const T* src = reinterpret_cast<const T*>(a.dh) + c;
+    float2 acc[NP];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) acc[p] = splat2(0.f);
+    for (int i0 = 0; i0 < n; i0 += kTileBatch) {
+      uint32_t w[kTileBatch][NW];
+#pragma unroll
+      for (int k = 0; k < kTileBatch; ++k) {
+        const uint2 e = kv[min(i0 + k, n - 1) + 1];
+        const bool on = i0 + k < n && e.x != ignored;
+        C::load(src + (int64_t)e.y * a.lddh, on ? lim : 0, w[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kTileBatch; ++k) {
+        const int i = i0 + k;
+        if (i >= n) break;
+        const unsigned id = kv[i + 1].x;
+        if (id == ignored) break;  // ignored tokens sort last
+#pragma unroll
+        for (int p = 0; p < NP; ++p) acc[p] = add2(acc[p], word_pair<D>(w[k], p));
+        if (i + 1 < n && kv[i + 2].x == id) continue;  // its last token in the tile
+        float v[E];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          v[2 * p] = acc[p].x;
+          v[2 * p + 1] = acc[p].y;
+          acc[p] = splat2(0.f);
+        }
+        const bool front = open_front && id == kv[1].x, back = i + 1 == n && kv[n + 1].x == id;
+        if (front || back) {
+          float* part = a.partial + ((size_t)2 * blockIdx.x + (front ? 0 : 1)) * a.Hp + c;
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (C::col(e) < lim) part[C::col(e)] = v[e];
+        } else {
+          store_grad<O, C>(a, id, c, lim, vec != 0, v);
+        }
+      }
     }
-    sum = 0.f;
   }
 }
 
-// Kernel 3: the ids whose tokens cross tiles; blockIdx.x is the tile boundary.
-template <typename D, bool F32OUT>
-__global__ void __launch_bounds__(256) lookup_grad_join_kernel(const LookupGradArgs a) {
-  using O = typename std::conditional<F32OUT, F32, D>::type;
+// Kernel 4: the ids whose tokens cross tiles.  A CTA looks at kJoinBounds tile
+// boundaries (blockIdx.x) for the first that an id crosses, and sums that id's
+// partial rows over 1024 columns (blockIdx.y): four row groups of 256 lanes,
+// four columns a lane, each group every fourth row, eight loads in flight; then
+// the groups in order.
+constexpr int kJoinBounds = 8;
+constexpr int kJoinThreads = 1024;
+
+template <typename O>
+__global__ void __launch_bounds__(kJoinThreads) lookup_grad_join_kernel(const LookupGradArgs a) {
+  constexpr int G = kJoinThreads / 256, U = 8;
   pdl_wait_primary();
-  const int64_t b = blockIdx.x;
-  const int64_t end = (b + 1) * kLookupTile;  // first token of tile b + 1
-  const unsigned id = __ldcg(a.sorted + end).x;
-  if (id == (unsigned)a.V || __ldcg(a.sorted + end - 1).x != id) return;  // nothing crosses here
-  if (b > 0 && __ldcg(a.sorted + b * kLookupTile - 1).x == id) return;    // an earlier boundary has it
-  const int j = blockIdx.y * 256 + threadIdx.x;
-  if (j >= a.H) return;
-  float sum = a.partial[((size_t)2 * b + 1) * a.Hp + j];
-  for (int64_t t = b + 1; t * kLookupTile < a.N && __ldcg(a.sorted + t * kLookupTile).x == id; ++t)
-    sum += a.partial[(size_t)2 * t * a.Hp + j];
-  const int64_t at = (int64_t)id * a.lddt + j;
-  const float old = a.accumulate ? load_elem<O>(a.dtable, at) : 0.f;
-  store_elem<O>(a.dtable, at, fmaf(a.scale, sum, old));
+  __shared__ unsigned first_id[kJoinBounds + 2], last_id[kJoinBounds + 2];
+  __shared__ float4 sums[G - 1][256];
+  const int64_t tiles = (a.N + kLookupTile - 1) / kLookupTile;
+  const int64_t b0 = (int64_t)blockIdx.x * kJoinBounds;
+  // tiles b0 - 1 .. b0 + kJoinBounds: their first and last ids
+  if (threadIdx.x < kJoinBounds + 2) {
+    const int64_t t = b0 - 1 + threadIdx.x;
+    const bool there = t >= 0 && t < tiles;
+    first_id[threadIdx.x] = there ? __ldcg(a.sorted + t * kLookupTile).x : 0xffffffffu;
+    last_id[threadIdx.x] = there ? __ldcg(a.sorted + min(t * kLookupTile + kLookupTile, a.N) - 1).x : 0xffffffffu;
+  }
+  __syncthreads();
+  const int g = threadIdx.x >> 8, lane = threadIdx.x & 255;
+  for (int k = 0; k < kJoinBounds; ++k) {
+    const int64_t b = b0 + k;  // between tiles b and b + 1
+    if (b + 1 >= tiles) break;
+    const unsigned id = first_id[k + 2];
+    if (id == (unsigned)a.V || last_id[k + 1] != id) continue;             // nothing crosses here
+    if (first_id[k + 1] == id && b > 0 && last_id[k] == id) continue;      // an earlier boundary has it
+    // the id's tiles: b, and those after it that begin with it
+    int64_t more = 0;
+    for (int64_t t = b + 1;; t += kJoinThreads) {
+      const int64_t at = t + threadIdx.x;
+      const int c = __syncthreads_count(at < tiles && __ldcg(a.sorted + at * kLookupTile).x == id);
+      more += c;
+      if (c < kJoinThreads) break;
+    }
+    for (int c0 = blockIdx.y * 1024; c0 < a.Hp; c0 += gridDim.y * 1024) {
+      const int c = c0 + lane * 4;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c < a.Hp) {
+        for (int64_t r0 = g; r0 <= more; r0 += G * U) {
+          float4 v[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int64_t r = r0 + u * G;
+            const int64_t slot = r == 0 ? 2 * b + 1 : 2 * (b + r);
+            v[u] = r <= more ? __ldcg(reinterpret_cast<const float4*>(a.partial + slot * a.Hp + c))
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            acc.x += v[u].x;
+            acc.y += v[u].y;
+            acc.z += v[u].z;
+            acc.w += v[u].w;
+          }
+        }
+      }
+      __syncthreads();
+      if (g > 0) sums[g - 1][lane] = acc;
+      __syncthreads();
+      if (g == 0 && c < a.H) {
+#pragma unroll
+        for (int q = 0; q < G - 1; ++q) {
+          const float4 o = sums[q][lane];
+          acc.x += o.x;
+          acc.y += o.y;
+          acc.z += o.z;
+          acc.w += o.w;
+        }
+        const float v[4] = {acc.x, acc.y, acc.z, acc.w};
+        const int64_t at = (int64_t)id * a.lddt + c;
+        for (int i = 0; i < 4 && c + i < a.H; ++i)
+          store_elem<O>(a.dtable, at + i, fmaf(a.scale, v[i], a.accumulate ? load_elem<O>(a.dtable, at + i) : 0.f));
+      }
+    }
+  }
 }
 
 template <typename K, typename... Args>
@@ -311,39 +598,59 @@ static cudaError_t launch_pdl(K kern, dim3 grid, dim3 block, size_t smem, cudaSt
   return cudaGetLastError();
 }
 
-template <typename D, bool F32OUT>
+template <typename D, typename O>
 static cudaError_t run_lookup_grad(const LookupGradArgs& a, const DeviceInfo& dev, cudaStream_t s) {
-  const SortPlan plan = sort_plan(a.V);
-  auto kern = lookup_grad_sort_kernel<D, F32OUT>;
-  const size_t smem = sizeof(int) * ((size_t)(kSortThreads / 32 + 2) * (1 << plan.bits) + kSortThreads / 32);
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaSuccess;
+  if (a.N > 0) {
+    const SortPlan plan = sort_plan(a.V);
+    const size_t smem = sizeof(int) * ((size_t)(kSortThreads / 32 + 2) * (1 << plan.bits) + kSortThreads / 32);
+    if (smem > 48 * 1024) {
+      e = cudaFuncSetAttribute(lookup_grad_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kSortCluster);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kSortCluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, lookup_grad_sort_kernel, a, plan);
+    if (e != cudaSuccess) return e;
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  // one cluster sorts; as many again as the GPU holds clear the gradient
-  const int clusters = a.accumulate ? 1 : std::max(2, dev.sm_count / kSortCluster);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(clusters * kSortCluster));
-  cfg.blockDim = dim3(kSortThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kSortCluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, plan);
-  if (e != cudaSuccess) return e;
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  if (a.N == 0) return cudaSuccess;
+  if (!a.accumulate) {
+    // three CTAs an SM: all of them fit at once beside the sort's, whose SMs
+    // have room for one each, so none starts late
+    const unsigned blocks = (unsigned)std::min<int64_t>(a.V, (int64_t)dev.sm_count * 3);
+    if (a.N == 0) {
+      lookup_grad_clear_kernel<O><<<blocks, kClearThreads, 0, s>>>(a);
+      return cudaGetLastError();
+    }
+    e = launch_pdl(lookup_grad_clear_kernel<O>, dim3(blocks), dim3(kClearThreads), 0, s, a);
+    if (e != cudaSuccess) return e;
+  }
+  using T = typename D::T;
+  using OT = typename O::T;
   const unsigned tiles = (unsigned)((a.N + kLookupTile - 1) / kLookupTile);
-  const unsigned cols = (unsigned)((a.H + 255) / 256);
-  e = launch_pdl(lookup_grad_tile_kernel<D, F32OUT>, dim3(tiles, cols), dim3(256), 0, s, a);
+  const int per = kTileThreads * 32 / (int)sizeof(T);
+  const dim3 grid(tiles, (unsigned)std::min((a.H + per - 1) / per, 1024));
+  GranuleRule in, out;
+  in.add(a.dh, a.lddh, sizeof(T));
+  out.add(a.dtable, a.lddt, sizeof(OT));
+  const int vec = out.bytes(a.H, sizeof(OT)) >= 16;
+  e = in.bytes(a.H, sizeof(T)) >= 16
+          ? launch_pdl(lookup_grad_tile_kernel<D, O, 16>, grid, dim3(kTileThreads), 0, s, a, vec)
+          : launch_pdl(lookup_grad_tile_kernel<D, O, (int)sizeof(T)>, grid, dim3(kTileThreads), 0, s, a, vec);
   if (e != cudaSuccess || tiles == 1) return e;
-  return launch_pdl(lookup_grad_join_kernel<D, F32OUT>, dim3(tiles - 1, cols), dim3(256), 0, s, a);
+  const dim3 joins((tiles - 1 + kJoinBounds - 1) / kJoinBounds, (unsigned)std::min((a.H + 1023) / 1024, 1024));
+  return launch_pdl(lookup_grad_join_kernel<O>, joins, dim3(kJoinThreads), 0, s, a);
 }
 
 template <typename D>
@@ -351,8 +658,8 @@ cudaError_t launch_lookup_grad(LookupGradArgs a, const DeviceInfo& dev, cudaStre
   (void)cudaGetLastError();  // drop a stale, non-sticky error left by an earlier call
   a.err = dev.err;
   if (a.N == 0 && a.accumulate) return cudaSuccess;
-  if (a.w_f32) return run_lookup_grad<D, true>(a, dev, s);
-  return run_lookup_grad<D, false>(a, dev, s);
+  if (a.w_f32) return run_lookup_grad<D, F32>(a, dev, s);
+  return run_lookup_grad<D, D>(a, dev, s);
 }
 
 }  // namespace normk
