@@ -208,7 +208,7 @@ cudaError_t launch_lookup(LookupArgs a, const DeviceInfo& dev, cudaStream_t s) {
 // Kernel 1 sorts the tokens by id, stably, on one cluster of eight CTAs.
 // Kernel 2, launched alongside it, clears the rows that no token names (not
 // when the gradient accumulates); it ends after kernel 1, so that waiting for
-// it is waiting for both.  Kernel 3 takes the sorted tokens in tiles of 32: a
+// it is waiting for both.  Kernel 3 takes the sorted tokens in tiles: a
 // tile sums the gradient rows of each id in it, in position order, and stores
 // the ids whose tokens all lie in the tile; the first and the last id of a tile
 // may have tokens in its neighbours, and leave one partial row each.  Kernel 4
@@ -247,6 +247,9 @@ __device__ __forceinline__ int ld_cluster_int(const int* local, unsigned rank) {
   return v;
 }
 
+// K > 0: a warp's part is at most 32*K items, which its lanes hold from the
+// count to the move; K = 0: any length, read twice.
+template <int K>
 __device__ __forceinline__ void sort_tokens(const LookupGradArgs& a, SortPlan plan, int* smem) {
   constexpr int NWARP = kSortThreads / 32;
   const int bins = 1 << plan.bits;
@@ -271,22 +274,39 @@ __device__ __forceinline__ void sort_tokens(const LookupGradArgs& a, SortPlan pl
       if (t < 0 || t == a.padding) t = a.V;
       return make_uint2((unsigned)t, (unsigned)i);
     };
+    auto digit = [&](uint2 kv) { return (int)((kv.x >> shift) & (unsigned)(bins - 1)); };
+    uint2 held[K > 0 ? K : 1];
+    if constexpr (K > 0) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (lo + 32 * k + lane < hi) held[k] = fetch(lo + 32 * k + lane);
+    }
     for (int b = lane; b < bins; b += 32) mine[b] = 0;
     __syncwarp();
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-      const bool on = i0 + lane < hi;
+    auto tally = [&](bool on, uint2 kv) {
       const unsigned act = __ballot_sync(0xffffffffu, on);
       if (on) {
-        const int d = (int)((fetch(i0 + lane).x >> shift) & (unsigned)(bins - 1));
+        const int d = digit(kv);
         const unsigned same = __match_any_sync(act, d);
         if ((same & below) == 0) mine[d] += __popc(same);
       }
       __syncwarp();
+    };
+    if constexpr (K > 0) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (lo + 32 * k < hi) tally(lo + 32 * k + lane < hi, held[k]);
+    } else {
+      for (int64_t i0 = lo; i0 < hi; i0 += 32) {
+        const bool on = i0 + lane < hi;
+        tally(on, on ? fetch(i0 + lane) : make_uint2(0u, 0u));
+      }
     }
     __syncthreads();
     // per bin: exclusive prefix over this CTA's warps, and its total
     for (int b = threadIdx.x; b < bins; b += kSortThreads) {
       int sum = 0;
+#pragma unroll 8
       for (int k = 0; k < NWARP; ++k) {
         const int c = count[k * bins + b];
         count[k * bins + b] = sum;
@@ -297,6 +317,7 @@ __device__ __forceinline__ void sort_tokens(const LookupGradArgs& a, SortPlan pl
     cluster_sync_all();  // every CTA's totals are there
     int all = 0, before = 0;
     if (threadIdx.x < bins) {
+#pragma unroll
       for (unsigned r = 0; r < kSortCluster; ++r) {
         const int c = ld_cluster_int(total + threadIdx.x, r);
         all += c;
@@ -318,20 +339,28 @@ __device__ __forceinline__ void sort_tokens(const LookupGradArgs& a, SortPlan pl
       base[threadIdx.x] = first;
     }
     __syncthreads();
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-      const bool on = i0 + lane < hi;
+    auto move = [&](bool on, uint2 kv) {
       const unsigned act = __ballot_sync(0xffffffffu, on);
       int d = 0;
       unsigned same = 0u;
       if (on) {
-        const uint2 kv = fetch(i0 + lane);
-        d = (int)((kv.x >> shift) & (unsigned)(bins - 1));
+        d = digit(kv);
         same = __match_any_sync(act, d);
         dst[base[d] + mine[d] + __popc(same & below)] = kv;
       }
       __syncwarp();  // every lane has read its counter
       if (on && (same & below) == 0) mine[d] += __popc(same);
       __syncwarp();
+    };
+    if constexpr (K > 0) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (lo + 32 * k < hi) move(lo + 32 * k + lane < hi, held[k]);
+    } else {
+      for (int64_t i0 = lo; i0 < hi; i0 += 32) {
+        const bool on = i0 + lane < hi;
+        move(on, on ? fetch(i0 + lane) : make_uint2(0u, 0u));
+      }
     }
     src = dst;
     cluster_sync_all();  // the pass's pairs are visible, its totals read
@@ -342,7 +371,15 @@ __device__ __forceinline__ void sort_tokens(const LookupGradArgs& a, SortPlan pl
 static __global__ void __launch_bounds__(kSortThreads) lookup_grad_sort_kernel(const LookupGradArgs a, const SortPlan plan) {
   extern __shared__ __align__(16) int smem_sort[];
   pdl_launch_dependents();
-  sort_tokens(a, plan, smem_sort);
+  constexpr int64_t kWarps = kSortCluster * kSortThreads / 32;
+  if (a.N <= kWarps * 32)
+    sort_tokens<1>(a, plan, smem_sort);
+  else if (a.N <= kWarps * 32 * 4)
+    sort_tokens<4>(a, plan, smem_sort);
+  else if (a.N <= kWarps * 32 * 8)
+    sort_tokens<8>(a, plan, smem_sort);
+  else
+    sort_tokens<0>(a, plan, smem_sort);
 }
 
 // Kernel 2.  CTA c clears its range of the table's rows: from a bitmap of the
@@ -352,12 +389,29 @@ static __global__ void __launch_bounds__(kSortThreads) lookup_grad_sort_kernel(c
 constexpr int kClearThreads = 512;
 constexpr int kClearMaxRange = 8192;  // rows a CTA marks at a time
 constexpr int kClearMarkBytes = 2048;
+constexpr int kClearZeros = 8192;  // bytes of zeros in shared memory, the source of its copies
+
+// Bulk copy from shared to global memory (both 16-byte aligned, bytes a
+// multiple of 16), and the wait for this thread's copies to have left shared
+// memory and been written.
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_s2g_drain() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
 
 template <typename O>
 __global__ void __launch_bounds__(kClearThreads) lookup_grad_clear_kernel(const LookupGradArgs a) {
   using T = typename O::T;
   __shared__ unsigned marks[kClearMaxRange / 32];
+  __shared__ __align__(16) unsigned char zeros[kClearZeros];
   pdl_launch_dependents();
+  for (int i = threadIdx.x; i < kClearZeros / 16; i += kClearThreads)
+    reinterpret_cast<uint4*>(zeros)[i] = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the __syncthreads below orders it for every thread)
   T* out = reinterpret_cast<T*>(a.dtable);
   const size_t row_bytes = (size_t)a.H * sizeof(T);
   const size_t bits = reinterpret_cast<uintptr_t>(out) | (size_t)a.lddt * sizeof(T) | row_bytes;
@@ -365,10 +419,12 @@ __global__ void __launch_bounds__(kClearThreads) lookup_grad_clear_kernel(const 
   int64_t lo, hi;
   cta_rows(a.V, blockIdx.x, gridDim.x, lo, hi);
   const bool mark = row_bytes >= (size_t)kClearMarkBytes && a.N * (a.tok64 ? 8 : 4) <= (hi - lo) * (int64_t)row_bytes / 4;
-  if (!mark && (bits & 15u) == 0 && a.lddt == a.H) {
-    uint4* p = reinterpret_cast<uint4*>(out);
-    const int64_t per = (int64_t)(row_bytes / 16);
-    for (int64_t i = lo * per + threadIdx.x; i < hi * per; i += kClearThreads) st_vec(p + i, make_uint4(0u, 0u, 0u, 0u));
+  if (!mark && (bits & 15u) == 0 && a.lddt == a.H) {  // one stretch of memory
+    __syncthreads();
+    unsigned char* p = reinterpret_cast<unsigned char*>(out + lo * a.H);
+    const int64_t bytes = (hi - lo) * (int64_t)row_bytes;
+    for (int64_t i = (int64_t)threadIdx.x * kClearZeros; i < bytes; i += (int64_t)kClearThreads * kClearZeros)
+      bulk_s2g(p + i, zeros, (uint32_t)min(bytes - i, (int64_t)kClearZeros));
     lo = hi;
   }
   for (int64_t v0 = lo; v0 < hi; v0 += kClearMaxRange) {
@@ -385,19 +441,23 @@ __global__ void __launch_bounds__(kClearThreads) lookup_grad_clear_kernel(const 
       }
       __syncthreads();
     }
-    for (int r = warp; r < n; r += kClearThreads / 32) {
-      if ((marks[r >> 5] >> (r & 31)) & 1u) continue;
-      unsigned char* row = reinterpret_cast<unsigned char*>(out + (v0 + r) * a.lddt);
-      if ((bits & 31u) == 0) {
-        const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-        for (size_t i = (size_t)lane * 32; i < row_bytes; i += 1024) st_vec32(row + i, z);
-      } else if ((bits & 15u) == 0) {
-        for (size_t i = (size_t)lane * 16; i < row_bytes; i += 512) st_vec(row + i, make_uint4(0u, 0u, 0u, 0u));
-      } else {
-        for (int j = lane; j < a.H; j += 32) reinterpret_cast<T*>(row)[j] = T(0.f);
+    if ((bits & 15u) == 0) {
+      // a thread a row, in bulk copies of the zeros
+      for (int r = threadIdx.x; r < n; r += kClearThreads) {
+        if ((marks[r >> 5] >> (r & 31)) & 1u) continue;
+        unsigned char* row = reinterpret_cast<unsigned char*>(out + (v0 + r) * a.lddt);
+        for (size_t i = 0; i < row_bytes; i += kClearZeros)
+          bulk_s2g(row + i, zeros, (uint32_t)min(row_bytes - i, (size_t)kClearZeros));
+      }
+    } else {
+      for (int r = warp; r < n; r += kClearThreads / 32) {
+        if ((marks[r >> 5] >> (r & 31)) & 1u) continue;
+        T* row = out + (v0 + r) * a.lddt;
+        for (int j = lane; j < a.H; j += 32) row[j] = T(0.f);
       }
     }
   }
+  bulk_s2g_drain();
   pdl_wait_primary();  // the sort
 }
 
@@ -444,11 +504,11 @@ __global__ void __launch_bounds__(kTileThreads) lookup_grad_tile_kernel(const Lo
   constexpr int E = C::E, NP = C::NP, NW = C::NW;
   pdl_launch_dependents();
   pdl_wait_primary();
-  __shared__ uint2 kv[kLookupTile + 2];  // with the neighbours' nearest ids
-  const int64_t first = (int64_t)blockIdx.x * kLookupTile;
-  const int n = (int)min((int64_t)kLookupTile, a.N - first);
+  __shared__ uint2 kv[kLookupMaxTile + 2];  // with the neighbours' nearest ids
+  const int64_t first = (int64_t)blockIdx.x * a.tile;
+  const int n = (int)min((int64_t)a.tile, a.N - first);
   const unsigned none = 0xffffffffu;  // no id (ids are at most V < 2^31)
-  for (int i = threadIdx.x; i < kLookupTile + 2; i += kTileThreads) {
+  for (int i = threadIdx.x; i < n + 2; i += kTileThreads) {
     const int64_t at = first + i - 1;
     kv[i] = at >= 0 && at < a.N ? __ldcg(a.sorted + at) : make_uint2(none, 0u);
   }
@@ -499,84 +559,70 @@ __global__ void __launch_bounds__(kTileThreads) lookup_grad_tile_kernel(const Lo
   }
 }
 
-// Kernel 4: the ids whose tokens cross tiles.  A CTA looks at kJoinBounds tile
-// boundaries (blockIdx.x) for the first that an id crosses, and sums that id's
-// partial rows over 1024 columns (blockIdx.y): four row groups of 256 lanes,
-// four columns a lane, each group every fourth row, eight loads in flight; then
-// the groups in order.
-constexpr int kJoinBounds = 8;
-constexpr int kJoinThreads = 1024;
+// Kernel 4: the ids whose tokens cross tiles.  The CTA of the first tile
+// boundary (blockIdx.x) that an id crosses sums its partial rows over 1024
+// columns (blockIdx.y): two row groups of 256 lanes, four columns a lane, each
+// group every other row, sixteen loads in flight; then the groups in order.
+constexpr int kJoinThreads = 512;
 
 template <typename O>
 __global__ void __launch_bounds__(kJoinThreads) lookup_grad_join_kernel(const LookupGradArgs a) {
-  constexpr int G = kJoinThreads / 256, U = 8;
+  constexpr int G = kJoinThreads / 256, U = 16;
   pdl_wait_primary();
-  __shared__ unsigned first_id[kJoinBounds + 2], last_id[kJoinBounds + 2];
   __shared__ float4 sums[G - 1][256];
-  const int64_t tiles = (a.N + kLookupTile - 1) / kLookupTile;
-  const int64_t b0 = (int64_t)blockIdx.x * kJoinBounds;
-  // tiles b0 - 1 .. b0 + kJoinBounds: their first and last ids
-  if (threadIdx.x < kJoinBounds + 2) {
-    const int64_t t = b0 - 1 + threadIdx.x;
-    const bool there = t >= 0 && t < tiles;
-    first_id[threadIdx.x] = there ? __ldcg(a.sorted + t * kLookupTile).x : 0xffffffffu;
-    last_id[threadIdx.x] = there ? __ldcg(a.sorted + min(t * kLookupTile + kLookupTile, a.N) - 1).x : 0xffffffffu;
-  }
-  __syncthreads();
+  const int64_t tile = a.tile, tiles = (a.N + tile - 1) / tile;
+  const int64_t b = blockIdx.x;  // between tiles b and b + 1
+  const unsigned id = __ldcg(a.sorted + (b + 1) * tile).x, left = __ldcg(a.sorted + (b + 1) * tile - 1).x;
+  const unsigned head = __ldcg(a.sorted + b * tile).x, tail = b > 0 ? __ldcg(a.sorted + b * tile - 1).x : 0xffffffffu;
+  if (id == (unsigned)a.V || left != id) return;  // nothing crosses here
+  if (head == id && tail == id) return;           // an earlier boundary has it
   const int g = threadIdx.x >> 8, lane = threadIdx.x & 255;
-  for (int k = 0; k < kJoinBounds; ++k) {
-    const int64_t b = b0 + k;  // between tiles b and b + 1
-    if (b + 1 >= tiles) break;
-    const unsigned id = first_id[k + 2];
-    if (id == (unsigned)a.V || last_id[k + 1] != id) continue;             // nothing crosses here
-    if (first_id[k + 1] == id && b > 0 && last_id[k] == id) continue;      // an earlier boundary has it
-    // the id's tiles: b, and those after it that begin with it
-    int64_t more = 0;
-    for (int64_t t = b + 1;; t += kJoinThreads) {
-      const int64_t at = t + threadIdx.x;
-      const int c = __syncthreads_count(at < tiles && __ldcg(a.sorted + at * kLookupTile).x == id);
-      more += c;
-      if (c < kJoinThreads) break;
+  // the id's tiles: b, and those after it that begin with it
+  int64_t more = 0;
+  for (int64_t t = b + 1;; t += kJoinThreads) {
+    const int64_t at = t + threadIdx.x;
+    const int c = __syncthreads_count(at < tiles && __ldcg(a.sorted + at * tile).x == id);
+    more += c;
+    if (c < kJoinThreads) break;
+  }
+  for (int c0 = blockIdx.y * 1024; c0 < a.Hp; c0 += gridDim.y * 1024) {
+    const int c = c0 + lane * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < a.Hp) {
+      for (int64_t r0 = g; r0 <= more; r0 += G * U) {
+        float4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t r = r0 + u * G;
+          const int64_t slot = r == 0 ? 2 * b + 1 : 2 * (b + r);
+          v[u] = r <= more ? __ldcg(reinterpret_cast<const float4*>(a.partial + slot * a.Hp + c))
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          acc.x += v[u].x;
+          acc.y += v[u].y;
+          acc.z += v[u].z;
+          acc.w += v[u].w;
+        }
+      }
     }
-    for (int c0 = blockIdx.y * 1024; c0 < a.Hp; c0 += gridDim.y * 1024) {
-      const int c = c0 + lane * 4;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c < a.Hp) {
-        for (int64_t r0 = g; r0 <= more; r0 += G * U) {
-          float4 v[U];
+    __syncthreads();
+    if (g > 0) sums[g - 1][lane] = acc;
+    __syncthreads();
+    if (g == 0 && c < a.H) {
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int64_t r = r0 + u * G;
-            const int64_t slot = r == 0 ? 2 * b + 1 : 2 * (b + r);
-            v[u] = r <= more ? __ldcg(reinterpret_cast<const float4*>(a.partial + slot * a.Hp + c))
-                             : make_float4(0.f, 0.f, 0.f, 0.f);
-          }
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            acc.x += v[u].x;
-            acc.y += v[u].y;
-            acc.z += v[u].z;
-            acc.w += v[u].w;
-          }
-        }
+      for (int q = 0; q < G - 1; ++q) {
+        const float4 o = sums[q][lane];
+        acc.x += o.x;
+        acc.y += o.y;
+        acc.z += o.z;
+        acc.w += o.w;
       }
-      __syncthreads();
-      if (g > 0) sums[g - 1][lane] = acc;
-      __syncthreads();
-      if (g == 0 && c < a.H) {
-#pragma unroll
-        for (int q = 0; q < G - 1; ++q) {
-          const float4 o = sums[q][lane];
-          acc.x += o.x;
-          acc.y += o.y;
-          acc.z += o.z;
-          acc.w += o.w;
-        }
-        const float v[4] = {acc.x, acc.y, acc.z, acc.w};
-        const int64_t at = (int64_t)id * a.lddt + c;
-        for (int i = 0; i < 4 && c + i < a.H; ++i)
-          store_elem<O>(a.dtable, at + i, fmaf(a.scale, v[i], a.accumulate ? load_elem<O>(a.dtable, at + i) : 0.f));
-      }
+      const float v[4] = {acc.x, acc.y, acc.z, acc.w};
+      const int64_t at = (int64_t)id * a.lddt + c;
+      for (int i = 0; i < 4 && c + i < a.H; ++i)
+        store_elem<O>(a.dtable, at + i, fmaf(a.scale, v[i], a.accumulate ? load_elem<O>(a.dtable, at + i) : 0.f));
     }
   }
 }
@@ -638,7 +684,7 @@ static cudaError_t run_lookup_grad(const LookupGradArgs& a, const DeviceInfo& de
   }
   using T = typename D::T;
   using OT = typename O::T;
-  const unsigned tiles = (unsigned)((a.N + kLookupTile - 1) / kLookupTile);
+  const unsigned tiles = (unsigned)((a.N + a.tile - 1) / a.tile);
   const int per = kTileThreads * 32 / (int)sizeof(T);
   const dim3 grid(tiles, (unsigned)std::min((a.H + per - 1) / per, 1024));
   GranuleRule in, out;
@@ -649,7 +695,7 @@ static cudaError_t run_lookup_grad(const LookupGradArgs& a, const DeviceInfo& de
           ? launch_pdl(lookup_grad_tile_kernel<D, O, 16>, grid, dim3(kTileThreads), 0, s, a, vec)
           : launch_pdl(lookup_grad_tile_kernel<D, O, (int)sizeof(T)>, grid, dim3(kTileThreads), 0, s, a, vec);
   if (e != cudaSuccess || tiles == 1) return e;
-  const dim3 joins((tiles - 1 + kJoinBounds - 1) / kJoinBounds, (unsigned)std::min((a.H + 1023) / 1024, 1024));
+  const dim3 joins(tiles - 1, (unsigned)std::min((a.H + 1023) / 1024, 1024));
   return launch_pdl(lookup_grad_join_kernel<O>, joins, dim3(kJoinThreads), 0, s, a);
 }
 
@@ -657,6 +703,7 @@ template <typename D>
 cudaError_t launch_lookup_grad(LookupGradArgs a, const DeviceInfo& dev, cudaStream_t s) {
   (void)cudaGetLastError();  // drop a stale, non-sticky error left by an earlier call
   a.err = dev.err;
+  a.tile = lookup_tile(a.N);
   if (a.N == 0 && a.accumulate) return cudaSuccess;
   if (a.w_f32) return run_lookup_grad<D, F32>(a, dev, s);
   return run_lookup_grad<D, D>(a, dev, s);

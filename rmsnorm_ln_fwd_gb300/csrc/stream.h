@@ -119,6 +119,7 @@ struct LookupGradArgs {
   uint2* sorted;  // (id, position), N of them; V as the id of an ignored token
   uint2* other;   // the sort's second buffer
   float* partial;  // [2 * tiles][Hp]
+  int tile;        // sorted tokens a tile (filled in by the launcher)
   unsigned* err;
 };
 
@@ -126,7 +127,10 @@ constexpr int kJoinMaxPartialsPerSm = 3;
 // Row groups a CTA of the gradient may have: an upper bound by the width, for
 // the workspace.
 inline int join_max_groups(int64_t H) { return H <= 512 ? 8 : H <= 1024 ? 4 : H <= 2048 ? 2 : 1; }
-constexpr int kLookupTile = 32;  // sorted tokens a tile of the table's gradient
+// Sorted tokens a tile of the table's gradient: few tokens take short tiles,
+// for the sake of their number.
+constexpr int kLookupMaxTile = 32;
+inline int lookup_tile(int64_t N) { return N <= 4096 ? 8 : N <= 8192 ? 16 : kLookupMaxTile; }
 
 // Device error bit of a token id outside the table.
 constexpr unsigned kErrBadToken = 4u;

@@ -52,7 +52,7 @@ size_t join_workspace(int64_t H, int64_t gate_rows, const DeviceInfo& dev) {
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-int64_t lookup_tiles(int64_t N) { return (N + normk::kLookupTile - 1) / normk::kLookupTile; }
+int64_t lookup_tiles(int64_t N) { return (N + normk::lookup_tile(N) - 1) / normk::lookup_tile(N); }
 
 // Two buffers of sorted pairs, then the tiles' partial rows.
 size_t lookup_workspace(int64_t N, int64_t H) {

@@ -407,7 +407,9 @@ def make_tokens(kind, N, V):
                                           (33, 1001, 600, "f16", "f16"), (65, 256, 513, "bf16", "bf16"),
                                           (2000, 48, 70000, "bf16", "f32"), (5000, 16, 300000, "f32", "f32"),
                                           (3333, 520, 1000, "f16", "f32"), (300, 4104, 64, "bf16", "bf16"),
-                                          (9000, 24, 511, "f32", "f32")])
+                                          (9000, 24, 511, "f32", "f32"), (20000, 8, 5000, "f32", "f32"),
+                                          (40000, 16, 140000, "bf16", "f32"), (70000, 8, 300, "f32", "f32"),
+                                          (5000, 1040, 3000, "bf16", "bf16"), (4097, 1001, 2500, "f32", "f32")])
 def test_lookup_grad(kind, N, H, V, dt, odt):
     tokens = make_tokens(kind, N, V)
     pad = V - 1 if kind == "padded" else -1
