@@ -205,10 +205,16 @@ cudaError_t launch_lookup(LookupArgs a, const DeviceInfo& dev, cudaStream_t s) {
 // ---------------------------------------------------------------------------
 // The table's gradient.
 //
-// Kernel 1 sorts the tokens by id, stably, on one cluster of eight CTAs.
-// Kernel 2, launched alongside it, clears the rows that no token names (not
-// when the gradient accumulates); it ends after kernel 1, so that waiting for
-// it is waiting for both.  Kernel 3 takes the sorted tokens in tiles: a
+// Kernel 1 sorts the tokens by id, stably, on one cluster of eight CTAs.  The
+// rows that no token names are cleared (not when the gradient accumulates) by
+// CTAs of kernel 3, which start beside the sort and go on beside the sums:
+// clearing alone is all writes, which run at 0.86 of the copy rate (5.85 TB/s
+// measured), and beside it the sums' reads come almost free.  For that they mark
+// the ids of their range of rows from the tokens themselves; where that would
+// cost more than it spares (short rows, or very many tokens) kernel 2, launched
+// beside the sort, clears every row before kernel 3 begins, and ends after the
+// sort, so that waiting for it is waiting for both.
+// Kernel 3 takes the sorted tokens in tiles: a
 // tile sums the gradient rows of each id in it, in position order, and stores
 // the ids whose tokens all lie in the tile; the first and the last id of a tile
 // may have tokens in its neighbours, and leave one partial row each.  Kernel 4
@@ -221,8 +227,9 @@ cudaError_t launch_lookup(LookupArgs a, const DeviceInfo& dev, cudaStream_t s) {
 // equal contiguous parts of the input; a pass counts each warp's digits in
 // shared memory, adds the counts up over warps and (through distributed shared
 // memory) CTAs into each warp's first place for each digit, and moves the
-// pairs in order, lanes of a digit ranked by a match across the warp.  No
-// atomics, so equal ids keep their order.
+// pairs in order, lanes of a digit ranked by a match across the warp, so equal
+// ids keep their order (only the counting uses atomics, whose order is lost in
+// the count).
 constexpr int kSortCluster = 8;
 constexpr int kSortThreads = 1024;
 constexpr int kSortMaxBits = 9;
@@ -283,24 +290,12 @@ __device__ __forceinline__ void sort_tokens(const LookupGradArgs& a, SortPlan pl
     }
     for (int b = lane; b < bins; b += 32) mine[b] = 0;
     __syncwarp();
-    auto tally = [&](bool on, uint2 kv) {
-      const unsigned act = __ballot_sync(0xffffffffu, on);
-      if (on) {
-        const int d = digit(kv);
-        const unsigned same = __match_any_sync(act, d);
-        if ((same & below) == 0) mine[d] += __popc(same);
-      }
-      __syncwarp();
-    };
     if constexpr (K > 0) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (lo + 32 * k < hi) tally(lo + 32 * k + lane < hi, held[k]);
+        if (lo + 32 * k + lane < hi) atomicAdd(&mine[digit(held[k])], 1);
     } else {
-      for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-        const bool on = i0 + lane < hi;
-        tally(on, on ? fetch(i0 + lane) : make_uint2(0u, 0u));
-      }
+      for (int64_t i = lo + lane; i < hi; i += 32) atomicAdd(&mine[digit(fetch(i))], 1);
     }
     __syncthreads();
     // per bin: exclusive prefix over this CTA's warps, and its total
@@ -371,6 +366,7 @@ __device__ __forceinline__ void sort_tokens(const LookupGradArgs& a, SortPlan pl
 static __global__ void __launch_bounds__(kSortThreads) lookup_grad_sort_kernel(const LookupGradArgs a, const SortPlan plan) {
   extern __shared__ __align__(16) int smem_sort[];
   pdl_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.owners[0] = make_int2(0, 0);
   constexpr int64_t kWarps = kSortCluster * kSortThreads / 32;
   if (a.N <= kWarps * 32)
     sort_tokens<1>(a, plan, smem_sort);
@@ -382,18 +378,15 @@ static __global__ void __launch_bounds__(kSortThreads) lookup_grad_sort_kernel(c
     sort_tokens<0>(a, plan, smem_sort);
 }
 
-// Kernel 2.  CTA c clears its range of the table's rows: from a bitmap of the
-// ids in the range that it draws from the tokens itself, or every row: reading
-// the tokens pays where the rows are long (kClearMarkBytes) and the tokens'
-// bytes at most a quarter of the range's.
-constexpr int kClearThreads = 512;
+constexpr int kClearThreads = 128;
 constexpr int kClearMaxRange = 8192;  // rows a CTA marks at a time
-constexpr int kClearMarkBytes = 2048;
-constexpr int kClearZeros = 8192;  // bytes of zeros in shared memory, the source of its copies
+// Clearing CTAs an SM (measured beside the sums, 16384 tokens into 131072x4096
+// bf16, us: 1: 251, 2: 227, 3: 231, 4: 208, 6: 212, 8: 224, 12: 245).
+constexpr int kClearPerSm = 4;
+constexpr int kClearZeros = 8192;     // bytes of zeros in shared memory, the source of its copies
 
 // Bulk copy from shared to global memory (both 16-byte aligned, bytes a
-// multiple of 16), and the wait for this thread's copies to have left shared
-// memory and been written.
+// multiple of 16), and the wait for this thread's copies to be written.
 __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
                : "memory");
@@ -403,61 +396,87 @@ __device__ __forceinline__ void bulk_s2g_drain() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+struct ClearSmem {
+  unsigned marks[kClearMaxRange / 32];
+  unsigned char zeros[kClearZeros];
+};
+
+// Clear part `part` of `parts` of the table's rows: those no token names
+// (a.mark), or all.
 template <typename O>
-__global__ void __launch_bounds__(kClearThreads) lookup_grad_clear_kernel(const LookupGradArgs a) {
+__device__ __forceinline__ void clear_rows(const LookupGradArgs& a, ClearSmem& sm, int part, int parts) {
   using T = typename O::T;
-  __shared__ unsigned marks[kClearMaxRange / 32];
-  __shared__ __align__(16) unsigned char zeros[kClearZeros];
-  pdl_launch_dependents();
-  for (int i = threadIdx.x; i < kClearZeros / 16; i += kClearThreads)
-    reinterpret_cast<uint4*>(zeros)[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = threadIdx.x; i < kClearZeros / 16; i += (int)blockDim.x)
+    reinterpret_cast<uint4*>(sm.zeros)[i] = make_uint4(0u, 0u, 0u, 0u);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the __syncthreads below orders it for every thread)
   T* out = reinterpret_cast<T*>(a.dtable);
   const size_t row_bytes = (size_t)a.H * sizeof(T);
   const size_t bits = reinterpret_cast<uintptr_t>(out) | (size_t)a.lddt * sizeof(T) | row_bytes;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int64_t lo, hi;
-  cta_rows(a.V, blockIdx.x, gridDim.x, lo, hi);
-  const bool mark = row_bytes >= (size_t)kClearMarkBytes && a.N * (a.tok64 ? 8 : 4) <= (hi - lo) * (int64_t)row_bytes / 4;
-  if (!mark && (bits & 15u) == 0 && a.lddt == a.H) {  // one stretch of memory
-    __syncthreads();
+  cta_rows(a.V, part, parts, lo, hi);
+  __syncthreads();
+  if (!a.mark && (bits & 15u) == 0 && a.lddt == a.H) {  // one stretch of memory
     unsigned char* p = reinterpret_cast<unsigned char*>(out + lo * a.H);
     const int64_t bytes = (hi - lo) * (int64_t)row_bytes;
-    for (int64_t i = (int64_t)threadIdx.x * kClearZeros; i < bytes; i += (int64_t)kClearThreads * kClearZeros)
-      bulk_s2g(p + i, zeros, (uint32_t)min(bytes - i, (int64_t)kClearZeros));
+    for (int64_t i = (int64_t)threadIdx.x * kClearZeros; i < bytes; i += (int64_t)(int)blockDim.x * kClearZeros)
+      bulk_s2g(p + i, sm.zeros, (uint32_t)min(bytes - i, (int64_t)kClearZeros));
     lo = hi;
   }
   for (int64_t v0 = lo; v0 < hi; v0 += kClearMaxRange) {
     const int n = (int)min(hi - v0, (int64_t)kClearMaxRange);
     __syncthreads();
-    for (int i = threadIdx.x; i < (n + 31) / 32; i += kClearThreads) marks[i] = 0u;
+    for (int i = threadIdx.x; i < (n + 31) / 32; i += (int)blockDim.x) sm.marks[i] = 0u;
     __syncthreads();
-    if (mark) {
-#pragma unroll 4
-      for (int64_t i = threadIdx.x; i < a.N; i += kClearThreads) {
-        const int64_t t = load_token(a.tokens, a.tok64, i, a.V, nullptr);
+    if (a.mark) {
+      auto mark = [&](int64_t t) {
         const int64_t at = t - v0;
-        if (t != a.padding && at >= 0 && at < n) atomicOr(&marks[at >> 5], 1u << (at & 31));
+        if (t >= 0 && t < a.V && t != a.padding && at >= 0 && at < n) atomicOr(&sm.marks[at >> 5], 1u << (at & 31));
+      };
+      // 16 bytes of tokens at a time where they are aligned, then the rest
+      const int per = a.tok64 ? 2 : 4;
+      const int64_t groups = (reinterpret_cast<uintptr_t>(a.tokens) & 15u) == 0 ? a.N / per : 0;
+#pragma unroll 8
+      for (int64_t i = threadIdx.x; i < groups; i += (int)blockDim.x) {
+        const uint4 u = ld_cached(reinterpret_cast<const uint4*>(a.tokens) + i);
+        if (a.tok64) {
+          mark((int64_t)(((unsigned long long)u.y << 32) | u.x));
+          mark((int64_t)(((unsigned long long)u.w << 32) | u.z));
+        } else {
+          mark((int)u.x);
+          mark((int)u.y);
+          mark((int)u.z);
+          mark((int)u.w);
+        }
       }
+      for (int64_t i = groups * per + threadIdx.x; i < a.N; i += (int)blockDim.x)
+        mark(load_token(a.tokens, a.tok64, i, a.V, nullptr));
       __syncthreads();
     }
     if ((bits & 15u) == 0) {
       // a thread a row, in bulk copies of the zeros
-      for (int r = threadIdx.x; r < n; r += kClearThreads) {
-        if ((marks[r >> 5] >> (r & 31)) & 1u) continue;
+      for (int r = threadIdx.x; r < n; r += (int)blockDim.x) {
+        if ((sm.marks[r >> 5] >> (r & 31)) & 1u) continue;
         unsigned char* row = reinterpret_cast<unsigned char*>(out + (v0 + r) * a.lddt);
         for (size_t i = 0; i < row_bytes; i += kClearZeros)
-          bulk_s2g(row + i, zeros, (uint32_t)min(row_bytes - i, (size_t)kClearZeros));
+          bulk_s2g(row + i, sm.zeros, (uint32_t)min(row_bytes - i, (size_t)kClearZeros));
       }
     } else {
-      for (int r = warp; r < n; r += kClearThreads / 32) {
-        if ((marks[r >> 5] >> (r & 31)) & 1u) continue;
+      for (int r = threadIdx.x >> 5; r < n; r += (int)blockDim.x / 32) {
+        if ((sm.marks[r >> 5] >> (r & 31)) & 1u) continue;
         T* row = out + (v0 + r) * a.lddt;
-        for (int j = lane; j < a.H; j += 32) row[j] = T(0.f);
+        for (int j = threadIdx.x & 31; j < a.H; j += 32) row[j] = T(0.f);
       }
     }
   }
   bulk_s2g_drain();
+}
+
+// Kernel 2 (where rows are not marked).
+template <typename O>
+__global__ void __launch_bounds__(kClearThreads) lookup_grad_clear_kernel(const LookupGradArgs a) {
+  __shared__ __align__(16) ClearSmem sm;
+  pdl_launch_dependents();
+  clear_rows<O>(a, sm, blockIdx.x, gridDim.x);
   pdl_wait_primary();  // the sort
 }
 
@@ -491,10 +510,10 @@ __device__ __forceinline__ void store_grad(const LookupGradArgs& a, int64_t id, 
   }
 }
 
-// Kernel 3: tiles of sorted tokens (blockIdx.x) by blocks of columns
-// (blockIdx.y), 32 bytes a thread.  The rows' addresses come from the sorted
-// pairs, so kBatch rows' loads are in flight at a time.
-constexpr int kTileThreads = 128;
+// Kernel 3: the first a.clearers CTAs clear rows; the others take tiles of
+// sorted tokens by blocks of columns, 32 bytes a thread.  The rows' addresses
+// come from the sorted pairs, so kTileBatch rows' loads are in flight at a time.
+constexpr int kTileThreads = kClearThreads;
 constexpr int kTileBatch = 8;
 
 template <typename D, typename O, int GB>
@@ -502,33 +521,40 @@ __global__ void __launch_bounds__(kTileThreads) lookup_grad_tile_kernel(const Lo
   using C = Chunk<D, GB, 32 / (int)sizeof(typename D::T)>;
   using T = typename D::T;
   constexpr int E = C::E, NP = C::NP, NW = C::NW;
-  pdl_launch_dependents();
-  pdl_wait_primary();
+  __shared__ __align__(16) ClearSmem sm;
   __shared__ uint2 kv[kLookupMaxTile + 2];  // with the neighbours' nearest ids
-  const int64_t first = (int64_t)blockIdx.x * a.tile;
+  pdl_launch_dependents();
+  if ((int)blockIdx.x < a.clearers) {
+    clear_rows<O>(a, sm, blockIdx.x, a.clearers);
+    pdl_wait_primary();
+    return;
+  }
+  pdl_wait_primary();
+  const unsigned tile = (blockIdx.x - a.clearers) / a.col_blocks, col_block = (blockIdx.x - a.clearers) % a.col_blocks;
+  const int64_t first = (int64_t)tile * a.tile;
   const int n = (int)min((int64_t)a.tile, a.N - first);
   const unsigned none = 0xffffffffu;  // no id (ids are at most V < 2^31)
-  for (int i = threadIdx.x; i < n + 2; i += kTileThreads) {
+  for (int i = threadIdx.x; i < n + 2; i += (int)blockDim.x) {
     const int64_t at = first + i - 1;
     kv[i] = at >= 0 && at < a.N ? __ldcg(a.sorted + at) : make_uint2(none, 0u);
   }
   __syncthreads();
   const unsigned ignored = (unsigned)a.V;
   const bool open_front = kv[0].x == kv[1].x;
-  for (int c0 = blockIdx.y * (kTileThreads * E); c0 < a.H; c0 += gridDim.y * (kTileThreads * E)) {
+  for (int c0 = col_block * ((int)blockDim.x * E); c0 < a.H; c0 += a.col_blocks * ((int)blockDim.x * E)) {
     const int c = c0 + C::base(threadIdx.x), lim = a.H - c;
     const T* src = reinterpret_cast<const T*>(a.dh) + c;
     float2 acc[NP];
 #pragma unroll
     for (int p = 0; p < NP; ++p) acc[p] = splat2(0.f);
-    for (int i0 = 0; i0 < n; i0 += kTileBatch) {
-      uint32_t w[kTileBatch][NW];
+    uint32_t w[kTileBatch][NW];
+    auto fetch = [&](int i, uint32_t (&into)[NW]) {
+      const uint2 e = kv[min(i, n - 1) + 1];
+      C::load(src + (int64_t)e.y * a.lddh, i < n && e.x != ignored ? lim : 0, into);
+    };
 #pragma unroll
-      for (int k = 0; k < kTileBatch; ++k) {
-        const uint2 e = kv[min(i0 + k, n - 1) + 1];
-        const bool on = i0 + k < n && e.x != ignored;
-        C::load(src + (int64_t)e.y * a.lddh, on ? lim : 0, w[k]);
-      }
+    for (int k = 0; k < kTileBatch; ++k) fetch(k, w[k]);
+    for (int i0 = 0; i0 < n; i0 += kTileBatch) {
 #pragma unroll
       for (int k = 0; k < kTileBatch; ++k) {
         const int i = i0 + k;
@@ -537,6 +563,7 @@ __global__ void __launch_bounds__(kTileThreads) lookup_grad_tile_kernel(const Lo
         if (id == ignored) break;  // ignored tokens sort last
 #pragma unroll
         for (int p = 0; p < NP; ++p) acc[p] = add2(acc[p], word_pair<D>(w[k], p));
+        if (i + kTileBatch < n) fetch(i + kTileBatch, w[k]);
         if (i + 1 < n && kv[i + 2].x == id) continue;  // its last token in the tile
         float v[E];
 #pragma unroll
@@ -546,8 +573,9 @@ __global__ void __launch_bounds__(kTileThreads) lookup_grad_tile_kernel(const Lo
           acc[p] = splat2(0.f);
         }
         const bool front = open_front && id == kv[1].x, back = i + 1 == n && kv[n + 1].x == id;
+        if (back && !front && c0 == 0 && threadIdx.x == 0) a.owners[atomicAdd(&a.owners[0].x, 1) + 1] = make_int2((int)tile, (int)id);
         if (front || back) {
-          float* part = a.partial + ((size_t)2 * blockIdx.x + (front ? 0 : 1)) * a.Hp + c;
+          float* part = a.partial + ((size_t)2 * tile + (front ? 0 : 1)) * a.Hp + c;
 #pragma unroll
           for (int e = 0; e < E; ++e)
             if (C::col(e) < lim) part[C::col(e)] = v[e];
@@ -559,70 +587,73 @@ __global__ void __launch_bounds__(kTileThreads) lookup_grad_tile_kernel(const Lo
   }
 }
 
-// Kernel 4: the ids whose tokens cross tiles.  The CTA of the first tile
-// boundary (blockIdx.x) that an id crosses sums its partial rows over 1024
-// columns (blockIdx.y): two row groups of 256 lanes, four columns a lane, each
-// group every other row, sixteen loads in flight; then the groups in order.
-constexpr int kJoinThreads = 512;
+// Kernel 4: the ids whose tokens cross tiles.  Each is listed once, by the tile
+// it begins in (in whatever order: they do not meet).  A CTA takes one after
+// another and sums its partial rows over 256 columns (blockIdx.y): four row
+// groups of 64 lanes, four columns a lane, each group every fourth row, eight
+// loads in flight; then the groups in order.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinLanes = 64;
 
 template <typename O>
 __global__ void __launch_bounds__(kJoinThreads) lookup_grad_join_kernel(const LookupGradArgs a) {
-  constexpr int G = kJoinThreads / 256, U = 16;
+  constexpr int G = kJoinThreads / kJoinLanes, U = 8;
   pdl_wait_primary();
-  __shared__ float4 sums[G - 1][256];
+  __shared__ float4 sums[G - 1][kJoinLanes];
   const int64_t tile = a.tile, tiles = (a.N + tile - 1) / tile;
-  const int64_t b = blockIdx.x;  // between tiles b and b + 1
-  const unsigned id = __ldcg(a.sorted + (b + 1) * tile).x, left = __ldcg(a.sorted + (b + 1) * tile - 1).x;
-  const unsigned head = __ldcg(a.sorted + b * tile).x, tail = b > 0 ? __ldcg(a.sorted + b * tile - 1).x : 0xffffffffu;
-  if (id == (unsigned)a.V || left != id) return;  // nothing crosses here
-  if (head == id && tail == id) return;           // an earlier boundary has it
-  const int g = threadIdx.x >> 8, lane = threadIdx.x & 255;
-  // the id's tiles: b, and those after it that begin with it
-  int64_t more = 0;
-  for (int64_t t = b + 1;; t += kJoinThreads) {
-    const int64_t at = t + threadIdx.x;
-    const int c = __syncthreads_count(at < tiles && __ldcg(a.sorted + at * tile).x == id);
-    more += c;
-    if (c < kJoinThreads) break;
-  }
-  for (int c0 = blockIdx.y * 1024; c0 < a.Hp; c0 += gridDim.y * 1024) {
-    const int c = c0 + lane * 4;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c < a.Hp) {
-      for (int64_t r0 = g; r0 <= more; r0 += G * U) {
-        float4 v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int64_t r = r0 + u * G;
-          const int64_t slot = r == 0 ? 2 * b + 1 : 2 * (b + r);
-          v[u] = r <= more ? __ldcg(reinterpret_cast<const float4*>(a.partial + slot * a.Hp + c))
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          acc.x += v[u].x;
-          acc.y += v[u].y;
-          acc.z += v[u].z;
-          acc.w += v[u].w;
-        }
-      }
+  const int g = threadIdx.x / kJoinLanes, lane = threadIdx.x % kJoinLanes;
+  const int listed = __ldcg(&a.owners[0].x);
+  for (int o = blockIdx.x; o < listed; o += gridDim.x) {
+    const int2 owner = __ldcg(a.owners + 1 + o);
+    const int64_t b = owner.x;
+    const unsigned id = (unsigned)owner.y;
+    // the id's tiles: b, and those after it that begin with it
+    int64_t more = 0;
+    for (int64_t t = b + 1;; t += kJoinThreads) {
+      const int64_t at = t + threadIdx.x;
+      const int c = __syncthreads_count(at < tiles && __ldcg(a.sorted + at * tile).x == id);
+      more += c;
+      if (c < kJoinThreads) break;
     }
-    __syncthreads();
-    if (g > 0) sums[g - 1][lane] = acc;
-    __syncthreads();
-    if (g == 0 && c < a.H) {
+    for (int c0 = blockIdx.y * (4 * kJoinLanes); c0 < a.Hp; c0 += gridDim.y * (4 * kJoinLanes)) {
+      const int c = c0 + lane * 4;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c < a.Hp) {
+        for (int64_t r0 = g; r0 <= more; r0 += G * U) {
+          float4 v[U];
 #pragma unroll
-      for (int q = 0; q < G - 1; ++q) {
-        const float4 o = sums[q][lane];
-        acc.x += o.x;
-        acc.y += o.y;
-        acc.z += o.z;
-        acc.w += o.w;
+          for (int u = 0; u < U; ++u) {
+            const int64_t r = r0 + u * G;
+            const int64_t at = r == 0 ? 2 * b + 1 : 2 * (b + r);
+            v[u] = r <= more ? __ldcg(reinterpret_cast<const float4*>(a.partial + at * a.Hp + c))
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            acc.x += v[u].x;
+            acc.y += v[u].y;
+            acc.z += v[u].z;
+            acc.w += v[u].w;
+          }
+        }
       }
-      const float v[4] = {acc.x, acc.y, acc.z, acc.w};
-      const int64_t at = (int64_t)id * a.lddt + c;
-      for (int i = 0; i < 4 && c + i < a.H; ++i)
-        store_elem<O>(a.dtable, at + i, fmaf(a.scale, v[i], a.accumulate ? load_elem<O>(a.dtable, at + i) : 0.f));
+      __syncthreads();
+      if (g > 0) sums[g - 1][lane] = acc;
+      __syncthreads();
+      if (g == 0 && c < a.H) {
+#pragma unroll
+        for (int q = 0; q < G - 1; ++q) {
+          const float4 part = sums[q][lane];
+          acc.x += part.x;
+          acc.y += part.y;
+          acc.z += part.z;
+          acc.w += part.w;
+        }
+        const float v[4] = {acc.x, acc.y, acc.z, acc.w};
+        const int64_t at = (int64_t)id * a.lddt + c;
+        for (int i = 0; i < 4 && c + i < a.H; ++i)
+          store_elem<O>(a.dtable, at + i, fmaf(a.scale, v[i], a.accumulate ? load_elem<O>(a.dtable, at + i) : 0.f));
+      }
     }
   }
 }
@@ -645,7 +676,7 @@ static cudaError_t launch_pdl(K kern, dim3 grid, dim3 block, size_t smem, cudaSt
 }
 
 template <typename D, typename O>
-static cudaError_t run_lookup_grad(const LookupGradArgs& a, const DeviceInfo& dev, cudaStream_t s) {
+static cudaError_t run_lookup_grad(LookupGradArgs& a, const DeviceInfo& dev, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (a.N > 0) {
     const SortPlan plan = sort_plan(a.V);
@@ -671,31 +702,44 @@ static cudaError_t run_lookup_grad(const LookupGradArgs& a, const DeviceInfo& de
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
+  using T = typename D::T;
+  using OT = typename O::T;
+  a.clearers = a.mark = 0;
   if (!a.accumulate) {
-    // three CTAs an SM: all of them fit at once beside the sort's, whose SMs
-    // have room for one each, so none starts late
-    const unsigned blocks = (unsigned)std::min<int64_t>(a.V, (int64_t)dev.sm_count * 3);
+    // A clearing CTA reads all tokens from L2, at about twice the rate of the
+    // rows it spares; below 2 KB a row the marks cost more than the rows.
+    const int64_t row_bytes = (int64_t)a.H * (int64_t)sizeof(OT);
+    const int64_t reads = (a.V / (dev.sm_count * kClearPerSm) + kClearMaxRange) / kClearMaxRange;
+    const int64_t token_bytes = a.N * (a.tok64 ? 8 : 4) * reads;
+    a.mark = a.N > 0 && row_bytes >= 2048 && kClearPerSm * dev.sm_count * token_bytes <= a.V * row_bytes / 2;
+    const unsigned blocks = (unsigned)std::min<int64_t>(a.V, dev.sm_count * kClearPerSm);
     if (a.N == 0) {
       lookup_grad_clear_kernel<O><<<blocks, kClearThreads, 0, s>>>(a);
       return cudaGetLastError();
     }
-    e = launch_pdl(lookup_grad_clear_kernel<O>, dim3(blocks), dim3(kClearThreads), 0, s, a);
-    if (e != cudaSuccess) return e;
+    if (a.mark) {
+      a.clearers = (int)blocks;
+    } else {
+      e = launch_pdl(lookup_grad_clear_kernel<O>, dim3(blocks), dim3(kClearThreads), 0, s, a);
+      if (e != cudaSuccess) return e;
+    }
   }
-  using T = typename D::T;
-  using OT = typename O::T;
   const unsigned tiles = (unsigned)((a.N + a.tile - 1) / a.tile);
-  const int per = kTileThreads * 32 / (int)sizeof(T);
-  const dim3 grid(tiles, (unsigned)std::min((a.H + per - 1) / per, 1024));
+  // as many threads as a row of 16 (fp32: 8) columns a thread has (all of them
+  // where they clear too)
+  const int threads = a.mark ? kTileThreads : std::min(kTileThreads, chunk_threads(a.H, 32 / (int)sizeof(T)));
+  const int per = threads * 32 / (int)sizeof(T);
+  a.col_blocks = std::min((a.H + per - 1) / per, 64);
+  const dim3 grid(a.clearers + tiles * a.col_blocks);
   GranuleRule in, out;
   in.add(a.dh, a.lddh, sizeof(T));
   out.add(a.dtable, a.lddt, sizeof(OT));
   const int vec = out.bytes(a.H, sizeof(OT)) >= 16;
   e = in.bytes(a.H, sizeof(T)) >= 16
-          ? launch_pdl(lookup_grad_tile_kernel<D, O, 16>, grid, dim3(kTileThreads), 0, s, a, vec)
-          : launch_pdl(lookup_grad_tile_kernel<D, O, (int)sizeof(T)>, grid, dim3(kTileThreads), 0, s, a, vec);
+          ? launch_pdl(lookup_grad_tile_kernel<D, O, 16>, grid, dim3(threads), 0, s, a, vec)
+          : launch_pdl(lookup_grad_tile_kernel<D, O, (int)sizeof(T)>, grid, dim3(threads), 0, s, a, vec);
   if (e != cudaSuccess || tiles == 1) return e;
-  const dim3 joins(tiles - 1, (unsigned)std::min((a.H + 1023) / 1024, 1024));
+  const dim3 joins(std::min<unsigned>(tiles - 1, 2 * dev.sm_count), (unsigned)std::min((a.H + 255) / 256, 64));
   return launch_pdl(lookup_grad_join_kernel<O>, joins, dim3(kJoinThreads), 0, s, a);
 }
 

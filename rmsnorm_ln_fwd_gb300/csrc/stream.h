@@ -119,7 +119,12 @@ struct LookupGradArgs {
   uint2* sorted;  // (id, position), N of them; V as the id of an ignored token
   uint2* other;   // the sort's second buffer
   float* partial;  // [2 * tiles][Hp]
-  int tile;        // sorted tokens a tile (filled in by the launcher)
+  int2* owners;    // [1 + tiles]: how many ids cross tiles; (the tile it begins in, id) of each
+  // filled in by the launcher:
+  int tile;        // sorted tokens a tile
+  int mark;        // only the rows that no token names are cleared
+  int clearers;    // CTAs that clear rows beside the tiles
+  int col_blocks;  // CTAs a tile
   unsigned* err;
 };
 

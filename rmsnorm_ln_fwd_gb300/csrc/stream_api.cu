@@ -54,9 +54,9 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 int64_t lookup_tiles(int64_t N) { return (N + normk::lookup_tile(N) - 1) / normk::lookup_tile(N); }
 
-// Two buffers of sorted pairs, then the tiles' partial rows.
+// Two buffers of sorted pairs, the list of crossing ids, the tiles' partial rows.
 size_t lookup_workspace(int64_t N, int64_t H) {
-  return 2 * align256((size_t)N * sizeof(uint2)) +
+  return 2 * align256((size_t)N * sizeof(uint2)) + align256((size_t)(1 + lookup_tiles(N)) * sizeof(int2)) +
          (size_t)2 * lookup_tiles(N) * normk::bwd_partial_stride((int)H) * sizeof(float);
 }
 
@@ -344,7 +344,8 @@ norm_status embedding_grad(const void* dh, int64_t lddh, const void* tokens, nor
     const size_t pairs = align256((size_t)N * sizeof(uint2));
     a.sorted = reinterpret_cast<uint2*>(w);
     a.other = reinterpret_cast<uint2*>(w + pairs);
-    a.partial = reinterpret_cast<float*>(w + 2 * pairs);
+    a.owners = reinterpret_cast<int2*>(w + 2 * pairs);
+    a.partial = reinterpret_cast<float*>(w + 2 * pairs + align256((size_t)(1 + lookup_tiles(N)) * sizeof(int2)));
   }
   DeviceInfo dev;
   if (!current_device_info(&dev)) return NORM_ERR_CUDA;
