@@ -7,7 +7,10 @@
 // the same kernels, only with narrower accesses.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
+#include "launch.h"
 
 namespace normk {
 
@@ -187,6 +190,39 @@ struct GranuleRule {
     const unsigned long long b = bits | (unsigned long long)H * es;
     return (b & 31u) == 0 ? 32 : (b & 15u) == 0 ? 16 : (int)es;
   }
+};
+
+// What a launcher asks the runtime about its kernel, asked once per device and
+// shape: at the sizes where a call is all latency, the questions cost more than
+// the launch.  One object per kernel (static in its launcher); plain atomics, so
+// that calls of several threads at worst ask twice.
+class KernelMemo {
+ public:
+  // Let the kernel have any dynamic shared memory up to `limit` (the same at
+  // every call).
+  template <typename K>
+  cudaError_t allow_smem(K kern, int limit, const DeviceInfo& dev) {
+    if (allowed_[dev.id].load(std::memory_order_acquire)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, limit);
+    if (e == cudaSuccess) allowed_[dev.id].store(true, std::memory_order_release);
+    return e;
+  }
+  // The CTAs (or, asked through `ask`, clusters) resident at once.
+  template <typename F>
+  int resident(int threads, size_t smem, const DeviceInfo& dev, F&& ask) {
+    const unsigned long long key = ((unsigned long long)smem << 32) | ((unsigned long long)threads << 16);
+    const unsigned long long seen = resident_[dev.id].load(std::memory_order_relaxed);
+    if (seen != 0 && (seen & ~0xffffull) == key) return (int)(seen & 0xffffull);
+    int n = 0;
+    if (ask(&n) != cudaSuccess || n < 1) return 1;
+    n = n < 0xffff ? n : 0xffff;
+    resident_[dev.id].store(key | (unsigned long long)n, std::memory_order_relaxed);
+    return n;
+  }
+
+ private:
+  std::atomic<bool> allowed_[kMaxDevices] = {};
+  std::atomic<unsigned long long> resident_[kMaxDevices] = {};
 };
 
 // Threads a row of H columns at E columns a thread: whole warps.

@@ -748,7 +748,8 @@ __global__ void join_grad_zero_kernel(const JoinGradArgs a) {
 template <typename D, int GB, bool RUNS, int MAXT, int MINB, int CL>
 static cudaError_t run_join_grad_rows(JoinGradArgs& a, const JoinRing& ring, const DeviceInfo& dev, cudaStream_t s) {
   auto kern = join_grad_rows_kernel<D, GB, RUNS, MAXT, MINB, CL>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ring.total);
+  static KernelMemo memo;
+  cudaError_t e = memo.allow_smem(kern, dev.max_smem_optin - kJoinStaticSmem, dev);
   if (e != cudaSuccess) return e;
   const int threads = ring.rpc * ring.tpr;
   const int64_t cap = std::min<int64_t>(kJoinMaxPartialsPerSm * dev.sm_count, (a.N + ring.rpc - 1) / ring.rpc);
@@ -758,7 +759,6 @@ static cudaError_t run_join_grad_rows(JoinGradArgs& a, const JoinRing& ring, con
   cfg.dynamicSmemBytes = ring.total;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
-  int resident = 0;
   if (CL > 1) {
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = CL;
@@ -766,11 +766,13 @@ static cudaError_t run_join_grad_rows(JoinGradArgs& a, const JoinRing& ring, con
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&resident, kern, &cfg) != cudaSuccess) resident = 1;
-  } else {
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kern, threads, ring.total) != cudaSuccess) resident = 1;
-    resident *= dev.sm_count;
   }
+  const int resident = memo.resident(threads, ring.total, dev, [&](int* n) {
+    if (CL > 1) return cudaOccupancyMaxActiveClusters(n, kern, &cfg);
+    const cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kern, threads, ring.total);
+    *n *= dev.sm_count;
+    return err;
+  });
   a.P = (int)std::max<int64_t>(1, std::min<int64_t>(cap, resident));
   a.U = (int)std::min<int64_t>(a.N, (int64_t)a.P * ring.rpc);
   cfg.gridDim = dim3((unsigned)(CL * a.P));

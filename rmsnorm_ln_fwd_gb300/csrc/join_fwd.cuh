@@ -261,8 +261,9 @@ static cudaError_t run_join_rows(const JoinArgs& a, int tpr, int rpc, const Devi
   auto kern = join_rows_kernel<D, GB, MAXT, MINB, CL>;
   const int threads = rpc * tpr;
   const size_t smem = sizeof(float) * ((size_t)rpc * 2 * (tpr / 32) * 4 + (size_t)threads * param_slot<Chunk<D, GB, kJoinCols<D>>::E, 2>());
+  static KernelMemo memo;
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = memo.allow_smem(kern, dev.max_smem_optin - 1024, dev);
     if (e != cudaSuccess) return e;
   }
   const int64_t want = std::min<int64_t>((a.N + rpc - 1) / rpc, 1 << 20);
@@ -272,7 +273,6 @@ static cudaError_t run_join_rows(const JoinArgs& a, int tpr, int rpc, const Devi
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
-  int resident = 0;
   if (CL > 1) {
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = CL;
@@ -280,11 +280,13 @@ static cudaError_t run_join_rows(const JoinArgs& a, int tpr, int rpc, const Devi
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&resident, kern, &cfg) != cudaSuccess) resident = 1;
-  } else {
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kern, threads, smem) != cudaSuccess) resident = 1;
-    resident *= dev.sm_count;
   }
+  const int resident = memo.resident(threads, smem, dev, [&](int* n) {
+    if (CL > 1) return cudaOccupancyMaxActiveClusters(n, kern, &cfg);
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kern, threads, smem);
+    *n *= dev.sm_count;
+    return e;
+  });
   cfg.gridDim = dim3((unsigned)(CL * std::max<int64_t>(1, std::min<int64_t>(want, resident))));
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, tpr);
   if (e != cudaSuccess) return e;

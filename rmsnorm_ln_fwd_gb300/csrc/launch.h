@@ -23,11 +23,14 @@ __host__ __device__ constexpr bool kind_is_ln(int k) { return k == KIND_LN || k 
 enum Path : int { PATH_AUTO = 0, PATH_ROWS = 1, PATH_LOOP = 2, PATH_STAGED = 3 };
 constexpr int kRowsAutoMaxThreads = 640;
 
+constexpr int kMaxDevices = 64;  // devices the library keeps attributes of
+
 struct DeviceInfo {
   int sm_count;
   int max_smem_optin;  // bytes of shared memory one CTA may opt into
   unsigned* err;       // this device's error-flag word (see norm_device_errors)
   int path;            // first kernel family to try (norm_set_kernel_path)
+  int id;              // CUDA device number
   void* split_event;   // cudaEvent_t recorded between the backward's two kernels, or null
                        // (norm_set_bwd_split_event; the reduction then runs without PDL)
 };

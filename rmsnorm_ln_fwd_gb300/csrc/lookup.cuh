@@ -153,12 +153,14 @@ static cudaError_t run_lookup_rows(const LookupArgs& a, const DeviceInfo& dev, c
   const int tpr = chunk_threads(a.H, E);
   const int rpc = tpr <= 256 ? 256 / tpr : 1, threads = rpc * tpr;
   const size_t smem = sizeof(float) * ((size_t)lookup_red_floats(rpc, tpr) + (size_t)tpr * param_slot<E, 1>());
+  static KernelMemo memo;
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = memo.allow_smem(kern, dev.max_smem_optin - 1024, dev);
     if (e != cudaSuccess) return e;
   }
-  int per_sm = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem) != cudaSuccess || per_sm < 1) per_sm = 1;
+  const int per_sm = memo.resident(threads, smem, dev, [&](int* n) {
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kern, threads, smem);
+  });
   const int64_t blocks = std::min<int64_t>((a.N + rpc - 1) / rpc, (int64_t)per_sm * dev.sm_count);
   kern<<<(unsigned)blocks, threads, smem, s>>>(a, tpr);
   return cudaGetLastError();
@@ -681,8 +683,9 @@ static cudaError_t run_lookup_grad(LookupGradArgs& a, const DeviceInfo& dev, cud
   if (a.N > 0) {
     const SortPlan plan = sort_plan(a.V);
     const size_t smem = sizeof(int) * ((size_t)(kSortThreads / 32 + 2) * (1 << plan.bits) + kSortThreads / 32);
+    static KernelMemo memo;
     if (smem > 48 * 1024) {
-      e = cudaFuncSetAttribute(lookup_grad_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      e = memo.allow_smem(lookup_grad_sort_kernel, dev.max_smem_optin - 1024, dev);
       if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};

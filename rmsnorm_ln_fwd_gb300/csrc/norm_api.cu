@@ -25,7 +25,7 @@ using normk::launch_result;
 
 namespace {
 
-constexpr int kMaxDevices = 64;
+using normk::kMaxDevices;
 
 std::mutex g_mu;
 DeviceInfo g_info[kMaxDevices];
@@ -82,6 +82,7 @@ bool device_info(int dev, DeviceInfo* out) {
         cudaSuccess)
       return false;
     if (d.sm_count < 1) return false;
+    d.id = dev;
     g_info[dev] = d;
     g_have[dev] = true;
   }

@@ -323,6 +323,26 @@ def rms_backward_from_output(dy, y, rstd, gamma=None, *, need_param_grads: bool 
     return out, dgamma
 
 
+def _call(name, device, *args):
+    """Call the C entry point `name` on `device` and its current stream.  Sets
+    the device only where it is not the current one already: for a single row
+    the call is all host time."""
+    fn = getattr(_lib.load(), name)
+    i = device.index
+    if torch.cuda.current_device() == i:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(i):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    if st != _lib.NORM_OK:
+        _lib.check(name, st)
+
+
+def _new_rows(x, H):
+    """A fresh contiguous tensor like x, and its row stride."""
+    return torch.empty_like(x, memory_format=torch.contiguous_format), max(H, 1)
+
+
 def _gate_view(gate, N, H, device, x_dtype):
     """The gate as (2-D view, rows, row stride, dtype code): shape (H,), or
     leading dims that flatten to B rows with B dividing N."""
@@ -361,21 +381,22 @@ def sandwich_rms(x, residual, gamma_post=None, gate=None, gamma_pre=None, eps: f
     gamma_pre = _vec(gamma_pre, H, "gamma_pre", x.device)
     wc = _w_code(xc, gamma_post, gamma_pre)
     gv, B, ldg, gc = _gate_view(gate, N, H, x.device, x.dtype)
-    h = torch.empty_like(x, memory_format=torch.contiguous_format) if h_out is None else h_out
-    hv, ldh = _grad_out(h, x, N, H, "h_out")
-    y, yv, ldy = None, None, 0
+    if h_out is None:
+        h, ldh = _new_rows(x, H)
+    else:
+        h, ldh = h_out, _grad_out(h_out, x, N, H, "h_out")[1]
+    y, ldy = None, 0
     if pre_norm:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format) if out is None else out
-        yv, ldy = _grad_out(y, x, N, H, "out")
+        if out is None:
+            y, ldy = _new_rows(x, H)
+        else:
+            y, ldy = out, _grad_out(out, x, N, H, "out")[1]
     rpost = torch.empty(N, device=x.device, dtype=torch.float32) if save_stats and post_norm else None
     rpre = torch.empty(N, device=x.device, dtype=torch.float32) if save_stats and pre_norm else None
     norms = (_lib.NORM_SANDWICH_POST if post_norm else 0) | (_lib.NORM_SANDWICH_PRE if pre_norm else 0)
-    lib = _lib.load()
-    with torch.cuda.device(x.device):
-        st = lib.sandwich_rms(xv.data_ptr(), ldx, rv.data_ptr(), ldr, _ptr(gamma_post), _ptr(gv), ldg, B,
-                              _ptr(gamma_pre), _ptr(yv), ldy, hv.data_ptr(), ldh, _ptr(rpost), _ptr(rpre), N, H,
-                              float(eps), float(residual_scale), norms, xc, wc, gc, _stream(x.device))
-    _lib.check("sandwich_rms", st)
+    _call("sandwich_rms", x.device, xv.data_ptr(), ldx, rv.data_ptr(), ldr, _ptr(gamma_post), _ptr(gv), ldg, B,
+          _ptr(gamma_pre), _ptr(y), ldy, h.data_ptr(), ldh, _ptr(rpost), _ptr(rpre), N, H, float(eps),
+          float(residual_scale), norms, xc, wc, gc)
     return y, h, rpost, rpre
 
 
@@ -425,10 +446,14 @@ def sandwich_rms_grad(dy, x, h, rstd_post, rstd_pre, gamma_post=None, gate=None,
         raise TypeError(f"param_dtype {wdt} not supported (float32, bfloat16 or float16)")
     wc = _w_code(_DT[wdt], gamma_post, gamma_pre)
     gv, B, ldg, gc = _gate_view(gate, N, H, x.device, x.dtype)
-    odx = torch.empty_like(x, memory_format=torch.contiguous_format) if dx is None else dx
-    oxv, lddx = _grad_out(odx, x, N, H, "dx")
-    odr = torch.empty_like(x, memory_format=torch.contiguous_format) if dres is None else dres
-    orv, lddr = _grad_out(odr, x, N, H, "dres")
+    if dx is None:
+        odx, lddx = _new_rows(x, H)
+    else:
+        odx, lddx = dx, _grad_out(dx, x, N, H, "dx")[1]
+    if dres is None:
+        odr, lddr = _new_rows(x, H)
+    else:
+        odr, lddr = dres, _grad_out(dres, x, N, H, "dres")[1]
     dgpost = dgate = dgpre = None
     ws, wsb = None, 0
     lib = _lib.load()
@@ -441,13 +466,10 @@ def sandwich_rms_grad(dy, x, h, rstd_post, rstd_pre, gamma_post=None, gate=None,
             dgate = torch.empty(gate.shape, device=x.device, dtype=gate.dtype)
         ws, wsb = _own_workspace(workspace, int(lib.sandwich_rms_workspace_bytes(H, B, x.device.index)), x.device)
     norms = (_lib.NORM_SANDWICH_POST if post else 0) | (_lib.NORM_SANDWICH_PRE if pre else 0)
-    with torch.cuda.device(x.device):
-        st = lib.sandwich_rms_grad(_ptr(dyv), lddy, xv.data_ptr(), ldx, _ptr(hv), ldh, _ptr(rpost), _ptr(rpre),
-                                   _ptr(gamma_post), _ptr(gv), ldg, B, _ptr(gamma_pre), _ptr(div), lddi,
-                                   oxv.data_ptr(), lddx, orv.data_ptr(), lddr, _ptr(dgpost), _ptr(dgate), H,
-                                   _ptr(dgpre), _ptr(ws), wsb, N, H, float(residual_scale), norms, xc, wc, gc,
-                                   _stream(x.device))
-    _lib.check("sandwich_rms_grad", st)
+    _call("sandwich_rms_grad", x.device, _ptr(dyv), lddy, xv.data_ptr(), ldx, _ptr(hv), ldh, _ptr(rpost), _ptr(rpre),
+          _ptr(gamma_post), _ptr(gv), ldg, B, _ptr(gamma_pre), _ptr(div), lddi, odx.data_ptr(), lddx, odr.data_ptr(),
+          lddr, _ptr(dgpost), _ptr(dgate), H, _ptr(dgpre), _ptr(ws), wsb, N, H, float(residual_scale), norms, xc, wc,
+          gc)
     return odx, odr, dgpost, dgate, dgpre
 
 
@@ -478,11 +500,11 @@ def _table(table):
 
 def _row_out(out, tokens, table, N, H, what):
     if out is None:
-        out = torch.empty((*tokens.shape, H), device=table.device, dtype=table.dtype)
-    ov, No, Ho, ld = _rows(out, what)
+        return torch.empty((*tokens.shape, H), device=table.device, dtype=table.dtype), max(H, 1)
+    _, No, Ho, ld = _rows(out, what)
     if (No, Ho) != (N, H) or out.dtype != table.dtype or out.device != table.device:
         raise ValueError(f"{what} must have {N} rows of {H} {table.dtype} columns on {table.device}")
-    return out, ov, ld
+    return out, ld
 
 
 def embedding_lookup(tokens, table, scale: float = 1.0, *, out=None):
@@ -492,12 +514,9 @@ def embedding_lookup(tokens, table, scale: float = 1.0, *, out=None):
     and sets NORM_DEVICE_ERR_BAD_TOKEN in the device error word."""
     tv, V, H, ldt, xc = _table(table)
     N, ic = _tokens(tokens, table.device)
-    h, hv, ldh = _row_out(out, tokens, table, N, H, "out")
-    lib = _lib.load()
-    with torch.cuda.device(table.device):
-        st = lib.embedding_lookup(tv.data_ptr(), ldt, V, tokens.data_ptr(), ic, hv.data_ptr(), ldh, N, H,
-                                  float(scale), xc, _stream(table.device))
-    _lib.check("embedding_lookup", st)
+    h, ldh = _row_out(out, tokens, table, N, H, "out")
+    _call("embedding_lookup", table.device, tv.data_ptr(), ldt, V, tokens.data_ptr(), ic, h.data_ptr(), ldh, N, H,
+          float(scale), xc)
     return h
 
 
@@ -510,15 +529,11 @@ def embedding_rms(tokens, table, gamma=None, eps: float = 1e-6, scale: float = 1
     N, ic = _tokens(tokens, table.device)
     gamma = _vec(gamma, H, "gamma", table.device)
     wc = _w_code(xc, gamma)
-    h, hv, ldh = _row_out(h_out, tokens, table, N, H, "h_out")
-    y, yv, ldy = _row_out(out, tokens, table, N, H, "out")
+    h, ldh = _row_out(h_out, tokens, table, N, H, "h_out")
+    y, ldy = _row_out(out, tokens, table, N, H, "out")
     rstd = torch.empty(N, device=table.device, dtype=torch.float32) if save_stats else None
-    lib = _lib.load()
-    with torch.cuda.device(table.device):
-        st = lib.embedding_rms(tv.data_ptr(), ldt, V, tokens.data_ptr(), ic, _ptr(gamma), yv.data_ptr(), ldy,
-                               hv.data_ptr(), ldh, _ptr(rstd), N, H, float(eps), float(scale), xc, wc,
-                               _stream(table.device))
-    _lib.check("embedding_rms", st)
+    _call("embedding_rms", table.device, tv.data_ptr(), ldt, V, tokens.data_ptr(), ic, _ptr(gamma), y.data_ptr(), ldy,
+          h.data_ptr(), ldh, _ptr(rstd), N, H, float(eps), float(scale), xc, wc)
     return y, h, rstd
 
 
@@ -546,9 +561,6 @@ def embedding_grad(dh, tokens, num_rows: int, scale: float = 1.0, *, padding_idx
         raise ValueError(f"out must be ({num_rows}, {H}) on {dh.device}")
     lib = _lib.load()
     ws, wsb = _own_workspace(workspace, int(lib.embedding_grad_workspace_bytes(N, H)), dh.device)
-    with torch.cuda.device(dh.device):
-        st = lib.embedding_grad(dv.data_ptr(), lddh, tokens.data_ptr(), ic, tv.data_ptr(), ldt, V, _ptr(ws), wsb, N,
-                                H, float(scale), -1 if padding_idx is None else int(padding_idx), int(accumulate), xc,
-                                wc, _stream(dh.device))
-    _lib.check("embedding_grad", st)
+    _call("embedding_grad", dh.device, dv.data_ptr(), lddh, tokens.data_ptr(), ic, tv.data_ptr(), ldt, V, _ptr(ws), wsb,
+          N, H, float(scale), -1 if padding_idx is None else int(padding_idx), int(accumulate), xc, wc)
     return out
