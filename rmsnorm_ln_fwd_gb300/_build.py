@@ -1,9 +1,12 @@
-"""Build libnorm.so (the C-ABI CUDA library) in-tree with nvcc for sm_103a.
+"""Build libnorm.so (the C-ABI CUDA library) in-tree with nvcc for sm_103a, and
+_bind.so (the Python binding of the residual-stream operators) with g++ against
+the installed PyTorch.
 
 Each .cu translation unit is compiled in parallel, then linked into a shared
-library with the CUDA runtime linked statically.  The library is rebuilt only
-when a source or header is newer than it, or when it was built for another
-CPU architecture (the GPU hosts are aarch64).
+library with the CUDA runtime linked statically; the binding links to it.  Both
+are rebuilt only when a source or header is newer, when they were built for
+another CPU architecture (the GPU hosts are aarch64), or, the binding, for
+another PyTorch.
 """
 
 from __future__ import annotations
@@ -13,6 +16,7 @@ import os
 import platform
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +24,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libnorm.so")
+BIND = os.path.join(PKG, "_bind.so")
+BIND_SRC = os.path.join(CSRC, "bind.cpp")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -55,19 +61,78 @@ def _elf_machine(path):
         return None
 
 
-def up_to_date(lib: str = LIB) -> bool:
+def _fresh(lib: str, inputs) -> bool:
+    """`lib` exists, for this CPU, and is no older than its inputs."""
     if not os.path.exists(lib):
         return False
     want = _ELF_MACHINE.get(platform.machine())
     if want is not None and _elf_machine(lib) != want:
         return False
     t = os.path.getmtime(lib)
-    return all(os.path.getmtime(p) <= t for p in _inputs())
+    return all(os.path.getmtime(p) <= t for p in inputs)
+
+
+def up_to_date(lib: str = LIB) -> bool:
+    return _fresh(lib, _inputs())
+
+
+def _bind_inputs():
+    return [BIND_SRC, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
+
+
+def _bind_stamp():
+    return os.path.join(BUILD_DIR, "bind.torch")
+
+
+def bind_up_to_date() -> bool:
+    import torch
+    try:
+        with open(_bind_stamp()) as f:
+            built_for = f.read()
+    except OSError:
+        return False
+    return built_for == torch.__version__ and _fresh(BIND, _bind_inputs())
+
+
+def _compile_bind() -> str:
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), "/usr/local/cuda/include", sysconfig.get_paths()["include"]]
+    obj = os.path.join(BUILD_DIR, "bind.cpp.o")
+    cmd = [os.environ.get("CXX", "g++"), "-c", BIND_SRC, "-o", obj, "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for i in include:
+        cmd += ["-isystem", i]
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError(f"g++ failed on bind.cpp:\n{p.stdout}\n{p.stderr}")
+    return obj
+
+
+def _link_bind(obj: str) -> None:
+    import torch
+    tlib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BIND + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, LIB, "-L", tlib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{tlib}"]
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError(f"link of the Python binding failed:\n{p.stdout}\n{p.stderr}")
+    os.replace(tmp, BIND)
+    with open(_bind_stamp(), "w") as f:
+        f.write(torch.__version__)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile every CUDA source for sm_103a and link libnorm.so; return its path."""
+    """Compile every CUDA source for sm_103a, link libnorm.so and the Python
+    binding; return the library's path."""
+    bind = force or not bind_up_to_date()
     if not force and not extra_flags and up_to_date():
+        if bind:
+            os.makedirs(BUILD_DIR, exist_ok=True)
+            _link_bind(_compile_bind())
         return LIB
     nvcc = nvcc_path()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -81,15 +146,19 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{p.stdout}\n{p.stderr}")
         return obj, p.stdout + p.stderr
 
-    with ThreadPoolExecutor(max_workers=max(1, min(len(sources()), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(sources()) + 1, os.cpu_count() or 1))) as ex:
+        bind_obj = ex.submit(_compile_bind) if bind else None
         results = list(ex.map(compile_one, sources()))
+        bind_obj = bind_obj.result() if bind else None
     tmp = LIB + ".tmp"
     # -ldl: the header-only NVTX ranges look their tool up with dlopen
-    cmd = [nvcc, "-shared", "-o", tmp] + [o for o, _ in results] + ARCH + ["-cudart", "static", "-ldl"]
+    cmd = [nvcc, "-shared", "-Xlinker", "-soname=libnorm.so", "-o", tmp] + [o for o, _ in results] + ARCH + ["-cudart", "static", "-ldl"]
     p = subprocess.run(cmd, capture_output=True, text=True)
     if p.returncode != 0:
         raise RuntimeError(f"link failed:\n{p.stdout}\n{p.stderr}")
     os.replace(tmp, LIB)
+    if bind:
+        _link_bind(bind_obj)
     if verbose:
         for _, log in results:
             print(log)

@@ -73,6 +73,7 @@ SIGNATURES = {
 
 _lock = threading.Lock()
 _lib = None
+_bind = None
 
 
 class NormError(RuntimeError):
@@ -102,6 +103,21 @@ def load() -> ctypes.CDLL:
                 fn.argtypes = args
             _lib = lib
     return _lib
+
+
+def bind():
+    """The C++ binding of the residual-stream operators (_bind.so), which links
+    to libnorm.so; raise if either is missing."""
+    global _bind
+    if _bind is None:
+        load()
+        import importlib
+        try:
+            _bind = importlib.import_module(__package__ + "._bind")
+        except ImportError as e:
+            raise RuntimeError("_bind.so could not be loaded; build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+    return _bind
 
 
 def status_str(status: int) -> str:

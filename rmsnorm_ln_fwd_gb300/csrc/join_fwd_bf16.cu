@@ -1,0 +1,9 @@
+// Block join forward kernels instantiated for bf16 rows.
+
+#include "join_fwd.cuh"
+
+namespace normk {
+
+template cudaError_t launch_join<BF16>(JoinArgs, const DeviceInfo&, cudaStream_t);
+
+}  // namespace normk

@@ -323,40 +323,8 @@ def rms_backward_from_output(dy, y, rstd, gamma=None, *, need_param_grads: bool 
     return out, dgamma
 
 
-def _call(name, device, *args):
-    """Call the C entry point `name` on `device` and its current stream.  Sets
-    the device only where it is not the current one already: for a single row
-    the call is all host time."""
-    fn = getattr(_lib.load(), name)
-    i = device.index
-    if torch.cuda.current_device() == i:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
-    else:
-        with torch.cuda.device(i):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
-    if st != _lib.NORM_OK:
-        _lib.check(name, st)
-
-
-def _new_rows(x, H):
-    """A fresh contiguous tensor like x, and its row stride."""
-    return torch.empty_like(x, memory_format=torch.contiguous_format), max(H, 1)
-
-
-def _gate_view(gate, N, H, device, x_dtype):
-    """The gate as (2-D view, rows, row stride, dtype code): shape (H,), or
-    leading dims that flatten to B rows with B dividing N."""
-    if gate is None:
-        return None, 0, 0, _DT[x_dtype]
-    gv, B, Hg, ldg = _rows(gate, "gate")
-    if Hg != H or gate.device != device:
-        raise ValueError(f"gate must have {H} columns on {device}")
-    if B < 1 or N % B != 0 or (N and B > N):
-        raise ValueError(f"gate has {B} rows, which do not divide the {N} rows into equal runs")
-    code = _dtype_code(gate, "gate")
-    if code not in (_DT[x_dtype], _lib.NORM_F32):
-        raise TypeError(f"gate: dtype {gate.dtype} must be the rows' or float32")
-    return gv, B, ldg, code
+# The residual-stream operators check and allocate in the C++ binding (a
+# one-row call is all host time: 24 us through ctypes).
 
 
 def sandwich_rms(x, residual, gamma_post=None, gate=None, gamma_pre=None, eps: float = 1e-6, *,
@@ -372,42 +340,8 @@ def sandwich_rms(x, residual, gamma_post=None, gate=None, gamma_pre=None, eps: f
     None).  ``h_out`` may be a fresh tensor (default), ``x`` or ``residual``
     itself.  Returns (y, h, rstd_post, rstd_pre), statistics (N,) fp32 (None
     where a norm is not taken or save_stats is False)."""
-    xv, N, H, ldx = _rows(x, "x")
-    xc = _dtype_code(x, "x")
-    rv, ldr = _grad_out(residual, x, N, H, "residual")
-    if gamma_post is not None and not post_norm or not pre_norm and (gamma_pre is not None or out is not None):
-        raise ValueError("gamma_post needs post_norm; gamma_pre and out need pre_norm")
-    gamma_post = _vec(gamma_post, H, "gamma_post", x.device)
-    gamma_pre = _vec(gamma_pre, H, "gamma_pre", x.device)
-    wc = _w_code(xc, gamma_post, gamma_pre)
-    gv, B, ldg, gc = _gate_view(gate, N, H, x.device, x.dtype)
-    if h_out is None:
-        h, ldh = _new_rows(x, H)
-    else:
-        h, ldh = h_out, _grad_out(h_out, x, N, H, "h_out")[1]
-    y, ldy = None, 0
-    if pre_norm:
-        if out is None:
-            y, ldy = _new_rows(x, H)
-        else:
-            y, ldy = out, _grad_out(out, x, N, H, "out")[1]
-    rpost = torch.empty(N, device=x.device, dtype=torch.float32) if save_stats and post_norm else None
-    rpre = torch.empty(N, device=x.device, dtype=torch.float32) if save_stats and pre_norm else None
-    norms = (_lib.NORM_SANDWICH_POST if post_norm else 0) | (_lib.NORM_SANDWICH_PRE if pre_norm else 0)
-    _call("sandwich_rms", x.device, xv.data_ptr(), ldx, rv.data_ptr(), ldr, _ptr(gamma_post), _ptr(gv), ldg, B,
-          _ptr(gamma_pre), _ptr(y), ldy, h.data_ptr(), ldh, _ptr(rpost), _ptr(rpre), N, H, float(eps),
-          float(residual_scale), norms, xc, wc, gc)
-    return y, h, rpost, rpre
-
-
-def _own_workspace(ws, need, device):
-    if need == 0:
-        raise RuntimeError("could not size the workspace (no CUDA device?)")
-    if ws is None:
-        return torch.empty((need + 3) // 4, device=device, dtype=torch.float32), need
-    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
-    return ws, ws.numel() * ws.element_size()
+    return _lib.bind().sandwich_rms(x, residual, gamma_post, gate, gamma_pre, eps, residual_scale, post_norm, pre_norm,
+                                    h_out, out, save_stats)
 
 
 def sandwich_rms_grad(dy, x, h, rstd_post, rstd_pre, gamma_post=None, gate=None, gamma_pre=None, dh_in=None, *,
@@ -422,89 +356,8 @@ def sandwich_rms_grad(dy, x, h, rstd_post, rstd_pre, gamma_post=None, gate=None,
     where there is no such parameter (a gamma that is None counts as ones and
     has a gradient); gamma gradients take the gammas' dtype (or ``param_dtype``,
     else x's), dgate the gate's dtype and shape."""
-    xv, N, H, ldx = _rows(x, "x")
-    xc = _dtype_code(x, "x")
-    post, pre = rstd_post is not None, rstd_pre is not None
-    if pre != (dy is not None) or pre != (h is not None):
-        raise ValueError("dy, h and rstd_pre come together (all None without the norm after the add)")
-    if not post and gamma_post is not None or not pre and gamma_pre is not None:
-        raise ValueError("gamma_post needs rstd_post; gamma_pre needs rstd_pre")
-    if not post and not pre:
-        raise ValueError("rstd_post and rstd_pre are both None: no norm to differentiate")
-    if dy is None and dh_in is None:
-        raise ValueError("dy and dh_in are both None: no gradient arrives")
-    dyv, lddy = _grad_out(dy, x, N, H, "dy") if pre else (None, 0)
-    hv, ldh = _grad_out(h, x, N, H, "h") if pre else (None, 0)
-    div, lddi = _grad_out(dh_in, x, N, H, "dh_in") if dh_in is not None else (None, 0)
-    rpost = _stats(rstd_post, N, "rstd_post", x.device) if post else None
-    rpre = _stats(rstd_pre, N, "rstd_pre", x.device) if pre else None
-    gamma_post = _vec(gamma_post, H, "gamma_post", x.device)
-    gamma_pre = _vec(gamma_pre, H, "gamma_pre", x.device)
-    given = next((g.dtype for g in (gamma_post, gamma_pre) if g is not None), None)
-    wdt = given or param_dtype or x.dtype
-    if wdt not in _DT:
-        raise TypeError(f"param_dtype {wdt} not supported (float32, bfloat16 or float16)")
-    wc = _w_code(_DT[wdt], gamma_post, gamma_pre)
-    gv, B, ldg, gc = _gate_view(gate, N, H, x.device, x.dtype)
-    if dx is None:
-        odx, lddx = _new_rows(x, H)
-    else:
-        odx, lddx = dx, _grad_out(dx, x, N, H, "dx")[1]
-    if dres is None:
-        odr, lddr = _new_rows(x, H)
-    else:
-        odr, lddr = dres, _grad_out(dres, x, N, H, "dres")[1]
-    dgpost = dgate = dgpre = None
-    ws, wsb = None, 0
-    lib = _lib.load()
-    if need_param_grads and (post or pre or gate is not None):
-        if post:
-            dgpost = torch.empty(H, device=x.device, dtype=wdt)
-        if pre:
-            dgpre = torch.empty(H, device=x.device, dtype=wdt)
-        if gate is not None:
-            dgate = torch.empty(gate.shape, device=x.device, dtype=gate.dtype)
-        ws, wsb = _own_workspace(workspace, int(lib.sandwich_rms_workspace_bytes(H, B, x.device.index)), x.device)
-    norms = (_lib.NORM_SANDWICH_POST if post else 0) | (_lib.NORM_SANDWICH_PRE if pre else 0)
-    _call("sandwich_rms_grad", x.device, _ptr(dyv), lddy, xv.data_ptr(), ldx, _ptr(hv), ldh, _ptr(rpost), _ptr(rpre),
-          _ptr(gamma_post), _ptr(gv), ldg, B, _ptr(gamma_pre), _ptr(div), lddi, odx.data_ptr(), lddx, odr.data_ptr(),
-          lddr, _ptr(dgpost), _ptr(dgate), H, _ptr(dgpre), _ptr(ws), wsb, N, H, float(residual_scale), norms, xc, wc,
-          gc)
-    return odx, odr, dgpost, dgate, dgpre
-
-
-_IT = {torch.int32: _lib.NORM_I32, torch.int64: _lib.NORM_I64}
-
-
-def _tokens(tokens, device):
-    """(N, index code) of a contiguous tensor of token ids."""
-    if not isinstance(tokens, torch.Tensor) or not tokens.is_cuda:
-        raise ValueError("tokens must be a CUDA tensor")
-    if tokens.dtype not in _IT:
-        raise TypeError(f"tokens: dtype {tokens.dtype} not supported (int32 or int64)")
-    if not tokens.is_contiguous():
-        raise ValueError("tokens must be contiguous")
-    if tokens.device != device:
-        raise ValueError(f"tokens are on {tokens.device}, the rows on {device}")
-    return tokens.numel(), _IT[tokens.dtype]
-
-
-def _table(table):
-    if not isinstance(table, torch.Tensor) or not table.is_cuda:
-        raise ValueError("table must be a CUDA tensor")
-    if table.dim() != 2:
-        raise ValueError("table must have two dims (rows, columns)")
-    tv, V, H, ldt = _rows(table, "table")
-    return tv, V, H, ldt, _dtype_code(table, "table")
-
-
-def _row_out(out, tokens, table, N, H, what):
-    if out is None:
-        return torch.empty((*tokens.shape, H), device=table.device, dtype=table.dtype), max(H, 1)
-    _, No, Ho, ld = _rows(out, what)
-    if (No, Ho) != (N, H) or out.dtype != table.dtype or out.device != table.device:
-        raise ValueError(f"{what} must have {N} rows of {H} {table.dtype} columns on {table.device}")
-    return out, ld
+    return _lib.bind().sandwich_rms_grad(dy, x, h, rstd_post, rstd_pre, gamma_post, gate, gamma_pre, dh_in,
+                                         residual_scale, need_param_grads, workspace, dx, dres, param_dtype)
 
 
 def embedding_lookup(tokens, table, scale: float = 1.0, *, out=None):
@@ -512,12 +365,7 @@ def embedding_lookup(tokens, table, scale: float = 1.0, *, out=None):
 
     ``tokens`` are int32 or int64.  An id outside the table gives a row of zeros
     and sets NORM_DEVICE_ERR_BAD_TOKEN in the device error word."""
-    tv, V, H, ldt, xc = _table(table)
-    N, ic = _tokens(tokens, table.device)
-    h, ldh = _row_out(out, tokens, table, N, H, "out")
-    _call("embedding_lookup", table.device, tv.data_ptr(), ldt, V, tokens.data_ptr(), ic, h.data_ptr(), ldh, N, H,
-          float(scale), xc)
-    return h
+    return _lib.bind().embedding_lookup(tokens, table, scale, out)
 
 
 def embedding_rms(tokens, table, gamma=None, eps: float = 1e-6, scale: float = 1.0, *, h_out=None, out=None,
@@ -525,16 +373,7 @@ def embedding_rms(tokens, table, gamma=None, eps: float = 1e-6, scale: float = 1
     """The start of a residual stream and its first norm: h = scale *
     table[tokens] and y = rmsnorm(h) * gamma, from the fp32 h.  Returns
     (y, h, rstd); ids outside the table as in embedding_lookup."""
-    tv, V, H, ldt, xc = _table(table)
-    N, ic = _tokens(tokens, table.device)
-    gamma = _vec(gamma, H, "gamma", table.device)
-    wc = _w_code(xc, gamma)
-    h, ldh = _row_out(h_out, tokens, table, N, H, "h_out")
-    y, ldy = _row_out(out, tokens, table, N, H, "out")
-    rstd = torch.empty(N, device=table.device, dtype=torch.float32) if save_stats else None
-    _call("embedding_rms", table.device, tv.data_ptr(), ldt, V, tokens.data_ptr(), ic, _ptr(gamma), y.data_ptr(), ldy,
-          h.data_ptr(), ldh, _ptr(rstd), N, H, float(eps), float(scale), xc, wc)
-    return y, h, rstd
+    return _lib.bind().embedding_rms(tokens, table, gamma, eps, scale, h_out, out, save_stats)
 
 
 def embedding_grad(dh, tokens, num_rows: int, scale: float = 1.0, *, padding_idx=None, out=None,
@@ -545,22 +384,4 @@ def embedding_grad(dh, tokens, num_rows: int, scale: float = 1.0, *, padding_idx
     ``padding_idx`` is a token without gradient.  ``out`` (num_rows, H), in dh's
     dtype or float32, is overwritten, or added to with ``accumulate``; a fresh
     one takes ``param_dtype`` (default: dh's dtype)."""
-    dv, N, H, lddh = _rows(dh, "dh")
-    xc = _dtype_code(dh, "dh")
-    Nt, ic = _tokens(tokens, dh.device)
-    if Nt != N:
-        raise ValueError(f"dh has {N} rows for {Nt} tokens")
-    if padding_idx is not None and not 0 <= padding_idx < num_rows:
-        raise ValueError(f"padding_idx {padding_idx} is not a row of the table")
-    if out is None:
-        if accumulate:
-            raise ValueError("accumulate needs out")
-        out = torch.empty((num_rows, H), device=dh.device, dtype=param_dtype or dh.dtype)
-    tv, V, Ho, ldt, wc = _table(out)
-    if (V, Ho) != (num_rows, H) or out.device != dh.device:
-        raise ValueError(f"out must be ({num_rows}, {H}) on {dh.device}")
-    lib = _lib.load()
-    ws, wsb = _own_workspace(workspace, int(lib.embedding_grad_workspace_bytes(N, H)), dh.device)
-    _call("embedding_grad", dh.device, dv.data_ptr(), lddh, tokens.data_ptr(), ic, tv.data_ptr(), ldt, V, _ptr(ws), wsb,
-          N, H, float(scale), -1 if padding_idx is None else int(padding_idx), int(accumulate), xc, wc)
-    return out
+    return _lib.bind().embedding_grad(dh, tokens, num_rows, scale, padding_idx, out, accumulate, param_dtype, workspace)
