@@ -298,15 +298,23 @@ static cudaError_t run_join(const JoinArgs& a, const DeviceInfo& dev, cudaStream
   *done = true;
   const int tpr = chunk_threads(a.H, kJoinCols<D>);
   if (tpr <= 256) return run_join_rows<D, GB, 256, (GB >= 16 ? 3 : 2), 1>(a, tpr, 256 / tpr, dev, s);
-  if (tpr <= kRowsAutoMaxThreads) return run_join_rows<D, GB, kRowsAutoMaxThreads, 1, 1>(a, tpr, 1, dev, s);
-  // wider rows: the smallest cluster with parts of at most 512 threads
+  // Wider rows: the smallest cluster with parts of at most 320 threads, two CTAs
+  // an SM, or in fp32 256 and three (us, one CTA of up to 640 threads or
+  // clusters of up to 512; 320x2; 256x3: bf16 8192x5120 56.4 as 320x2 without a
+  // cluster, 6000x6144 57.6; 52.5; 64.2, 4096x8192 49.6; 50.1; 59.6, 2048x16384
+  // 52.1; 52.1; 67.8, fp32 2048x8192 48.7; 48.1; 44.3, 1024x16384 51.0; 50.1;
+  // 47.8).  80 registers, three CTAs of 256 threads, spill the clusters of half
+  // precision.
+  constexpr bool F32ROWS = D::VEC == 4;
+  constexpr int T = F32ROWS ? 256 : 320, M = F32ROWS ? (GB >= 16 ? 3 : 2) : 2;
+  if (tpr <= T) return run_join_rows<D, GB, T, M, 1>(a, tpr, 1, dev, s);
   auto threads = [&](int cl) {
     constexpr int GE = Chunk<D, GB, kJoinCols<D>>::GE;
     return chunk_threads((a.H + cl * GE - 1) / (cl * GE) * GE, kJoinCols<D>);
   };
-  if (threads(2) <= 512) return run_join_rows<D, GB, 512, 1, 2>(a, threads(2), 1, dev, s);
-  if (threads(4) <= 512) return run_join_rows<D, GB, 512, 1, 4>(a, threads(4), 1, dev, s);
-  if (threads(8) <= 512) return run_join_rows<D, GB, 512, 1, 8>(a, threads(8), 1, dev, s);
+  if (threads(2) <= T) return run_join_rows<D, GB, T, M, 2>(a, threads(2), 1, dev, s);
+  if (threads(4) <= T) return run_join_rows<D, GB, T, M, 4>(a, threads(4), 1, dev, s);
+  if (threads(8) <= T) return run_join_rows<D, GB, T, M, 8>(a, threads(8), 1, dev, s);
   *done = false;
   return cudaSuccess;
 }
