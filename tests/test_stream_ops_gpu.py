@@ -577,3 +577,94 @@ def test_stream_captured_and_on_other_streams():
         torch.cuda.synchronize()
         for g, outs in graphs:
             assert all(torch.equal(a, b) for a, b in zip(want, outs))
+
+
+@pytest.mark.parametrize("N,H,B", [(1, 1, 1), (37, 1000, 1), (300, 257, 3), (5, 16384, 5), (24, 64, 0)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_loop_kernels(N, H, B, dt):
+    """The kernels for any width and alignment, which otherwise only very wide
+    rows reach, on ordinary ones."""
+    c = join_inputs(N, H, DT[dt], torch.float32, B, seed=N)
+    table = rnd((20, H), 3, DT[dt])
+    tokens = torch.arange(N, device=DEV) % 20
+    _lib.set_kernel_path(2)
+    try:
+        out = nl.sandwich_rms(c["x"], c["res"], c["gpost"], c["gate"], c["gpre"], 1e-5, residual_scale=0.75)
+        grad, rpost, rpre = run_join_grad(c, True, True)
+        y, h, r = nl.embedding_rms(tokens, table, c["gpre"], 1e-5, 1.5)
+    finally:
+        _lib.set_kernel_path(0)
+    torch.cuda.synchronize()
+    check_join(c, out, 1e-5, 0.75, True, True)
+    check_join_grad(c, grad, rpost, rpre, 0.75)
+    ry, rh, rr = S.lookup_forward(tokens.tolist(), n64(table), 1.5, n64(c["gpre"]), 1e-5)
+    close(h, rh, U * np.abs(rh), "h")
+    close(y, ry, 2 * steps(H) * U * np.abs(ry), "y")
+
+
+def test_offsets_past_32_bits():
+    """Rows, and rows of a table, more than 2^31 elements apart."""
+    N, H, ld = 3, 1040, 1_200_000_000
+    small = join_inputs(N, H, torch.bfloat16, torch.bfloat16, 1, seed=8)
+
+    def far(t):
+        buf = torch.empty((N - 1) * ld + H, dtype=t.dtype, device=DEV)
+        view = buf.as_strided((N, H), (ld, 1))
+        view.copy_(t)
+        return view
+
+    c = {k: far(v) if k in ("x", "res") else v for k, v in small.items()}
+    want = nl.sandwich_rms(small["x"], small["res"], small["gpost"], small["gate"], small["gpre"])
+    got = nl.sandwich_rms(c["x"], c["res"], c["gpost"], c["gate"], c["gpre"], h_out=far(small["x"]))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    del got
+    g, rpost, rpre = run_join_grad(small, True, True)
+    f = nl.sandwich_rms_grad(small["dy"], c["x"], c["res"], rpost, rpre, c["gpost"], c["gate"], c["gpre"], small["dh"],
+                             residual_scale=0.75)
+    assert all(torch.equal(a, b) for a, b in zip(f, g))
+    tokens = torch.tensor([2, 0, 2], device=DEV)
+    assert torch.equal(nl.embedding_lookup(tokens, c["x"]), small["x"][tokens])
+    out = far(small["x"])
+    nl.embedding_grad(small["dy"], tokens, N, out=out)
+    assert torch.equal(out.contiguous(), nl.embedding_grad(small["dy"], tokens, N))
+
+
+def test_calls_at_once_on_two_streams():
+    """Calls that overlap on the GPU do not meet: each has its own workspace."""
+    c = [join_inputs(2000, 1024, torch.bfloat16, torch.bfloat16, 8, seed=i) for i in range(2)]
+    tok = [torch.from_numpy(make_tokens("skewed", 2000, 500 + i)).to(DEV) for i in range(2)]
+    st = [torch.cuda.Stream() for _ in range(2)]
+    want = [(run_join_grad(c[i], True, True)[0], nl.embedding_grad(c[i]["dy"], tok[i], 500 + i)) for i in range(2)]
+    rp = [[torch.from_numpy(S._rstd(n64(c[i][k]), 1e-5)).float().to(DEV) for k in ("x", "res")] for i in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i in range(2):
+            with torch.cuda.stream(st[i]):
+                d = c[i]
+                got[i].append((nl.sandwich_rms_grad(d["dy"], d["x"], d["res"], *rp[i], d["gpost"], d["gate"], d["gpre"],
+                                                    d["dh"], residual_scale=0.75),
+                               nl.embedding_grad(d["dy"], tok[i], 500 + i)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g, e in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i][0])) and torch.equal(e, want[i][1])
+
+
+def test_expanded_and_permuted_tensors_are_refused():
+    x = torch.zeros((6, 64), device=DEV, dtype=torch.bfloat16)
+    with pytest.raises(nl.NormError):
+        nl.sandwich_rms(x, x[:1].expand(6, 64))
+    with pytest.raises(nl.NormError):
+        nl.sandwich_rms(x, x.clone(), gate=x[:1].expand(3, 64))
+    t = torch.zeros((4, 5, 64), device=DEV)
+    with pytest.raises(ValueError, match="flatten"):
+        nl.sandwich_rms(t.transpose(0, 1), torch.zeros((5, 4, 64), device=DEV))
+    with pytest.raises(ValueError, match="contiguous"):
+        nl.sandwich_rms(t[..., ::2], t[..., ::2])
+    with pytest.raises(TypeError):
+        nl.sandwich_rms(t.double(), t.double())
+
+
+def test_device_words_of_the_far_kernels_stay_clear():
+    assert _lib.device_errors() == 0
