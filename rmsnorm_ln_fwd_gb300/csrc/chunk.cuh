@@ -148,9 +148,11 @@ __device__ __forceinline__ void lds_pairs(uint32_t p, float2 (&v)[2]) {
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0].x), "=f"(v[0].y), "=f"(v[1].x), "=f"(v[1].y) : "r"(p));
 }
 
-// Sum four values over a row group of nw <= 32 warps, as group_sum: the warp
-// stage is a reduce-scatter (six shuffles; value k ends in lanes 8k..8k+7).
-// `sh` holds 2*nw*4 floats; parity alternates per call.
+// Sum four values over a row group of nw <= kSum4Warps warps, as group_sum: the
+// warp stage is a reduce-scatter (six shuffles; value k ends in lanes
+// 8k..8k+7).  `sh` holds kSum4Floats floats; parity alternates per call.
+constexpr int kSum4Warps = 24;
+constexpr int kSum4Floats = 2 * 4 * kSum4Warps;
 __device__ __forceinline__ void group_sum4(float (&v)[4], float* sh, int nw, int wig, int lane, int bar_id, int parity) {
   const bool hi4 = (lane & 16) != 0;
   float k0 = hi4 ? v[2] : v[0], k1 = hi4 ? v[3] : v[1];
@@ -166,18 +168,18 @@ __device__ __forceinline__ void group_sum4(float (&v)[4], float* sh, int nw, int
     for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, k, 8 * i);
     return;
   }
-  float* buf = sh + parity * nw * 4;
-  if ((lane & 7) == 0) buf[wig * 4 + (lane >> 3)] = k;
+  // buf[value][warp]; eight lanes a value then add up the warps' partials
+  float* buf = sh + parity * (4 * kSum4Warps) + (lane >> 3) * kSum4Warps;
+  if ((lane & 7) == 0) buf[wig] = k;
   named_barrier(bar_id, nw * 32);
-  const int P = pow2_ceil(nw);
-  const int src = lane & (P - 1);
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (src < nw) s = *reinterpret_cast<const float4*>(buf + 4 * src);
-  v[0] = s.x;
-  v[1] = s.y;
-  v[2] = s.z;
-  v[3] = s.w;
-  warp_sum_pow2<4>(v, P);
+  float x = 0.f;
+#pragma unroll
+  for (int i = 0; i < kSum4Warps / 8; ++i)
+    if ((lane & 7) + 8 * i < nw) x += buf[(lane & 7) + 8 * i];
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, x, 8 * i);
 }
 
 // Granule that every given row tensor allows: 32, 16 or one element.

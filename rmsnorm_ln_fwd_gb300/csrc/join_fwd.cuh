@@ -123,8 +123,9 @@ __global__ void __launch_bounds__(MAXT, MINB) join_rows_kernel(const JoinArgs a,
   const float inv_h = 1.f / (float)a.H;
   const bool w_f32 = a.w_f32 != 0, g_f32 = a.g_f32 != 0;
   const size_t wes = w_f32 ? 4 : sizeof(T), ges = g_f32 ? 4 : sizeof(T);
-  float* sh = sh_join + group * (2 * nw * 4);
-  float* slot = sh_join + rpc * (2 * nw * 4) + threadIdx.x * SLOT;
+  float* sh = sh_join + group * kSum4Floats;
+  float* slot = sh_join + rpc * kSum4Floats + threadIdx.x * SLOT;
+  const uint32_t slot32 = smem_u32(slot);
   const int bar_id = 1 + group;
 
   // this group's rows: strided, or (several gate rows) one contiguous range
@@ -136,9 +137,22 @@ __global__ void __launch_bounds__(MAXT, MINB) join_rows_kernel(const JoinArgs a,
     step = 1;
   }
   uint32_t nx[C::NW], nr[C::NW];
+  // Pointers that step from row to row save instructions, but not the registers
+  // of three CTAs an SM (they spilled there: 8192x4096 bf16 45.9 -> 53.1 us).
+  constexpr bool STEPS = MINB < 3;
+  const int64_t at0 = c0 + b;
+  const T* xp = reinterpret_cast<const T*>(a.x) + (STEPS ? row * a.ldx : 0) + at0;
+  const T* resp = reinterpret_cast<const T*>(a.res) + (STEPS ? row * a.ldr : 0) + at0;
+  T* hp = reinterpret_cast<T*>(a.h) + (STEPS ? row * a.ldh : 0) + at0;
+  T* yp = reinterpret_cast<T*>(a.y) + (STEPS ? row * a.ldy : 0) + at0;
+  const int64_t xstep = step * a.ldx, rstep = step * a.ldr, hstep = step * a.ldh, ystep = step * a.ldy;
   auto fetch = [&](int64_t r) {
-    C::load(reinterpret_cast<const T*>(a.x) + r * a.ldx + c0 + b, lim, nx);
-    C::load(reinterpret_cast<const T*>(a.res) + r * a.ldr + c0 + b, lim, nr);
+    C::load(STEPS ? xp : xp + r * a.ldx, lim, nx);
+    C::load(STEPS ? resp : resp + r * a.ldr, lim, nr);
+    if constexpr (STEPS) {
+      xp += xstep;
+      resp += rstep;
+    }
   };
   if (row < end) fetch(row);
 
@@ -191,7 +205,7 @@ __global__ void __launch_bounds__(MAXT, MINB) join_rows_kernel(const JoinArgs a,
 #pragma unroll
     for (int q = 0; q < NP / 2; ++q) {
       float2 w[2];
-      get_pairs(slot, q, w);
+      lds_pairs(slot32 + 16 * q, w);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int p = 2 * q + i;
@@ -214,14 +228,14 @@ __global__ void __launch_bounds__(MAXT, MINB) join_rows_kernel(const JoinArgs a,
     }
     const float rp = a.post ? rsqrtf(s[0] * inv_h + a.eps) : 1.f;
     const float2 rp2 = splat2(rp);
-    T* hrow = reinterpret_cast<T*>(a.h) + row * a.ldh + c0 + b;
     uint32_t out[C::NW];
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
       f[p] = fma2(f[p], rp2, mul2(word_pair<D>(rw, p), alpha2));
       pair_word<D>(out, p, f[p]);
     }
-    C::store(hrow, lim, out);
+    C::store(STEPS ? hp : hp + row * a.ldh, lim, out);
+    if constexpr (STEPS) hp += hstep;
     const bool writer = t == 0 && crank == 0;
     if (writer && a.rpost) a.rpost[row] = rp;
     if (!a.pre) continue;
@@ -247,11 +261,12 @@ __global__ void __launch_bounds__(MAXT, MINB) join_rows_kernel(const JoinArgs a,
 #pragma unroll
     for (int q = 0; q < NP / 2; ++q) {
       float2 g[2];
-      get_pairs(slot + E, q, g);
+      lds_pairs(slot32 + 4 * E + 16 * q, g);
 #pragma unroll
       for (int i = 0; i < 2; ++i) pair_word<D>(out, 2 * q + i, mul2(mul2(f[2 * q + i], rn2), g[i]));
     }
-    C::store(reinterpret_cast<T*>(a.y) + row * a.ldy + c0 + b, lim, out);
+    C::store(STEPS ? yp : yp + row * a.ldy, lim, out);
+    if constexpr (STEPS) yp += ystep;
   }
   if constexpr (CL > 1) cluster_sync_all();  // no CTA leaves while a partner may still write to it
 }
@@ -260,7 +275,7 @@ template <typename D, int GB, int MAXT, int MINB, int CL>
 static cudaError_t run_join_rows(const JoinArgs& a, int tpr, int rpc, const DeviceInfo& dev, cudaStream_t s) {
   auto kern = join_rows_kernel<D, GB, MAXT, MINB, CL>;
   const int threads = rpc * tpr;
-  const size_t smem = sizeof(float) * ((size_t)rpc * 2 * (tpr / 32) * 4 + (size_t)threads * param_slot<Chunk<D, GB, kJoinCols<D>>::E, 2>());
+  const size_t smem = sizeof(float) * ((size_t)rpc * kSum4Floats + (size_t)threads * param_slot<Chunk<D, GB, kJoinCols<D>>::E, 2>());
   static KernelMemo memo;
   if (smem > 48 * 1024) {
     cudaError_t e = memo.allow_smem(kern, dev.max_smem_optin - 1024, dev);
@@ -297,7 +312,16 @@ template <typename D, int GB>
 static cudaError_t run_join(const JoinArgs& a, const DeviceInfo& dev, cudaStream_t s, bool* done) {
   *done = true;
   const int tpr = chunk_threads(a.H, kJoinCols<D>);
-  if (tpr <= 256) return run_join_rows<D, GB, 256, (GB >= 16 ? 3 : 2), 1>(a, tpr, 256 / tpr, dev, s);
+  // One warp a row, and fp32: three CTAs an SM; else two, which leave the
+  // registers for stepping pointers (us, three; two: bf16 65536x256 29.6; 31.9,
+  // 8192x1024 14.6; 13.3, 8192x4096 46.9; 47.2, 16384x4096 with eight gates 93.8;
+  // 88.8, fp16 8192x2056 27.0; 24.8).
+  if (tpr <= 256) {
+    if constexpr (GB >= 16) {
+      if (D::VEC == 4 || tpr == 32) return run_join_rows<D, GB, 256, 3, 1>(a, tpr, 256 / tpr, dev, s);
+    }
+    return run_join_rows<D, GB, 256, 2, 1>(a, tpr, 256 / tpr, dev, s);
+  }
   // Wider rows: the smallest cluster with parts of at most 320 threads, two CTAs
   // an SM, or in fp32 256 and three (us, one CTA of up to 640 threads or
   // clusters of up to 512; 320x2; 256x3: bf16 8192x5120 56.4 as 320x2 without a
