@@ -419,7 +419,9 @@ norm_status norm_selftest_bounded_wait(unsigned long long limit_ns, norm_stream_
  * process.  0 = automatic (the default), 1 = register rows (else the strided
  * loop), 2 = strided loop only, 3 = bulk-copy pipeline first.  A family is
  * used only where the call meets its requirements (alignment, row width);
- * every family computes the same results within rounding.
+ * every family computes the same results within rounding.  The block join and
+ * the token lookup have two families: 2 is their loop, anything else the
+ * automatic choice.
  */
 norm_status norm_set_kernel_path(int path);
 

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kJoinGradLoopThreads) join_grad_loop_kernel(co
       const Elem e = load(j);
       const float dh = fmaf(rn, fmaf(-e.hh, c, e.g), e.in);
       store_elem<D>(dres, j, a.alpha * dh);
-      store_elem<D>(dx, j, ro * fmaf(e.w, dh, -e.oh * k));
+      store_elem<D>(dx, j, a.rpost ? ro * fmaf(e.w, dh, -e.oh * k) : e.w * dh);
       if (want_pre) pre[j] = fmaf(e.dyv, e.hh, pre[j]);
       if (want_a) {
         const float sum = fmaf(dh, e.oh, acc[j]);
@@ -417,6 +417,7 @@ __global__ void __launch_bounds__(MAXT, MINB) join_grad_rows_kernel(const JoinGr
     }
   };
   const float2 alpha2 = splat2(a.alpha);
+  const bool post = a.rpost != nullptr;
   int parity = 0, buf = 0;
   unsigned phase = 0u, it = 0;  // phase: parity of the ring's current turn
   float nrn = 0.f, nro = 1.f;   // the next row's statistics
@@ -524,7 +525,9 @@ __global__ void __launch_bounds__(MAXT, MINB) join_grad_rows_kernel(const JoinGr
         const float2 dh = fma2(h, nc2, fma2(dyr, gp[i], word_pair<D>(iw, p)));
         pair_word<D>(od, p, mul2(dh, alpha2));
         const float2 dr = mul2(dh, ro2);
-        pair_word<D>(ox, p, fma2(x, nk2, mul2(dr, w[i])));
+        float2 o = mul2(dr, w[i]);
+        if (post) o = fma2(x, nk2, o);  // (0 times an infinite x is no 0)
+        pair_word<D>(ox, p, o);
         acc_pre[p] = fma2(dyr, h, acc_pre[p]);
         acc[p] = fma2(dr, x, acc[p]);
       }

@@ -331,7 +331,9 @@ static cudaError_t run_join(const JoinArgs& a, const DeviceInfo& dev, cudaStream
   // precision.
   constexpr bool F32ROWS = D::VEC == 4;
   constexpr int T = F32ROWS ? 256 : 320, M = F32ROWS ? (GB >= 16 ? 3 : 2) : 2;
-  if (tpr <= T) return run_join_rows<D, GB, T, M, 1>(a, tpr, 1, dev, s);
+  if constexpr (!F32ROWS) {
+    if (tpr <= T) return run_join_rows<D, GB, T, M, 1>(a, tpr, 1, dev, s);
+  }
   auto threads = [&](int cl) {
     constexpr int GE = Chunk<D, GB, kJoinCols<D>>::GE;
     return chunk_threads((a.H + cl * GE - 1) / (cl * GE) * GE, kJoinCols<D>);

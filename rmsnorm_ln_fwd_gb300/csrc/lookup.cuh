@@ -410,7 +410,8 @@ struct ClearSmem {
 template <typename O>
 __device__ __forceinline__ void clear_rows(const LookupGradArgs& a, ClearSmem& sm, int part, int parts) {
   using T = typename O::T;
-  for (int i = threadIdx.x; i < kClearZeros / 16; i += (int)blockDim.x)
+  const int nt = blockDim.x;
+  for (int i = threadIdx.x; i < kClearZeros / 16; i += nt)
     reinterpret_cast<uint4*>(sm.zeros)[i] = make_uint4(0u, 0u, 0u, 0u);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the __syncthreads below orders it for every thread)
   T* out = reinterpret_cast<T*>(a.dtable);
@@ -422,14 +423,14 @@ __device__ __forceinline__ void clear_rows(const LookupGradArgs& a, ClearSmem& s
   if (!a.mark && (bits & 15u) == 0 && a.lddt == a.H) {  // one stretch of memory
     unsigned char* p = reinterpret_cast<unsigned char*>(out + lo * a.H);
     const int64_t bytes = (hi - lo) * (int64_t)row_bytes;
-    for (int64_t i = (int64_t)threadIdx.x * kClearZeros; i < bytes; i += (int64_t)(int)blockDim.x * kClearZeros)
+    for (int64_t i = (int64_t)threadIdx.x * kClearZeros; i < bytes; i += (int64_t)nt * kClearZeros)
       bulk_s2g(p + i, sm.zeros, (uint32_t)min(bytes - i, (int64_t)kClearZeros));
     lo = hi;
   }
   for (int64_t v0 = lo; v0 < hi; v0 += kClearMaxRange) {
     const int n = (int)min(hi - v0, (int64_t)kClearMaxRange);
     __syncthreads();
-    for (int i = threadIdx.x; i < (n + 31) / 32; i += (int)blockDim.x) sm.marks[i] = 0u;
+    for (int i = threadIdx.x; i < (n + 31) / 32; i += nt) sm.marks[i] = 0u;
     __syncthreads();
     if (a.mark) {
       auto mark = [&](int64_t t) {
@@ -440,7 +441,7 @@ __device__ __forceinline__ void clear_rows(const LookupGradArgs& a, ClearSmem& s
       const int per = a.tok64 ? 2 : 4;
       const int64_t groups = (reinterpret_cast<uintptr_t>(a.tokens) & 15u) == 0 ? a.N / per : 0;
 #pragma unroll 8
-      for (int64_t i = threadIdx.x; i < groups; i += (int)blockDim.x) {
+      for (int64_t i = threadIdx.x; i < groups; i += nt) {
         const uint4 u = ld_cached(reinterpret_cast<const uint4*>(a.tokens) + i);
         if (a.tok64) {
           mark((int64_t)(((unsigned long long)u.y << 32) | u.x));
@@ -452,20 +453,20 @@ __device__ __forceinline__ void clear_rows(const LookupGradArgs& a, ClearSmem& s
           mark((int)u.w);
         }
       }
-      for (int64_t i = groups * per + threadIdx.x; i < a.N; i += (int)blockDim.x)
+      for (int64_t i = groups * per + threadIdx.x; i < a.N; i += nt)
         mark(load_token(a.tokens, a.tok64, i, a.V, nullptr));
       __syncthreads();
     }
     if ((bits & 15u) == 0) {
       // a thread a row, in bulk copies of the zeros
-      for (int r = threadIdx.x; r < n; r += (int)blockDim.x) {
+      for (int r = threadIdx.x; r < n; r += nt) {
         if ((sm.marks[r >> 5] >> (r & 31)) & 1u) continue;
         unsigned char* row = reinterpret_cast<unsigned char*>(out + (v0 + r) * a.lddt);
         for (size_t i = 0; i < row_bytes; i += kClearZeros)
           bulk_s2g(row + i, sm.zeros, (uint32_t)min(row_bytes - i, (size_t)kClearZeros));
       }
     } else {
-      for (int r = threadIdx.x >> 5; r < n; r += (int)blockDim.x / 32) {
+      for (int r = threadIdx.x >> 5; r < n; r += nt / 32) {
         if ((sm.marks[r >> 5] >> (r & 31)) & 1u) continue;
         T* row = out + (v0 + r) * a.lddt;
         for (int j = threadIdx.x & 31; j < a.H; j += 32) row[j] = T(0.f);
@@ -525,6 +526,7 @@ __global__ void __launch_bounds__(kTileThreads) lookup_grad_tile_kernel(const Lo
   using C = Chunk<D, GB, 32 / (int)sizeof(typename D::T)>;
   using T = typename D::T;
   constexpr int E = C::E, NP = C::NP, NW = C::NW;
+  const int nt = blockDim.x;
   __shared__ __align__(16) ClearSmem sm;
   __shared__ uint2 kv[kLookupMaxTile + 2];  // with the neighbours' nearest ids
   pdl_launch_dependents();
@@ -538,14 +540,14 @@ __global__ void __launch_bounds__(kTileThreads) lookup_grad_tile_kernel(const Lo
   const int64_t first = (int64_t)tile * a.tile;
   const int n = (int)min((int64_t)a.tile, a.N - first);
   const unsigned none = 0xffffffffu;  // no id (ids are at most V < 2^31)
-  for (int i = threadIdx.x; i < n + 2; i += (int)blockDim.x) {
+  for (int i = threadIdx.x; i < n + 2; i += nt) {
     const int64_t at = first + i - 1;
     kv[i] = at >= 0 && at < a.N ? __ldcg(a.sorted + at) : make_uint2(none, 0u);
   }
   __syncthreads();
   const unsigned ignored = (unsigned)a.V;
   const bool open_front = kv[0].x == kv[1].x;
-  for (int c0 = col_block * ((int)blockDim.x * E); c0 < a.H; c0 += a.col_blocks * ((int)blockDim.x * E)) {
+  for (int c0 = col_block * (nt * E); c0 < a.H; c0 += a.col_blocks * (nt * E)) {
     const int c = c0 + C::base(threadIdx.x), lim = a.H - c;
     const T* src = reinterpret_cast<const T*>(a.dh) + c;
     float2 acc[NP];

@@ -306,6 +306,18 @@ def test_join_bad_rows_stay_alone(H, bad):
     assert not torch.isfinite(got[0][4]).all()
 
 
+@pytest.mark.parametrize("H", [64, 1001, 5120])
+def test_join_grad_without_post_norm_leaves_x_out_of_dx(H):
+    """dx = gate * dh then: an infinite x reaches dgate, not dx."""
+    c = join_inputs(6, H, torch.bfloat16, torch.bfloat16, 1, seed=2)
+    want, _, _ = run_join_grad(c, False, True)
+    c["x"] = c["x"].clone()
+    c["x"][3, H // 3] = float("inf")
+    got, _, _ = run_join_grad(c, False, True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[4], want[4])
+    assert not torch.isfinite(got[3][H // 3]) and torch.isfinite(got[3][:H // 3]).all()
+
+
 def test_join_cancelling_stream():
     """A block output that cancels the stream almost everywhere: the second
     norm's sum is far smaller than its terms.  The rows are exact multiples, so
