@@ -785,52 +785,55 @@ static cudaError_t run_join_grad_rows(JoinGradArgs& a, const JoinRing& ring, con
 }
 
 // CTAs of at most MAXT threads, MINB an SM, in clusters of the fewest CTAs a row
-// (1, 2, 4, 8) whose part of it fits the threads and at least two row buffers;
-// *done = false where none does.
-template <typename D, int GB, bool RUNS, int MAXT, int MINB>
-static cudaError_t run_join_grad_shape(JoinGradArgs& a, const DeviceInfo& dev, cudaStream_t s, bool* done) {
+// (CL0 to CL1, powers of two) whose part of it fits the threads and at least two
+// row buffers; false where none does.
+template <typename D, int GB, bool RUNS, int MAXT, int MINB, int CL0, int CL1>
+static bool run_join_grad_shape(JoinGradArgs& a, const DeviceInfo& dev, cudaStream_t s, cudaError_t* e) {
   using C = Chunk<D, GB, kJoinGradCols<D>>;
-  *done = true;
-  for (int cl = 1; cl <= 8; cl *= 2) {
-    const JoinRing r = join_ring<C::E>(a.H, C::ES, C::GE, cl, RUNS, MAXT, MINB, dev.max_smem_optin);
-    if (r.tpr > MAXT || r.nb < kJoinMinBuffers) continue;
-    if (cl == 1) return run_join_grad_rows<D, GB, RUNS, MAXT, MINB, 1>(a, r, dev, s);
-    if (cl == 2) return run_join_grad_rows<D, GB, RUNS, MAXT, MINB, 2>(a, r, dev, s);
-    if (cl == 4) return run_join_grad_rows<D, GB, RUNS, MAXT, MINB, 4>(a, r, dev, s);
-    return run_join_grad_rows<D, GB, RUNS, MAXT, MINB, 8>(a, r, dev, s);
+  const JoinRing r = join_ring<C::E>(a.H, C::ES, C::GE, CL0, RUNS, MAXT, MINB, dev.max_smem_optin);
+  if (r.tpr <= MAXT && r.nb >= kJoinMinBuffers) {
+    *e = run_join_grad_rows<D, GB, RUNS, MAXT, MINB, CL0>(a, r, dev, s);
+    return true;
   }
-  *done = false;
-  return cudaSuccess;
+  if constexpr (CL0 < CL1) return run_join_grad_shape<D, GB, RUNS, MAXT, MINB, 2 * CL0, CL1>(a, dev, s, e);
+  return false;
 }
 
+// Measured (us, bf16 unless said; in brackets the CTAs a row; groups of narrower
+// rows share a CTA):
+//   threads x CTAs an SM      160x3      256x2      512x1
+//   16384x1280                 63.2       54.0       49.2
+//   16384x2048                 70.1       73.9       72.6
+//   8192x4096                  76.6 (2)   73.1       71.8
+//   8192x5120                  86.8 (2)  102.9 (2)   90.4
+//   6000x6144                 103.1 (4)   82.4 (2)   77.0
+//   4096x8192                  82.4 (4)   73.6 (2)   71.4
+//   4096x10240                 89.7 (4)  111.3 (4)  110.1 (2)
+//   2048x16384                 92.8 (8)   78.0 (4)   81.4 (2)
+//   8197x2056 fp16, 7 gates    59.5       66.4       55.9
+//   fp32 4096x4096             66.8 (4)   70.9 (2)   66.7
+//   fp32 2048x8192             70.3 (8)   69.9 (4)   69.2 (2)
+// So: one warp a row in 256x2 (its eight groups are a CTA); rows, or groups of
+// rows, of up to 512 threads in one CTA; wider ones in clusters, 160x3 where the
+// part of at most 256 threads has no more than 160.  fp32, eight columns a thread
+// and half the instructions a byte, keeps the large CTA throughout.
 template <typename D, int GB, bool RUNS>
 static cudaError_t run_join_grad(JoinGradArgs& a, const DeviceInfo& dev, cudaStream_t s, bool* done) {
-  // Measured (us, bf16 unless said; in brackets the CTAs a row of each shape):
-  //   threads x CTAs an SM      160x3    256x2    512x1
-  //   16384x2048                 75.3     71.6       -
-  //   8192x4096 (cluster of 2)   76.2     73.5*    84.4*   (* one CTA a row)
-  //   8192x5120 (2)              86.4    112.7    103.3*
-  //   4096x8192 (4; 2)           91.0     80.8     79.0*
-  //   2048x16384 (8; 4; 2)      102.0     85.6     89.7
-  //   8197x2056 fp16, 7 gates    58.8*    69.9*       -
-  //   fp32 4096x4096 (4; 2)      67.6     71.1     65.7*
-  //   fp32 2048x8192 (8; 4; 2)   69.0     70.6     69.0
-  // Half precision takes 256x2, or 160x3 where the part of a row that fits 256
-  // threads has 129 to 160; fp32, eight columns a thread and half the
-  // instructions a byte, one large CTA.
+  cudaError_t e = cudaSuccess;
+  *done = true;
   const int whole = chunk_threads(a.H, kJoinGradCols<D>);
   if constexpr (D::VEC == 4) {
-    if (whole <= 256) return run_join_grad_shape<D, GB, RUNS, 256, 2>(a, dev, s, done);
-    return run_join_grad_shape<D, GB, RUNS, 512, 1>(a, dev, s, done);
+    if (whole == 32 && run_join_grad_shape<D, GB, RUNS, 256, 2, 1, 1>(a, dev, s, &e)) return e;
+    if (run_join_grad_shape<D, GB, RUNS, 512, 1, 1, 8>(a, dev, s, &e)) return e;
   } else {
     int part = whole;
     while (part > 256) part = (part / 2 + 31) / 32 * 32;
-    if (part > 128 && part <= 160) {
-      cudaError_t e = run_join_grad_shape<D, GB, RUNS, 160, 3>(a, dev, s, done);
-      if (*done) return e;
-    }
-    return run_join_grad_shape<D, GB, RUNS, 256, 2>(a, dev, s, done);
+    if (whole > 256 && part <= 160 && run_join_grad_shape<D, GB, RUNS, 160, 3, 2, 8>(a, dev, s, &e)) return e;
+    if (whole > 32 && whole <= 512 && run_join_grad_shape<D, GB, RUNS, 512, 1, 1, 1>(a, dev, s, &e)) return e;
+    if (run_join_grad_shape<D, GB, RUNS, 256, 2, 1, 8>(a, dev, s, &e)) return e;
   }
+  *done = false;
+  return cudaSuccess;
 }
 
 template <typename D>

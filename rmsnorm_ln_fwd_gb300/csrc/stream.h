@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "launch.h"
 
 namespace normk {
@@ -130,8 +132,12 @@ struct LookupGradArgs {
 
 constexpr int kJoinMaxPartialsPerSm = 3;
 // Row groups a CTA of the gradient may have: an upper bound by the width, for
-// the workspace.
-inline int join_max_groups(int64_t H) { return H <= 512 ? 8 : H <= 1024 ? 4 : H <= 2048 ? 2 : 1; }
+// the workspace (groups of at least one warp for every 512 columns, at most 512
+// threads and eight groups a CTA).
+inline int join_max_groups(int64_t H) {
+  const int64_t warps = (H + 511) / 512;
+  return warps >= 16 ? 1 : (int)std::min<int64_t>(8, 16 / warps);
+}
 // Sorted tokens a tile of the table's gradient: few tokens take short tiles,
 // for the sake of their number.
 constexpr int kLookupMaxTile = 32;

@@ -202,6 +202,20 @@ def test_lookup_grad_refusals(lib):
     assert g(xd=BF16, wd=F16) == UNSUPPORTED
 
 
+@pytest.mark.parametrize("es,E", [(2, 16), (4, 8)])
+def test_row_groups_stay_within_the_workspace(es, E):
+    """The gradient's row groups a CTA (512 or 256 threads, whole warps for E
+    columns a thread, at most eight) against the bound the workspace is sized
+    by: transcriptions of both rules, every width."""
+    for H in range(1, 20000):
+        warps = (H + 511) // 512
+        bound = 1 if warps >= 16 else min(8, 16 // warps)
+        tpr = (H + 32 * E - 1) // (32 * E) * 32
+        for threads in (256, 512):
+            if tpr <= threads:
+                assert min(threads // tpr, 8) <= bound
+
+
 def test_host_tensors_are_refused():
     x, v = torch.zeros(4, 8), torch.ones(8)
     r = torch.ones(4)
