@@ -73,6 +73,14 @@ inline bool any_overlap(const Span (&a)[NA], const Span (&b)[NB]) {
   return false;
 }
 
+// Whether every pointer is a multiple of its element size (null is).
+template <size_t N>
+inline bool elements_aligned(const void* const (&p)[N], size_t es) {
+  for (const void* q : p)
+    if (reinterpret_cast<uintptr_t>(q) % es != 0) return false;
+  return true;
+}
+
 constexpr Span kNoSpan{0, 0};
 
 // Two row tensors may be the same buffer (same pointer and stride) or

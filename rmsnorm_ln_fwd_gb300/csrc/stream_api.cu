@@ -74,6 +74,9 @@ norm_status lookup_common(const void* table, int64_t ldt, int64_t V, const void*
   if (N == 0) return NORM_OK;
   if (table == nullptr || tokens == nullptr || h == nullptr || (norm && y == nullptr)) return NORM_ERR_INVALID_VALUE;
   const size_t es = elem_size(xd);
+  if (!elements_aligned({table, h, norm ? y : nullptr}, es) || !elements_aligned({gamma}, elem_size(wd)) ||
+      !elements_aligned({tokens}, index_size(itype)) || !elements_aligned({rstd}, 4))
+    return NORM_ERR_INVALID_VALUE;
   if (!ld_ok(ldt, V, H, es) || !ld_ok(ldh, N, H, es) || (norm && !ld_ok(ldy, N, H, es))) return NORM_ERR_INVALID_VALUE;
   {
     const Span in[] = {rows_span(table, V, ldt, H, es), vec_span(tokens, N, index_size(itype)),
@@ -129,6 +132,9 @@ norm_status sandwich_rms(const void* x, int64_t ldx, const void* residual, int64
   if (!gate_rows_ok(gate, gate_rows, ldgate, N, H, ges)) return NORM_ERR_INVALID_VALUE;
   if (N == 0) return NORM_OK;
   if (!x || !residual || !h_out || (pre && !y)) return NORM_ERR_INVALID_VALUE;
+  if (!elements_aligned({x, residual, h_out, y}, es) || !elements_aligned({gamma_post, gamma_pre}, wes) ||
+      !elements_aligned({gate}, ges) || !elements_aligned({rstd_post, rstd_pre}, 4))
+    return NORM_ERR_INVALID_VALUE;
   if (!ld_ok(ldx, N, H, es) || !ld_ok(ldr, N, H, es) || !ld_ok(ldh, N, H, es) || (pre && !ld_ok(ldy, N, H, es)))
     return NORM_ERR_INVALID_VALUE;
   if (!same_or_disjoint(h_out, ldh, x, ldx, N, H, es) || !same_or_disjoint(h_out, ldh, residual, ldr, N, H, es))
@@ -209,6 +215,7 @@ norm_status sandwich_rms_grad(const void* dy, int64_t lddy, const void* x, int64
                          dgate ? rows_span(dgate, gate_rows, lddgate, H, ges) : kNoSpan};
   if (overlap(pgrads[0], pgrads[1]) || overlap(pgrads[0], pgrads[2]) || overlap(pgrads[1], pgrads[2]))
     return NORM_ERR_INVALID_VALUE;
+  if (!elements_aligned({dgamma_post, dgamma_pre}, wes) || !elements_aligned({dgate}, ges)) return NORM_ERR_INVALID_VALUE;
   JoinGradArgs a{};
   a.dgpost = dgamma_post;
   a.dgate = dgate;
@@ -233,6 +240,9 @@ norm_status sandwich_rms_grad(const void* dy, int64_t lddy, const void* x, int64
     return launch(dev);
   }
   if (!x || !dx || !dres || (post && !rstd_post) || (pre && (!dy || !h || !rstd_pre)) || (!dy && !dh_in))
+    return NORM_ERR_INVALID_VALUE;
+  if (!elements_aligned({dy, x, h, dh_in, dx, dres}, es) || !elements_aligned({gamma_post, gamma_pre}, wes) ||
+      !elements_aligned({gate}, ges) || !elements_aligned({rstd_post, rstd_pre}, 4))
     return NORM_ERR_INVALID_VALUE;
   if (!ld_ok(ldx, N, H, es) || !ld_ok(lddx, N, H, es) || !ld_ok(lddres, N, H, es) ||
       (pre && (!ld_ok(lddy, N, H, es) || !ld_ok(ldh, N, H, es))) || (dh_in && !ld_ok(lddh_in, N, H, es)))
@@ -328,10 +338,12 @@ norm_status embedding_grad(const void* dh, int64_t lddh, const void* tokens, nor
       padding_idx >= V || dtable == nullptr)
     return NORM_ERR_INVALID_VALUE;
   const size_t es = elem_size(x_dtype), wes = elem_size(w_dtype);
-  if (!ld_ok(lddt, V, H, wes)) return NORM_ERR_INVALID_VALUE;
+  if (!ld_ok(lddt, V, H, wes) || !elements_aligned({dtable}, wes)) return NORM_ERR_INVALID_VALUE;
   LookupGradArgs a{};
   if (N > 0) {
-    if (dh == nullptr || tokens == nullptr || !ld_ok(lddh, N, H, es)) return NORM_ERR_INVALID_VALUE;
+    if (dh == nullptr || tokens == nullptr || !ld_ok(lddh, N, H, es) || !elements_aligned({dh}, es) ||
+        !elements_aligned({tokens}, index_size(token_type)))
+      return NORM_ERR_INVALID_VALUE;
     const Span in[] = {rows_span(dh, N, lddh, H, es), vec_span(tokens, N, index_size(token_type))};
     const Span out[] = {rows_span(dtable, V, lddt, H, wes)};
     if (any_overlap(in, out)) return NORM_ERR_INVALID_VALUE;

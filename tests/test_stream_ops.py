@@ -194,7 +194,7 @@ def test_lookup_grad_refusals(lib):
         a.update(kw)
         return lib.embedding_grad(*a.values())
     for kw in (dict(dh=None), dict(k=None), dict(dt=None), dict(V=0), dict(H=0), dict(N=-1), dict(pad=10),
-               dict(pad=-2), dict(scale=float("nan")), dict(lddh=63), dict(lddt=63), dict(dt=M), dict(dt=2 * M)):
+               dict(pad=-2), dict(scale=float("nan")), dict(dh=M + 1), dict(dt=3 * M + 1), dict(k=2 * M + 4), dict(lddh=63), dict(lddt=63), dict(dt=M), dict(dt=2 * M)):
         assert g(**kw) == INVALID, kw
     for kw in (dict(ws=None), dict(wsb=need - 1), dict(ws=4 * M + 8), dict(ws=M), dict(ws=3 * M)):
         assert g(**kw) == WORKSPACE, kw
@@ -214,6 +214,20 @@ def test_row_groups_stay_within_the_workspace(es, E):
         for threads in (256, 512):
             if tpr <= threads:
                 assert min(threads // tpr, 8) <= bound
+
+
+def test_pointers_between_elements_are_refused(lib):
+    E = 10 * M
+    for kw in (dict(x=M + 1), dict(r=2 * M + 1), dict(y=3 * M + 1), dict(h=4 * M + 1), dict(gpost=E + 1),
+               dict(gpre=E + 1), dict(gate=E + 1, B=1), dict(rpost=E + 2), dict(rpre=E + 2),
+               dict(gpre=E + 2, wd=F32), dict(gate=E + 2, B=1, gd=F32)):
+        assert _join(lib, **kw) == INVALID, kw
+    for kw in (dict(dy=M + 1), dict(x=2 * M + 1), dict(h=3 * M + 1), dict(rpost=4 * M + 2), dict(dh=6 * M + 1),
+               dict(dx=7 * M + 1), dict(dr=8 * M + 1), dict(dgpre=E + 1), dict(gate=E, B=1, dgate=11 * M + 1)):
+        assert _grad(lib, **kw) == INVALID, kw
+    for kw in (dict(t=M + 1), dict(k=2 * M + 4), dict(k=2 * M + 2, it=I32), dict(y=3 * M + 1), dict(h=4 * M + 1),
+               dict(g=5 * M + 1), dict(rstd=5 * M + 2)):
+        assert _look(lib, **kw) == INVALID, kw
 
 
 def test_host_tensors_are_refused():
