@@ -272,6 +272,9 @@ __global__ void __launch_bounds__(MAXT, MINB) join_grad_rows_kernel(const JoinGr
   join_unit_rows<RUNS>(a, unit, units, row, left, step);
   const int64_t first_row = row, end = row + left * step;  // (RUNS: step is 1)
 
+  if (a.early) pdl_launch_dependents();
+  pdl_wait_primary();
+
   // Copies: lane 8k + i of the group's first warp serves tensor k.
   const int ck = lane >> 3, ci = lane & 7;
   const T* next = nullptr;  // the tensor's next row to ask for
@@ -604,6 +607,7 @@ constexpr int kJoinReduceUnroll = 8;
 
 template <typename D, int RG>
 __global__ void __launch_bounds__(256) join_grad_reduce_kernel(const JoinGradArgs a, int by_boundary) {
+  if (a.early) pdl_launch_dependents();
   pdl_wait_primary();  // launched as a programmatic dependent of the main kernel
   const int what = blockIdx.y;
   const float* src;
@@ -756,32 +760,18 @@ static cudaError_t run_join_grad_rows(JoinGradArgs& a, const JoinRing& ring, con
   if (e != cudaSuccess) return e;
   const int threads = ring.rpc * ring.tpr;
   const int64_t cap = std::min<int64_t>(kJoinMaxPartialsPerSm * dev.sm_count, (a.N + ring.rpc - 1) / ring.rpc);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(CL * cap));
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = ring.total;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  if (CL > 1) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CL;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-  }
+  FirstLaunch first((unsigned)threads, ring.total, s, CL);
+  first.cfg.gridDim = dim3((unsigned)(CL * cap));
   const int resident = memo.resident(threads, ring.total, dev, [&](int* n) {
-    if (CL > 1) return cudaOccupancyMaxActiveClusters(n, kern, &cfg);
+    if (CL > 1) return cudaOccupancyMaxActiveClusters(n, kern, &first.cfg);
     const cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kern, threads, ring.total);
     *n *= dev.sm_count;
     return err;
   });
   a.P = (int)std::max<int64_t>(1, std::min<int64_t>(cap, resident));
   a.U = (int)std::min<int64_t>(a.N, (int64_t)a.P * ring.rpc);
-  cfg.gridDim = dim3((unsigned)(CL * a.P));
-  e = cudaLaunchKernelEx(&cfg, kern, a, ring);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  a.early = CL * a.P < dev.sm_count;
+  return first.launch((unsigned)(CL * a.P), a.early != 0, kern, a, ring);
 }
 
 // CTAs of at most MAXT threads, MINB an SM, in clusters of the fewest CTAs a row
@@ -866,6 +856,7 @@ cudaError_t launch_join_grad(JoinGradArgs a, const DeviceInfo& dev, cudaStream_t
   }
   if (!done) {
     a.P = a.U = (int)std::min<int64_t>(a.N, kJoinMaxPartialsPerSm * dev.sm_count);
+    a.early = 0;
     join_grad_loop_kernel<D><<<(unsigned)a.P, kJoinGradLoopThreads, 0, s>>>(a);
     e = cudaGetLastError();
   }

@@ -128,6 +128,20 @@ __global__ void __launch_bounds__(MAXT, MINB) join_rows_kernel(const JoinArgs a,
   const uint32_t slot32 = smem_u32(slot);
   const int bar_id = 1 + group;
 
+  if constexpr (CL > 1) {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&xbar[i], 1);
+        mbar_init(&xbar2[i], 1);
+      }
+      xabort = 0;
+      fence_barrier_init();
+    }
+    cluster_sync_all();  // every CTA's mbarriers exist before any CTA sends to them
+  }
+  pdl_launch_dependents();
+  pdl_wait_primary();
+
   // this group's rows: strided, or (several gate rows) one contiguous range
   const int64_t units = (int64_t)(gridDim.x / CL) * rpc, unit = (int64_t)(blockIdx.x / CL) * rpc + group;
   const bool runs = a.run < a.N;
@@ -179,17 +193,6 @@ __global__ void __launch_bounds__(MAXT, MINB) join_rows_kernel(const JoinArgs a,
     for (int e = 0; e < E; ++e) f[e] = 1.f;
     C::scale_by_param(at(a.gpre, c0, wes), w_f32, b, lim, f);
     put_params<E>(slot + E, f);
-  }
-  if constexpr (CL > 1) {
-    if (threadIdx.x == 0) {
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&xbar[i], 1);
-        mbar_init(&xbar2[i], 1);
-      }
-      xabort = 0;
-      fence_barrier_init();
-    }
-    cluster_sync_all();  // every CTA's mbarriers exist before any CTA sends to them
   }
 
   const float2 alpha2 = splat2(a.alpha);
@@ -282,30 +285,16 @@ static cudaError_t run_join_rows(const JoinArgs& a, int tpr, int rpc, const Devi
     if (e != cudaSuccess) return e;
   }
   const int64_t want = std::min<int64_t>((a.N + rpc - 1) / rpc, 1 << 20);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(CL * want));
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  if (CL > 1) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CL;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-  }
+  FirstLaunch first((unsigned)threads, smem, s, CL);
+  first.cfg.gridDim = dim3((unsigned)(CL * want));
   const int resident = memo.resident(threads, smem, dev, [&](int* n) {
-    if (CL > 1) return cudaOccupancyMaxActiveClusters(n, kern, &cfg);
+    if (CL > 1) return cudaOccupancyMaxActiveClusters(n, kern, &first.cfg);
     const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kern, threads, smem);
     *n *= dev.sm_count;
     return e;
   });
-  cfg.gridDim = dim3((unsigned)(CL * std::max<int64_t>(1, std::min<int64_t>(want, resident))));
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, tpr);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  const int64_t grid = CL * std::max<int64_t>(1, std::min<int64_t>(want, resident));
+  return first.launch((unsigned)grid, CL == 1 || grid < dev.sm_count, kern, a, tpr);
 }
 
 template <typename D, int GB>

@@ -95,6 +95,8 @@ __global__ void __launch_bounds__(MAXT, MINB) lookup_rows_kernel(const LookupArg
   auto fetch = [&](int64_t tok) {
     C::load(reinterpret_cast<const T*>(a.table) + (tok < 0 ? 0 : tok) * a.ldt + b, tok < 0 ? 0 : lim, nx);
   };
+  pdl_launch_dependents();
+  pdl_wait_primary();
   int64_t tok2 = -1;  // the next row's
   if (row < a.N) {
     fetch(token(row));
@@ -162,8 +164,8 @@ static cudaError_t run_lookup_rows(const LookupArgs& a, const DeviceInfo& dev, c
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kern, threads, smem);
   });
   const int64_t blocks = std::min<int64_t>((a.N + rpc - 1) / rpc, (int64_t)per_sm * dev.sm_count);
-  kern<<<(unsigned)blocks, threads, smem, s>>>(a, tpr);
-  return cudaGetLastError();
+  FirstLaunch first((unsigned)threads, smem, s, 1);
+  return first.launch((unsigned)blocks, true, kern, a, tpr);
 }
 
 // 32 bytes a thread up to 1024 threads, in fp32 64 bytes beyond.

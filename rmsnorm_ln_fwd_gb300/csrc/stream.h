@@ -78,6 +78,7 @@ struct JoinGradArgs {
   float alpha;
   int w_f32, g_f32;
   int P, U;  // partial rows; row units (U = P * row groups of a CTA)
+  int early;  // a small grid, which lets the kernels behind it come up at once
   unsigned* err;
 };
 

@@ -680,3 +680,53 @@ def test_expanded_and_permuted_tensors_are_refused():
 
 def test_device_words_of_the_far_kernels_stay_clear():
     assert _lib.device_errors() == 0
+
+
+@pytest.mark.parametrize("N,H", [(1, 256), (8, 4096), (700, 1024), (4000, 512), (300, 8192)])
+def test_calls_close_behind_one_another(N, H):
+    """Kernels start while the ones before them drain: what those wrote (rows,
+    parameters, the stream in place, the gradient's inputs) has to be seen, and
+    what they read not overwritten.  The same run with a wait after every call
+    gives the same bits."""
+    dt = torch.bfloat16
+    src = [rnd((N, H), i, dt) for i in range(3)]
+    table = rnd((64, H), 7, dt)
+    tokens = torch.from_numpy(make_tokens("skewed", N, 64)).to(DEV)
+
+    def go(wait):
+        def sync():
+            if wait:
+                torch.cuda.synchronize()
+        x, stream, out = src[0].clone(), src[1].clone(), torch.empty_like(src[0])
+        gamma, gate = torch.ones(H, device=DEV, dtype=dt), torch.full((H,), 0.5, device=DEV, dtype=dt)
+        seen = []
+        for i in range(40):
+            x.copy_(src[i % 3])
+            sync()
+            gamma.mul_(1.0 + 0.01 * (i % 5))
+            sync()
+            y, h, rp, rq = nl.sandwich_rms(x, stream, gamma, gate, gamma, residual_scale=0.5, h_out=stream, out=out)
+            sync()
+            y2, h2, _, _ = nl.sandwich_rms(y, h, gamma, gate, gamma, residual_scale=0.5)
+            sync()
+            dx, dr, a, b, c = nl.sandwich_rms_grad(y2, x, h, rp, rq, gamma, gate, gamma, h2, residual_scale=0.5)
+            sync()
+            x.zero_()
+            sync()
+            e, eh, _ = nl.embedding_rms(tokens, table, gamma)
+            sync()
+            t = nl.embedding_grad(dr, tokens, 64)
+            sync()
+            table.copy_(t)
+            sync()
+            gamma.copy_(torch.ones_like(gamma))
+            sync()
+            seen += [y.clone(), h.clone(), y2, dx, dr, a, b, c, e, eh, t]
+        torch.cuda.synchronize()
+        return seen
+
+    keep = table.clone()
+    want = go(True)
+    for _ in range(2):
+        table.copy_(keep)
+        assert all(torch.equal(a, b) for a, b in zip(want, go(False)))
