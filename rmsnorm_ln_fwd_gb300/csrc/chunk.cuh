@@ -197,7 +197,7 @@ struct GranuleRule {
 // Launch configuration of a call's first kernel: clusters of `cl` CTAs, and,
 // with `early`, programmatic stream serialization, so that its CTAs come up while
 // the kernel before it drains (one after another, 8192x1024 bf16 sandwich_rms
-// 18.3 -> 15.6 us a call).  Such a kernel reads and writes no global memory
+// 18.4 -> 15.9 us a call).  Such a kernel reads and writes no global memory
 // before pdl_wait_primary(), after which the kernels before it are through, and
 // every CTA passes it, so that a kernel that waits for this one has waited for
 // those too.  Not for large persistent grids of clusters: brought up one by one

@@ -63,14 +63,14 @@ __global__ void __launch_bounds__(kLookupLoopThreads) lookup_loop_kernel(const L
   }
 }
 
-// Register rows.  A row group of tpr threads, E columns a thread (chunk.cuh),
-// walks rows row, row + stride, ...: the next row's columns are in flight while
-// this one is scaled, reduced and written, and the token of the row after that,
-// whose address they would otherwise wait for.
 // Floats of the row sums' scratch in front of the parameter slots, which need
 // 16-byte alignment.
 __host__ __device__ inline int lookup_red_floats(int rpc, int tpr) { return (rpc * 2 * (tpr / 32) + 3) & ~3; }
 
+// Register rows.  A row group of tpr threads, E columns a thread (chunk.cuh),
+// walks rows row, row + stride, ...: the next row's columns are in flight while
+// this one is scaled, reduced and written, and the token of the row after that,
+// whose address they would otherwise wait for.
 template <typename D, int GB, int E_, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) lookup_rows_kernel(const LookupArgs a, const int tpr) {
   using C = Chunk<D, GB, E_>;
@@ -368,7 +368,9 @@ __device__ __forceinline__ void sort_tokens(const LookupGradArgs& a, SortPlan pl
   }
 }
 
-// Kernel 1.
+// Kernel 1.  Launched without programmatic serialization: the clearing CTAs
+// behind it write the table before they wait, so all that came before the call
+// has to be through when this kernel starts.
 static __global__ void __launch_bounds__(kSortThreads) lookup_grad_sort_kernel(const LookupGradArgs a, const SortPlan plan) {
   extern __shared__ __align__(16) int smem_sort[];
   pdl_launch_dependents();

@@ -213,7 +213,7 @@ def test_join_strides_and_margins(N, H, ld, off, dt):
     p = {k: padded(c[k], ld, off)[0] for k in ("x", "res", "dy", "dh")}
     bufs = {k: padded(torch.zeros_like(c["x"]), ld, off) for k in ("y", "h", "dx", "dr")}
     # a gate that is a column slice of a wider tensor
-    wide = torch.full((1, 3 * H), 5.0, dtype=DT[dt], device=DEV)
+    wide = torch.full((1, 2 * H + 64), 5.0, dtype=DT[dt], device=DEV)
     wide[:, H:2 * H] = c["gate"]
     gate = wide[:, H:2 * H]
     y, h, rpost, rpre = nl.sandwich_rms(p["x"], p["res"], c["gpost"], gate, c["gpre"], 1e-5, residual_scale=0.75,
