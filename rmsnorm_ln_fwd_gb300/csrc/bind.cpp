@@ -59,8 +59,8 @@ struct Rows {
   int64_t N = 0, H = 0, ld = 0;
 };
 
-Rows rows(const Tensor& t, const char* what) {
-  cuda_tensor(t, what);
+// The rows of a tensor on any device.
+Rows row_view(const Tensor& t, const char* what) {
   const int64_t d = t.dim();
   if (d < 1) value_error(std::string(what) + " must have at least one dim");
   Rows r;
@@ -68,22 +68,30 @@ Rows rows(const Tensor& t, const char* what) {
   r.H = t.size(d - 1);
   if (r.H > 1 && t.stride(d - 1) != 1) value_error(std::string(what) + ": the last dim must be contiguous");
   r.N = 1;
-  int64_t ld = 0, reach = 0;  // the row stride; what the next outer dim's stride has to be
+  // The innermost dim of several rows gives the row stride; every dim outside
+  // it has to start where the ones inside end (`reach`).  An expanded dim has
+  // stride 0 and counts like any other: beside a dim with another stride it does
+  // not flatten, and a row stride of 0 is refused by the library.
+  bool seen = false, flat = true;
+  int64_t ld = 0, reach = 0;
   for (int64_t i = d - 2; i >= 0; --i) {
     const int64_t n = t.size(i);
     r.N *= n;
     if (n <= 1) continue;
-    if (ld == 0) {
+    if (!seen) {
+      seen = true;
       ld = reach = t.stride(i);
     } else if (t.stride(i) != reach) {
-      reach = -1;
+      flat = false;
     }
-    if (reach >= 0) reach *= n;
+    reach *= n;
   }
-  if (r.N > 1 && reach < 0) value_error(std::string(what) + ": leading dims do not flatten to one row stride");
+  if (r.N > 1 && !flat) value_error(std::string(what) + ": leading dims do not flatten to one row stride");
   r.ld = r.N > 1 ? ld : std::max<int64_t>(r.H, 1);
   return r;
 }
+
+Rows rows(const Tensor& t, const char* what) { return row_view(cuda_tensor(t, what), what); }
 
 // A tensor that matches the rows of `ref`.
 Rows like(const Tensor& t, const Tensor& ref, const Rows& of, const char* what) {
@@ -340,6 +348,10 @@ py::object embedding_grad_(const Tensor& dh, const Tensor& tokens, int64_t num_r
 }  // namespace
 
 PYBIND11_MODULE(_bind, m) {
+  m.def("row_view", [](const Tensor& t) {  // (N, H, ld) of a tensor on any device, for tests
+    const Rows r = row_view(t, "t");
+    return py::make_tuple(r.N, r.H, r.ld);
+  });
   m.def("sandwich_rms", &sandwich_rms_);
   m.def("sandwich_rms_grad", &sandwich_rms_grad_);
   m.def("embedding_lookup", &embedding_lookup_);

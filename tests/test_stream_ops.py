@@ -332,3 +332,42 @@ def test_tile_partials_cover_every_token_once(tokens):
         done[v] = got
     assert sorted(used) == sorted(partial)
     assert done == {v: [i for i, w in enumerate(tokens) if w == v] for v in set(tokens)}
+
+
+# ------------------------------------------------------------------ the binding's row views
+
+def _row_view(t):
+    _build.build()
+    return _lib.bind().row_view(t)
+
+
+@pytest.mark.parametrize("shape,strides", [((5, 8), (8, 1)), ((5, 8), (11, 1)), ((2, 3, 8), (24, 8, 1)),
+                                           ((2, 3, 8), (30, 10, 1)), ((2, 1, 3, 8), (24, 7, 8, 1)), ((1, 8), (0, 1)),
+                                           ((4, 1, 8), (9, 0, 1)), ((1, 3, 8), (0, 8, 1)), ((3, 1), (5, 77)),
+                                           ((2, 3, 4, 8), (120, 40, 10, 1)), ((8,), (1,))])
+def test_row_views(shape, strides):
+    """Row r of the view is the r-th row of the tensor, in order."""
+    t = torch.arange(1000.0).as_strided(shape, strides)
+    N, H, ld = _row_view(t)
+    assert torch.equal(torch.arange(1000.0).as_strided((N, H), (ld, 1)), t.reshape(N, H))
+
+
+@pytest.mark.parametrize("shape,strides", [
+    ((4, 6, 8), (8, 0, 1)),        # a row for each sequence, over its tokens: the gradient of y.sum(1)
+    ((4, 6, 8), (0, 8, 1)),        # over the sequences
+    ((4, 3, 6, 8), (24, 8, 0, 1)), ((4, 3, 6, 8), (8, 0, 0, 1)), ((4, 3, 6, 8), (8, 0, 8, 1)), ((4, 3, 6, 8), (0, 8, 0, 1)),
+    ((4, 1, 6, 8), (8, 8, 0, 1)), ((4, 6, 1, 8), (8, 0, 8, 1)),
+    ((4, 6, 8), (8, 32, 1)), ((4, 6, 8), (50, 8, 1)), ((4, 6, 8), (48, 8, 2)), ((4, 6, 8), (1, 8, 1))])
+def test_row_views_that_do_not_flatten(shape, strides):
+    with pytest.raises(ValueError, match="flatten|contiguous"):
+        _row_view(torch.zeros(2000).as_strided(shape, strides))
+
+
+@pytest.mark.parametrize("shape", [(6, 8), (4, 6, 8), (2, 3, 6, 8)])
+def test_row_views_of_one_expanded_row(shape, lib):
+    """One row for all: a row stride of 0, which the library refuses."""
+    t = torch.zeros(8).expand(shape)
+    N, H, ld = _row_view(t)
+    assert ld == 0 and N * H == t.numel()
+    assert _join(lib, N=N, H=H, ldx=ld) == _join(lib, N=N, H=H, ldr=ld) == _join(lib, N=N, H=H, ldh=ld) == INVALID
+    assert _grad(lib, N=N, H=H, lddy=ld) == _grad(lib, N=N, H=H, lddh=ld) == _grad(lib, N=N, H=H, lddx=ld) == INVALID

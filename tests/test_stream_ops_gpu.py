@@ -730,3 +730,53 @@ def test_calls_close_behind_one_another(N, H):
     for _ in range(2):
         table.copy_(keep)
         assert all(torch.equal(a, b) for a, b in zip(want, go(False)))
+
+
+def _expanded(B, T, H, dt):
+    """(B, T, H) tensors over fewer rows: a row a sequence, the rows of one
+    sequence, one row."""
+    t = torch.zeros((B, T, H), device=DEV, dtype=dt)
+    return [t[:, :1].expand(B, T, H), t[:1].expand(B, T, H), t[:1, :1].expand(B, T, H)]
+
+
+def test_expanded_rows_of_more_dims_are_refused():
+    """Every row tensor of every call, before anything is launched (the views
+    themselves are checked on the CPU)."""
+    B, T, H, V = 4, 6, 64, 10
+    x = torch.zeros((B, T, H), device=DEV, dtype=torch.bfloat16)
+    r = torch.ones(B * T, device=DEV)
+    tok = torch.zeros((B, T), device=DEV, dtype=torch.int64)
+    table = torch.zeros((V, H), device=DEV, dtype=torch.bfloat16)
+    grad = dict(dy=x, x=x, h=x, rstd_post=r, rstd_pre=r, dh_in=x)
+    for e in _expanded(B, T, H, torch.bfloat16):
+        calls = [lambda: nl.sandwich_rms(e, x), lambda: nl.sandwich_rms(x, e), lambda: nl.sandwich_rms(x, x, gate=e),
+                 lambda: nl.sandwich_rms(x, x, h_out=e), lambda: nl.sandwich_rms(x, x, out=e),
+                 lambda: nl.embedding_lookup(tok, table, out=e), lambda: nl.embedding_rms(tok, table, h_out=e),
+                 lambda: nl.embedding_rms(tok, table, out=e), lambda: nl.embedding_grad(e, tok, V)]
+        calls += [lambda k=k: nl.sandwich_rms_grad(**{**grad, k: e}) for k in ("dy", "x", "h", "dh_in")]
+        calls += [lambda k=k: nl.sandwich_rms_grad(**grad, **{k: e}) for k in ("gate", "dx", "dres")]
+        for i, call in enumerate(calls):
+            with pytest.raises((ValueError, nl.NormError)):
+                call()
+                raise AssertionError(i)
+
+
+def test_the_gradient_of_a_sum_over_tokens():
+    """y.sum(1) with a factor a sequence sends back a row a sequence, expanded
+    over its tokens: refused as it is, taken after contiguous()."""
+    B, T, H = 4, 6, 64
+    c = join_inputs(B * T, H, torch.float32, torch.float32, 1)
+    y = torch.zeros((B, T, H), device=DEV, requires_grad=True)
+    dy, = torch.autograd.grad((y.sum(1) * rnd((B, H), 3, torch.float32)).sum(), y)
+    assert dy.stride() == (H, 0, 1)
+    rpost, rpre = (torch.from_numpy(S._rstd(n64(c[k]), 1e-5)).float().to(DEV) for k in ("x", "res"))
+
+    def call(dy):
+        return nl.sandwich_rms_grad(dy, c["x"], c["res"], rpost, rpre, c["gpost"], c["gate"], c["gpre"], c["dh"],
+                                    residual_scale=0.75)
+    with pytest.raises(ValueError, match="flatten"):
+        call(dy)
+    with pytest.raises(ValueError, match="flatten"):
+        nl.embedding_grad(dy, torch.zeros((B, T), device=DEV, dtype=torch.int64), 3)
+    c["dy"] = dy.contiguous().view(B * T, H)
+    check_join_grad(c, call(dy.contiguous()), rpost, rpre, 0.75)
