@@ -489,6 +489,11 @@ __global__ void __launch_bounds__(MAXT, MINB) join_grad_rows_kernel(const JoinGr
           if ((lane & 7) + 8 * i < nw) part += from[(lane & 7) + 8 * i];
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+      } else {
+        // one warp: what the barrier orders besides the sums, its lanes' reads of
+        // this buffer before the refill and the end elements put into the others
+        // before their reads (shuffles order no memory)
+        __syncwarp();
       }
 #pragma unroll
       for (int k = 0; k < 3; ++k) s[k] = __shfl_sync(0xffffffffu, part, 8 * k);

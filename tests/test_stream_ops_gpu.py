@@ -780,3 +780,18 @@ def test_the_gradient_of_a_sum_over_tokens():
         nl.embedding_grad(dy, torch.zeros((B, T), device=DEV, dtype=torch.int64), 3)
     c["dy"] = dy.contiguous().view(B * T, H)
     check_join_grad(c, call(dy.contiguous()), rpost, rpre, 0.75)
+
+
+@pytest.mark.parametrize("gates", [0, 1])
+@pytest.mark.parametrize("N,H,dt", [(24000, 96, "bf16"), (24000, 97, "f16"), (24000, 130, "f32"), (24001, 61, "f32"),
+                                    (8000, 513, "f16"), (3000, 2057, "f16"), (2000, 4096, "bf16"), (1000, 5121, "f16"),
+                                    (700, 4097, "f32"), (500, 16384, "bf16")])
+def test_join_grad_refills_its_buffers(N, H, dt, gates):
+    """Six rows and more a row group, which has at most four buffers: rows of
+    one warp and of several, aligned and not (whose ends are loaded early and
+    stored a row later), in one CTA and in clusters."""
+    c = join_inputs(N, H, DT[dt], DT[dt], gates, seed=N + gates)
+    out, rpost, rpre = run_join_grad(c, True, True)
+    check_join_grad(c, out, rpost, rpre, 0.75)
+    again, _, _ = run_join_grad(c, True, True)
+    assert all(torch.equal(a, b) for a, b in zip(out, again) if a is not None)
