@@ -360,8 +360,8 @@ norm_status embedding_rms(const void* table, int64_t ldt, int64_t V, const void*
                           norm_stream_t stream);
 
 /*
- * Bytes of device workspace embedding_grad needs for N tokens of H columns.
- * Returns 0 if an argument is out of range.
+ * Bytes of device workspace embedding_grad needs for up to N tokens of H columns
+ * (never fewer for more tokens).  Returns 0 if an argument is out of range.
  */
 size_t embedding_grad_workspace_bytes(int64_t N, int64_t H);
 
@@ -375,8 +375,8 @@ size_t embedding_grad_workspace_bytes(int64_t N, int64_t H);
  *   dtype or NORM_F32), clear of the inputs.
  * padding_idx: a token that has no gradient, or -1.  Tokens outside [0, V) are
  *   left out and raise NORM_DEVICE_ERR_BAD_TOKEN.
- * workspace: embedding_grad_workspace_bytes(N, H) bytes, 16-byte aligned;
- *   calls that share it must be ordered.
+ * workspace: embedding_grad_workspace_bytes(N, H) bytes (or those of a larger
+ *   N), 16-byte aligned; calls that share it must be ordered.
  */
 norm_status embedding_grad(const void* dh, int64_t lddh, const void* tokens, norm_itype token_type, void* dtable,
                            int64_t lddt, int64_t V, void* workspace, size_t workspace_bytes, int64_t N, int64_t H,

@@ -143,6 +143,12 @@ inline int join_max_groups(int64_t H) {
 // for the sake of their number.
 constexpr int kLookupMaxTile = 32;
 inline int lookup_tile(int64_t N) { return N <= 4096 ? 8 : N <= 8192 ? 16 : kLookupMaxTile; }
+// The most tiles any batch of up to N tokens has: the tiles of N, but from 4096
+// tokens on not fewer than the 512 that 4096 (of eight) and 8192 (of 16) have.
+inline int64_t lookup_max_tiles(int64_t N) {
+  const int64_t tiles = (N + lookup_tile(N) - 1) / lookup_tile(N);
+  return N >= 4096 ? std::max<int64_t>(tiles, 512) : tiles;
+}
 
 // Device error bit of a token id outside the table.
 constexpr unsigned kErrBadToken = 4u;

@@ -52,12 +52,12 @@ size_t join_workspace(int64_t H, int64_t gate_rows, const DeviceInfo& dev) {
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-int64_t lookup_tiles(int64_t N) { return (N + normk::lookup_tile(N) - 1) / normk::lookup_tile(N); }
-
-// Two buffers of sorted pairs, the list of crossing ids, the tiles' partial rows.
+// Two buffers of sorted pairs, the list of crossing ids, the tiles' partial
+// rows: room for the tiles of any batch of up to N tokens.
 size_t lookup_workspace(int64_t N, int64_t H) {
-  return 2 * align256((size_t)N * sizeof(uint2)) + align256((size_t)(1 + lookup_tiles(N)) * sizeof(int2)) +
-         (size_t)2 * lookup_tiles(N) * normk::bwd_partial_stride((int)H) * sizeof(float);
+  const int64_t tiles = normk::lookup_max_tiles(N);
+  return 2 * align256((size_t)N * sizeof(uint2)) + align256((size_t)(1 + tiles) * sizeof(int2)) +
+         (size_t)2 * tiles * normk::bwd_partial_stride((int)H) * sizeof(float);
 }
 
 size_t index_size(norm_itype t) { return t == NORM_I64 ? 8 : 4; }
@@ -357,7 +357,7 @@ norm_status embedding_grad(const void* dh, int64_t lddh, const void* tokens, nor
     a.sorted = reinterpret_cast<uint2*>(w);
     a.other = reinterpret_cast<uint2*>(w + pairs);
     a.owners = reinterpret_cast<int2*>(w + 2 * pairs);
-    a.partial = reinterpret_cast<float*>(w + 2 * pairs + align256((size_t)(1 + lookup_tiles(N)) * sizeof(int2)));
+    a.partial = reinterpret_cast<float*>(w + 2 * pairs + align256((size_t)(1 + normk::lookup_max_tiles(N)) * sizeof(int2)));
   }
   DeviceInfo dev;
   if (!current_device_info(&dev)) return NORM_ERR_CUDA;

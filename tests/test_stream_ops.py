@@ -371,3 +371,16 @@ def test_row_views_of_one_expanded_row(shape, lib):
     assert ld == 0 and N * H == t.numel()
     assert _join(lib, N=N, H=H, ldx=ld) == _join(lib, N=N, H=H, ldr=ld) == _join(lib, N=N, H=H, ldh=ld) == INVALID
     assert _grad(lib, N=N, H=H, lddy=ld) == _grad(lib, N=N, H=H, lddh=ld) == _grad(lib, N=N, H=H, lddx=ld) == INVALID
+
+
+@pytest.mark.parametrize("H", [1, 64, 4096])
+def test_lookup_grad_workspace_grows_with_the_tokens(lib, H):
+    """A workspace for a batch serves every smaller one: short tiles for few
+    tokens must not ask for more than long tiles for many."""
+    sizes = [lib.embedding_grad_workspace_bytes(n, H)
+             for n in [0, 1, 7, 8, 9, *range(4080, 4120), 6000, *range(8180, 8210), 16384, 16385, 20000, 1 << 20]]
+    assert sizes == sorted(sizes)
+    # what a call needs at least: two buffers of pairs, and two partial rows and an owner a tile
+    for n, tile in ((4096, 8), (4097, 16), (8192, 16), (8193, 32), (100000, 32)):
+        tiles = -(-n // tile)
+        assert lib.embedding_grad_workspace_bytes(n, H) >= 16 * n + 8 * (1 + tiles) + 8 * tiles * H

@@ -795,3 +795,13 @@ def test_join_grad_refills_its_buffers(N, H, dt, gates):
     check_join_grad(c, out, rpost, rpre, 0.75)
     again, _, _ = run_join_grad(c, True, True)
     assert all(torch.equal(a, b) for a, b in zip(out, again) if a is not None)
+
+
+def test_lookup_grad_one_workspace_for_smaller_batches():
+    H, V = 72, 400
+    ws = torch.empty(_lib.load().embedding_grad_workspace_bytes(10000, H), device=DEV, dtype=torch.uint8)
+    dh = rnd((10000, H), 1, torch.bfloat16)
+    for n in (10000, 8193, 8192, 8000, 4097, 4096, 33, 1):
+        tok = torch.from_numpy(make_tokens("skewed", n, V)).to(DEV)
+        out = nl.embedding_grad(dh[:n], tok, V, workspace=ws)
+        assert torch.equal(out, nl.embedding_grad(dh[:n], tok, V))
