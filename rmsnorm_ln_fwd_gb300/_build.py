@@ -14,6 +14,7 @@ from __future__ import annotations
 import glob
 import os
 import platform
+import re
 import shutil
 import subprocess
 import sysconfig
@@ -80,18 +81,20 @@ def _bind_inputs():
     return [BIND_SRC, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
-def _bind_stamp():
-    return os.path.join(BUILD_DIR, "bind.torch")
+def bind_torch():
+    """The PyTorch version _bind.so was compiled for, read from the file (to load
+    it beside another one is undefined); None without one."""
+    try:
+        with open(BIND, "rb") as f:
+            m = re.search(rb"norm_bind_torch=([^\0]+)\0", f.read())
+    except OSError:
+        return None
+    return m.group(1).decode() if m else None
 
 
 def bind_up_to_date() -> bool:
     import torch
-    try:
-        with open(_bind_stamp()) as f:
-            built_for = f.read()
-    except OSError:
-        return False
-    return built_for == torch.__version__ and _fresh(BIND, _bind_inputs())
+    return bind_torch() == str(torch.__version__) and _fresh(BIND, _bind_inputs())
 
 
 def _compile_bind() -> str:
@@ -102,7 +105,7 @@ def _compile_bind() -> str:
                os.path.join(cuda, "include"), "/usr/local/cuda/include", sysconfig.get_paths()["include"]]
     obj = os.path.join(BUILD_DIR, "bind.cpp.o")
     cmd = [os.environ.get("CXX", "g++"), "-c", BIND_SRC, "-o", obj, "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE,
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DNORM_BIND_TORCH="{torch.__version__}"']
     for i in include:
         cmd += ["-isystem", i]
     p = subprocess.run(cmd, capture_output=True, text=True)
@@ -121,8 +124,6 @@ def _link_bind(obj: str) -> None:
     if p.returncode != 0:
         raise RuntimeError(f"link of the Python binding failed:\n{p.stdout}\n{p.stderr}")
     os.replace(tmp, BIND)
-    with open(_bind_stamp(), "w") as f:
-        f.write(torch.__version__)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:

@@ -107,11 +107,20 @@ def load() -> ctypes.CDLL:
 
 def bind():
     """The C++ binding of the residual-stream operators (_bind.so), which links
-    to libnorm.so; raise if either is missing."""
+    to libnorm.so; raise if either is missing, or if it was built for another
+    PyTorch than the installed one."""
     global _bind
     if _bind is None:
         load()
         import importlib
+
+        import torch
+
+        from . import _build
+        built_for = _build.bind_torch()
+        if built_for is not None and built_for != str(torch.__version__):
+            raise RuntimeError(f"_bind.so was built for PyTorch {built_for}, not for {torch.__version__}; build it again "
+                               "with `python -c 'import __graft_entry__ as g; g.build()'`")
         try:
             _bind = importlib.import_module(__package__ + "._bind")
         except ImportError as e:

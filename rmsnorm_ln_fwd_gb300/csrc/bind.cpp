@@ -347,6 +347,10 @@ py::object embedding_grad_(const Tensor& dh, const Tensor& tokens, int64_t num_r
 
 }  // namespace
 
+// The PyTorch this is compiled against, found in the file before it is loaded.
+extern "C" __attribute__((used)) const char norm_bind_torch[];
+const char norm_bind_torch[] = "norm_bind_torch=" NORM_BIND_TORCH;
+
 PYBIND11_MODULE(_bind, m) {
   m.def("row_view", [](const Tensor& t) {  // (N, H, ld) of a tensor on any device, for tests
     const Rows r = row_view(t, "t");

@@ -384,3 +384,18 @@ def test_lookup_grad_workspace_grows_with_the_tokens(lib, H):
     for n, tile in ((4096, 8), (4097, 16), (8192, 16), (8193, 32), (100000, 32)):
         tiles = -(-n // tile)
         assert lib.embedding_grad_workspace_bytes(n, H) >= 16 * n + 8 * (1 + tiles) + 8 * tiles * H
+
+
+def test_a_binding_for_another_pytorch_is_not_loaded(tmp_path, monkeypatch):
+    _build.build()
+    with open(_build.BIND, "rb") as f:
+        built = f.read()
+    mark = b"norm_bind_torch=" + torch.__version__.encode()
+    assert built.count(mark) == 1 and _build.bind_torch() == torch.__version__ and _build.bind_up_to_date()
+    other = tmp_path / "_bind.so"
+    other.write_bytes(built.replace(mark, mark[:-1] + b"?"))
+    monkeypatch.setattr(_build, "BIND", str(other))
+    monkeypatch.setattr(_lib, "_bind", None)
+    assert not _build.bind_up_to_date()
+    with pytest.raises(RuntimeError, match="built for PyTorch"):
+        _lib.bind()
