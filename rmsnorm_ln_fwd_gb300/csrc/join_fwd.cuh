@@ -20,6 +20,7 @@
 namespace normk {
 
 constexpr int kJoinLoopThreads = 256;
+constexpr float kJoinLeastEps = 1e-18f;  // (1.4e-45 / eps: 1.4e-27, under 2^-29 of eps)
 // Columns a thread of the register rows: 32 bytes.
 template <typename D>
 constexpr int kJoinCols = 32 / (int)sizeof(typename D::T);
@@ -94,7 +95,9 @@ __global__ void __launch_bounds__(kJoinLoopThreads) join_loop_kernel(const JoinA
 // so the three sums meet in the same exchange as sum(x^2).  Where the terms
 // cancel (sum(h^2) under a quarter of them) or overflow, the row takes a second
 // exchange over h itself; every thread holds the same sums, so the branch is
-// uniform.
+// uniform.  So do all rows with an eps under kJoinLeastEps: squares of w*x that
+// underflow (2^-149 = 1.4e-45 an element) stand for up to 1.4e-45 / eps of
+// mean(h^2), which is nothing beside eps only above it.
 //
 // CL > 1: a cluster of CL CTAs shares each row, in parts of equal whole granules
 // (the last one or two may be shorter or empty).
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(MAXT, MINB) join_rows_kernel(const JoinArgs a,
     if (!a.pre) continue;
     const float terms = fmaf(rp * rp, s[3], s[1]);
     float ss = fmaf(2.f * rp, s[2], terms);
-    if (!(ss < __int_as_float(0x7f800000)) || 4.f * ss < terms) {
+    if (a.eps < kJoinLeastEps || !(ss < __int_as_float(0x7f800000)) || 4.f * ss < terms) {
       float2 h2 = splat2(0.f);
 #pragma unroll
       for (int p = 0; p < NP; ++p) h2 = fma2(f[p], f[p], h2);

@@ -805,3 +805,15 @@ def test_lookup_grad_one_workspace_for_smaller_batches():
         tok = torch.from_numpy(make_tokens("skewed", n, V)).to(DEV)
         out = nl.embedding_grad(dh[:n], tok, V, workspace=ws)
         assert torch.equal(out, nl.embedding_grad(dh[:n], tok, V))
+
+
+@pytest.mark.parametrize("H", [64, 1001, 5120])
+def test_join_tiny_eps(H):
+    """A block output whose squares underflow but whose norm does not: with
+    eps = 1e-30 values of 1e-23 become 1e-8, whose squares count against eps."""
+    x = torch.full((3, H), 1e-23, device=DEV)
+    x[1] *= torch.sign(rnd((H,), 1, torch.float32))
+    c = dict(x=x, res=torch.zeros_like(x), gpost=rnd((H,), 2, torch.float32, 1.0, 0.1), gate=None,
+             gpre=rnd((H,), 3, torch.float32, 1.0, 0.1))
+    out = nl.sandwich_rms(x, c["res"], c["gpost"], None, c["gpre"], 1e-30)
+    check_join(c, out, 1e-30, 1.0, True, True)
