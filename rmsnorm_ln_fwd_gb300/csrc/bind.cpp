@@ -142,12 +142,14 @@ Gate gate_view(const Opt& t, const Rows& of, const Tensor& ref) {
   const Rows r = rows(*t, "gate");
   if (r.H != of.H || t->device() != ref.device())
     value_error("gate must have " + std::to_string(of.H) + " columns on " + ref.device().str());
-  if (r.N < 1 || of.N % r.N != 0 || (of.N > 0 && r.N > of.N))
+  const bool none = r.N == 0 && of.N == 0;  // no sequences: no gate rows, and nothing reads one
+  if (!none && (r.N < 1 || of.N % r.N != 0 || (of.N > 0 && r.N > of.N)))
     value_error("gate has " + std::to_string(r.N) + " rows, which do not divide the " + std::to_string(of.N) +
                 " rows into equal runs");
   const norm_dtype c = code(t->scalar_type(), "gate");
   if (c != g.dt && c != NORM_F32)
     type_error("gate: dtype " + name_of(t->scalar_type()) + " must be the rows' or float32");
+  if (none) return g;
   g.p = r.p;
   g.rows = r.N;
   g.ld = r.ld;

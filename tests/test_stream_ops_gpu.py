@@ -817,3 +817,18 @@ def test_join_tiny_eps(H):
              gpre=rnd((H,), 3, torch.float32, 1.0, 0.1))
     out = nl.sandwich_rms(x, c["res"], c["gpost"], None, c["gpre"], 1e-30)
     check_join(c, out, 1e-30, 1.0, True, True)
+
+
+def test_join_gates_of_an_empty_batch():
+    """No sequences: no gate rows either, and gradients of those shapes."""
+    x = torch.empty((0, 5, 64), device=DEV, dtype=torch.bfloat16)
+    r = torch.empty((0, 5), device=DEV)
+    gate = torch.empty((0, 1, 64), device=DEV, dtype=torch.bfloat16)
+    y, h, a, b = nl.sandwich_rms(x, x, None, gate)
+    assert y.shape == h.shape == x.shape and a.numel() == b.numel() == 0
+    dx, dr, dp, dg, dn = nl.sandwich_rms_grad(x, x, x, r, r, None, gate)
+    assert dx.shape == dr.shape == x.shape and dg.shape == gate.shape
+    assert dp.shape == dn.shape == (64,) and not dp.any() and not dn.any()
+    some = torch.zeros((5, 64), device=DEV, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="divide"):
+        nl.sandwich_rms(some, some, None, gate)
