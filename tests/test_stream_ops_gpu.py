@@ -832,3 +832,113 @@ def test_join_gates_of_an_empty_batch():
     some = torch.zeros((5, 64), device=DEV, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="divide"):
         nl.sandwich_rms(some, some, None, gate)
+
+
+@pytest.mark.parametrize("N,H,dt", [(30000, 64, "bf16"), (30000, 65, "f16"), (30001, 24, "f32"), (4000, 1001, "f32"),
+                                    (4000, 4096, "bf16"), (2500, 2057, "f16"), (1000, 16384, "bf16")])
+def test_lookup_several_rows_a_group(N, H, dt):
+    """Three rows and more a row group: the row and the token after the one at
+    work are asked for ahead, bad tokens among them."""
+    V = 300
+    table = rnd((V, H), H, DT[dt])
+    gamma = rnd((H,), 2, DT[dt], 1.0, 0.1)
+    tokens = make_tokens("skewed", N, V)
+    tokens[::97] = V
+    tokens[5::1009] = -1
+    tok = torch.from_numpy(tokens).to(DEV)
+    y, h, rstd = nl.embedding_rms(tok, table, gamma, 1e-5, 1.5)
+    only = nl.embedding_lookup(tok.int(), table, 1.5)
+    torch.cuda.synchronize()
+    assert torch.equal(only, h) and _lib.device_errors() == _lib.NORM_DEVICE_ERR_BAD_TOKEN
+    # a row depends on its token alone: the oracle's row of each token, and zeros
+    ry, rh, rr = S.lookup_forward(list(range(V)) + [V], n64(table), 1.5, n64(gamma), 1e-5)
+    row = np.where((tokens < 0) | (tokens >= V), V, tokens)
+    k = steps(H) * U
+    close(h, rh[row], U * np.abs(rh[row]), "h")
+    close(rstd, rr[row], k * rr[row], "rstd")
+    close(y, ry[row], 2 * k * np.abs(ry[row]), "y")
+
+
+@pytest.mark.parametrize("kind", KINDS + ["bad"])
+@pytest.mark.parametrize("N,H,V,dt,odt,ld,it,off", [
+    (40, 1040, 20000, "bf16", "bf16", 1040, torch.int64, 0), (600, 1040, 3000, "bf16", "bf16", 1040, torch.int64, 0),
+    (601, 1040, 3000, "f16", "f16", 1048, torch.int32, 1), (333, 1041, 2000, "bf16", "bf16", 1041, torch.int64, 1),
+    (500, 520, 4000, "f16", "f32", 523, torch.int32, 3), (300, 5000, 200, "f32", "f32", 5000, torch.int64, 0),
+    (4, 1024, 700, "bf16", "f32", 1024, torch.int32, 0)])
+def test_lookup_grad_marked_clearing(kind, N, H, V, dt, odt, ld, it, off):
+    """Few tokens, rows of 2 KB and more: the rows that no token names are
+    cleared beside the sums, by marks made from the tokens. The table's rows are
+    aligned, padded or shifted, the tokens 16-byte aligned or not."""
+    tokens = make_tokens("uniform" if kind == "bad" else kind, N, V)
+    if kind == "bad":
+        tokens[::3] = V
+        tokens[1::7] = -5
+    pad = V - 1 if kind == "padded" else -1
+    buf = torch.zeros(N + off, device=DEV, dtype=it)
+    tok = buf[off:]
+    tok.copy_(torch.from_numpy(tokens))
+    dh = rnd((N, H), N, DT[dt])
+    view, whole, rest = padded(torch.full((V, H), 3.0, dtype=DT[odt], device=DEV), ld)
+    out = nl.embedding_grad(dh, tok, V, 1.5, padding_idx=None if pad < 0 else pad, out=view)
+    torch.cuda.synchronize()
+    assert torch.all(whole[rest] == -77.0)
+    assert _lib.device_errors() == (_lib.NORM_DEVICE_ERR_BAD_TOKEN if kind == "bad" else 0)
+    d = n64(dh)
+    ref = S.lookup_backward(d, tokens, V, 1.5, pad)
+    terms = S.lookup_backward(np.abs(d), tokens, V, 1.5, pad)
+    counts = np.bincount(tokens[(tokens >= 0) & (tokens < V)], minlength=V)
+    close(out, ref, (40 + counts[:, None] / 8) * U * terms, "dtable")  # tiles of eight
+    assert not out[torch.from_numpy((counts == 0) | (np.arange(V) == pad)).to(DEV)].any()
+
+
+def test_lookup_grad_marks_in_several_ranges():
+    """More table rows a clearing CTA than it marks at a time (8192)."""
+    V, H = 5_300_000, 1024
+    tokens = torch.tensor([0, 1, 8191, 8192, 8716, 8717, 8718, 3_000_000, V - 1, V - 1, 8192], device=DEV)
+    dh = rnd((len(tokens), H), 1, torch.bfloat16)
+    out = torch.full((V, H), 3.0, device=DEV, dtype=torch.bfloat16)
+    nl.embedding_grad(dh, tokens, V, out=out)
+    ids = tokens.unique()
+    want = S.lookup_backward(n64(dh), torch.searchsorted(ids, tokens).tolist(), len(ids))
+    close(out[ids], want, 4 * U * 2 * np.abs(want).max(), "dtable")
+    out[ids] = 0
+    assert not any(part.any() for part in out.split(500_000))
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("N,H,B", [(300, 1024, 0), (301, 1001, 1), (96, 5120, 8), (40, 40008, 2)])
+def test_join_without_parameters_and_stream_gradient(N, H, B, dt):
+    """dh_in and the gammas left out: zeros and ones, with gradients of the ones."""
+    c = join_inputs(N, H, DT[dt], DT[dt], B, seed=H)
+    ones, c["dh"] = torch.ones(H, device=DEV), torch.zeros_like(c["x"])
+    c["gpost"] = c["gpre"] = ones
+    out = nl.sandwich_rms(c["x"], c["res"], None, c["gate"], None, 1e-5, residual_scale=0.75)
+    check_join(c, out, 1e-5, 0.75, True, True)
+    rpost, rpre = (torch.from_numpy(S._rstd(n64(c[k]), 1e-5)).float().to(DEV) for k in ("x", "res"))
+    for p in (True, False):  # (without the norm after the block too)
+        grad = nl.sandwich_rms_grad(c["dy"], c["x"], c["res"], rpost if p else None, rpre, None, c["gate"], None, None,
+                                    residual_scale=0.75, param_dtype=torch.float32)
+        check_join_grad(c, grad, rpost if p else None, rpre, 0.75)
+        assert grad[4].dtype == torch.float32
+
+
+@pytest.mark.parametrize("wdt,gdt", [("x", "f32"), ("f32", "x"), ("f32", "f32")])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("N,H,B", [(300, 1024, 1), (300, 1024, 4), (303, 1001, 3), (60, 16384, 5)])
+def test_join_parameter_dtypes(N, H, B, dt, wdt, gdt):
+    """Gammas in the rows' dtype with an fp32 gate, and the other way round."""
+    wt, gt = (DT[dt if d == "x" else d] for d in (wdt, gdt))
+    c = join_inputs(N, H, DT[dt], wt, B, seed=N, gdt=gt)
+    out = nl.sandwich_rms(c["x"], c["res"], c["gpost"], c["gate"], c["gpre"], 1e-5, residual_scale=0.75)
+    check_join(c, out, 1e-5, 0.75, True, True)
+    out, rpost, rpre = run_join_grad(c, True, True)
+    assert out[2].dtype == out[4].dtype == wt and out[3].dtype == gt
+    check_join_grad(c, out, rpost, rpre, 0.75)
+
+
+@pytest.mark.parametrize("H,dt", [(30704, "bf16"), (30720, "bf16"), (32768, "f16"), (32769, "f16"), (32768, "f32")])
+def test_join_grad_widest_rows_with_gates_of_runs(H, dt):
+    """Where several gate rows leave no room for two row buffers, the loop runs."""
+    c = join_inputs(12, H, DT[dt], torch.float32, 4, seed=H)
+    out, rpost, rpre = run_join_grad(c, True, True)
+    check_join_grad(c, out, rpost, rpre, 0.75)
