@@ -942,3 +942,71 @@ def test_join_grad_widest_rows_with_gates_of_runs(H, dt):
     c = join_inputs(12, H, DT[dt], torch.float32, 4, seed=H)
     out, rpost, rpre = run_join_grad(c, True, True)
     check_join_grad(c, out, rpost, rpre, 0.75)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_behind_an_event_of_another_stream(captured):
+    """What a call waits for besides the kernel before it in its own stream: an
+    event behind long work elsewhere, copies and memsets. Eager, and as the edges
+    of a graph."""
+    N, H, V = 64, 1024, 50
+    a = rnd((4096, 4096), 1, torch.bfloat16, std=0.02)
+    src = rnd((N, H), 2, torch.bfloat16)
+    table = rnd((V, H), 3, torch.bfloat16)
+    tokens = torch.from_numpy(make_tokens("skewed", N, V)).to(DEV)
+    x, res, tok, dy = torch.empty_like(src), torch.empty_like(src), torch.empty_like(tokens), torch.empty_like(src)
+    stats = torch.ones(N, device=DEV)
+    side = torch.cuda.Stream()
+
+    def go():
+        main = torch.cuda.current_stream()
+        x.zero_()
+        dy.zero_()
+        tok.zero_()
+        outs = []
+        for i in range(3):
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                b = a @ a
+                for _ in range(3):
+                    b = b @ a
+                x.copy_(src * (i + 1) + 0 * b[:N, :H])
+                dy.copy_(src + 0 * b[:N, :H])
+                tok.copy_(tokens)
+            res.copy_(src)   # the kernel before the call in its own stream ends long before the event
+            main.wait_stream(side)
+            y, h, _, _ = nl.sandwich_rms(x, res)
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                x.add_(b[:N, :H] * 0)
+            main.wait_stream(side)
+            outs += [y, h, *nl.sandwich_rms_grad(dy, x, h, stats, stats)]
+            e, eh, _ = nl.embedding_rms(tok, table)
+            tok.fill_(1)
+            outs += [e, eh, nl.embedding_grad(dy, tok, V)]
+            x.zero_()
+            dy.zero_()
+            tok.zero_()
+        return outs
+
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = go()
+        for _ in range(3):
+            g.replay()
+    else:
+        got = go()
+    torch.cuda.synchronize()
+    want = []
+    for i in range(3):
+        xs = src * (i + 1)
+        y, h, _, _ = nl.sandwich_rms(xs, src)
+        torch.cuda.synchronize()
+        want += [y, h, *nl.sandwich_rms_grad(src, xs, h, stats, stats)]
+        torch.cuda.synchronize()
+        e, eh, _ = nl.embedding_rms(tokens, table)
+        torch.cuda.synchronize()
+        want += [e, eh, nl.embedding_grad(src, torch.ones_like(tokens), V)]
+    for p, q in zip(got, want):
+        assert (p is None and q is None) or torch.equal(p, q)
