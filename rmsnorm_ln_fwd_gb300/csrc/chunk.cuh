@@ -118,13 +118,6 @@ __device__ __forceinline__ void put_params(float* slot, const float (&f)[E]) {
     *reinterpret_cast<float4*>(slot + 4 * q) = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
 }
 
-// Pairs 2q and 2q + 1 of a parameter vector.
-__device__ __forceinline__ void get_pairs(const float* slot, int q, float2 (&p)[2]) {
-  const float4 v = *reinterpret_cast<const float4*>(slot + 4 * q);
-  p[0] = make_float2(v.x, v.y);
-  p[1] = make_float2(v.z, v.w);
-}
-
 // Shared memory by 32-bit address.
 template <int W>
 __device__ __forceinline__ void lds_words(uint32_t p, uint32_t* w) {
@@ -144,6 +137,7 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t p) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(p));
   return v;
 }
+// Pairs 0 and 1 at p (16-byte aligned).
 __device__ __forceinline__ void lds_pairs(uint32_t p, float2 (&v)[2]) {
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0].x), "=f"(v[0].y), "=f"(v[1].x), "=f"(v[1].y) : "r"(p));
 }
