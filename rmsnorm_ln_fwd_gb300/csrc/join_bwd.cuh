@@ -183,7 +183,9 @@ constexpr int kJoinRedOff = kJoinShiftOff + kJoinMaxGroups * kJoinMaxBuffers * k
 
 constexpr int kJoinStaticSmem = 512;  // of the kernel's own, at most
 
-// The ring of a CTA of at most `threads` threads, `ctas` of them an SM.
+// The ring of a CTA of at most `threads` threads, `ctas` of them an SM.  Several
+// gate rows (`runs`) hold a third vector a thread beside its two parameters, the
+// share of dgamma_post of the runs that have ended.
 template <int E>
 inline JoinRing join_ring(int H, int es, int ge, int cl, bool runs, int threads, int ctas, int max_smem) {
   JoinRing r{};
@@ -812,6 +814,24 @@ static bool run_join_grad_shape(JoinGradArgs& a, const DeviceInfo& dev, cudaStre
 // rows, of up to 512 threads in one CTA; wider ones in clusters, 160x3 where the
 // part of at most 256 threads has no more than 160.  fp32, eight columns a thread
 // and half the instructions a byte, keeps the large CTA throughout.
+//
+// Several gate rows: their third parameter vector (join_ring) leaves a CTA that
+// is full of threads without its second row buffer: in half precision from 448 to
+// 512, 944 to 1024, 1912 to 2048, 3864 to 4096, 7760 to 8192 and 15144 to 16384
+// columns.  Those rows go to the clusters of 256x2, of two to eight CTAs of one to
+// four warps, with an exchange a row (us, bf16: one gate; eight gate rows; one for
+// each 128 rows; in brackets the CTAs a row where they are several):
+//   65536x512                  77.4      294.6 (2)  313.3 (2)
+//   32768x1024                 74.9      158.8 (2)  181.1 (2)
+//   16384x2048                 73.6      111.9 (2)  134.2 (2)
+//   16384x2560                 88.4       92.6      118.9
+//   8192x4096                  72.9      123.1 (2)  143.6 (2)
+//   8192x5120                  87.0 (2)  115.0 (2)  138.2 (2)
+//   4096x8192                  71.9      136.3 (4)  141.9 (4)
+//   2048x16384                 77.5 (4)  164.2 (8)  166.8 (8)
+//   fp32 4096x4096             67.0       71.2
+// Past 30272 columns (element by element 30208) nothing fits and the loop runs
+// (1024x30720: 81.0 with one gate, 1695 with eight).
 template <typename D, int GB, bool RUNS>
 static cudaError_t run_join_grad(JoinGradArgs& a, const DeviceInfo& dev, cudaStream_t s, bool* done) {
   cudaError_t e = cudaSuccess;
