@@ -135,6 +135,22 @@ struct Gate {
   norm_dtype dt = NORM_F32;
 };
 
+// Whether `t` would broadcast over an outer dim of `ref` and follow a dim inside
+// it, as (1, T, H) does against (B, T, H).  Gate rows serve runs of consecutive
+// rows, which is something else.
+bool broadcasts_outer(const Tensor& t, const Tensor& ref) {
+  if (t.dim() != ref.dim()) return false;
+  bool open = false, follows = false;
+  for (int64_t i = 0; i + 1 < t.dim(); ++i) {
+    if (t.size(i) != ref.size(i) && t.size(i) != 1) return false;
+    if (t.size(i) == ref.size(i))
+      follows |= open && ref.size(i) > 1;
+    else
+      open = true;
+  }
+  return follows;
+}
+
 Gate gate_view(const Opt& t, const Rows& of, const Tensor& ref) {
   Gate g;
   g.dt = code(ref.scalar_type(), "x");
@@ -142,6 +158,8 @@ Gate gate_view(const Opt& t, const Rows& of, const Tensor& ref) {
   const Rows r = rows(*t, "gate");
   if (r.H != of.H || t->device() != ref.device())
     value_error("gate must have " + std::to_string(of.H) + " columns on " + ref.device().str());
+  if (broadcasts_outer(*t, ref))
+    value_error("gate: a row serves a run of consecutive rows; dims that follow a broadcast one are not taken");
   const bool none = r.N == 0 && of.N == 0;  // no sequences: no gate rows, and nothing reads one
   if (!none && (r.N < 1 || of.N % r.N != 0 || (of.N > 0 && r.N > of.N)))
     value_error("gate has " + std::to_string(r.N) + " rows, which do not divide the " + std::to_string(of.N) +

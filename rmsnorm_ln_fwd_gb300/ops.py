@@ -335,7 +335,8 @@ def sandwich_rms(x, residual, gamma_post=None, gate=None, gamma_pre=None, eps: f
 
     ``x`` is a block's output, ``residual`` the stream it is added to.  ``gate``
     is None, one vector (H,) for all rows, or (B, ..., H) with one row for each
-    of B equal runs of rows (for (B, T, H) rows: one for each sequence).
+    of B equal runs of rows (for (B, T, H) rows: one for each sequence; not one
+    for each position, and (1, T, H) is refused).
     ``post_norm=False`` takes x as it is, ``pre_norm=False`` writes h only (y is
     None).  ``h_out`` may be a fresh tensor (default), ``x`` or ``residual``
     itself.  Returns (y, h, rstd_post, rstd_pre), statistics (N,) fp32 (None

@@ -1012,3 +1012,27 @@ def test_calls_behind_an_event_of_another_stream(captured):
         want += [e, eh, nl.embedding_grad(src, torch.ones_like(tokens), V)]
     for p, q in zip(got, want):
         assert (p is None and q is None) or torch.equal(p, q)
+
+
+@pytest.mark.parametrize("x,gate", [((4, 6, 64), (1, 6, 64)), ((2, 3, 6, 64), (1, 3, 1, 64)),
+                                    ((2, 3, 6, 64), (2, 1, 6, 64)), ((2, 3, 6, 64), (1, 3, 6, 64))])
+def test_gates_of_positions_are_refused(x, gate):
+    """Shapes that would broadcast over an outer dim are no runs of rows."""
+    t, g = (torch.zeros(s, device=DEV) for s in (x, gate))
+    r = torch.ones(t.numel() // 64, device=DEV)
+    with pytest.raises(ValueError, match="run of consecutive rows"):
+        nl.sandwich_rms(t, t, gate=g)
+    with pytest.raises(ValueError, match="run of consecutive rows"):
+        nl.sandwich_rms_grad(t, t, t, r, r, None, g)
+
+
+@pytest.mark.parametrize("x,gate", [((4, 6, 64), (4, 1, 64)), ((4, 6, 64), (4, 6, 64)), ((4, 6, 64), (1, 1, 64)),
+                                    ((1, 6, 64), (1, 6, 64)), ((2, 3, 6, 64), (2, 3, 1, 64)), ((4, 6, 64), (8, 1, 64)),
+                                    ((4, 1, 6, 64), (4, 1, 1, 64)), ((4, 6, 64), (64,)), ((4, 6, 64), (1, 64))])
+def test_gate_shapes_are_runs_of_rows(x, gate):
+    t, res, g = rnd(x, 1, torch.float32), rnd(x, 2, torch.float32), rnd(gate, 3, torch.float32)
+    N = t.numel() // 64
+    rows = g.reshape(-1, 64).repeat_interleave(N // (g.numel() // 64), 0).reshape(x)
+    y, h, _, _ = nl.sandwich_rms(t, res, gate=g, post_norm=False)
+    want = res.double() + rows.double() * t.double()
+    assert (h.double() - want).abs().max() <= 2 * U * (res.abs() + (rows * t).abs()).max()  # (the product and the sum)
