@@ -383,6 +383,127 @@ norm_status embedding_grad(const void* dh, int64_t lddh, const void* tokens, nor
                            float scale, int64_t padding_idx, int accumulate, norm_dtype x_dtype, norm_dtype w_dtype,
                            norm_stream_t stream);
 
+/*
+ * Heads of a projection: a (B, T, H, D) tensor of D contiguous columns a head,
+ * by its strides in elements (none negative; that of a dim of one is not
+ * looked at).  (B, T, H, D) and (B, H, T, D) layouts, and the queries' or keys'
+ * part of a fused projection's output, are such.
+ */
+typedef struct {
+  void* data;
+  int64_t batch_stride, token_stride, head_stride;
+} norm_heads;
+
+/*
+ * Rotation by position.  cos, sin [rows x cos_stride / sin_stride] of columns/2
+ * elements in `dtype` (the row dtype or NORM_F32): the angles of position p are
+ * in row p.  columns: how many of a head's first columns are rotated, even.
+ * Pair i of them is columns (i, i + columns/2), or with interleaved != 0 columns
+ * (2i, 2i + 1).  positions: one for each token, by its strides (0: shared), or
+ * NULL: token t of each sequence has position t, and T is at most `rows`.
+ */
+typedef struct {
+  const void* cos;
+  int64_t cos_stride;
+  const void* sin;
+  int64_t sin_stride;
+  int64_t rows, columns;
+  norm_dtype dtype;
+  int interleaved;
+  const void* positions;
+  norm_itype position_type;
+  int64_t position_batch_stride, position_token_stride;
+} norm_rotation;
+
+/*
+ * RMSNorm of each head of queries and keys, and the rotation by their tokens'
+ * positions, in one pass (the norm inside an attention block).  For each head x:
+ *   n = x * rstd * gamma,  rstd = 1/sqrt(sum_j x_j^2 / D + eps),
+ *   y_a = n_a * cos - n_b * sin,  y_b = n_b * cos + n_a * sin  for each rotated
+ *   pair (a, b),  y_j = n_j for the other columns; all in fp32, rounded once.
+ * q [B, T, q_heads, D], k [B, T, k_heads, D]: either may have no heads (and is
+ *   then NULL).  D is at most 512, heads at most 65535 a side.
+ * gamma_q, gamma_k [D] or NULL (ones).  rotation: NULL for the norm alone.
+ * q_out, k_out: outputs of distinct elements.  Each may be exactly its input (in
+ *   place); otherwise they are clear of the inputs and of each other.  Parts of
+ *   one fused tensor count as clear where their columns are.
+ * A token whose position is outside the table gives heads of zeros and raises
+ * NORM_DEVICE_ERR_BAD_POSITION.
+ */
+norm_status head_rms_rotary(const norm_heads* q, int64_t q_heads, const norm_heads* k, int64_t k_heads,
+                            const void* gamma_q, const void* gamma_k, const norm_heads* q_out, const norm_heads* k_out,
+                            const norm_rotation* rotation, int64_t B, int64_t T, int64_t D, float eps,
+                            norm_dtype x_dtype, norm_dtype w_dtype, norm_stream_t stream);
+
+/*
+ * Bytes of device workspace head_rms_rotary_grad needs for heads of D columns on
+ * CUDA device `device`; independent of all else.  Returns 0 if an argument is out
+ * of range or the device cannot be queried.
+ */
+size_t head_rms_rotary_workspace_bytes(int64_t D, int device);
+
+/*
+ * Gradient of head_rms_rotary from its inputs (statistics are formed again).  For
+ * each head, u the gradient dy turned back by its token's angles:
+ *   w  = u * gamma,
+ *   dx = rstd * (w - x * rstd^2 * sum(w * x) / D),
+ *   dgamma = sum over all tokens and the side's heads of u * x * rstd.
+ * dyq, dyk: the outputs' gradients; q, k: the forward's inputs.
+ * dq, dk: each may be exactly its dyq or dyk; otherwise clear of the inputs and
+ *   of each other, as the forward's outputs.
+ * dgamma_q, dgamma_k [D] in w_dtype, or NULL to skip.  Overwritten; zero with no
+ *   tokens.  A token with a position outside the table has no gradient.
+ * workspace: head_rms_rotary_workspace_bytes(D, device) bytes, 16-byte aligned;
+ *   needed only when a dgamma is.  Calls that share it must be ordered.
+ * Sums have a fixed order: the same inputs give the same bits.
+ */
+norm_status head_rms_rotary_grad(const norm_heads* dyq, const norm_heads* q, int64_t q_heads, const norm_heads* dyk,
+                                 const norm_heads* k, int64_t k_heads, const void* gamma_q, const void* gamma_k,
+                                 const norm_heads* dq, const norm_heads* dk, void* dgamma_q, void* dgamma_k,
+                                 const norm_rotation* rotation, void* workspace, size_t workspace_bytes, int64_t B,
+                                 int64_t T, int64_t D, float eps, norm_dtype x_dtype, norm_dtype w_dtype,
+                                 norm_stream_t stream);
+
+/*
+ * Log probabilities of given tokens: the end of a residual stream.  For each row
+ * z of V logits, a = scale (> 0; an inverse temperature), m = max_j z_j:
+ *   l = log(sum_j exp(a (z_j - m))),  p_j = exp(a (z_j - m) - l),
+ *   logprob = a (z_t - m) - l for the row's token t,
+ *   entropy = -sum_j p_j log p_j  (a term with p_j = 0 counts as 0),
+ *   lse = a m + l,  stats = (m, l), kept apart for token_logprobs_grad,
+ *   and the `top` most probable tokens, larger logits first and equal ones by id.
+ * logits [N x ldl] in `dtype`.  tokens [N], contiguous, or NULL (no logprob).  A
+ *   row whose token is ignore_index has logprob 0.  A token outside [0, V) has so
+ *   too and raises NORM_DEVICE_ERR_BAD_TOKEN.
+ * logprob [N] (with tokens), entropy [N], lse [N], stats [N x 2, 8-byte aligned]:
+ *   fp32; entropy, lse and stats may be NULL.  top_logprobs fp32, top_ids int64
+ *   [N x top]; top is at most NORM_MAX_TOP, 0 for none (then both NULL).
+ * A logit of -inf has probability 0 and is no alternative: where fewer than `top`
+ *   are left, the rest is id -1 with log probability -inf (NaN is none either).
+ *   A row that is -inf throughout has logprob, lse and stats of -inf and entropy
+ *   0.  A row with a NaN or +inf has NaN in all but its maximum and its ids.
+ * N is at most 2^28.
+ */
+#define NORM_MAX_TOP 32
+norm_status token_logprobs(const void* logits, int64_t ldl, const void* tokens, norm_itype token_type, float scale,
+                           int64_t ignore_index, float* logprob, float* entropy, float* lse, float* stats,
+                           float* top_logprobs, int64_t* top_ids, int64_t top, int64_t N, int64_t V, norm_dtype dtype,
+                           norm_stream_t stream);
+
+/*
+ * Gradient of the logits from those of token_logprobs' outputs, fp32 [N] or NULL
+ * (zeros; not all of them):
+ *   dlogits_j = a (dlogprob (1[j = t] - p_j) + dlse p_j - dentropy p_j (log p_j + entropy)).
+ * stats [N x 2], entropy [N] (with dentropy): the forward's.  tokens as in the
+ *   forward (read only with dlogprob); a row without a token has no dlogprob.
+ * dlogits [N x lddl]: may be exactly logits (in place), else clear of it.
+ * A row that is -inf throughout has no gradient.  The alternatives have none.
+ */
+norm_status token_logprobs_grad(const float* dlogprob, const void* logits, int64_t ldl, const void* tokens,
+                                norm_itype token_type, const float* stats, const float* entropy, const float* dentropy,
+                                const float* dlse, float scale, int64_t ignore_index, void* dlogits, int64_t lddl,
+                                int64_t N, int64_t V, norm_dtype dtype, norm_stream_t stream);
+
 /* A static, human-readable name for a status code (never NULL). */
 const char* norm_status_str(norm_status status);
 
@@ -403,6 +524,7 @@ const char* norm_last_error(void);
 #define NORM_DEVICE_ERR_WAIT_TIMEOUT 1u
 #define NORM_DEVICE_ERR_BAD_COPY 2u /* a bulk copy failed its bounds check and was skipped */
 #define NORM_DEVICE_ERR_BAD_TOKEN 4u /* a token id outside its table was met (and left out) */
+#define NORM_DEVICE_ERR_BAD_POSITION 8u /* a position outside the rotation's table was met (and left out) */
 norm_status norm_device_errors(int device, unsigned int* flags, int clear);
 
 /*

@@ -29,6 +29,9 @@ NORM_SANDWICH_POST = 1
 NORM_SANDWICH_PRE = 2
 
 NORM_DEVICE_ERR_BAD_TOKEN = 4
+NORM_DEVICE_ERR_BAD_POSITION = 8
+
+NORM_MAX_TOP = 32
 
 # name -> (restype, argtypes), one entry per function declared in include/norm.h
 _P = ctypes.c_void_p
@@ -62,6 +65,12 @@ SIGNATURES = {
     "embedding_grad_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
     "embedding_grad": (_I, [_P, _I64, _P, _I, _P, _I64, _I64, _P, ctypes.c_size_t, _I64, _I64, _F, _I64, _I, _I, _I,
                             _P]),
+    "head_rms_rotary": (_I, [_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _I64, _F, _I, _I, _P]),
+    "head_rms_rotary_workspace_bytes": (ctypes.c_size_t, [_I64, _I]),
+    "head_rms_rotary_grad": (_I, [_P, _P, _I64, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _I64,
+                                  _I64, _I64, _F, _I, _I, _P]),
+    "token_logprobs": (_I, [_P, _I64, _P, _I, _F, _I64, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P]),
+    "token_logprobs_grad": (_I, [_P, _P, _I64, _P, _I, _P, _P, _P, _P, _F, _I64, _P, _I64, _I64, _I64, _I, _P]),
     "norm_status_str": (ctypes.c_char_p, [_I]),
     "norm_abi_version": (_I, []),
     "norm_last_error": (ctypes.c_char_p, []),
@@ -70,6 +79,20 @@ SIGNATURES = {
     "norm_set_kernel_path": (_I, [_I]),
     "norm_set_bwd_split_event": (_I, [_P]),
 }
+
+
+
+class Heads(ctypes.Structure):
+    """norm_heads: a (B, T, H, D) tensor by its strides."""
+    _fields_ = [("data", _P), ("batch_stride", _I64), ("token_stride", _I64), ("head_stride", _I64)]
+
+
+class Rotation(ctypes.Structure):
+    """norm_rotation."""
+    _fields_ = [("cos", _P), ("cos_stride", _I64), ("sin", _P), ("sin_stride", _I64), ("rows", _I64),
+                ("columns", _I64), ("dtype", _I), ("interleaved", _I), ("positions", _P), ("position_type", _I),
+                ("position_batch_stride", _I64), ("position_token_stride", _I64)]
+
 
 _lock = threading.Lock()
 _lib = None

@@ -1,6 +1,7 @@
-// Python binding of the residual-stream operators: the argument checks, output
-// allocation and C calls of sandwich_rms, embedding_lookup and their gradients,
-// against PyTorch's C++ interface.  It computes nothing.
+// Python binding of the residual-stream operators, of the per-head norm and of
+// the log probabilities: the argument checks, output allocation and C calls of
+// sandwich_rms, embedding_lookup, head_rms_rotary, token_logprobs and their
+// gradients, against PyTorch's C++ interface.  It computes nothing.
 //
 // These calls are made for single rows as well, where the call is all host
 // time: through ctypes a one-row sandwich_rms cost 24 us of it, of which the
@@ -365,6 +366,233 @@ py::object embedding_grad_(const Tensor& dh, const Tensor& tokens, int64_t num_r
   return obj(table);
 }
 
+// ------------------------------------------------- heads of queries and keys
+
+// A (T, H, D) or (B, T, H, D) tensor.
+struct HeadsOf {
+  norm_heads h{};
+  int64_t B = 1, T = 0, H = 0, D = 0;
+};
+
+HeadsOf heads_view(const Tensor& t, const char* what) {
+  const int64_t d = t.dim();
+  if (d != 3 && d != 4) value_error(std::string(what) + " must be (T, heads, D) or (B, T, heads, D)");
+  HeadsOf r;
+  if (d == 4) {
+    r.B = t.size(0);
+    r.h.batch_stride = t.stride(0);
+  }
+  r.T = t.size(d - 3);
+  r.H = t.size(d - 2);
+  r.D = t.size(d - 1);
+  if (r.D > 1 && t.stride(d - 1) != 1) value_error(std::string(what) + ": the last dim must be contiguous");
+  r.h.token_stride = t.stride(d - 3);
+  r.h.head_stride = t.stride(d - 2);
+  r.h.data = t.data_ptr();
+  return r;
+}
+
+HeadsOf heads(const Tensor& t, const char* what) { return heads_view(cuda_tensor(t, what), what); }
+
+// Heads of another tensor's tokens, columns, dtype and device; `H` < 0: of any number.
+HeadsOf heads_like(const Tensor& t, const Tensor& ref, int64_t H, const char* what) {
+  const HeadsOf r = heads(t, what);
+  if (t.dim() != ref.dim() || t.scalar_type() != ref.scalar_type() || t.device() != ref.device() ||
+      r.D != ref.size(-1) || r.T != ref.size(-3) || (ref.dim() == 4 && r.B != ref.size(0)) || (H >= 0 && r.H != H))
+    value_error(std::string(what) + " must match the tokens, columns, heads, dtype (" + name_of(ref.scalar_type()) +
+                ") and device (" + ref.device().str() + ") of what it belongs to");
+  return r;
+}
+
+// cos, sin and positions; returns whether there is a rotation.
+bool rotation_of(const Opt& cos, const Opt& sin, const Opt& positions, bool interleaved, const Tensor& q, const HeadsOf& of,
+                 norm_rotation* r) {
+  if (cos.has_value() != sin.has_value()) value_error("cos and sin come together");
+  if (!cos) {
+    if (positions) value_error("positions need cos and sin");
+    return false;
+  }
+  for (const Tensor* t : {&*cos, &*sin}) {
+    const char* what = t == &*cos ? "cos" : "sin";
+    cuda_tensor(*t, what);
+    if (t->dim() != 2 || t->sizes() != cos->sizes() || (t->size(1) > 1 && t->stride(1) != 1))
+      value_error("cos and sin must be (rows, rotated columns / 2) with contiguous columns");
+    if (t->device() != q.device()) value_error(std::string(what) + " is on " + t->device().str() + ", q on " + q.device().str());
+    if (t->scalar_type() != cos->scalar_type()) type_error("cos and sin must share a dtype");
+  }
+  *r = norm_rotation{};
+  r->dtype = code(cos->scalar_type(), "cos");
+  if (cos->scalar_type() != q.scalar_type() && r->dtype != NORM_F32)
+    type_error("cos: dtype " + name_of(cos->scalar_type()) + " must be q's or float32");
+  r->rows = cos->size(0);
+  r->columns = 2 * cos->size(1);
+  if (r->columns < 2 || r->columns > of.D)
+    value_error("cos has " + std::to_string(cos->size(1)) + " columns: 1 to " + std::to_string(of.D / 2) + " are wanted");
+  r->cos = cos->data_ptr();
+  r->sin = sin->data_ptr();
+  r->cos_stride = r->rows > 1 ? cos->stride(0) : std::max<int64_t>(cos->size(1), 1);
+  r->sin_stride = r->rows > 1 ? sin->stride(0) : std::max<int64_t>(sin->size(1), 1);
+  r->interleaved = interleaved;
+  if (!positions) {
+    if (of.T > r->rows && of.B > 0)
+      value_error(std::to_string(of.T) + " tokens a sequence, but the table has " + std::to_string(r->rows) + " rows");
+    return true;
+  }
+  const Tensor& p = cuda_tensor(*positions, "positions");
+  if (p.scalar_type() != at::kInt && p.scalar_type() != at::kLong)
+    type_error("positions: dtype " + name_of(p.scalar_type()) + " not supported (int32 or int64)");
+  if (p.device() != q.device()) value_error("positions are on " + p.device().str() + ", q on " + q.device().str());
+  const int64_t d = p.dim();
+  if (d < 1 || d > q.dim() - 2 || p.size(d - 1) != of.T || (d == 2 && p.size(0) != of.B && p.size(0) != 1))
+    value_error("positions must be (T,)" + std::string(q.dim() == 4 ? " or (B, T)" : "") + ", T = " + std::to_string(of.T));
+  if (of.B * of.T > 0 && r->rows == 0) value_error("the table has no rows");
+  r->positions = p.data_ptr();
+  r->position_type = p.scalar_type() == at::kLong ? NORM_I64 : NORM_I32;
+  r->position_token_stride = p.stride(d - 1);
+  r->position_batch_stride = d == 2 && p.size(0) > 1 ? p.stride(0) : 0;
+  return true;
+}
+
+py::tuple head_rms_rotary_(const Tensor& q, const Opt& k, const Opt& gamma_q, const Opt& gamma_k, const Opt& cos,
+                           const Opt& sin, const Opt& positions, double eps, bool interleaved, const Opt& q_out,
+                           const Opt& k_out) {
+  const HeadsOf qh = heads(q, "q");
+  const norm_dtype xc = code(q.scalar_type(), "q");
+  if (!k && (gamma_k || k_out)) value_error("gamma_k and k_out need k");
+  const HeadsOf kh = k ? heads_like(*k, q, -1, "k") : HeadsOf();
+  const void* gq = vec(gamma_q, qh.D, "gamma_q", q);
+  const void* gk = vec(gamma_k, qh.D, "gamma_k", q);
+  if (gamma_q && gamma_k && gamma_q->scalar_type() != gamma_k->scalar_type()) type_error("gamma_q and gamma_k must share a dtype");
+  const norm_dtype wc = gamma_q ? code(gamma_q->scalar_type(), "gamma") : gamma_k ? code(gamma_k->scalar_type(), "gamma") : xc;
+  norm_rotation rot;
+  const bool turned = rotation_of(cos, sin, positions, interleaved, q, qh, &rot);
+  const c10::cuda::CUDAGuard guard(q.device());
+  const Tensor qo = q_out ? *q_out : new_like(q);
+  const HeadsOf qoh = q_out ? heads_like(qo, q, qh.H, "q_out") : heads_view(qo, "q_out");
+  Tensor ko;
+  HeadsOf koh;
+  if (k) {
+    ko = k_out ? *k_out : new_like(*k);
+    koh = k_out ? heads_like(ko, q, kh.H, "k_out") : heads_view(ko, "k_out");
+  }
+  if (qh.H + kh.H > 0)
+    check("head_rms_rotary",
+          head_rms_rotary(&qh.h, qh.H, k ? &kh.h : nullptr, kh.H, qh.H ? gq : nullptr, kh.H ? gk : nullptr, &qoh.h,
+                          k ? &koh.h : nullptr, turned ? &rot : nullptr, qh.B, qh.T, qh.D, (float)eps, xc, wc, stream_of(q)));
+  return py::make_tuple(obj(qo), obj(ko));
+}
+
+py::tuple head_rms_rotary_grad_(const Tensor& dyq, const Opt& dyk, const Tensor& q, const Opt& k, const Opt& gamma_q,
+                                const Opt& gamma_k, const Opt& cos, const Opt& sin, const Opt& positions, double eps,
+                                bool interleaved, bool need_param_grads, const Opt& workspace, const Opt& dq, const Opt& dk,
+                                std::optional<at::ScalarType> param_dtype) {
+  const HeadsOf qh = heads(q, "q");
+  const norm_dtype xc = code(q.scalar_type(), "q");
+  if (k.has_value() != dyk.has_value()) value_error("k and dyk come together");
+  if (!k && (gamma_k || dk)) value_error("gamma_k and dk need k");
+  const HeadsOf dyqh = heads_like(dyq, q, qh.H, "dyq");
+  const HeadsOf kh = k ? heads_like(*k, q, -1, "k") : HeadsOf();
+  const HeadsOf dykh = k ? heads_like(*dyk, q, kh.H, "dyk") : HeadsOf();
+  const void* gq = vec(gamma_q, qh.D, "gamma_q", q);
+  const void* gk = vec(gamma_k, qh.D, "gamma_k", q);
+  if (gamma_q && gamma_k && gamma_q->scalar_type() != gamma_k->scalar_type()) type_error("gamma_q and gamma_k must share a dtype");
+  const at::ScalarType wt = gamma_q   ? gamma_q->scalar_type()
+                            : gamma_k ? gamma_k->scalar_type()
+                                      : param_dtype.value_or(q.scalar_type());
+  const norm_dtype wc = code(wt, "param_dtype");
+  if (qh.H == 0 || (k && kh.H == 0)) value_error("q and k must have heads");
+  norm_rotation rot;
+  const bool turned = rotation_of(cos, sin, positions, interleaved, q, qh, &rot);
+  const c10::cuda::CUDAGuard guard(q.device());
+  const Tensor qo = dq ? *dq : new_like(q);
+  const HeadsOf qoh = dq ? heads_like(qo, q, qh.H, "dq") : heads_view(qo, "dq");
+  Tensor ko, dgq, dgk, ws;
+  HeadsOf koh;
+  if (k) {
+    ko = dk ? *dk : new_like(*k);
+    koh = dk ? heads_like(ko, q, kh.H, "dk") : heads_view(ko, "dk");
+  }
+  size_t wsb = 0;
+  if (need_param_grads) {
+    dgq = new_vec(qh.D, q, wt);
+    if (k) dgk = new_vec(qh.D, q, wt);
+    ws = workspace_of(workspace, head_rms_rotary_workspace_bytes(qh.D, q.get_device()), q, &wsb);
+  }
+  auto ptr = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+  check("head_rms_rotary_grad",
+        head_rms_rotary_grad(&dyqh.h, &qh.h, qh.H, k ? &dykh.h : nullptr, k ? &kh.h : nullptr, kh.H, gq, gk, &qoh.h,
+                             k ? &koh.h : nullptr, ptr(dgq), ptr(dgk), turned ? &rot : nullptr, ptr(ws), wsb, qh.B, qh.T,
+                             qh.D, (float)eps, xc, wc, stream_of(q)));
+  return py::make_tuple(obj(qo), obj(ko), obj(dgq), obj(dgk));
+}
+
+// ------------------------------------------------------ log probabilities
+
+constexpr int64_t kNoToken = INT64_MIN;
+
+// The token of each row, of the leading dims' number.
+const void* row_tokens(const Opt& tokens, const Tensor& logits, int64_t N, norm_itype* type) {
+  if (!tokens) return nullptr;
+  *type = tokens_of(*tokens, logits);
+  if (tokens->numel() != N)
+    value_error(std::to_string(N) + " rows of logits, but " + std::to_string(tokens->numel()) + " tokens");
+  return tokens->data_ptr();
+}
+
+py::tuple token_logprobs_(const Tensor& logits, const Opt& tokens, double scale, int64_t top, std::optional<int64_t> ignore,
+                          bool entropy) {
+  const Rows zr = rows(logits, "logits");
+  const norm_dtype xc = code(logits.scalar_type(), "logits");
+  norm_itype it = NORM_I64;
+  const void* tp = row_tokens(tokens, logits, zr.N, &it);
+  if (top < 0 || top > NORM_MAX_TOP)
+    value_error("top must be 0 to " + std::to_string(NORM_MAX_TOP) + ", not " + std::to_string(top));
+  const c10::cuda::CUDAGuard guard(logits.device());
+  const auto f32 = logits.options().dtype(at::kFloat).requires_grad(false);
+  const at::IntArrayRef lead = logits.sizes().slice(0, logits.dim() - 1);
+  std::vector<int64_t> more(lead.begin(), lead.end());
+  Tensor lp, en, lse, st, tlp, tid;
+  if (tokens) lp = at::empty(lead, f32);
+  if (entropy) en = at::empty(lead, f32);
+  lse = at::empty(lead, f32);
+  more.push_back(2);
+  st = at::empty(more, f32);
+  if (top) {
+    more.back() = top;
+    tlp = at::empty(more, f32);
+    tid = at::empty(more, f32.dtype(at::kLong));
+  }
+  auto ptr = [](const Tensor& t) { return t.defined() ? t.data_ptr<float>() : nullptr; };
+  check("token_logprobs", token_logprobs(zr.p, zr.ld, tp, it, (float)scale, ignore.value_or(kNoToken), ptr(lp), ptr(en),
+                                         ptr(lse), ptr(st), ptr(tlp), top ? tid.data_ptr<int64_t>() : nullptr, top, zr.N,
+                                         zr.H, xc, stream_of(logits)));
+  return py::make_tuple(obj(lp), obj(en), obj(lse), obj(st), obj(tlp), obj(tid));
+}
+
+py::object token_logprobs_grad_(const Opt& dlogprob, const Tensor& logits, const Opt& tokens, const Tensor& row_stats,
+                                const Opt& entropy, const Opt& dentropy, const Opt& dlse, double scale,
+                                std::optional<int64_t> ignore, const Opt& out) {
+  const Rows zr = rows(logits, "logits");
+  const norm_dtype xc = code(logits.scalar_type(), "logits");
+  norm_itype it = NORM_I64;
+  const void* tp = row_tokens(tokens, logits, zr.N, &it);
+  if (dlogprob && !tokens) value_error("dlogprob needs tokens");
+  if (dentropy && !entropy) value_error("dentropy needs entropy");
+  if (!dlogprob && !dentropy && !dlse) value_error("dlogprob, dentropy and dlse are all None: no gradient arrives");
+  const float* dlp = stats(dlogprob, zr.N, "dlogprob", logits);
+  const float* en = stats(entropy, zr.N, "entropy", logits);
+  const float* den = stats(dentropy, zr.N, "dentropy", logits);
+  const float* dl = stats(dlse, zr.N, "dlse", logits);
+  const float* st = stats(Opt(row_stats), 2 * zr.N, "stats", logits);
+  const c10::cuda::CUDAGuard guard(logits.device());
+  const Tensor dz = out ? *out : new_like(logits);
+  const Rows dr = out ? like(dz, logits, zr, "out") : Rows{dz.data_ptr(), zr.N, zr.H, std::max<int64_t>(zr.H, 1)};
+  check("token_logprobs_grad",
+        token_logprobs_grad(dlp, zr.p, zr.ld, tp, it, st, en, den, dl, (float)scale, ignore.value_or(kNoToken), dr.p, dr.ld,
+                            zr.N, zr.H, xc, stream_of(logits)));
+  return obj(dz);
+}
+
 }  // namespace
 
 // The PyTorch this is compiled against, found in the file before it is loaded.
@@ -381,4 +609,12 @@ PYBIND11_MODULE(_bind, m) {
   m.def("embedding_lookup", &embedding_lookup_);
   m.def("embedding_rms", &embedding_rms_);
   m.def("embedding_grad", &embedding_grad_);
+  m.def("heads_view", [](const Tensor& t) {  // (B, T, H, D, strides) of a tensor on any device, for tests
+    const HeadsOf h = heads_view(t, "t");
+    return py::make_tuple(h.B, h.T, h.H, h.D, h.h.batch_stride, h.h.token_stride, h.h.head_stride);
+  });
+  m.def("head_rms_rotary", &head_rms_rotary_);
+  m.def("head_rms_rotary_grad", &head_rms_rotary_grad_);
+  m.def("token_logprobs", &token_logprobs_);
+  m.def("token_logprobs_grad", &token_logprobs_grad_);
 }

@@ -201,6 +201,7 @@ struct FirstLaunch {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   FirstLaunch(unsigned threads, size_t smem, cudaStream_t s, int cl) {
+    cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -215,7 +216,7 @@ struct FirstLaunch {
   }
   template <typename K, typename... Args>
   cudaError_t launch(unsigned grid, bool early, K kern, Args... args) {
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim.x = grid;
     cfg.numAttrs = early ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
     return e != cudaSuccess ? e : cudaGetLastError();

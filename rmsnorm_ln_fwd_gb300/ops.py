@@ -386,3 +386,66 @@ def embedding_grad(dh, tokens, num_rows: int, scale: float = 1.0, *, padding_idx
     dtype or float32, is overwritten, or added to with ``accumulate``; a fresh
     one takes ``param_dtype`` (default: dh's dtype)."""
     return _lib.bind().embedding_grad(dh, tokens, num_rows, scale, padding_idx, out, accumulate, param_dtype, workspace)
+
+
+# The operators inside the attention block and at the end of the stream, in the
+# C++ binding as well.
+
+
+def head_rms_rotary(q, k=None, gamma_q=None, gamma_k=None, cos=None, sin=None, positions=None, eps: float = 1e-6, *,
+                    interleaved: bool = False, q_out=None, k_out=None):
+    """RMSNorm of each head of the queries and keys, and the rotation by their
+    tokens' positions: n = x * rstd * gamma, then for each pair (a, b) of its
+    rotated columns n_a * cos - n_b * sin and n_b * cos + n_a * sin.
+
+    ``q`` is (T, Hq, D) or (B, T, Hq, D), ``k`` (or None) the same with Hk heads,
+    in any strides with contiguous heads (parts of a fused projection, transposed
+    (B, H, T, D) tensors).  ``cos`` and ``sin`` are (rows, R/2), in float32 or the
+    rows' dtype: the first R columns of a head are rotated, in pairs (i, i + R/2)
+    or, ``interleaved``, (2i, 2i + 1).  Without them only the norm is taken.
+    ``positions`` are int32 or int64, (T,) or (B, T); None: 0, 1, ... in each
+    sequence.  A position outside the table gives zeros and sets
+    NORM_DEVICE_ERR_BAD_POSITION in the device error word.  ``q_out`` and ``k_out``
+    may be fresh (default, contiguous), ``q`` and ``k`` themselves, or any clear
+    tensor.  Returns (q_out, k_out)."""
+    return _lib.bind().head_rms_rotary(q, k, gamma_q, gamma_k, cos, sin, positions, eps, interleaved, q_out, k_out)
+
+
+def head_rms_rotary_grad(dyq, dyk, q, k=None, gamma_q=None, gamma_k=None, cos=None, sin=None, positions=None,
+                         eps: float = 1e-6, *, interleaved: bool = False, need_param_grads: bool = True, workspace=None,
+                         dq=None, dk=None, param_dtype=None):
+    """Gradient of head_rms_rotary from its inputs and its outputs' gradients.
+
+    ``dq`` may be ``dyq`` and ``dk`` may be ``dyk`` itself (default: fresh,
+    contiguous).  Returns (dq, dk, dgamma_q, dgamma_k); a gamma that is None counts
+    as ones and has a gradient, in the other gamma's dtype (or ``param_dtype``, else
+    q's); dk and dgamma_k are None without k, both dgamma without
+    ``need_param_grads``."""
+    return _lib.bind().head_rms_rotary_grad(dyq, dyk, q, k, gamma_q, gamma_k, cos, sin, positions, eps, interleaved,
+                                            need_param_grads, workspace, dq, dk, param_dtype)
+
+
+def token_logprobs(logits, tokens=None, scale: float = 1.0, *, top: int = 0, ignore_index=None, entropy: bool = True):
+    """Log probabilities of ``tokens`` under softmax(scale * logits), one a row,
+    with the rows' entropy and their ``top`` most probable tokens.
+
+    ``tokens`` are int32 or int64 of the leading dims' shape (or None).  A row
+    whose token is ``ignore_index`` has log probability 0; so has one whose token
+    is outside the vocabulary, which sets NORM_DEVICE_ERR_BAD_TOKEN.  Returns
+    (logprob, entropy, lse, stats, top_logprobs, top_ids): lse is the log of the
+    sum of exp(scale * logits), stats (..., 2) what token_logprobs_grad needs, the
+    alternatives (..., top) in descending order, equal logits by id, int64; -1
+    where fewer tokens are left than asked for (logits of -inf are not listed).
+    None stands for what was not asked for."""
+    return _lib.bind().token_logprobs(logits, tokens, scale, top, ignore_index, entropy)
+
+
+def token_logprobs_grad(dlogprob, logits, tokens, stats, entropy=None, dentropy=None, dlse=None, scale: float = 1.0, *,
+                        ignore_index=None, out=None):
+    """Gradient of the logits from those of token_logprobs' log probabilities,
+    entropies and lse (float32, one a row, contiguous; None for zeros).
+
+    ``stats`` and, with ``dentropy``, ``entropy`` are the forward's.  ``out`` may be
+    ``logits`` itself.  The alternatives have no gradient."""
+    return _lib.bind().token_logprobs_grad(dlogprob, logits, tokens, stats, entropy, dentropy, dlse, scale, ignore_index,
+                                           out)
