@@ -27,34 +27,43 @@
 
 namespace normk {
 
+// Two CTAs of eight warps an SM, 128 registers.  (us, 16384 and 8192 tokens of 32+8
+// heads of 128, bf16, forward and gradient: 59.8, 51.8; five CTAs of four warps
+// 59.9, 57; three of six 59.4, 68; three of eight, 80 registers, 59.8, 69.)
 constexpr int kHeadWarps = 8;
+constexpr int kHeadPerSm = 2;
 constexpr int kHeadThreads = 32 * kHeadWarps;
 
 // A lane's 16 columns: [c0, c0 + n0) and [c1, c1 + n1), in halves [0, R/2) and
 // [R/2, R), or past R; with PAIRS neighbours.  CA columns an access.  As fp32,
 // pair i (of eight) is element i of `a` and of `b`.
-template <typename D, int CA, bool PAIRS>
+// FULL > 0: heads of FULL columns, all of them rotated, a power of two: what
+// follows from that is known at compile time.
+template <typename D, int CA, bool PAIRS, int FULL>
 struct HeadLane {
   using T = typename D::T;
   static constexpr int ES = (int)sizeof(T);
   static constexpr int NW = 16 * ES / 4;  // packed words
-  int c0, c1, n0, n1;
-  int nr;  // rotated pairs
-  int p0;  // the first one's table column
+  int c0, c1_, n0_, n1_;
+  int nr_;  // rotated pairs
+
+  __device__ __forceinline__ int c1() const { return FULL ? c0 + (PAIRS ? 8 : FULL / 2) : c1_; }
+  __device__ __forceinline__ int n0() const { return FULL ? 8 : n0_; }
+  __device__ __forceinline__ int n1() const { return FULL ? 8 : n1_; }
+  __device__ __forceinline__ int nr() const { return FULL ? 8 : nr_; }
 
   __device__ __forceinline__ HeadLane(int unit, int cols, int R) {
     const int rot = R / 2, units = (rot + 7) / 8;
     if (PAIRS || unit >= units) {
       c0 = PAIRS ? 16 * unit : R + 16 * (unit - units);
-      c1 = c0 + 8;
-      n0 = clamp8(cols - c0);
-      n1 = clamp8(cols - c1);
-      p0 = 8 * unit;
-      nr = PAIRS ? clamp8(rot - p0) : 0;
+      c1_ = c0 + 8;
+      n0_ = clamp8(cols - c0);
+      n1_ = clamp8(cols - c1_);
+      nr_ = PAIRS ? clamp8(rot - 8 * unit) : 0;
     } else {
-      c0 = p0 = 8 * unit;
-      c1 = rot + c0;
-      n0 = n1 = nr = clamp8(rot - c0);
+      c0 = 8 * unit;
+      c1_ = rot + c0;
+      n0_ = n1_ = nr_ = clamp8(rot - c0);
     }
   }
   __device__ static __forceinline__ int clamp8(int n) { return n < 0 ? 0 : n > 8 ? 8 : n; }
@@ -108,12 +117,12 @@ struct HeadLane {
     }
   }
   __device__ __forceinline__ void load(const T* head, uint32_t (&w)[NW]) const {
-    load_half(head + c0, n0, w);
-    load_half(head + c1, n1, w + NW / 2);
+    load_half(head + c0, n0(), w);
+    load_half(head + c1(), n1(), w + NW / 2);
   }
   __device__ __forceinline__ void store(T* head, const uint32_t (&w)[NW]) const {
-    store_half(head + c0, n0, w);
-    store_half(head + c1, n1, w + NW / 2);
+    store_half(head + c0, n0(), w);
+    store_half(head + c1(), n1(), w + NW / 2);
   }
   __device__ static __forceinline__ void unpack(const uint32_t (&w)[NW], float2 (&a)[4], float2 (&b)[4]) {
     if constexpr (PAIRS) {
@@ -148,288 +157,448 @@ struct HeadLane {
   }
   // Column of pair i's members, or -1 past the head.
   __device__ __forceinline__ int col_a(int i) const {
-    if constexpr (PAIRS) return 2 * i < n0 + n1 ? c0 + 2 * i : -1;
-    return i < n0 ? c0 + i : -1;
+    if constexpr (PAIRS) return 2 * i < n0() + n1() ? c0 + 2 * i : -1;
+    return i < n0() ? c0 + i : -1;
   }
   __device__ __forceinline__ int col_b(int i) const {
-    if constexpr (PAIRS) return 2 * i + 1 < n0 + n1 ? c0 + 2 * i + 1 : -1;
-    return i < n1 ? c1 + i : -1;
+    if constexpr (PAIRS) return 2 * i + 1 < n0() + n1() ? c0 + 2 * i + 1 : -1;
+    return i < n1() ? c1() + i : -1;
   }
-  // gamma of the lane's columns (null: ones), 0 past the head.
-  __device__ __forceinline__ void gamma(const void* g, bool f32, float2 (&a)[4], float2 (&b)[4]) const {
-    float v[16];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int ca = col_a(i), cb = col_b(i);
-      v[i] = ca < 0 ? 0.f : g ? load_param<D>(g, ca, f32) : 1.f;
-      v[8 + i] = cb < 0 ? 0.f : g ? load_param<D>(g, cb, f32) : 1.f;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      a[k] = make_float2(v[2 * k], v[2 * k + 1]);
-      b[k] = make_float2(v[8 + 2 * k], v[9 + 2 * k]);
-    }
-  }
-  // The lane's columns of one table row.
-  __device__ __forceinline__ void table(const void* t, int64_t row, int64_t ld, bool f32, bool vec, float2 (&c)[4]) const {
-    if (vec) {
-      const float* p = reinterpret_cast<const float*>(t) + row * ld + p0;
+  // Every rotated pair turned by the angles in the lane's slot; the others stay,
+  // whatever they hold.  BACK: the other way.
+  template <bool BACK>
+  __device__ __forceinline__ void turn(float2 (&a)[4], float2 (&b)[4], uint32_t slot) const {
+    if (nr() == 8) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float4 v = 4 * k < nr ? *reinterpret_cast<const float4*>(p + 4 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
-        c[2 * k] = make_float2(v.x, v.y);
-        c[2 * k + 1] = make_float2(v.z, v.w);
-      }
-      return;
-    }
-    const void* p = reinterpret_cast<const unsigned char*>(t) + (row * ld + p0) * (f32 ? 4 : ES);
-    float v[8];
+        float2 c[2], s[2];
+        lds_pairs(slot + 16 * k, c);
+        lds_pairs(slot + 32 + 16 * k, s);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < nr ? load_param<D>(p, i, f32) : 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) c[k] = make_float2(v[2 * k], v[2 * k + 1]);
-  }
-  // Every rotated pair turned by (c, s); the others stay, whatever they hold.
-  __device__ __forceinline__ void turn(float2 (&a)[4], float2 (&b)[4], const float2 (&c)[4], const float2 (&s)[4]) const {
-    if (nr == 8) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 m = mul2(b[k], s[k]), u = a[k];
-        a[k] = fma2(u, c[k], make_float2(-m.x, -m.y));
-        b[k] = fma2(u, s[k], mul2(b[k], c[k]));
-      }
-    } else if (nr > 0) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (2 * k < nr) {
-          const float u = a[k].x;
-          a[k].x = fmaf(u, c[k].x, -(b[k].x * s[k].x));
-          b[k].x = fmaf(u, s[k].x, b[k].x * c[k].x);
+        for (int i = 0; i < 2; ++i) {
+          float2& x = BACK ? b[2 * k + i] : a[2 * k + i];
+          float2& y = BACK ? a[2 * k + i] : b[2 * k + i];
+          const float2 u = sub2(mul2(x, c[i]), mul2(y, s[i]));
+          y = fma2(y, c[i], mul2(x, s[i]));
+          x = u;
         }
-        if (2 * k + 1 < nr) {
-          const float u = a[k].y;
-          a[k].y = fmaf(u, c[k].y, -(b[k].y * s[k].y));
-          b[k].y = fmaf(u, s[k].y, b[k].y * c[k].y);
+      }
+    } else if (nr() > 0) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float* x = reinterpret_cast<float*>(BACK ? b : a);
+        float* y = reinterpret_cast<float*>(BACK ? a : b);
+#pragma unroll
+        for (int i = 2 * k; i < 2 * k + 2; ++i) {
+          if (i < nr()) {
+            const float c = __uint_as_float(lds_u32(slot + 4 * i)), s = __uint_as_float(lds_u32(slot + 32 + 4 * i));
+            const float u = x[i] * c - y[i] * s;
+            y[i] = fmaf(y[i], c, x[i] * s);
+            x[i] = u;
+          }
         }
       }
     }
   }
 };
 
-__device__ __forceinline__ int64_t head_position(const HeadArgs& a, int64_t b, int64_t t) {
-  if (a.positions == nullptr) return t;
-  const int64_t i = b * a.pb + t * a.pt;
-  return a.pos64 ? reinterpret_cast<const long long*>(a.positions)[i] : (int64_t) reinterpret_cast<const int*>(a.positions)[i];
-}
+// A lane's parameters in shared memory: 16 floats and four of padding, so that
+// the 16-byte reads of eight lanes fall into distinct banks.
+constexpr int kHeadSlot = 20;
 
-// U heads of a group are in flight at a time.
-template <typename D, int CA, bool PAIRS, int U>
-__global__ void __launch_bounds__(kHeadThreads, 2) head_rotary_kernel(const HeadArgs a) {
-  using Lane = HeadLane<D, CA, PAIRS>;
-  using T = typename D::T;
-  const int lane = threadIdx.x & 31;
-  const int groups = 32 / a.lanes, group = lane / a.lanes;
-  const Lane me(lane & (a.lanes - 1), a.D, a.R);
-  const float inv_d = 1.f / (float)a.D;
-  const int heads = a.side[0].heads + a.side[1].heads;
-  const int share = ((heads + a.slices - 1) / a.slices + groups - 1) / groups * groups;
-  const int64_t items = a.N * a.slices;
-  pdl_launch_dependents();
-  pdl_wait_primary();
-  for (int64_t item = (int64_t)blockIdx.x * kHeadWarps + (threadIdx.x >> 5); item < items;
-       item += (int64_t)gridDim.x * kHeadWarps) {
-    const int64_t n = a.slices == 1 ? item : item / a.slices;
-    const int slice = a.slices == 1 ? 0 : (int)(item - n * a.slices);
-    const int64_t b = a.B == 1 ? 0 : n / a.T, t = n - b * a.T;
-    bool good = true;
-    float2 c[4], s[4];
-    if (a.R) {
-      const int64_t pos = head_position(a, b, t);
-      good = pos >= 0 && pos < a.table_rows;
-      if (good) {
-        me.table(a.cos, pos, a.ldcos, a.c_f32, a.cvec, c);
-        me.table(a.sin, pos, a.ldsin, a.c_f32, a.cvec, s);
-      } else if (lane == 0) {
-        atomicOr(a.err, kErrBadPosition);
-      }
-    }
-#pragma unroll 1
-    for (int k = 0; k < 2; ++k) {
-      const HeadSide& side = a.side[k];
-      const int from = max(slice * share - (k ? a.side[0].heads : 0), 0);
-      const int to = min((slice + 1) * share - (k ? a.side[0].heads : 0), side.heads);
-      if (from >= to) continue;
-      float2 ga[4], gb[4];
-      me.gamma(side.gamma, a.w_f32, ga, gb);
-      const T* x = reinterpret_cast<const T*>(side.x.p) + b * side.x.sb + t * side.x.st;
-      T* y = reinterpret_cast<T*>(side.y.p) + b * side.y.sb + t * side.y.st;
-#pragma unroll 1
-      for (int h = from + group; h - group < to; h += U * groups) {
-        uint32_t w[U][Lane::NW];
+// gamma of a side in slots (null: ones; 0 past the head).
+template <typename Lane, typename D>
+__device__ __forceinline__ void head_gamma(float* slots, const HeadArgs& a, const void* g, int t, int nt) {
+  for (int unit = t; unit < a.lanes; unit += nt) {
+    const Lane l(unit, a.D, a.R);
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-          if (h + i * groups < to) me.load(x + (h + i * groups) * side.x.sh, w[i]);
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          float2 p[4], q[4];
-          Lane::unpack(w[i], p, q);
-          float2 sum = splat2(0.f);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sum = fma2(q[j], q[j], fma2(p[j], p[j], sum));
-          float v[1] = {sum.x + sum.y};
-          warp_sum_pow2<1>(v, a.lanes);
-          const float2 r = splat2(good ? rsqrtf(fmaf(v[0], inv_d, a.eps)) : 0.f);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            p[j] = mul2(mul2(p[j], r), ga[j]);
-            q[j] = mul2(mul2(q[j], r), gb[j]);
-          }
-          me.turn(p, q, c, s);
-          Lane::pack(p, q, w[i]);
-          if (!good) {
-#pragma unroll
-            for (int j = 0; j < Lane::NW; ++j) w[i][j] = 0u;
-          }
-          if (h + i * groups < to) me.store(y + (h + i * groups) * side.y.sh, w[i]);
-        }
-      }
+    for (int i = 0; i < 8; ++i) {
+      const int ca = l.col_a(i), cb = l.col_b(i);
+      slots[unit * kHeadSlot + i] = ca < 0 ? 0.f : g ? load_param<D>(g, ca, a.w_f32) : 1.f;
+      slots[unit * kHeadSlot + 8 + i] = cb < 0 ? 0.f : g ? load_param<D>(g, cb, a.w_f32) : 1.f;
     }
   }
 }
 
-// The gradient.  A CTA takes one side (queries: the first a.ctas[0] CTAs), whose
-// warps walk the tokens with each column's part of dgamma in registers; the parts
-// meet in shared memory and become the CTA's partial row.
-template <typename D, int CA, bool PAIRS, int U>
-__global__ void __launch_bounds__(kHeadThreads, 2) head_rotary_grad_kernel(const HeadArgs a) {
-  using Lane = HeadLane<D, CA, PAIRS>;
+// A token of the batch.
+struct HeadToken {
+  unsigned b, t;
+  __device__ __forceinline__ HeadToken(const HeadArgs& a, unsigned n) : b(a.B == 1 ? 0u : n / (unsigned)a.T), t(n - b * (unsigned)a.T) {}
+  __device__ __forceinline__ void step(const HeadArgs& a) {
+    if (++t == (unsigned)a.T) {
+      t = 0;
+      ++b;
+    }
+  }
+};
+
+// A warp's share of the work, in units of one head a group: the units of all
+// tokens, a.its each, are shared out evenly, whichever tokens they fall into.
+struct HeadShare {
+  unsigned first;  // the token of the first one
+  int lo;          // and which of its units that is
+  int64_t left;    // units
+  __device__ __forceinline__ HeadShare(const HeadArgs& a, int warp) {
+    const int64_t u = warp * a.each + min((int64_t)warp, a.extra);
+    left = a.each + (warp < a.extra);
+    first = (unsigned)(u < (int64_t(1) << 31) ? (unsigned)u / (unsigned)a.its : u / a.its);
+    lo = (int)(u - (int64_t)first * a.its);
+  }
+  // Units [lo, hi) of the token at hand; false behind the last.
+  __device__ __forceinline__ bool take(const HeadArgs& a, int& from, int& to) {
+    if (left <= 0) return false;
+    from = lo;
+    to = (int)min((int64_t)a.its, lo + left);
+    left -= to - from;
+    lo = 0;
+    return true;
+  }
+};
+
+// The angles of a warp's tokens: positions two tokens ahead and table rows one
+// ahead are in registers, the token's own angles in the warp's slots.
+template <typename D, int LANES>
+struct HeadAngles {
+  static constexpr int AHEAD = LANES == 16 ? 8 : 4;  // values of a table row a lane holds: 128 or 256
+  const HeadArgs& a;
+  float* slots;
+  int lane;
+  HeadToken ahead;  // the token whose position is to be fetched
+  int tokens;       // that are left from it on
+  int64_t pos;      // the position of the token after the next one
+  int64_t row;      // the next one's, and its table row
+  float v[AHEAD];
+  bool next_good;
+
+  __device__ __forceinline__ HeadAngles(const HeadArgs& a_, float* slots_, int lane_, const HeadToken& first, int tokens_)
+      : a(a_), slots(slots_), lane(lane_), ahead(first), tokens(tokens_), pos(0), row(0), next_good(true) {
+    if (!a.R) return;
+    fetch_position();
+    fetch_row();
+    fetch_position();
+  }
+  __device__ __forceinline__ void fetch_position() {
+    if (tokens-- <= 0) return;
+    pos = ahead.t;
+    if (a.positions) {
+      const int64_t i = ahead.b * a.pb + ahead.t * a.pt;
+      pos = a.pos64 ? reinterpret_cast<const long long*>(a.positions)[i]
+                    : (int64_t) reinterpret_cast<const int*>(a.positions)[i];
+    }
+    ahead.step(a);
+  }
+  // Value e of the row [cos | sin].
+  __device__ __forceinline__ float value(int e) const {
+    const int half = a.R / 2;
+    const void* t = e < half ? a.cos : a.sin;
+    const int64_t at = row * (e < half ? a.ldcos : a.ldsin) + (e < half ? e : e - half);
+    return a.c_f32 ? reinterpret_cast<const float*>(t)[at] : load_elem<D>(t, at);
+  }
+  __device__ __forceinline__ void put(int e, float x) const {
+    const int half = a.R / 2, i = e < half ? e : e - half;
+    slots[i / 8 * kHeadSlot + i % 8 + (e < half ? 0 : 8)] = x;
+  }
+  __device__ __forceinline__ void fetch_row() {
+    row = pos;
+    next_good = row >= 0 && row < a.table_rows;
+    if (!next_good) return;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (lane + 32 * k < a.R) v[k] = value(lane + 32 * k);
+  }
+  // The next token's angles go into the slots, and those after it are asked for.
+  // Whether its position is in the table.
+  __device__ __forceinline__ bool turn_over() {
+    if (!a.R) return true;
+    const bool good = next_good;
+    __syncwarp();  // the lanes are through with the angles before
+    if (good) {
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k)
+        if (lane + 32 * k < a.R) put(lane + 32 * k, v[k]);
+      for (int e = lane + 32 * AHEAD; e < a.R; e += 32) put(e, value(e));
+    } else if (lane == 0) {
+      atomicOr(a.err, kErrBadPosition);
+    }
+    __syncwarp();
+    fetch_row();
+    fetch_position();
+    return good;
+  }
+};
+
+// Where a token's heads are: I is 32 bits where every tensor of the call has
+// fewer than 2^31 elements from its first to its last, else 64.  Offsets of head 0
+// of the queries, and of where head 0 would be if the keys' went on behind them.
+template <typename I>
+struct HeadPlace {
+  I q, k;
+  __device__ __forceinline__ HeadPlace(const HeadToken& n, const HeadView& vq, const HeadView& vk, int hq)
+      : q((I)n.b * (I)vq.sb + (I)n.t * (I)vq.st), k((I)n.b * (I)vk.sb + (I)n.t * (I)vk.st - (I)hq * (I)vk.sh) {}
+};
+template <typename T, typename I>
+__device__ __forceinline__ T* head_at(const HeadView& q, const HeadView& k, const HeadPlace<I>& p, int hq, int h) {
+  const bool first = h < hq;
+  const I at = first ? p.q + (I)h * (I)q.sh : p.k + (I)h * (I)k.sh;
+  return reinterpret_cast<T*>(first ? q.p : k.p) + at;
+}
+
+// Sum over each `lanes` lanes; LANES: as a compile-time value, or 0.
+template <int K, int LANES>
+__device__ __forceinline__ void lanes_sum(float (&v)[K], int lanes) {
+  warp_sum_pow2<K>(v, LANES ? LANES : lanes);
+}
+
+// U heads of a group are in flight, over the ends of tokens, while as many are at
+// work.  LANES > 0: heads of 16 * LANES columns, all rotated.
+template <typename D, int CA, bool PAIRS, int U, int LANES, typename I>
+__global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_kernel(const HeadArgs a) {
+  using Lane = HeadLane<D, CA, PAIRS, 16 * LANES>;
   using T = typename D::T;
-  extern __shared__ float parts[];  // [warps][D]
+  extern __shared__ __align__(16) float slots[];  // gamma of both sides, each warp's angles
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int groups = 32 / a.lanes, group = lane / a.lanes;
-  const Lane me(lane & (a.lanes - 1), a.D, a.R);
+  const int lanes = LANES ? LANES : a.lanes;
+  const int groups = 32 / lanes, group = lane / lanes, unit = lane & (lanes - 1);
+  const Lane me(unit, a.D, a.R);
   const float inv_d = 1.f / (float)a.D;
-  const bool keys = (int)blockIdx.x >= a.ctas[0];
-  const HeadSide& side = a.side[keys];
-  const int cta = keys ? blockIdx.x - a.ctas[0] : blockIdx.x, ctas = a.ctas[keys], slices = a.slice[keys];
-  const int share = ((side.heads + slices - 1) / slices + groups - 1) / groups * groups;
-  const int64_t items = a.N * slices;
-  float2 da[4], db[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) da[j] = db[j] = splat2(0.f);
+  const int hq = a.side[0].heads, heads = hq + a.side[1].heads;
+  const uint32_t gammas = smem_u32(slots + unit * kHeadSlot);
+  float* angles = slots + (2 + warp) * lanes * kHeadSlot;
+  const uint32_t angle = smem_u32(angles + unit * kHeadSlot);
   pdl_launch_dependents();
   pdl_wait_primary();
-  float2 ga[4], gb[4];
-  me.gamma(side.gamma, a.w_f32, ga, gb);
-  for (int64_t item = (int64_t)cta * kHeadWarps + warp; item < items; item += (int64_t)ctas * kHeadWarps) {
-    const int64_t n = slices == 1 ? item : item / slices;
-    const int from = slices == 1 ? 0 : (int)(item - n * slices) * share, to = min(from + share, side.heads);
-    const int64_t b = a.B == 1 ? 0 : n / a.T, t = n - b * a.T;
-    bool good = true;
-    float2 c[4], s[4];
-    if (a.R) {
-      const int64_t pos = head_position(a, b, t);
-      good = pos >= 0 && pos < a.table_rows;
-      if (good) {
-        me.table(a.cos, pos, a.ldcos, a.c_f32, a.cvec, c);
-        me.table(a.sin, pos, a.ldsin, a.c_f32, a.cvec, s);
+  HeadShare share(a, blockIdx.x * kHeadWarps + warp);
+  HeadToken token(a, share.first);
+  const int tokens = share.left > 0 ? (int)((share.lo + share.left + a.its - 1) / a.its) : 0;
+  HeadPlace<I> src(token, a.side[0].x, a.side[1].x, hq), dst(token, a.side[0].y, a.side[1].y, hq);
+  uint32_t next[U][Lane::NW];
+  auto fetch = [&](int h, int to) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[j] = make_float2(-s[j].x, -s[j].y);
-      } else if (lane == 0) {
-        atomicOr(a.err, kErrBadPosition);
-      }
-    }
-    const T* x = reinterpret_cast<const T*>(side.x.p) + b * side.x.sb + t * side.x.st;
-    const T* dy = reinterpret_cast<const T*>(side.dy.p) + b * side.dy.sb + t * side.dy.st;
-    T* dx = reinterpret_cast<T*>(side.y.p) + b * side.y.sb + t * side.y.st;
+    for (int i = 0; i < U; ++i)
+      if (h + i * groups < to) me.load(head_at<T, I>(a.side[0].x, a.side[1].x, src, hq, h + i * groups), next[i]);
+  };
+  int lo, hi, from, to;
+  // the next token's units as heads [from, to), whose first ones are asked for
+  auto enter = [&] {
+    if (!share.take(a, lo, hi)) return false;
+    from = lo * groups + group;
+    to = min(hi * groups, heads);
+    src = HeadPlace<I>(token, a.side[0].x, a.side[1].x, hq);
+    dst = HeadPlace<I>(token, a.side[0].y, a.side[1].y, hq);
+    token.step(a);
+    fetch(from, to);
+    return true;
+  };
+  HeadAngles<D, LANES> way(a, angles, lane, token, tokens);
+  bool on = enter();
+  for (int k = 0; k < 2; ++k)
+    head_gamma<Lane, D>(slots + k * lanes * kHeadSlot, a, a.side[k].gamma, threadIdx.x, kHeadThreads);
+  __syncthreads();
+  while (on) {
+    const bool good = way.turn_over();
+    const HeadPlace<I> here = dst;
+    const int end = to;
 #pragma unroll 1
-    for (int h = from + group; h - group < to; h += U * groups) {
-      uint32_t w[U][Lane::NW], g[U][Lane::NW];
+    for (int h = from, more = 1; more; h += U * groups) {
+      uint32_t now[U][Lane::NW];
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int j = 0; j < Lane::NW; ++j) now[i][j] = next[i][j];
+      more = h - group + U * groups < end;
+      if (more)
+        fetch(h + U * groups, end);
+      else
+        on = enter();
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        if (h + i * groups < to) {
-          me.load(x + (h + i * groups) * side.x.sh, w[i]);
-          me.load(dy + (h + i * groups) * side.dy.sh, g[i]);
-        }
-      }
+        const int k = h + i * groups;
+        if (k - group >= end) break;  // the same for the whole warp
+        float2 p[4], q[4];
+        Lane::unpack(now[i], p, q);
+        float2 sum = splat2(0.f);
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        float2 p[4], q[4], u[4], v[4];
-        Lane::unpack(w[i], p, q);
-        Lane::unpack(g[i], u, v);
-        me.turn(u, v, c, s);
-        float2 sx = splat2(0.f), sw = splat2(0.f);
+        for (int j = 0; j < 4; ++j) sum = fma2(q[j], q[j], fma2(p[j], p[j], sum));
+        float v[1] = {sum.x + sum.y};
+        lanes_sum<1, LANES>(v, lanes);
+        const float2 r = splat2(rsqrtf(fmaf(v[0], inv_d, a.eps)));
+        const uint32_t gamma = gammas + (k < hq ? 0 : lanes * kHeadSlot * 4);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          sx = fma2(q[j], q[j], fma2(p[j], p[j], sx));
-          sw = fma2(mul2(v[j], gb[j]), q[j], fma2(mul2(u[j], ga[j]), p[j], sw));
+        for (int j = 0; j < 2; ++j) {
+          float2 g[2];
+          lds_pairs(gamma + 16 * j, g);
+          p[2 * j] = mul2(mul2(p[2 * j], r), g[0]);
+          p[2 * j + 1] = mul2(mul2(p[2 * j + 1], r), g[1]);
+          lds_pairs(gamma + 32 + 16 * j, g);
+          q[2 * j] = mul2(mul2(q[2 * j], r), g[0]);
+          q[2 * j + 1] = mul2(mul2(q[2 * j + 1], r), g[1]);
         }
-        float m[2] = {sx.x + sx.y, sw.x + sw.y};
-        warp_sum_pow2<2>(m, a.lanes);
-        const float r = rsqrtf(fmaf(m[0], inv_d, a.eps));
-        // dx = rstd (w - x rstd^2 mean(w x))
-        const float2 r2 = splat2(r), k2 = splat2(-(m[1] * inv_d) * r * r);
-        if (good && h + i * groups < to) {
-          float2 o[4];
+        if (good) {
+          me.template turn<false>(p, q, angle);
+          Lane::pack(p, q, now[i]);
+        } else {  // the token has no position: zeros
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            da[j] = fma2(u[j], mul2(p[j], r2), da[j]);
-            db[j] = fma2(v[j], mul2(q[j], r2), db[j]);
-            o[j] = mul2(fma2(p[j], k2, mul2(u[j], ga[j])), r2);
-            q[j] = mul2(fma2(q[j], k2, mul2(v[j], gb[j])), r2);
-          }
-          Lane::pack(o, q, w[i]);
+          for (int j = 0; j < Lane::NW; ++j) now[i][j] = 0u;
         }
-        if (!good) {
-#pragma unroll
-          for (int j = 0; j < Lane::NW; ++j) w[i][j] = 0u;
-        }
-        if (h + i * groups < to) me.store(dx + (h + i * groups) * side.y.sh, w[i]);
+        if (k < end) me.store(head_at<T, I>(a.side[0].y, a.side[1].y, here, hq, k), now[i]);
       }
     }
   }
-  if (!a.want) return;
-  // groups of a warp, then the warps, in a fixed order
+}
+
+// The gradient.  A lane sums dgamma of its columns, for either side, in slots of
+// its own in shared memory (in registers, with a change of sides at every token,
+// they cost the second buffer's: fp32 4096x32+8x128 47.5 -> 52.3 us); a CTA's sums
+// become its partial row.  The next head of a group is in flight while one is at
+// work.
+template <typename D, int CA, bool PAIRS, int LANES, typename I>
+__global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_grad_kernel(const HeadArgs a) {
+  using Lane = HeadLane<D, CA, PAIRS, 16 * LANES>;
+  using T = typename D::T;
+  extern __shared__ __align__(16) float slots[];  // gamma of both sides, each warp's angles, each lane's sums
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lanes = LANES ? LANES : a.lanes;
+  const int groups = 32 / lanes, group = lane / lanes, unit = lane & (lanes - 1);
+  const Lane me(unit, a.D, a.R);
+  const float inv_d = 1.f / (float)a.D;
+  const int hq = a.side[0].heads, heads = hq + a.side[1].heads;
+  const uint32_t gammas = smem_u32(slots + unit * kHeadSlot);
+  float* angles = slots + (2 + warp) * lanes * kHeadSlot;
+  const uint32_t angle = smem_u32(angles + unit * kHeadSlot);
+  float* sums = slots + (2 + kHeadWarps) * lanes * kHeadSlot;  // [warp][side][lane]
+  float* mine = sums + (warp * 64 + lane) * kHeadSlot;
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  HeadShare share(a, blockIdx.x * kHeadWarps + warp);
+  HeadToken token(a, share.first);
+  const int tokens = share.left > 0 ? (int)((share.lo + share.left + a.its - 1) / a.its) : 0;
+  uint32_t wx[Lane::NW], wy[Lane::NW];
+  struct Both {
+    HeadPlace<I> x, dy;
+  };
+  auto places = [&] {
+    return Both{HeadPlace<I>(token, a.side[0].x, a.side[1].x, hq), HeadPlace<I>(token, a.side[0].dy, a.side[1].dy, hq)};
+  };
+  auto load = [&](const Both& at, int h, uint32_t (&x)[Lane::NW], uint32_t (&dy)[Lane::NW]) {
+    me.load(head_at<T, I>(a.side[0].x, a.side[1].x, at.x, hq, h), x);
+    me.load(head_at<T, I>(a.side[0].dy, a.side[1].dy, at.dy, hq, h), dy);
+  };
+  // the first token's units as heads [first, last)
+  int lo = 0, hi = 0;
+  bool on = share.take(a, lo, hi);
+  int first = lo * groups + group, last = min(hi * groups, heads);
+  Both src = places();
+  if (first < last) load(src, first, wx, wy);
+  HeadAngles<D, LANES> way(a, angles, lane, token, tokens);
+  for (int k = 0; k < 2; ++k) {
+    head_gamma<Lane, D>(slots + k * lanes * kHeadSlot, a, a.side[k].gamma, threadIdx.x, kHeadThreads);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float v[4] = {da[j].x, da[j].y, db[j].x, db[j].y};
-    for (int off = a.lanes; off < 32; off <<= 1) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
-    }
-    if (group == 0) {
-      float* row = parts + warp * a.D;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (me.col_a(2 * j + i) >= 0) row[me.col_a(2 * j + i)] = v[i];
-        if (me.col_b(2 * j + i) >= 0) row[me.col_b(2 * j + i)] = v[2 + i];
-      }
-    }
+    for (int j = 0; j < 4; ++j) reinterpret_cast<float4*>(mine + k * 32 * kHeadSlot)[j] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < a.D; i += kHeadThreads) {
-    float sum = 0.f;
+  while (on) {
+    const HeadPlace<I> dst(token, a.side[0].y, a.side[1].y, hq);
+    const int from = first, end = last;
+    // the token behind this one
+    lo = hi = 0;
+    on = share.take(a, lo, hi);
+    if (on) token.step(a);
+    first = lo * groups + group;
+    last = min(hi * groups, heads);
+    const Both then = places();
+    const bool good = way.turn_over();
+#pragma unroll 1
+    for (int k = from; k - group < end; k += groups) {
+      float2 p[4], q[4], u[4], v[4];
+      Lane::unpack(wx, p, q);
+      Lane::unpack(wy, u, v);
+      if (k - group + groups < end) {
+        if (k + groups < end) load(src, k + groups, wx, wy);
+      } else if (first < last) {
+        load(then, first, wx, wy);
+      }
+      const int which = k < hq ? 0 : 1;
+      if (good) me.template turn<true>(u, v, angle);
+      float2 sx = splat2(0.f), sw = splat2(0.f);
+      const uint32_t gamma = gammas + which * lanes * kHeadSlot * 4;
 #pragma unroll
-    for (int w = 0; w < kHeadWarps; ++w) sum += parts[w * a.D + i];
-    a.ws[(int64_t)blockIdx.x * a.D + i] = sum;
+      for (int j = 0; j < 2; ++j) {
+        float2 g[2], e[2];
+        lds_pairs(gamma + 16 * j, g);
+        lds_pairs(gamma + 32 + 16 * j, e);
+#pragma unroll
+        for (int l = 0; l < 2; ++l) {
+          const int c = 2 * j + l;
+          sx = fma2(q[c], q[c], fma2(p[c], p[c], sx));
+          sw = fma2(mul2(v[c], e[l]), q[c], fma2(mul2(u[c], g[l]), p[c], sw));
+        }
+      }
+      float m[2] = {sx.x + sx.y, sw.x + sw.y};
+      lanes_sum<2, LANES>(m, lanes);
+      if (k >= end) continue;  // no lane exchanges anything below
+      uint32_t o[Lane::NW];
+      if (good) {
+        const float r = rsqrtf(fmaf(m[0], inv_d, a.eps));
+        // dx = rstd (w - x rstd^2 mean(w x)); w is formed again rather than kept
+        const float2 r2 = splat2(r), k2 = splat2(-(m[1] * inv_d) * r * r);
+        float4* at = reinterpret_cast<float4*>(mine + which * 32 * kHeadSlot);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float4 x = at[j], y = at[2 + j];
+          const float2 x0 = fma2(u[2 * j], mul2(p[2 * j], r2), make_float2(x.x, x.y));
+          const float2 x1 = fma2(u[2 * j + 1], mul2(p[2 * j + 1], r2), make_float2(x.z, x.w));
+          const float2 y0 = fma2(v[2 * j], mul2(q[2 * j], r2), make_float2(y.x, y.y));
+          const float2 y1 = fma2(v[2 * j + 1], mul2(q[2 * j + 1], r2), make_float2(y.z, y.w));
+          at[j] = make_float4(x0.x, x0.y, x1.x, x1.y);
+          at[2 + j] = make_float4(y0.x, y0.y, y1.x, y1.y);
+          float2 g[2], e[2];
+          lds_pairs(gamma + 16 * j, g);
+          lds_pairs(gamma + 32 + 16 * j, e);
+#pragma unroll
+          for (int l = 0; l < 2; ++l) {
+            const int c = 2 * j + l;
+            p[c] = mul2(fma2(p[c], k2, mul2(u[c], g[l])), r2);
+            q[c] = mul2(fma2(q[c], k2, mul2(v[c], e[l])), r2);
+          }
+        }
+        Lane::pack(p, q, o);
+      } else {  // the token has no position: no gradient
+#pragma unroll
+        for (int j = 0; j < Lane::NW; ++j) o[j] = 0u;
+      }
+      me.store(head_at<T, I>(a.side[0].y, a.side[1].y, dst, hq, k), o);
+    }
+    src = then;
+  }
+  if (!a.want) return;
+  __syncthreads();
+  // column by column, over warps and groups in a fixed order
+  for (int i = threadIdx.x; i < 2 * lanes * 16; i += kHeadThreads) {
+    const int k = i / (lanes * 16), l = i / 16 % lanes, e = i % 16;
+    float sum = 0.f;
+    for (int w = 0; w < kHeadWarps; ++w)
+      for (int g = 0; g < groups; ++g) sum += sums[(w * 64 + k * 32 + g * lanes + l) * kHeadSlot + e];
+    const Lane that(l, a.D, a.R);
+    const int col = e < 8 ? that.col_a(e) : that.col_b(e - 8);
+    if (col >= 0) a.ws[((int64_t)blockIdx.x * 2 + k) * a.D + col] = sum;
   }
 }
 
-// dgamma from its side's partial rows: a CTA takes 32 columns of one side, its
+// dgamma from the CTAs' partial rows: a CTA takes 32 columns of one side, its
 // warps rows in turn.
 template <typename D>
-__global__ void __launch_bounds__(512) head_gamma_reduce_kernel(const HeadArgs a) {
+__global__ void __launch_bounds__(512) head_gamma_reduce_kernel(const HeadArgs a, const int rows) {
   __shared__ float sh[16][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + lane, k = blockIdx.y;
   void* dg = a.side[k].dgamma;
   pdl_launch_dependents();
   pdl_wait_primary();
-  const float* ws = a.ws + (int64_t)(k ? a.ctas[0] : 0) * a.D + i;
+  const float* ws = a.ws + k * a.D + i;
   float sum = 0.f;
   if (i < a.D) {
 #pragma unroll 4
-    for (int p = warp; p < a.ctas[k]; p += 16) sum += ws[(int64_t)p * a.D];
+    for (int p = warp; p < rows; p += 16) sum += ws[(int64_t)p * 2 * a.D];
   }
   sh[warp][lane] = sum;
   __syncthreads();
@@ -474,90 +643,112 @@ template <typename D>
 void head_plan(HeadArgs& a, const DeviceInfo& dev) {
   a.err = dev.err;
   a.lanes = head_lanes(a);
-  const unsigned long long bits = (unsigned long long)reinterpret_cast<uintptr_t>(a.cos) |
-                                  (unsigned long long)reinterpret_cast<uintptr_t>(a.sin) |
-                                  (unsigned long long)((a.ldcos | a.ldsin) * 4) | (unsigned long long)(a.R / 2 * 4);
-  a.cvec = a.R && a.c_f32 && (bits & 15) == 0;
 }
 
-// Warps that share a token's heads: more than one where tokens are few.
-inline int head_slices(const HeadArgs& a, int heads, int64_t warps) {
-  const int groups = 32 / a.lanes;
-  const int64_t most = (heads + groups - 1) / groups, want = (warps + a.N - 1) / a.N;
-  return (int)std::max<int64_t>(1, std::min(most, want));
-}
-
-template <typename D, int CA, bool PAIRS>
-cudaError_t run_head_rotary(HeadArgs a, const DeviceInfo& dev, cudaStream_t s) {
-  constexpr int U = sizeof(typename D::T) == 2 ? 4 : 2;
-  a.slices = head_slices(a, a.side[0].heads + a.side[1].heads, (int64_t)dev.sm_count * 16);
-  const int64_t ctas = (a.N * a.slices + kHeadWarps - 1) / kHeadWarps;
-  FirstLaunch first(kHeadThreads, 0, s, 1);
-  return first.launch((unsigned)std::min<int64_t>(ctas, 1 << 20), true, head_rotary_kernel<D, CA, PAIRS, U>, a);
-}
-
-template <typename D, int CA, bool PAIRS>
-cudaError_t run_head_rotary_grad(HeadArgs& a, const DeviceInfo& dev, cudaStream_t s) {
-  constexpr int U = sizeof(typename D::T) == 2 ? 2 : 1;
-  auto kern = head_rotary_grad_kernel<D, CA, PAIRS, U>;
-  const size_t smem = a.want ? sizeof(float) * kHeadWarps * a.D : 0;
-  static KernelMemo memo;
+// The kernel on as many CTAs as are resident, or fewer.
+template <typename K>
+cudaError_t run_heads(K kern, HeadArgs& a, size_t smem, int most_per_sm, KernelMemo& memo, const DeviceInfo& dev, cudaStream_t s,
+                      int* ctas) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = memo.allow_smem(kern, dev.max_smem_optin - 1024, dev);
+    if (e != cudaSuccess) return e;
+  }
   const int resident = memo.resident(kHeadThreads, smem, dev, [&](int* n) {
     const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kern, kHeadThreads, smem);
-    *n = std::min(*n, kHeadGradMaxPerSm) * dev.sm_count;
+    *n = std::min(*n, most_per_sm) * dev.sm_count;
     return e;
   });
-  // the resident CTAs, shared by the sides as their heads are
-  const int heads = a.side[0].heads + a.side[1].heads;
-  for (int k = 0; k < 2; ++k) {
-    a.ctas[k] = 0;
-    if (!a.side[k].heads) continue;
-    const int most = std::max(1, (int)((int64_t)resident * a.side[k].heads / heads));
-    a.slice[k] = head_slices(a, a.side[k].heads, (int64_t)most * kHeadWarps);
-    a.ctas[k] = (int)std::min<int64_t>((a.N * a.slice[k] + kHeadWarps - 1) / kHeadWarps, most);
-  }
+  const int groups = 32 / a.lanes;
+  a.its = (a.side[0].heads + a.side[1].heads + groups - 1) / groups;
+  const int64_t units = a.N * a.its;
+  *ctas = (int)std::min<int64_t>((units + kHeadWarps - 1) / kHeadWarps, resident);
+  a.each = units / ((int64_t)*ctas * kHeadWarps);
+  a.extra = units % ((int64_t)*ctas * kHeadWarps);
   FirstLaunch first(kHeadThreads, smem, s, 1);
-  return first.launch((unsigned)(a.ctas[0] + a.ctas[1]), true, kern, a);
+  return first.launch((unsigned)*ctas, true, kern, a);
 }
 
-// f(columns an access, whether pairs are neighbours) as compile-time values.
-template <typename D, typename F>
-cudaError_t head_variants(int access, bool pairs, F&& f) {
-  constexpr int V = 16 / (int)sizeof(typename D::T);
-  auto with = [&](auto ca) {
-    return pairs ? f(ca, std::integral_constant<bool, true>{}) : f(ca, std::integral_constant<bool, false>{});
-  };
-  if (access == V) return with(std::integral_constant<int, V>{});
-  if constexpr (V == 8) {
-    if (access == 4) return with(std::integral_constant<int, 4>{});
+template <typename D, int CA, bool PAIRS, int LANES, typename I>
+cudaError_t run_head_rotary(HeadArgs a, const DeviceInfo& dev, cudaStream_t s) {
+  constexpr int U = sizeof(typename D::T) == 2 ? 2 : 1;  // 64 bytes of a lane
+  static KernelMemo memo;
+  int ctas;
+  return run_heads(head_rotary_kernel<D, CA, PAIRS, U, LANES, I>, a, sizeof(float) * (2 + kHeadWarps) * a.lanes * kHeadSlot, 32,
+                   memo, dev, s, &ctas);
+}
+
+template <typename D, int CA, bool PAIRS, int LANES, typename I>
+cudaError_t run_head_rotary_grad(HeadArgs a, const DeviceInfo& dev, cudaStream_t s, int* ctas) {
+  static KernelMemo memo;
+  return run_heads(head_rotary_grad_kernel<D, CA, PAIRS, LANES, I>, a,
+                   sizeof(float) * ((2 + kHeadWarps) * a.lanes + 64 * kHeadWarps) * kHeadSlot, kHeadGradMaxPerSm, memo, dev, s, ctas);
+}
+
+// Whether every tensor has fewer than 2^31 elements from its first to its last.
+inline bool head_offsets_fit(const HeadArgs& a, bool grad) {
+  for (const HeadSide& s : a.side) {
+    if (!s.heads) continue;
+    for (const HeadView* v : {&s.x, &s.y, &s.dy}) {
+      if (v == &s.dy && !grad) continue;
+      if ((a.B - 1) * v->sb + (a.T - 1) * v->st + (s.heads - 1) * v->sh + a.D >= (int64_t(1) << 31)) return false;
+    }
   }
-  return with(std::integral_constant<int, 1>{});
+  return true;
+}
+
+// f(columns an access, whether pairs are neighbours, lanes a head of 64, 128 or 256
+// rotated columns or 0, an offset's type) as compile-time values.
+template <typename D, typename F>
+cudaError_t head_variants(const HeadArgs& a, bool grad, F&& f) {
+  constexpr int V = 16 / (int)sizeof(typename D::T);
+  const int access = head_access<D>(a, grad);
+  auto with = [&](auto ca, auto l, auto off) {
+    return a.interleaved && a.R ? f(ca, std::integral_constant<bool, true>{}, l, off)
+                                : f(ca, std::integral_constant<bool, false>{}, l, off);
+  };
+  using Any = std::integral_constant<int, 0>;
+  if (!head_offsets_fit(a, grad))
+    return access == V ? with(std::integral_constant<int, V>{}, Any{}, int64_t{})
+                       : with(std::integral_constant<int, 1>{}, Any{}, int64_t{});
+  if (access == V) {
+    const std::integral_constant<int, V> ca;
+    if (a.R == a.D && a.D == 16 * a.lanes) {
+      if (a.D == 64) return with(ca, std::integral_constant<int, 4>{}, uint32_t{});
+      if (a.D == 128) return with(ca, std::integral_constant<int, 8>{}, uint32_t{});
+      if (a.D == 256) return with(ca, std::integral_constant<int, 16>{}, uint32_t{});
+    }
+    return with(ca, Any{}, uint32_t{});
+  }
+  if constexpr (V == 8) {
+    if (access == 4) return with(std::integral_constant<int, 4>{}, Any{}, uint32_t{});
+  }
+  return with(std::integral_constant<int, 1>{}, Any{}, uint32_t{});
 }
 
 template <typename D>
 cudaError_t launch_head_rotary(HeadArgs a, const DeviceInfo& dev, cudaStream_t s) {
   (void)cudaGetLastError();  // drop a stale, non-sticky error left by an earlier call
   head_plan<D>(a, dev);
-  return head_variants<D>(head_access<D>(a, false), a.interleaved && a.R, [&](auto ca, auto pairs) {
-    return run_head_rotary<D, decltype(ca)::value, decltype(pairs)::value>(a, dev, s);
+  return head_variants<D>(a, false, [&](auto ca, auto pairs, auto l, auto off) {
+    return run_head_rotary<D, decltype(ca)::value, decltype(pairs)::value, decltype(l)::value, decltype(off)>(a, dev, s);
   });
 }
 
 template <typename D>
 cudaError_t launch_head_rotary_grad(HeadArgs a, const DeviceInfo& dev, cudaStream_t s) {
   (void)cudaGetLastError();
-  a.ctas[0] = a.ctas[1] = 0;
+  int rows = 0;
   if (a.N > 0) {
     head_plan<D>(a, dev);
-    const cudaError_t e = head_variants<D>(head_access<D>(a, true), a.interleaved && a.R, [&](auto ca, auto pairs) {
-      return run_head_rotary_grad<D, decltype(ca)::value, decltype(pairs)::value>(a, dev, s);
+    const cudaError_t e = head_variants<D>(a, true, [&](auto ca, auto pairs, auto l, auto off) {
+      return run_head_rotary_grad<D, decltype(ca)::value, decltype(pairs)::value, decltype(l)::value, decltype(off)>(a, dev, s, &rows);
     });
     if (e != cudaSuccess) return e;
   }
   if (!a.want) return cudaSuccess;
   FirstLaunch second(512, 0, s, 1);
   second.cfg.gridDim.y = 2;
-  return second.launch((unsigned)((a.D + 31) / 32), true, head_gamma_reduce_kernel<D>, a);
+  return second.launch((unsigned)((a.D + 31) / 32), true, head_gamma_reduce_kernel<D>, a, rows);
 }
 
 }  // namespace normk

@@ -45,25 +45,22 @@ struct HeadArgs {
   int pos64;
   int interleaved;
   unsigned* err;
-  // gradient only: fp32 partial rows of dgamma, D columns: the
-  // queries' CTAs, then the keys'
+  // gradient only: fp32 partial rows [CTA][side][D] of dgamma
   float* ws;
   int want;  // whether any dgamma is wanted
   // filled in by the launcher:
   int lanes;   // a head, a power of two
-  int slices;    // warps that share a token's heads (forward)
-  int slice[2];  // the same for each side (gradient)
-  int ctas[2];   // of each side (gradient)
-  int cvec;    // cos and sin rows take 16-byte loads
+  int its;        // units of a token: heads a group has to take
+  int64_t each;   // units a warp, and how many warps have one more
+  int64_t extra;
 };
 
 // Device error bit of a position outside the table.
 constexpr unsigned kErrBadPosition = 8u;
 
-// CTAs the gradient may have an SM; its partial rows (each side has one CTA at
-// least).
+// CTAs the gradient may have an SM, and its partial rows.
 constexpr int kHeadGradMaxPerSm = 4;
-inline size_t head_grad_partials(const DeviceInfo& dev) { return (size_t)kHeadGradMaxPerSm * dev.sm_count + 2; }
+inline size_t head_grad_partials(const DeviceInfo& dev) { return (size_t)2 * kHeadGradMaxPerSm * dev.sm_count; }
 
 template <typename D>
 cudaError_t launch_head_rotary(HeadArgs a, const DeviceInfo& dev, cudaStream_t s);

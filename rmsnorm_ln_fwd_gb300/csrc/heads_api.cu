@@ -20,7 +20,7 @@ using normk::launch_result;
 namespace {
 
 constexpr int64_t kMaxHeads = 65535;
-constexpr int64_t kMaxTokens = int64_t(1) << 40;
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1;
 
 // A (B, T, H, D) tensor; strides of dims of one element are 0.
 struct Heads {
@@ -107,7 +107,7 @@ norm_status take_rotation(const norm_rotation* r, int64_t B, int64_t T, int64_t 
   a->R = (int)r->columns;
   a->interleaved = r->interleaved != 0;
   if (B * T == 0) return NORM_OK;
-  if (!r->cos || !r->sin || !elements_aligned({r->cos, r->sin}, es) || r->rows < 1 || r->rows > kMaxTokens ||
+  if (!r->cos || !r->sin || !elements_aligned({r->cos, r->sin}, es) || r->rows < 1 || r->rows > (int64_t(1) << 40) ||
       !ld_ok(r->cos_stride, r->rows, half, es) || !ld_ok(r->sin_stride, r->rows, half, es))
     return NORM_ERR_INVALID_VALUE;
   in[0] = rows_span(r->cos, r->rows, r->cos_stride, half, es);
@@ -151,6 +151,13 @@ cudaError_t by_dtype(norm_dtype d, F&& f) {
 
 cudaStream_t cuda_stream(norm_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
+// Whether a head of D columns, R of them rotated, is at most 32 units of 16: with
+// halves, the rotated columns and the others are units of their own.
+bool units_ok(int64_t D, const HeadArgs& a) {
+  const int64_t units = a.interleaved || a.R == 0 ? (D + 15) / 16 : (a.R / 2 + 7) / 8 + (D - a.R + 15) / 16;
+  return units <= 32;
+}
+
 bool sizes_ok(int64_t B, int64_t T, int64_t D, int64_t hq, int64_t hk) {
   return B >= 0 && T >= 0 && (B == 0 || T <= kMaxTokens / B) && D >= 1 && D <= normk::kHeadMaxCols && hq >= 0 &&
          hk >= 0 && hq <= kMaxHeads && hk <= kMaxHeads && hq + hk > 0;
@@ -179,6 +186,7 @@ norm_status head_rms_rotary(const norm_heads* q, int64_t q_heads, const norm_hea
     Span rot[3];
     st = take_rotation(rotation, B, T, D, x_dtype, &a, rot);
     if (st != NORM_OK) return st;
+    if (!units_ok(D, a)) return NORM_ERR_INVALID_VALUE;
     std::copy(rot, rot + 3, in);
   }
   if (B * T == 0) return NORM_OK;
@@ -256,6 +264,7 @@ norm_status head_rms_rotary_grad(const norm_heads* dyq, const norm_heads* q, int
     Span rot[3];
     st = take_rotation(rotation, B, T, D, x_dtype, &a, rot);
     if (st != NORM_OK) return st;
+    if (!units_ok(D, a)) return NORM_ERR_INVALID_VALUE;
     std::copy(rot, rot + 3, in);
   }
   a.B = B;

@@ -20,10 +20,14 @@
 
 namespace normk {
 
-constexpr int kLogprobThreads = 512;  // most of a CTA
+// Threads and chunks in flight (us; 4096x131072 bf16, 333x50001 fp16, 16384x4096
+// bf16): 256 threads and three chunks 159, 12.7, 27.7; four 159, 13.5, 27.5; two
+// 167, 12.5, 28; 128 threads 198, 14.7, 83; two buffers of one or two chunks 165
+// and 189.  64 registers, four CTAs an SM; three (80 registers) 169, 11.5, 29.7.
+constexpr int kLogprobThreads = 256;  // of a CTA
+constexpr int kLogprobChunks = 3;     // of a thread in flight
+constexpr int kLogprobPerSm = 4;      // CTAs
 constexpr int kLogprobMaxCluster = 8;
-constexpr int kTopCandidates = 2048;
-constexpr int kTopGroups = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.402823466e38f;
 // Differences this far down (in powers of two) are nothing beside 1; a product
@@ -50,17 +54,14 @@ struct LogitChunk {
   __device__ static __forceinline__ int lead(const T* row) {
     return (int)((reinterpret_cast<uintptr_t>(row) & 31u) / ES);
   }
-  __device__ static __forceinline__ void fill(uint32_t (&w)[8]) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) w[k] = kMasked;
-  }
   // Columns [col, col + GE) of the row; -inf outside [0, V).
   __device__ static __forceinline__ void load(const T* row, int col, int V, uint32_t (&w)[8]) {
     if (col >= 0 && col + GE <= V) {
       ld_stream32(row + col, w);
       return;
     }
-    fill(w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = kMasked;
 #pragma unroll
     for (int e = 0; e < GE; ++e) {
       if (col + e >= 0 && col + e < V) {
@@ -109,16 +110,27 @@ __device__ __forceinline__ float key_value(unsigned long long k) {
 }
 __device__ __forceinline__ int key_col(unsigned long long k) { return (int)(0xffffffffu - (uint32_t)k); }
 
-// Sort `n` keys in shared memory, largest first, with all threads of the CTA;
-// those behind n up to the next power of two are overwritten.
-__device__ __forceinline__ void sort_keys(unsigned long long* key, int n) {
+// The threads of a row: `n` of them (whole warps, a power of two), thread `t`.
+struct RowGroup {
+  int n, t, bar;
+  __device__ __forceinline__ void sync() const {
+    if (n == 32)
+      __syncwarp();
+    else
+      named_barrier(bar, n);
+  }
+};
+
+// Sort `n` keys in shared memory, largest first; those behind n up to the next
+// power of two are overwritten.
+__device__ __forceinline__ void sort_keys(const RowGroup& g, unsigned long long* key, int n) {
   int size = 1;
   while (size < n) size <<= 1;
-  for (int i = n + threadIdx.x; i < size; i += blockDim.x) key[i] = 0;
-  __syncthreads();
+  for (int i = n + g.t; i < size; i += g.n) key[i] = 0;
+  g.sync();
   for (int k = 2; k <= size; k <<= 1) {
     for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int i = threadIdx.x; i < size / 2; i += blockDim.x) {
+      for (int i = g.t; i < size / 2; i += g.n) {
         const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
         const unsigned long long x = key[lo], y = key[hi];
         if ((x < y) == ((lo & k) == 0)) {
@@ -126,13 +138,50 @@ __device__ __forceinline__ void sort_keys(unsigned long long* key, int n) {
           key[hi] = x;
         }
       }
-      __syncthreads();
+      g.sync();
     }
   }
 }
 
-__device__ __forceinline__ unsigned long long warp_max64(unsigned long long v, int lanes) {
-  for (int off = 1; off < lanes; off <<= 1) {
+// Where a key goes among `n`: the number of larger ones.  Two keys a
+// load and eight loads in flight; key is 16-byte aligned and holds zeros up to a
+// multiple of 16.
+__device__ __forceinline__ int key_rank(const unsigned long long* key, int n, unsigned long long k) {
+  int rank = 0;
+#pragma unroll 1
+  for (int i = 0; i < n; i += 16) {
+    ulonglong2 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = reinterpret_cast<const ulonglong2*>(key + i)[j];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rank += (v[j].x > k) + (v[j].y > k);
+  }
+  return rank;
+}
+
+// The first `top` of `n` keys (different ones, or 0) into best, 0 where there are fewer;
+// best is all zeros before.  Few keys go to their ranks, which takes no barrier (to
+// sort 64 takes 21): a key a thread, or 128.
+__device__ __forceinline__ void best_keys(const RowGroup& g, unsigned long long* key, int n, int top, unsigned long long* best) {
+  if (n <= max(g.n, 128)) {
+    if (n + g.t < (n + 15) / 16 * 16) key[n + g.t] = 0ull;
+    g.sync();
+#pragma unroll 1
+    for (int i = g.t; i < n; i += g.n) {
+      const unsigned long long k = key[i];
+      const int rank = key_rank(key, n, k);
+      if (rank < top && k != 0) best[rank] = k;
+    }
+  } else {
+    sort_keys(g, key, n);
+    if (g.t < min(n, top)) best[g.t] = key[g.t];
+  }
+  g.sync();
+}
+
+__device__ __forceinline__ unsigned long long warp_max64(unsigned long long v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
     const unsigned long long o = __shfl_xor_sync(0xffffffffu, v, off);
     v = o > v ? o : v;
   }
@@ -155,74 +204,82 @@ struct RowSums {
   }
 };
 
-struct TopShared {
+// Shared memory of a row's alternatives.  512 candidates: a row that is constant,
+// or masked with one value, has 16 columns of one thread for each alternative.
+constexpr int kTopCandidates = 512;
+struct __align__(16) TopShared {
   unsigned long long key[kTopCandidates];
-  unsigned long long group[kTopGroups];
-  unsigned long long tau;
-  int list[kLogprobThreads];
-  int listed, found;
   unsigned long long best[kMaxTop];
+  int listed, found;
+  unsigned char list[kLogprobThreads];
 };
+// Followed by each warp's largest keys, one a lane.
+__host__ __device__ constexpr int top_bytes(int rows) { return rows * (int)sizeof(TopShared) + 8 * kLogprobThreads; }
 
-// The first `top` keys of this CTA's chunks [first, last) into sh.best (0 where
-// there are fewer).  Each thread comes with its largest logit and the chunk it
-// met it in first.  A key at that chunk's last column is no larger than the key
-// of the logit itself, so at least `top` logits reach tau, the top-th largest of
-// those over groups of threads; all that do are in the chunks of threads whose
-// own key does.  Only those chunks are read again (they are in L2): a 25th of the
-// row for 20 of 512 threads.
+// The first `top` keys of the chunks [first, last) into sh.best (0 where there
+// are fewer).  Each thread comes with its largest logit and the chunk it met it
+// in first.  A key at that chunk's last column is no larger than the key of the
+// logit itself, so at least `top` logits reach tau, the top-th largest of those
+// over 32 groups of threads (the same lane of each warp); all that do are in the
+// chunks of threads whose own key does.  Only those chunks are read again (they
+// are in L2): a 12th of the row for 20 of 256 threads.
 template <typename D>
-__device__ __forceinline__ void cta_top(TopShared& sh, const typename D::T* z, int a0, int V, int first, int last, int top,
-                                        float mx, int mi) {
+__device__ __forceinline__ void row_top(const RowGroup& g, TopShared& sh, unsigned long long* lanes, const typename D::T* z,
+                                        int a0, int V, int first, int last, int top, float mx, int mi) {
   using L = LogitChunk<D>;
   const int lane = threadIdx.x & 31;
   const float none = __int_as_float(0xff800000);
   const unsigned long long mine = mx > none ? top_key(mx, mi * L::GE - a0 + L::GE - 1) : 0ull;
-  const int per = max(1, (int)blockDim.x / kTopGroups), groups = blockDim.x / per;
-  if (threadIdx.x == 0) {
-    sh.tau = 1ull;
-    sh.listed = sh.found = 0;
+  if (g.t < kMaxTop) sh.best[g.t] = 0ull;
+  if (g.t == 0) sh.listed = sh.found = 0;
+  unsigned long long most = mine;
+  if (g.n > 32) lanes[g.t] = mine;
+  g.sync();
+  if (g.n > 32) {
+#pragma unroll
+    for (int i = 0; i < kLogprobThreads / 32; ++i) {
+      const unsigned long long o = 32 * i < g.n ? lanes[32 * i + lane] : 0ull;
+      most = o > most ? o : most;
+    }
   }
-  const unsigned long long g = warp_max64(mine, per);
-  if (lane % per == 0) sh.group[threadIdx.x / per] = g;
-  __syncthreads();
-  if (threadIdx.x < groups) {
-    const unsigned long long k = sh.group[threadIdx.x];
-    int rank = 0;
-    for (int i = 0; i < groups; ++i) rank += sh.group[i] > k;
-    if (k != 0 && rank == top - 1) sh.tau = k;
-  }
-  __syncthreads();
-  const unsigned long long tau = sh.tau;
-  if (mine >= tau) sh.list[atomicAdd(&sh.listed, 1)] = threadIdx.x;
-  __syncthreads();
-  const int each = (last - first + blockDim.x - 1) / blockDim.x;  // chunks a thread
+  int rank = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) rank += __shfl_sync(0xffffffffu, most, i) > most;
+  const unsigned at = __ballot_sync(0xffffffffu, rank == top - 1 && most != 0);
+  // fewer groups than alternatives have a logit at all: any logit will do
+  const unsigned long long tau = at ? __shfl_sync(0xffffffffu, most, __ffs(at) - 1) : 1ull;
+  const unsigned in = __ballot_sync(0xffffffffu, mine >= tau);
+  int slot = 0;
+  if (lane == 0 && in) slot = atomicAdd(&sh.listed, __popc(in));
+  slot = __shfl_sync(0xffffffffu, slot, 0) + __popc(in & ((1u << lane) - 1u));
+  if (mine >= tau) sh.list[slot] = (unsigned char)g.t;
+  g.sync();
+  const int each = (last - first + g.n - 1) / g.n;  // chunks a thread
   const int pairs = sh.listed * each;
-  for (int p = threadIdx.x; p < pairs; p += blockDim.x) {
-    const int i = first + sh.list[p / each] + (p % each) * blockDim.x;
+  const float least = at ? key_value(tau) : none;
+  for (int p = g.t; p < pairs; p += g.n) {
+    const int i = first + sh.list[p / each] + (p % each) * g.n;
     if (i >= last) continue;
     uint32_t w[8];
     const int col = i * L::GE - a0;
     L::load(z, col, V, w);
+    if (!(L::max(w) >= least)) continue;
 #pragma unroll
     for (int e = 0; e < L::GE; ++e) {
       const float2 f = word_pair<D>(w, e / 2);
       const float v = e & 1 ? f.y : f.x;
-      if (v > none) {
+      if (v >= least && v > none) {
         const unsigned long long k = top_key(v, col + e);
         if (k >= tau) {
-          const int at = atomicAdd(&sh.found, 1);
-          if (at < kTopCandidates) sh.key[at] = k;
+          const int to = atomicAdd(&sh.found, 1);
+          if (to < kTopCandidates) sh.key[to] = k;
         }
       }
     }
   }
-  __syncthreads();
-  const int found = sh.found;
-  if (found <= kTopCandidates) {
-    sort_keys(sh.key, found);
-    if (threadIdx.x < kMaxTop) sh.best[threadIdx.x] = threadIdx.x < min(found, top) ? sh.key[threadIdx.x] : 0ull;
-    __syncthreads();
+  g.sync();
+  if (sh.found <= kTopCandidates) {
+    best_keys(g, sh.key, sh.found, top, sh.best);
     return;
   }
   // More than fit (the largest logits crowd into few threads' chunks): one after
@@ -230,7 +287,7 @@ __device__ __forceinline__ void cta_top(TopShared& sh, const typename D::T* z, i
   unsigned long long before = ~0ull;
   for (int r = 0; r < top; ++r) {
     unsigned long long best = 0;
-    for (int i = first + threadIdx.x; i < last; i += blockDim.x) {
+    for (int i = first + g.t; i < last; i += g.n) {
       uint32_t w[8];
       const int col = i * L::GE - a0;
       L::load(z, col, V, w);
@@ -244,15 +301,19 @@ __device__ __forceinline__ void cta_top(TopShared& sh, const typename D::T* z, i
         }
       }
     }
-    best = warp_max64(best, 32);
-    if (lane == 0) sh.group[threadIdx.x >> 5] = best;
-    __syncthreads();
-    for (int i = 0; i < (int)blockDim.x / 32; ++i) best = sh.group[i] > best ? sh.group[i] : best;
-    if (threadIdx.x == 0) sh.best[r] = best;
+    best = warp_max64(best);
+    if (lane == 0) lanes[g.t >> 5] = best;
+    g.sync();
+    for (int i = 0; i < g.n / 32; ++i) best = lanes[i] > best ? lanes[i] : best;
+    if (g.t == 0) sh.best[r] = best;
     before = best;
-    __syncthreads();
+    g.sync();
   }
 }
+
+// cluster_sync_all in its two halves.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float cluster_ld_f32(const float* local, unsigned rank) {
   unsigned a;
@@ -269,90 +330,96 @@ __device__ __forceinline__ unsigned long long cluster_ld_u64(const unsigned long
   return v;
 }
 
-// The whole row's sums in thread 0 (and its maximum in every thread).
-__device__ __forceinline__ void cta_sums(RowSums& r, float c2, float (*red)[kLogprobThreads / 32]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+// The sums over each eight lanes, in all of them.
+__device__ __forceinline__ void eight_sums(RowSums& r, float c2) {
+  r.ref = fmaxf(r.mx, kLowest);
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) r.mx = fmaxf(r.mx, __shfl_xor_sync(0xffffffffu, r.mx, off));
+  r.move(fmaxf(r.mx, kLowest), c2);
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) {
+    r.s += __shfl_xor_sync(0xffffffffu, r.s, off);
+    r.u += __shfl_xor_sync(0xffffffffu, r.u, off);
+  }
+}
+
+// The sums over a row's threads, in all of them.  red: 3 floats a warp.
+__device__ __forceinline__ void row_sums(const RowGroup& g, RowSums& r, float c2, float* red) {
+  const int lane = threadIdx.x & 31, warp = g.t >> 5, warps = g.n >> 5;
   float m = r.mx;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  if (warps > 1) {
-    if (lane == 0) red[0][warp] = m;
-    __syncthreads();
-    m = lane < warps ? red[0][lane] : r.mx;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  }
   r.mx = m;
   r.move(fmaxf(m, kLowest), c2);
   float v[2] = {r.s, r.u};
   warp_sum<2>(v);
-  if (warps > 1) {
-    if (lane == 0) {
-      red[1][warp] = v[0];
-      red[2][warp] = v[1];
-    }
-    __syncthreads();
-    v[0] = lane < warps ? red[1][lane] : 0.f;
-    v[1] = lane < warps ? red[2][lane] : 0.f;
-    warp_sum<2>(v);
-  }
   r.s = v[0];
   r.u = v[1];
+  if (warps == 1) return;
+  if (lane == 0) {
+    red[3 * warp] = r.mx;
+    red[3 * warp + 1] = r.s;
+    red[3 * warp + 2] = r.u;
+  }
+  g.sync();
+  // eight lanes take the warps' sums, and the others the same, so that all end
+  // with the same bits
+  const int from = lane & 7;
+  const bool on = from < warps;
+  r.mx = on ? red[3 * from] : __int_as_float(0xff800000);
+  r.s = on ? red[3 * from + 1] : 0.f;
+  r.u = on ? red[3 * from + 2] : 0.f;
+  eight_sums(r, c2);
 }
 
-// One row a CTA, or a row a cluster of `cl`, whose CTAs take consecutive parts
-// of its chunks.  U chunks of a thread are in flight at a time.
+// A row for a.tpr threads, or for a cluster of a.cl CTAs, which take consecutive
+// parts of its chunks.  U chunks of a thread are in flight at a time.
 template <typename D, bool ENT, bool TOP>
-__global__ void __launch_bounds__(kLogprobThreads, 2) logprob_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(kLogprobThreads, kLogprobPerSm) logprob_kernel(const LogprobArgs a) {
   using L = LogitChunk<D>;
   using T = typename D::T;
-  constexpr int U = 4;
-  __shared__ float red[3][kLogprobThreads / 32];
+  constexpr int U = kLogprobChunks;
+  static_assert(kLogprobThreads <= 256 && kLogprobMaxCluster <= 8, "eight sums");
+  extern __shared__ __align__(16) unsigned char top_raw[];
+  __shared__ float red[3 * kLogprobThreads / 32];
   __shared__ float part_sums[3];
-  __shared__ __align__(16) unsigned char top_raw[TOP ? sizeof(TopShared) : 16];
-  TopShared& ts = *reinterpret_cast<TopShared*>(top_raw);
+  const int gid = threadIdx.x / a.tpr, rows = kLogprobThreads / a.tpr;
+  const RowGroup g{a.tpr, (int)threadIdx.x - gid * a.tpr, 1 + gid};
+  TopShared& ts = reinterpret_cast<TopShared*>(top_raw)[gid];
+  unsigned long long* lanes = reinterpret_cast<unsigned long long*>(top_raw + rows * sizeof(TopShared)) + gid * a.tpr;
   pdl_launch_dependents();
   pdl_wait_primary();
   const int crank = a.cl > 1 ? (int)cluster_ctarank() : 0;
-  const int64_t row = blockIdx.x / a.cl;
+  const int64_t row = a.cl > 1 ? blockIdx.x / a.cl : (int64_t)blockIdx.x * rows + gid;
+  if (row >= a.N) return;
   const T* z = reinterpret_cast<const T*>(a.z) + row * a.ldz;
   const int a0 = L::lead(z);
   const int chunks = (a.V + a0 + L::GE - 1) / L::GE, part = (chunks + a.cl - 1) / a.cl;
   const int first = min(crank * part, chunks), last = min(first + part, chunks);
   const float c2 = a.scale * kLog2e;
 
-  // the row's token, and its logit, for the end
-  float zt = 0.f;
-  int has = 0;
-  if (crank == 0 && threadIdx.x == 0 && a.tokens) {
-    const int64_t tok = a.tok64 ? reinterpret_cast<const long long*>(a.tokens)[row]
-                                : (int64_t) reinterpret_cast<const int*>(a.tokens)[row];
-    if (tok != a.ignore) {
-      if (tok >= 0 && tok < a.V) {
-        has = 1;
-        zt = load_elem<D>(z, tok);
-      } else {
-        atomicOr(a.err, kErrBadToken);
-      }
-    }
-  }
+  // the row's token, looked at when the row is through
+  int64_t tok = a.ignore;
+  if (g.t == 0 && a.tokens)
+    tok = a.tok64 ? reinterpret_cast<const long long*>(a.tokens)[row] : (int64_t) reinterpret_cast<const int*>(a.tokens)[row];
 
   const float none = __int_as_float(0xff800000);
   RowSums r{none, kLowest, 0.f, 0.f};
   float2 s2 = splat2(0.f), u2 = splat2(0.f);
   int mi = 0;
-  for (int base = first + threadIdx.x; base < last; base += U * blockDim.x) {
-    uint32_t w[U][8];
+  auto fetch = [&](uint32_t (&w)[U][8], int base) {
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const int i = base + k * blockDim.x;
+      const int i = base + k * g.n;
       if (i < last) L::load(z, i * L::GE - a0, a.V, w[k]);
     }
+  };
+  auto take = [&](const uint32_t (&w)[U][8], int base) {
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      if (base + k * (int)blockDim.x >= last) break;
+      if (base + k * g.n >= last) break;
       const float cm = L::max(w[k]);
-      if (TOP && cm > r.mx) mi = base + k * blockDim.x;
+      if (TOP && cm > r.mx) mi = base + k * g.n;
       r.mx = fmaxf(r.mx, cm);
       if ((cm - r.ref) * c2 > kSlack) {
         r.s = s2.x + s2.y;
@@ -362,91 +429,76 @@ __global__ void __launch_bounds__(kLogprobThreads, 2) logprob_kernel(const Logpr
         u2 = make_float2(r.u, 0.f);
       }
       const float2 ref2 = splat2(r.ref), cc = splat2(c2);
-      float2 du = splat2(0.f);
 #pragma unroll
       for (int j = 0; j < L::GE / 2; ++j) {
         const float2 x = mul2(sub2(word_pair<D>(w[k], j), ref2), cc);
         const float2 e = make_float2(ex2(x.x), ex2(x.y));
         s2 = add2(s2, e);
-        if (ENT) du = fma2(e, x, du);
-      }
-      if (ENT) {
-        if (isnan(du.x + du.y)) {  // a logit of -inf: 0 times its -inf counts as 0
-          du = splat2(0.f);
-#pragma unroll
-          for (int j = 0; j < L::GE / 2; ++j) {
-            const float2 x = mul2(sub2(word_pair<D>(w[k], j), ref2), cc);
-            du = fma2(make_float2(ex2(x.x), ex2(x.y)), make_float2(fmaxf(x.x, kFarDown), fmaxf(x.y, kFarDown)), du);
-          }
-        }
-        u2 = add2(u2, du);
+        // 0 times the -inf of a logit of -inf counts as 0
+        if (ENT) u2 = fma2(e, make_float2(fmaxf(x.x, kFarDown), fmaxf(x.y, kFarDown)), u2);
       }
     }
+  };
+  for (int base = first + g.t; base < last; base += U * g.n) {
+    uint32_t w[U][8];
+    fetch(w, base);
+    take(w, base);
   }
   r.s = s2.x + s2.y;
   r.u = u2.x + u2.y;
-  const float my_max = r.mx;
-  cta_sums(r, c2, red);
-  if constexpr (TOP) cta_top<D>(ts, z, a0, a.V, first, last, a.top, my_max, mi);
+  const bool has = tok != a.ignore && tok >= 0 && tok < a.V;
+  const float zt = has ? load_elem<D>(z, tok) : 0.f;  // comes in beside the sums
+  if constexpr (TOP) row_top<D>(g, ts, lanes, z, a0, a.V, first, last, a.top, r.mx, mi);
+  row_sums(g, r, c2, red + 3 * (gid * a.tpr / 32));
   if (a.cl > 1) {
-    if (threadIdx.x == 0) {
+    if (g.t == 0) {
       part_sums[0] = r.mx;
       part_sums[1] = r.s;
       part_sums[2] = r.u;
     }
     cluster_sync_all();
     if (crank == 0) {
-      if (threadIdx.x < 32) {
-        const bool on = (int)threadIdx.x < a.cl;
-        RowSums q{none, kLowest, 0.f, 0.f};
-        if (on) {
-          q.mx = cluster_ld_f32(&part_sums[0], threadIdx.x);
-          q.s = cluster_ld_f32(&part_sums[1], threadIdx.x);
-          q.u = cluster_ld_f32(&part_sums[2], threadIdx.x);
-          q.ref = fmaxf(q.mx, kLowest);
-        }
-        float m = q.mx;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        q.move(fmaxf(m, kLowest), c2);
-        float v[2] = {q.s, q.u};
-        warp_sum<2>(v);
-        r = RowSums{m, fmaxf(m, kLowest), v[0], v[1]};
-      }
+      const int from = threadIdx.x & 7;
+      const bool on = from < a.cl;
+      r.mx = on ? cluster_ld_f32(&part_sums[0], from) : none;
+      r.s = on ? cluster_ld_f32(&part_sums[1], from) : 0.f;
+      r.u = on ? cluster_ld_f32(&part_sums[2], from) : 0.f;
+      eight_sums(r, c2);
       if constexpr (TOP) {
-        for (int i = threadIdx.x; i < a.cl * a.top; i += blockDim.x)
-          ts.key[i] = cluster_ld_u64(&ts.best[i % a.top], (unsigned)(i / a.top));
+        for (int i = g.t; i < a.cl * a.top; i += g.n) ts.key[i] = cluster_ld_u64(&ts.best[i % a.top], (unsigned)(i / a.top));
       }
       __syncwarp();
     }
-    cluster_sync_all();  // no CTA leaves, or writes its parts again, while they are read
-    if (crank != 0) return;
+    cluster_arrive();  // no CTA leaves while its part is read
+    if (crank != 0) {
+      cluster_wait();
+      return;
+    }
     if constexpr (TOP) {
-      __syncthreads();
-      sort_keys(ts.key, a.cl * a.top);
-      if (threadIdx.x < kMaxTop) ts.best[threadIdx.x] = threadIdx.x < a.top ? ts.key[threadIdx.x] : 0ull;
+      g.sync();
+      if (g.t < kMaxTop) ts.best[g.t] = 0ull;
+      best_keys(g, ts.key, a.cl * a.top, a.top, ts.best);
     }
   }
   const float log_sum = logf(r.s);  // 0 gives -inf
-  if (threadIdx.x == 0) {
+  if (g.t == 0) {
     if (a.stats) a.stats[row] = make_float2(r.mx, log_sum);
     if (a.lse) a.lse[row] = r.mx == none ? log_sum : fmaf(a.scale, r.mx, log_sum);
     // log 2 turns the sums of exponents of two into those of e
     if (ENT && a.entropy) a.entropy[row] = r.s == 0.f ? 0.f : log_sum - 0.6931471805599453f * (r.u / r.s);
+    if (a.logprob && !has && tok != a.ignore) atomicOr(a.err, kErrBadToken);
     if (a.logprob) a.logprob[row] = !has ? 0.f : r.s == 0.f ? none : fmaf(a.scale, zt - r.mx, -log_sum);
   }
   if constexpr (TOP) {
-    if (threadIdx.x == 0) {
-      part_sums[0] = r.mx;
-      part_sums[1] = log_sum;
+    if (g.t < a.top) {
+      const unsigned long long k = ts.best[g.t];
+      a.top_id[row * a.top + g.t] = k ? key_col(k) : -1;
+      a.top_logprob[row * a.top + g.t] = k ? fmaf(a.scale, key_value(k) - r.mx, -log_sum) : none;
     }
-    __syncthreads();
-    if ((int)threadIdx.x < a.top) {
-      const unsigned long long k = ts.best[threadIdx.x];
-      a.top_id[row * a.top + threadIdx.x] = k ? key_col(k) : -1;
-      a.top_logprob[row * a.top + threadIdx.x] =
-          k ? fmaf(a.scale, key_value(k) - part_sums[0], -part_sums[1]) : none;
-    }
+  }
+  if (a.cl > 1) {
+    __syncwarp();
+    cluster_wait();
   }
 }
 
@@ -547,14 +599,22 @@ template <typename D, bool ENT, bool TOP>
 cudaError_t run_logprob(LogprobArgs a, const DeviceInfo& dev, cudaStream_t s) {
   constexpr int GE = LogitChunk<D>::GE;
   const int chunks = a.V / GE + 1;
-  // few rows: clusters share them, as long as a CTA keeps 256 chunks
+  // Few rows: clusters share them, as long as the CTAs all fit at once and keep 128
+  // chunks each (64x131072 bf16 8.6 -> 6.7 us as 512 CTAs; 333x50001 as 666, which
+  // do not fit, 12.7 -> 16.1).
   a.cl = 1;
-  while (a.cl < kLogprobMaxCluster && a.N * a.cl * 2 <= 2 * (int64_t)dev.sm_count && chunks / (a.cl * 2) >= 256) a.cl *= 2;
-  const int want = (chunks / a.cl + 3) / 4;
-  int threads = 32;
-  while (threads < kLogprobThreads && threads < want) threads *= 2;
-  FirstLaunch first((unsigned)threads, 0, s, a.cl);
-  return first.launch((unsigned)(a.N * a.cl), true, logprob_kernel<D, ENT, TOP>, a);
+  while (a.cl < kLogprobMaxCluster && a.N * a.cl * 2 <= kLogprobPerSm * (int64_t)dev.sm_count && chunks / (a.cl * 2) >= 128)
+    a.cl *= 2;
+  // Otherwise 16 chunks a thread, or two with alternatives, whose threads each keep
+  // a candidate: what a row costs besides its logits is the same for each warp (us,
+  // 16384x4096 bf16 with 16, 8, 4 chunks a thread 27.6, 33, 51; 1024x2000 with 20
+  // alternatives 9.8 with four, 8.4 with two).
+  constexpr int each = TOP ? 2 : 16;
+  a.tpr = a.cl > 1 ? kLogprobThreads : 32;
+  while (a.tpr < kLogprobThreads && a.tpr * each < chunks) a.tpr *= 2;
+  const int rows = kLogprobThreads / a.tpr;
+  FirstLaunch first(kLogprobThreads, TOP ? top_bytes(rows) : 0, s, a.cl);
+  return first.launch((unsigned)(a.cl > 1 ? a.N * a.cl : (a.N + rows - 1) / rows), true, logprob_kernel<D, ENT, TOP>, a);
 }
 
 template <typename D>

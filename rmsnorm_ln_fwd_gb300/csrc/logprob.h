@@ -32,7 +32,8 @@ struct LogprobArgs {
   int V;
   unsigned* err;
   // filled in by the launcher:
-  int cl;  // CTAs that share a row
+  int cl;   // CTAs that share a row
+  int tpr;  // threads a row
 };
 
 struct LogprobGradArgs {

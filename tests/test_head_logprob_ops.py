@@ -178,7 +178,11 @@ def test_rotary_refusals(lib):
             table=dict(rot=_rotation(cos=3 * M)), positions=dict(rot=_rotation(positions=3 * M + 8)),
             # the rotation
             R0=dict(rot=_rotation(columns=0)), odd_columns=dict(rot=_rotation(columns=63)),
-            past=dict(rot=_rotation(columns=66)), rows0=dict(rot=_rotation(rows=0)), rows=dict(rot=_rotation(rows=2)),
+            past=dict(rot=_rotation(columns=66)),
+            # 33 units of 16 columns
+            units=dict(D=512, rot=_rotation(columns=510, cos_stride=255, sin_stride=255), q=_heads(M, 6144, 2048, 512),
+                       k=_heads(2 * M, 6144, 2048, 512), qo=_heads(3 * M, 6144, 2048, 512), ko=_heads(4 * M, 6144, 2048, 512)),
+            tokens=dict(B=1, T=1 << 31, rot=None), rows0=dict(rot=_rotation(rows=0)), rows=dict(rot=_rotation(rows=2)),
             negrows=dict(rot=_rotation(rows=-1)), cosstride=dict(rot=_rotation(cos_stride=31)), nocos=dict(rot=_rotation(cos=None)),
             nosin=dict(rot=_rotation(sin=None)), oddcos=dict(rot=_rotation(cos=8 * M + 2)),
             oddpos=dict(rot=_rotation(positions=10 * M + 4)),
