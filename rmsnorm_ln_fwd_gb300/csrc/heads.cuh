@@ -120,6 +120,38 @@ struct HeadLane {
     load_half(head + c0, n0(), w);
     load_half(head + c1(), n1(), w + NW / 2);
   }
+  // Copy n columns (of eight) into a 16-byte granule of shared memory; zeros for the
+  // rest.
+  __device__ static __forceinline__ void copy_granule(const T* p, int n, uint32_t to) {
+    constexpr int B = CA * ES;
+    static_assert(ES == 2 && (B == 16 || B == 8), "copies of 16 or 8 bytes");
+#pragma unroll
+    for (int k = 0; k < 8 / CA; ++k) {
+      const T* from = k * CA < n ? p + k * CA : p;
+      if constexpr (B == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(k * CA < n ? 16 : 0) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + k * B), "l"(from), "r"(k * CA < n ? 8 : 0) : "memory");
+    }
+  }
+  // Copy the group's part of a head into its lanes' granules: kLaneBytes a lane,
+  // the second one of a lane kNext behind the first.  Neighbours are copied in the
+  // order of the columns, to addresses in that order, each lane for others: a lane's
+  // own two granules in turn, or addresses far apart, ask for each 32-byte sector
+  // twice (70.8 us for 45.6).
+  static constexpr int kLaneBytes = PAIRS ? 32 : 16, kNext = PAIRS ? 16 : 512;
+  __device__ __forceinline__ void copy(const T* head, int unit, int lanes, int cols, uint32_t to) const {
+    if constexpr (PAIRS) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int g = unit + j * lanes, n = FULL ? 8 : clamp8(cols - 8 * g);
+        copy_granule(head + (n ? 8 * g : 0), n, to + (g - 2 * unit) * 16);
+      }
+    } else {
+      copy_granule(head + (n0() ? c0 : 0), n0(), to);
+      copy_granule(head + (n1() ? c1() : 0), n1(), to + kNext);
+    }
+  }
   __device__ __forceinline__ void store(T* head, const uint32_t (&w)[NW]) const {
     store_half(head + c0, n0(), w);
     store_half(head + c1(), n1(), w + NW / 2);
@@ -343,6 +375,62 @@ __device__ __forceinline__ T* head_at(const HeadView& q, const HeadView& k, cons
   return reinterpret_cast<T*>(first ? q.p : k.p) + at;
 }
 
+// The gradient's inputs on their way to a lane: x and dy of its columns.
+// RegisterRing holds one head.  CopyRing has copies of two in flight to shared
+// memory (half precision, where 16 or 8 bytes can be copied), which no register
+// pays for: bf16 8192x32+8x128 50.4 -> 45.6 us.  A slot is written again an
+// iteration after its values were used, with the head's sums, which all lanes
+// exchange, in between.
+template <typename Lane, typename T>
+struct RegisterRing {
+  static constexpr int AHEAD = 1;
+  static constexpr int BYTES = 0;  // of shared memory a warp
+  uint32_t x[Lane::NW], y[Lane::NW];
+  __device__ __forceinline__ RegisterRing(unsigned char*, int, int, int, int) {}
+  __device__ __forceinline__ void fetch(const Lane& me, bool on, const T* px, const T* py) {
+    if (!on) return;
+    me.load(px, x);
+    me.load(py, y);
+  }
+  __device__ __forceinline__ void take(uint32_t (&tx)[Lane::NW], uint32_t (&ty)[Lane::NW]) const {
+#pragma unroll
+    for (int j = 0; j < Lane::NW; ++j) {
+      tx[j] = x[j];
+      ty[j] = y[j];
+    }
+  }
+};
+template <typename Lane, typename T>
+struct CopyRing {
+  static constexpr int AHEAD = 2;
+  static constexpr int SLOTS = AHEAD + 1;
+  static constexpr int BYTES = SLOTS * 2048;
+  uint32_t base;  // of the lane's granules
+  int unit, lanes, cols;
+  int in = 0, out = 0;
+  __device__ __forceinline__ CopyRing(unsigned char* smem, int lane, int unit_, int lanes_, int cols_)
+      : base(smem_u32(smem) + lane * Lane::kLaneBytes), unit(unit_), lanes(lanes_), cols(cols_) {}
+  // One group of copies a call, empty without a head.
+  __device__ __forceinline__ void fetch(const Lane& me, bool on, const T* px, const T* py) {
+    if (on) {
+      me.copy(px, unit, lanes, cols, base + in * 2048);
+      me.copy(py, unit, lanes, cols, base + in * 2048 + 1024);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    in = in + 1 == SLOTS ? 0 : in + 1;
+  }
+  __device__ __forceinline__ void take(uint32_t (&tx)[Lane::NW], uint32_t (&ty)[Lane::NW]) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+    __syncwarp();  // every lane's copies are there
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      lds_words<4>(base + out * 2048 + j * Lane::kNext, tx + 4 * j);
+      lds_words<4>(base + out * 2048 + 1024 + j * Lane::kNext, ty + 4 * j);
+    }
+    out = out + 1 == SLOTS ? 0 : out + 1;
+  }
+};
+
 // Sum over each `lanes` lanes; LANES: as a compile-time value, or 0.
 template <int K, int LANES>
 __device__ __forceinline__ void lanes_sum(float (&v)[K], int lanes) {
@@ -446,16 +534,24 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_kernel(c
   }
 }
 
-// The gradient.  A lane sums dgamma of its columns, for either side, in slots of
+// The gradient.  A lane sums dgamma of its columns, for either side, in granules of
 // its own in shared memory (in registers, with a change of sides at every token,
-// they cost the second buffer's: fp32 4096x32+8x128 47.5 -> 52.3 us); a CTA's sums
-// become its partial row.  The next head of a group is in flight while one is at
+// fp32 4096x32+8x128 47.5 -> 52.3 us); a CTA's sums become its partial row.  The
+// next heads of a group are in flight, over the ends of tokens, while one is at
 // work.
+template <typename D, int CA, bool PAIRS, int LANES>
+struct HeadGradRing {
+  using Lane = HeadLane<D, CA, PAIRS, 16 * LANES>;
+  using T = typename D::T;
+  static constexpr bool COPIES = sizeof(T) == 2 && CA >= 4;
+  using Type = std::conditional_t<COPIES, CopyRing<Lane, T>, RegisterRing<Lane, T>>;
+};
 template <typename D, int CA, bool PAIRS, int LANES, typename I>
 __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_grad_kernel(const HeadArgs a) {
   using Lane = HeadLane<D, CA, PAIRS, 16 * LANES>;
   using T = typename D::T;
-  extern __shared__ __align__(16) float slots[];  // gamma of both sides, each warp's angles, each lane's sums
+  using Ring = typename HeadGradRing<D, CA, PAIRS, LANES>::Type;
+  extern __shared__ __align__(16) float slots[];  // gamma of both sides, each warp's angles, sums and ring
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int lanes = LANES ? LANES : a.lanes;
   const int groups = 32 / lanes, group = lane / lanes, unit = lane & (lanes - 1);
@@ -465,58 +561,62 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_grad_ker
   const uint32_t gammas = smem_u32(slots + unit * kHeadSlot);
   float* angles = slots + (2 + warp) * lanes * kHeadSlot;
   const uint32_t angle = smem_u32(angles + unit * kHeadSlot);
-  float* sums = slots + (2 + kHeadWarps) * lanes * kHeadSlot;  // [warp][side][lane]
-  float* mine = sums + (warp * 64 + lane) * kHeadSlot;
+  float4* sums = reinterpret_cast<float4*>(slots + (2 + kHeadWarps) * lanes * kHeadSlot);  // [warp][side][granule][lane]
+  float4* mine = sums + warp * 256 + lane;
+  Ring ring(reinterpret_cast<unsigned char*>(sums + kHeadWarps * 256) + warp * Ring::BYTES, lane, unit, lanes, a.D);
   pdl_launch_dependents();
   pdl_wait_primary();
-  HeadShare share(a, blockIdx.x * kHeadWarps + warp);
-  HeadToken token(a, share.first);
+  // the heads that are fetched, AHEAD units before those that are at work
+  HeadShare share(a, blockIdx.x * kHeadWarps + warp), work = share;
+  HeadToken token(a, share.first), ahead = token;
   const int tokens = share.left > 0 ? (int)((share.lo + share.left + a.its - 1) / a.its) : 0;
-  uint32_t wx[Lane::NW], wy[Lane::NW];
-  struct Both {
-    HeadPlace<I> x, dy;
+  HeadPlace<I> px(ahead, a.side[0].x, a.side[1].x, hq), py(ahead, a.side[0].dy, a.side[1].dy, hq);
+  int fk = 0, fend = 0;  // the next head to fetch (of group 0), and the end of the token's
+  bool first = true;
+  auto fetch = [&] {
+    if (fk >= fend) {
+      int lo, hi;
+      if (!share.take(a, lo, hi)) {
+        ring.fetch(me, false, nullptr, nullptr);
+        return;
+      }
+      if (!first) {
+        ahead.step(a);
+        px = HeadPlace<I>(ahead, a.side[0].x, a.side[1].x, hq);
+        py = HeadPlace<I>(ahead, a.side[0].dy, a.side[1].dy, hq);
+      }
+      first = false;
+      fk = lo * groups;
+      fend = min(hi * groups, heads);
+    }
+    const int k = fk + group;
+    ring.fetch(me, k < fend, head_at<T, I>(a.side[0].x, a.side[1].x, px, hq, k), head_at<T, I>(a.side[0].dy, a.side[1].dy, py, hq, k));
+    fk += groups;
   };
-  auto places = [&] {
-    return Both{HeadPlace<I>(token, a.side[0].x, a.side[1].x, hq), HeadPlace<I>(token, a.side[0].dy, a.side[1].dy, hq)};
-  };
-  auto load = [&](const Both& at, int h, uint32_t (&x)[Lane::NW], uint32_t (&dy)[Lane::NW]) {
-    me.load(head_at<T, I>(a.side[0].x, a.side[1].x, at.x, hq, h), x);
-    me.load(head_at<T, I>(a.side[0].dy, a.side[1].dy, at.dy, hq, h), dy);
-  };
-  // the first token's units as heads [first, last)
-  int lo = 0, hi = 0;
-  bool on = share.take(a, lo, hi);
-  int first = lo * groups + group, last = min(hi * groups, heads);
-  Both src = places();
-  if (first < last) load(src, first, wx, wy);
+#pragma unroll
+  for (int i = 0; i < Ring::AHEAD; ++i) fetch();
   HeadAngles<D, LANES> way(a, angles, lane, token, tokens);
-  for (int k = 0; k < 2; ++k) {
+  for (int k = 0; k < 2; ++k)
     head_gamma<Lane, D>(slots + k * lanes * kHeadSlot, a, a.side[k].gamma, threadIdx.x, kHeadThreads);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) reinterpret_cast<float4*>(mine + k * 32 * kHeadSlot)[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
+  for (int j = 0; j < 8; ++j) mine[32 * j] = make_float4(0.f, 0.f, 0.f, 0.f);
   __syncthreads();
-  while (on) {
+  int lo, hi;
+  for (bool more = work.take(a, lo, hi); more; more = work.take(a, lo, hi)) {
     const HeadPlace<I> dst(token, a.side[0].y, a.side[1].y, hq);
-    const int from = first, end = last;
-    // the token behind this one
-    lo = hi = 0;
-    on = share.take(a, lo, hi);
-    if (on) token.step(a);
-    first = lo * groups + group;
-    last = min(hi * groups, heads);
-    const Both then = places();
+    token.step(a);
+    const int end = min(hi * groups, heads);
     const bool good = way.turn_over();
 #pragma unroll 1
-    for (int k = from; k - group < end; k += groups) {
+    for (int k = lo * groups + group; k - group < end; k += groups) {
       float2 p[4], q[4], u[4], v[4];
-      Lane::unpack(wx, p, q);
-      Lane::unpack(wy, u, v);
-      if (k - group + groups < end) {
-        if (k + groups < end) load(src, k + groups, wx, wy);
-      } else if (first < last) {
-        load(then, first, wx, wy);
+      {
+        uint32_t wx[Lane::NW], wy[Lane::NW];
+        ring.take(wx, wy);
+        Lane::unpack(wx, p, q);
+        Lane::unpack(wy, u, v);
       }
+      fetch();
       const int which = k < hq ? 0 : 1;
       if (good) me.template turn<true>(u, v, angle);
       float2 sx = splat2(0.f), sw = splat2(0.f);
@@ -541,16 +641,16 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_grad_ker
         const float r = rsqrtf(fmaf(m[0], inv_d, a.eps));
         // dx = rstd (w - x rstd^2 mean(w x)); w is formed again rather than kept
         const float2 r2 = splat2(r), k2 = splat2(-(m[1] * inv_d) * r * r);
-        float4* at = reinterpret_cast<float4*>(mine + which * 32 * kHeadSlot);
+        float4* at = mine + which * 128;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float4 x = at[j], y = at[2 + j];
+          const float4 x = at[32 * j], y = at[32 * (2 + j)];
           const float2 x0 = fma2(u[2 * j], mul2(p[2 * j], r2), make_float2(x.x, x.y));
           const float2 x1 = fma2(u[2 * j + 1], mul2(p[2 * j + 1], r2), make_float2(x.z, x.w));
           const float2 y0 = fma2(v[2 * j], mul2(q[2 * j], r2), make_float2(y.x, y.y));
           const float2 y1 = fma2(v[2 * j + 1], mul2(q[2 * j + 1], r2), make_float2(y.z, y.w));
-          at[j] = make_float4(x0.x, x0.y, x1.x, x1.y);
-          at[2 + j] = make_float4(y0.x, y0.y, y1.x, y1.y);
+          at[32 * j] = make_float4(x0.x, x0.y, x1.x, x1.y);
+          at[32 * (2 + j)] = make_float4(y0.x, y0.y, y1.x, y1.y);
           float2 g[2], e[2];
           lds_pairs(gamma + 16 * j, g);
           lds_pairs(gamma + 32 + 16 * j, e);
@@ -568,7 +668,6 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_grad_ker
       }
       me.store(head_at<T, I>(a.side[0].y, a.side[1].y, dst, hq, k), o);
     }
-    src = then;
   }
   if (!a.want) return;
   __syncthreads();
@@ -577,18 +676,20 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_grad_ker
     const int k = i / (lanes * 16), l = i / 16 % lanes, e = i % 16;
     float sum = 0.f;
     for (int w = 0; w < kHeadWarps; ++w)
-      for (int g = 0; g < groups; ++g) sum += sums[(w * 64 + k * 32 + g * lanes + l) * kHeadSlot + e];
+      for (int g = 0; g < groups; ++g)
+        sum += reinterpret_cast<const float*>(sums + (w * 2 + k) * 128 + e / 4 * 32 + g * lanes + l)[e % 4];
     const Lane that(l, a.D, a.R);
     const int col = e < 8 ? that.col_a(e) : that.col_b(e - 8);
     if (col >= 0) a.ws[((int64_t)blockIdx.x * 2 + k) * a.D + col] = sum;
   }
 }
 
-// dgamma from the CTAs' partial rows: a CTA takes 32 columns of one side, its
-// warps rows in turn.
+// dgamma from the CTAs' partial rows: a CTA takes 32 columns of one side, each
+// warp a 32nd of the rows, all of whose loads are in flight at once.
+constexpr int kHeadReduceWarps = 32;
 template <typename D>
-__global__ void __launch_bounds__(512) head_gamma_reduce_kernel(const HeadArgs a, const int rows) {
-  __shared__ float sh[16][33];
+__global__ void __launch_bounds__(32 * kHeadReduceWarps) head_gamma_reduce_kernel(const HeadArgs a, const int rows) {
+  __shared__ float sh[kHeadReduceWarps][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + lane, k = blockIdx.y;
   void* dg = a.side[k].dgamma;
@@ -597,16 +698,22 @@ __global__ void __launch_bounds__(512) head_gamma_reduce_kernel(const HeadArgs a
   const float* ws = a.ws + k * a.D + i;
   float sum = 0.f;
   if (i < a.D) {
-#pragma unroll 4
-    for (int p = warp; p < rows; p += 16) sum += ws[(int64_t)p * 2 * a.D];
+    constexpr int B = 10;  // rows a warp has of those of two CTAs an SM
+    for (int p = warp; p < rows; p += B * kHeadReduceWarps) {
+      float v[B];
+#pragma unroll
+      for (int j = 0; j < B; ++j)
+        v[j] = p + j * kHeadReduceWarps < rows ? ws[(int64_t)(p + j * kHeadReduceWarps) * 2 * a.D] : 0.f;
+      sum += tree_sum<B>(v);
+    }
   }
   sh[warp][lane] = sum;
   __syncthreads();
   if (warp != 0 || i >= a.D || dg == nullptr) return;
-  float v[16];
+  float v[kHeadReduceWarps];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] = sh[j][lane];
-  const float total = tree_sum<16>(v);
+  for (int j = 0; j < kHeadReduceWarps; ++j) v[j] = sh[j][lane];
+  const float total = tree_sum<kHeadReduceWarps>(v);
   if (a.w_f32)
     reinterpret_cast<float*>(dg)[i] = total;
   else
@@ -681,7 +788,9 @@ template <typename D, int CA, bool PAIRS, int LANES, typename I>
 cudaError_t run_head_rotary_grad(HeadArgs a, const DeviceInfo& dev, cudaStream_t s, int* ctas) {
   static KernelMemo memo;
   return run_heads(head_rotary_grad_kernel<D, CA, PAIRS, LANES, I>, a,
-                   sizeof(float) * ((2 + kHeadWarps) * a.lanes + 64 * kHeadWarps) * kHeadSlot, kHeadGradMaxPerSm, memo, dev, s, ctas);
+                   sizeof(float) * (2 + kHeadWarps) * a.lanes * kHeadSlot +
+                       kHeadWarps * (4096 + HeadGradRing<D, CA, PAIRS, LANES>::Type::BYTES),
+                   kHeadGradMaxPerSm, memo, dev, s, ctas);
 }
 
 // Whether every tensor has fewer than 2^31 elements from its first to its last.
@@ -746,7 +855,7 @@ cudaError_t launch_head_rotary_grad(HeadArgs a, const DeviceInfo& dev, cudaStrea
     if (e != cudaSuccess) return e;
   }
   if (!a.want) return cudaSuccess;
-  FirstLaunch second(512, 0, s, 1);
+  FirstLaunch second(32 * kHeadReduceWarps, 0, s, 1);
   second.cfg.gridDim.y = 2;
   return second.launch((unsigned)((a.D + 31) / 32), true, head_gamma_reduce_kernel<D>, a, rows);
 }
