@@ -544,7 +544,7 @@ norm_status norm_selftest_bounded_wait(unsigned long long limit_ns, norm_stream_
  * used only where the call meets its requirements (alignment, row width);
  * every family computes the same results within rounding.  The block join and
  * the token lookup have two families: 2 is their loop, anything else the
- * automatic choice.
+ * automatic choice.  The per-head norm and the log probabilities have one.
  */
 norm_status norm_set_kernel_path(int path);
 

@@ -54,10 +54,17 @@ struct LogitChunk {
   __device__ static __forceinline__ int lead(const T* row) {
     return (int)((reinterpret_cast<uintptr_t>(row) & 31u) / ES);
   }
-  // Columns [col, col + GE) of the row; -inf outside [0, V).
+  // Columns [col, col + GE) of the row; -inf outside [0, V).  AGAIN: a chunk here and
+  // there, which asks L2 for no more than itself.
+  template <bool AGAIN = false>
   __device__ static __forceinline__ void load(const T* row, int col, int V, uint32_t (&w)[8]) {
     if (col >= 0 && col + GE <= V) {
-      ld_stream32(row + col, w);
+      if constexpr (AGAIN)
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(row + col));
+      else
+        ld_stream32(row + col, w);
       return;
     }
 #pragma unroll
@@ -221,8 +228,10 @@ __host__ __device__ constexpr int top_bytes(int rows) { return rows * (int)sizeo
 // in first.  A key at that chunk's last column is no larger than the key of the
 // logit itself, so at least `top` logits reach tau, the top-th largest of those
 // over 32 groups of threads (the same lane of each warp); all that do are in the
-// chunks of threads whose own key does.  Only those chunks are read again (they
-// are in L2): a 12th of the row for 20 of 256 threads.
+// chunks of threads whose own key does.  Only those chunks are read again: a 12th of
+// the row for 20 of 256 threads, most of them still in L2.  (us, 1x131072 bf16 with 20
+// of them 8.4, without 4.1; 1024x131072 64; 47; ranks among 128 groups by reads of
+// shared memory 10.3 and 65.)
 template <typename D>
 __device__ __forceinline__ void row_top(const RowGroup& g, TopShared& sh, unsigned long long* lanes, const typename D::T* z,
                                         int a0, int V, int first, int last, int top, float mx, int mi) {
@@ -262,7 +271,7 @@ __device__ __forceinline__ void row_top(const RowGroup& g, TopShared& sh, unsign
     if (i >= last) continue;
     uint32_t w[8];
     const int col = i * L::GE - a0;
-    L::load(z, col, V, w);
+    L::template load<true>(z, col, V, w);
     if (!(L::max(w) >= least)) continue;
 #pragma unroll
     for (int e = 0; e < L::GE; ++e) {
@@ -502,13 +511,15 @@ __global__ void __launch_bounds__(kLogprobThreads, kLogprobPerSm) logprob_kernel
   }
 }
 
-// The gradient: tiles of U * tx chunks of one row, 256 / tx rows a CTA.  SAME:
+// The gradient: tiles of U * tx chunks of one row, 128 / tx rows a CTA.  SAME:
 // logits and gradient have the same lead, so that aligned chunks of the one are
-// aligned in the other.
-constexpr int kLogprobGradThreads = 256;
-constexpr int kLogprobGradU = 2;
+// aligned in the other.  (us, 4096x131072 bf16, 333x50001 bf16: 128 threads and three
+// chunks 309, 12.2; two 333, 12.9; four 315, 12.1; 256 and three 313, 12.5; two 342,
+// 13.6; one 382, 14.5; 512 and two 349, 15.4.)
+constexpr int kLogprobGradThreads = 128;
+constexpr int kLogprobGradU = 3;
 template <typename D, bool ENT, bool SAME>
-__global__ void __launch_bounds__(kLogprobGradThreads, 4) logprob_grad_kernel(const LogprobGradArgs a) {
+__global__ void __launch_bounds__(kLogprobGradThreads, 8) logprob_grad_kernel(const LogprobGradArgs a) {
   using L = LogitChunk<D>;
   using T = typename D::T;
   constexpr int U = kLogprobGradU;
@@ -630,7 +641,9 @@ cudaError_t launch_logprob_grad(LogprobGradArgs a, const DeviceInfo& dev, cudaSt
   (void)cudaGetLastError();
   using L = LogitChunk<D>;
   a.err = dev.err;
-  const int chunks = (a.V + L::GE - 1) / L::GE + 1;  // of any lead
+  // a row's chunks: one more where rows do not begin at 32 bytes
+  const bool leads = ((reinterpret_cast<uintptr_t>(a.z) | (a.N > 1 ? (uintptr_t)(a.ldz * (int64_t)sizeof(typename D::T)) : 0u)) & 31u) != 0;
+  const int chunks = (a.V + L::GE - 1) / L::GE + leads;
   a.tx = 32;
   while (a.tx < kLogprobGradThreads && a.tx * kLogprobGradU < chunks) a.tx *= 2;
   a.tiles = (chunks + a.tx * kLogprobGradU - 1) / (a.tx * kLogprobGradU);
