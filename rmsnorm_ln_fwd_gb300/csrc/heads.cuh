@@ -29,12 +29,11 @@
 
 namespace normk {
 
-// Two CTAs of eight warps an SM, up to 128 registers.  (us, 16384 tokens of 32+8
+// Two CTAs (kHeadPerSm) of eight warps an SM, up to 128 registers.  (us, 16384 tokens of 32+8
 // heads of 128 bf16 forward, and 8192 backward while the gradient still held its next
 // head in registers: 59.8, 51.8; five CTAs of four warps 59.9, 57; three of six 59.4,
 // 68; three of eight, 80 registers, 59.8, 69.)
 constexpr int kHeadWarps = 8;
-constexpr int kHeadPerSm = 2;
 constexpr int kHeadThreads = 32 * kHeadWarps;
 
 // A lane's 16 columns: [c0, c0 + n0) and [c1, c1 + n1), in halves [0, R/2) and
@@ -72,7 +71,14 @@ struct HeadLane {
   __device__ static __forceinline__ int clamp8(int n) { return n < 0 ? 0 : n > 8 ? 8 : n; }
 
   __device__ static __forceinline__ void load_half(const T* p, int n, uint32_t* w) {
-    if constexpr (CA * ES == 16) {
+    if constexpr (CA * ES == 32) {
+      if (n > 0) {
+        ld_stream32(p, *reinterpret_cast<uint32_t(*)[8]>(w));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = 0u;
+      }
+    } else if constexpr (CA * ES == 16) {
 #pragma unroll
       for (int k = 0; k < 8 / CA; ++k) {
         const uint4 u = k * CA < n ? ld_stream(p + k * CA) : make_uint4(0u, 0u, 0u, 0u);
@@ -101,7 +107,9 @@ struct HeadLane {
     }
   }
   __device__ static __forceinline__ void store_half(T* p, int n, const uint32_t* w) {
-    if constexpr (CA * ES == 16) {
+    if constexpr (CA * ES == 32) {
+      if (n > 0) st_vec32(p, *reinterpret_cast<const uint32_t(*)[8]>(w));
+    } else if constexpr (CA * ES == 16) {
 #pragma unroll
       for (int k = 0; k < 8 / CA; ++k)
         if (k * CA < n) st_vec(p + k * CA, make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
@@ -731,8 +739,8 @@ inline int head_lanes(const HeadArgs& a) {
   return lanes;
 }
 
-// Columns an access: 16 bytes, 8, or one element, whichever divides every
-// column that an access starts at, and fits every tensor.
+// Columns an access: eight (16 bytes of half precision, 32 of fp32), four or one,
+// whichever divides every column that an access starts at, and fits every tensor.
 template <typename D>
 int head_access(const HeadArgs& a, bool grad) {
   constexpr int ES = (int)sizeof(typename D::T);
@@ -746,22 +754,21 @@ int head_access(const HeadArgs& a, bool grad) {
       bits |= (unsigned long long)((v->sb | v->st | v->sh) * ES);
     }
   }
-  return (bits & 15) == 0 ? 16 / ES : ES == 2 && (bits & 7) == 0 ? 4 : 1;
+  return (bits & (8 * ES - 1)) == 0 ? 8 : (bits & (4 * ES - 1)) == 0 ? 4 : 1;
 }
 
 // The kernel on as many CTAs as are resident, or fewer.  Its units are shared out
 // to the warps one by one: whole tokens would leave some warps with four and others
 // with three of 8192 (56 us for 51.8).
 template <typename K>
-cudaError_t run_heads(K kern, HeadArgs& a, size_t smem, int most_per_sm, KernelMemo& memo, const DeviceInfo& dev, cudaStream_t s,
-                      int* ctas) {
+cudaError_t run_heads(K kern, HeadArgs& a, size_t smem, KernelMemo& memo, const DeviceInfo& dev, cudaStream_t s, int* ctas) {
   if (smem > 48 * 1024) {
     const cudaError_t e = memo.allow_smem(kern, dev.max_smem_optin - 1024, dev);
     if (e != cudaSuccess) return e;
   }
   const int resident = memo.resident(kHeadThreads, smem, dev, [&](int* n) {
     const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kern, kHeadThreads, smem);
-    *n = std::min(*n, most_per_sm) * dev.sm_count;
+    *n = std::min(*n, kHeadPerSm) * dev.sm_count;
     return e;
   });
   const int groups = 32 / a.lanes;
@@ -779,8 +786,8 @@ cudaError_t run_head_rotary(HeadArgs a, const DeviceInfo& dev, cudaStream_t s) {
   constexpr int U = sizeof(typename D::T) == 2 ? 2 : 1;  // 64 bytes of a lane
   static KernelMemo memo;
   int ctas;
-  return run_heads(head_rotary_kernel<D, CA, PAIRS, U, LANES, I>, a, sizeof(float) * (2 + kHeadWarps) * a.lanes * kHeadSlot, 32,
-                   memo, dev, s, &ctas);
+  return run_heads(head_rotary_kernel<D, CA, PAIRS, U, LANES, I>, a, sizeof(float) * (2 + kHeadWarps) * a.lanes * kHeadSlot, memo,
+                   dev, s, &ctas);
 }
 
 template <typename D, int CA, bool PAIRS, int LANES, typename I>
@@ -789,7 +796,7 @@ cudaError_t run_head_rotary_grad(HeadArgs a, const DeviceInfo& dev, cudaStream_t
   return run_heads(head_rotary_grad_kernel<D, CA, PAIRS, LANES, I>, a,
                    sizeof(float) * (2 + kHeadWarps) * a.lanes * kHeadSlot +
                        kHeadWarps * (4096 + HeadGradRing<D, CA, PAIRS, LANES>::Type::BYTES),
-                   kHeadGradMaxPerSm, memo, dev, s, ctas);
+                   memo, dev, s, ctas);
 }
 
 // Whether every tensor has fewer than 2^31 elements from its first to its last.
@@ -808,29 +815,22 @@ inline bool head_offsets_fit(const HeadArgs& a, bool grad) {
 // rotated columns or 0, an offset's type) as compile-time values.
 template <typename D, typename F>
 cudaError_t head_variants(const HeadArgs& a, bool grad, F&& f) {
-  constexpr int V = 16 / (int)sizeof(typename D::T);
   const int access = head_access<D>(a, grad);
   auto with = [&](auto ca, auto l, auto off) {
     return a.interleaved && a.R ? f(ca, std::integral_constant<bool, true>{}, l, off)
                                 : f(ca, std::integral_constant<bool, false>{}, l, off);
   };
-  using Any = std::integral_constant<int, 0>;
-  if (!head_offsets_fit(a, grad))
-    return access == V ? with(std::integral_constant<int, V>{}, Any{}, int64_t{})
-                       : with(std::integral_constant<int, 1>{}, Any{}, int64_t{});
-  if (access == V) {
-    const std::integral_constant<int, V> ca;
-    if (a.R == a.D && a.D == 16 * a.lanes) {
-      if (a.D == 64) return with(ca, std::integral_constant<int, 4>{}, uint32_t{});
-      if (a.D == 128) return with(ca, std::integral_constant<int, 8>{}, uint32_t{});
-      if (a.D == 256) return with(ca, std::integral_constant<int, 16>{}, uint32_t{});
-    }
-    return with(ca, Any{}, uint32_t{});
+  const std::integral_constant<int, 8> eight;
+  const std::integral_constant<int, 4> four;
+  const std::integral_constant<int, 1> one;
+  const std::integral_constant<int, 0> any;
+  if (!head_offsets_fit(a, grad)) return access == 8 ? with(eight, any, int64_t{}) : with(one, any, int64_t{});
+  if (access == 8 && a.R == a.D && a.D == 16 * a.lanes) {
+    if (a.D == 64) return with(eight, std::integral_constant<int, 4>{}, uint32_t{});
+    if (a.D == 128) return with(eight, std::integral_constant<int, 8>{}, uint32_t{});
+    if (a.D == 256) return with(eight, std::integral_constant<int, 16>{}, uint32_t{});
   }
-  if constexpr (V == 8) {
-    if (access == 4) return with(std::integral_constant<int, 4>{}, Any{}, uint32_t{});
-  }
-  return with(std::integral_constant<int, 1>{}, Any{}, uint32_t{});
+  return access == 8 ? with(eight, any, uint32_t{}) : access == 4 ? with(four, any, uint32_t{}) : with(one, any, uint32_t{});
 }
 
 template <typename D>

@@ -58,9 +58,9 @@ struct HeadArgs {
 // Device error bit of a position outside the table.
 constexpr unsigned kErrBadPosition = 8u;
 
-// CTAs the gradient may have an SM, and its partial rows.
-constexpr int kHeadGradMaxPerSm = 4;
-inline size_t head_grad_partials(const DeviceInfo& dev) { return (size_t)2 * kHeadGradMaxPerSm * dev.sm_count; }
+// CTAs an SM, and the gradient's partial rows.
+constexpr int kHeadPerSm = 2;
+inline size_t head_grad_partials(const DeviceInfo& dev) { return (size_t)2 * kHeadPerSm * dev.sm_count; }
 
 template <typename D>
 cudaError_t launch_head_rotary(HeadArgs a, const DeviceInfo& dev, cudaStream_t s);

@@ -72,10 +72,11 @@ bool same(const Heads& a, const Heads& b) {
   return a.v.p == b.v.p && a.v.sb == b.v.sb && a.v.st == b.v.st && a.v.sh == b.v.sh && a.H == b.H;
 }
 
-// Whether two tensors of one type share no element: their ranges are apart, or
-// they are parts of one period, as the queries and keys of a fused projection
-// are: both repeat at multiples of it, and the columns that they take of it are
-// apart.
+// Whether two tensors of one type and of the same batches and tokens share no
+// element: their ranges are apart, or they are parts of one period, as the queries
+// and keys of a fused projection are: both repeat at multiples of it, and the
+// columns that they take of it are apart.  The period is a token, or a batch (in
+// either order, whichever is inside the other).
 bool apart(const Heads& a, const Heads& b) {
   if (!overlap(a.span(), b.span())) return true;
   const intptr_t bytes = (intptr_t)(reinterpret_cast<uintptr_t>(b.v.p) - reinterpret_cast<uintptr_t>(a.v.p));
@@ -86,12 +87,20 @@ bool apart(const Heads& a, const Heads& b) {
     const int64_t r = ((delta % period) + period) % period;
     return wa <= period && r >= wa && r + wb <= period;
   };
-  // tokens repeat within a batch, whose start is a multiple of the token's period
-  if (a.T > 1 && a.v.st == b.v.st && (a.B == 1 || (a.v.sb % a.v.st == 0 && b.v.sb % b.v.st == 0)) &&
-      within(a.v.st, (a.H - 1) * a.v.sh + a.D, (b.H - 1) * b.v.sh + b.D))
+  // inner and outer strides of the dims of more than one
+  struct Outer {
+    int64_t inner, n_inner, outer;  // outer: 0 with one such dim
+  };
+  auto outer = [](const Heads& h) {
+    if (h.B <= 1 || h.T <= 1) return h.B > 1 ? Outer{h.v.sb, h.B, 0} : Outer{h.v.st, h.T, 0};
+    return h.v.st <= h.v.sb ? Outer{h.v.st, h.T, h.v.sb} : Outer{h.v.sb, h.B, h.v.st};
+  };
+  const Outer oa = outer(a), ob = outer(b);
+  const int64_t wa = (a.H - 1) * a.v.sh + a.D, wb = (b.H - 1) * b.v.sh + b.D;
+  if (oa.inner > 0 && oa.inner == ob.inner && oa.outer % oa.inner == 0 && ob.outer % ob.inner == 0 && within(oa.inner, wa, wb))
     return true;
-  return a.B > 1 && a.v.sb == b.v.sb &&
-         within(a.v.sb, (a.T - 1) * a.v.st + (a.H - 1) * a.v.sh + a.D, (b.T - 1) * b.v.st + (b.H - 1) * b.v.sh + b.D);
+  return oa.outer > 0 && oa.outer == ob.outer &&
+         within(oa.outer, (oa.n_inner - 1) * oa.inner + wa, (ob.n_inner - 1) * ob.inner + wb);
 }
 
 size_t index_size(norm_itype t) { return t == NORM_I64 ? 8 : 4; }

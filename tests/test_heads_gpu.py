@@ -212,6 +212,28 @@ def test_in_place_has_the_same_bits(dt, layout):
         assert torch.equal(q._base[..., -2 * 96:], whole[..., -2 * 96:])
 
 
+@pytest.mark.parametrize("order", ["decode", "tokens first", "heads first", "one sequence"])
+def test_in_place_on_a_fused_projection(order):
+    """Queries and keys whose elements are between one another's, in the layouts in which projections leave them."""
+    hq, hk, D = 6, 2, 64
+    B, T = {"decode": (8, 1), "one sequence": (1, 21)}.get(order, (3, 11))
+    if order == "tokens first":    # (T, B, heads * D)
+        base = rnd((T, B, hq + 2 * hk, D), 40, torch.bfloat16).transpose(0, 1)
+    elif order == "heads first":   # (B, heads, T, D)
+        base = rnd((B, hq + 2 * hk, T, D), 40, torch.bfloat16).transpose(1, 2)
+    else:
+        base = rnd((B, T, hq + 2 * hk, D), 40, torch.bfloat16)
+    q, k, v = base[:, :, :hq], base[:, :, hq:hq + hk], base[:, :, hq + hk:].clone()
+    c = dict(q=q, k=k, gq=rnd((D,), 41, torch.bfloat16, 1.0, 0.2), gk=rnd((D,), 42, torch.bfloat16, 1.0, 0.2), pos=None)
+    c["cos"], c["sin"] = tables(64, D)
+    want = call(c)
+    call(c, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(base[:, :, hq + hk:], v)
+    # into another's place: the keys' heads over the last query heads
+    with pytest.raises(nl.NormError):
+        call(c, q_out=q, k_out=base[:, :, hq - 1:hq - 1 + hk])
+
+
 def test_outputs_in_other_layouts_and_margins():
     c = make(2, 11, 4, 2, 64, 32, "bf16", layout="fused", seed=5)
     want = call(c)
@@ -408,6 +430,21 @@ def test_capture_and_replay_with_new_inputs():
         torch.cuda.synchronize()
         for a, b in zip(out + grad, want):
             assert torch.equal(a, b)
+
+
+def test_in_inference_mode_and_from_leaves():
+    c = make(2, 5, 4, 2, 64, 64, "bf16", seed=19)
+    want = call(c) + call_grad(c)
+    with torch.inference_mode():
+        got = call(c) + call_grad(c)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    d = {n: None if t is None else (t.requires_grad_() if t.is_floating_point() else t) for n, t in c.items()}
+    got = call(d) + call_grad(d)
+    for a, b in zip(got, want):
+        assert not a.requires_grad and torch.equal(a, b)
+    got[0].mul_(2)  # outputs are ordinary tensors, whatever they share
+    assert torch.equal(got[1], want[1]) and torch.equal(got[0], want[0] * 2)
 
 
 def test_two_streams_at_once():

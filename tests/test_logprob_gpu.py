@@ -90,7 +90,8 @@ def check(z, tokens, scale, out, top=0, ignore=None, entropy=True):
         want = O.top_ids(Z, top)
         got = tid.cpu().numpy().reshape(-1, top)
         assert tid.dtype == torch.int64 and np.array_equal(got, want)
-        xx = np.where(want < 0, -np.inf, np.take_along_axis(x, np.maximum(want, 0), 1) - rl[:, None])
+        with np.errstate(invalid="ignore"):
+            xx = np.where(want < 0, -np.inf, np.take_along_axis(x, np.maximum(want, 0), 1) - rl[:, None])
         xa = np.take_along_axis(ax, np.maximum(want, 0), 1)
         same_or_close(tlp.reshape(-1, top), xx, dl[:, None] + 4 * U * xa, "top_logprobs")
     else:
@@ -391,6 +392,26 @@ def test_capture_replay_and_two_streams():
             assert torch.equal(a, b)
 
 
+def test_one_row_without_a_batch_dim_and_inference_mode():
+    z, tokens = make(1, 777, "bf16", seed=30)
+    want = nl.token_logprobs(z, tokens, top=3)
+    got = nl.token_logprobs(z[0], tokens[0], top=3)
+    assert got[0].shape == () and got[3].shape == (2,) and got[5].shape == (3,)
+    with torch.inference_mode():
+        more = nl.token_logprobs(z, tokens.view(1), top=3)
+        one = torch.ones((), device=DEV)
+        d = nl.token_logprobs_grad(one, z[0], tokens[0], got[3], got[1], one)
+    for a, b, c in zip(got, want, more):
+        assert torch.equal(a.reshape(b.shape), b) and torch.equal(b, c)
+    assert d.shape == (777,)
+    check_grad(z, tokens, 1.0, d.view(1, -1), want[3], want[1], one.view(1), one.view(1), None)
+    got = nl.token_logprobs(z.requires_grad_(), tokens, top=3)
+    assert not got[0].requires_grad
+    got[0].fill_(7.0)  # ordinary tensors, whatever they share
+    for a, b in zip(got[1:], want[1:]):
+        assert torch.equal(a, b)
+
+
 def test_empty_batch():
     z = torch.empty(0, 30, device=DEV)
     out = nl.token_logprobs(z, torch.empty(0, device=DEV, dtype=torch.long), top=2)
@@ -514,6 +535,7 @@ def test_together_as_a_model_uses_them():
     # nothing, of which fp32 keeps U at best, and log(1 + d) with it: the 200 U (+ 8 U E|x|, E|x| < 1 there) above are
     # absolute, and the entropies here (1e-6 at most) are smaller than that.
     for a, b in ((lp, rlp), (ent, rent), (lse, rlse)):
+        b = b.detach()
         assert float((a - b).abs().max()) < 1e-4 * float(b.abs().max()) + 208 * U
     assert torch.equal(ti, logp.topk(3, -1).indices)
     for (n, _), w in zip(P.items(), want):
