@@ -20,12 +20,16 @@
 
 namespace normk {
 
-// Threads and chunks in flight (us; 4096x131072 bf16, 333x50001 fp16, 16384x4096
-// bf16): 256 threads and three chunks 159, 12.7, 27.7; four 159, 13.5, 27.5; two
-// 167, 12.5, 28; 128 threads 198, 14.7, 83; two buffers of one or two chunks 165
-// and 189.  64 registers, four CTAs an SM; three (80 registers) 169, 11.5, 29.7.
+// 256 threads a CTA (us, 4096x131072, 333x50001 and 16384x4096 bf16: 159, 13, 28;
+// 128 threads 198, 14.7, 83).  The kernel comes in three shapes of chunks that a
+// thread has in flight and CTAs an SM, by how many CTAs there are: 3 and 4 where they
+// fill the GPU, 4 and 3 (80 registers) where three an SM hold them all, 6 and 2 where
+// two do, except in clusters of more than two, which two an SM may not hold.  (us, as
+// 3 and 4; 4 and 3; 6 and 2: 4096x131072 159; 169; 184, 333x50001 12.8; 11.1; 16.3,
+// 150x50001 in clusters of two 9.2; 7.0; 6.4, 2000x4096 7.2; 6.2; 5.3, 32x131072 with
+// 20 alternatives in clusters of eight 11.5; 10.3; 12.8.  Four chunks and four CTAs,
+// 64 registers, 159, 13.5; two 167, 12.5.)
 constexpr int kLogprobThreads = 256;  // of a CTA
-constexpr int kLogprobChunks = 3;     // of a thread in flight
 constexpr int kLogprobPerSm = 4;      // CTAs
 constexpr int kLogprobMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -150,9 +154,8 @@ __device__ __forceinline__ void sort_keys(const RowGroup& g, unsigned long long*
   }
 }
 
-// Where a key goes among `n`: the number of larger ones.  Two keys a
-// load and eight loads in flight; key is 16-byte aligned and holds zeros up to a
-// multiple of 16.
+// Where a key goes among `n`: the number of larger ones.  Two keys a load and eight
+// loads in flight; key is 16-byte aligned and holds zeros up to a multiple of 16.
 __device__ __forceinline__ int key_rank(const unsigned long long* key, int n, unsigned long long k) {
   int rank = 0;
 #pragma unroll 1
@@ -166,11 +169,12 @@ __device__ __forceinline__ int key_rank(const unsigned long long* key, int n, un
   return rank;
 }
 
-// The first `top` of `n` keys (different ones, or 0) into best, 0 where there are fewer;
-// best is all zeros before.  Few keys go to their ranks, which takes no barrier (to
-// sort 64 takes 21): a key a thread, or 128.
+// The first `top` of `n` keys (different ones, or 0) into best, 0 where there are
+// fewer; best is all zeros before.  Keys go to their ranks, which takes no barrier,
+// as long as a thread has few of them (320 candidates of a row masked with one value,
+// 256 threads: 13.0 us a call for 16.1 by sorting).
 __device__ __forceinline__ void best_keys(const RowGroup& g, unsigned long long* key, int n, int top, unsigned long long* best) {
-  if (n <= max(g.n, 128)) {
+  if (n <= max(2 * g.n, 128)) {
     if (n + g.t < (n + 15) / 16 * 16) key[n + g.t] = 0ull;
     g.sync();
 #pragma unroll 1
@@ -383,11 +387,10 @@ __device__ __forceinline__ void row_sums(const RowGroup& g, RowSums& r, float c2
 
 // A row for a.tpr threads, or for a cluster of a.cl CTAs, which take consecutive
 // parts of its chunks.  U chunks of a thread are in flight at a time.
-template <typename D, bool ENT, bool TOP>
-__global__ void __launch_bounds__(kLogprobThreads, kLogprobPerSm) logprob_kernel(const LogprobArgs a) {
+template <typename D, bool ENT, bool TOP, int U, int PER_SM>
+__global__ void __launch_bounds__(kLogprobThreads, PER_SM) logprob_kernel(const LogprobArgs a) {
   using L = LogitChunk<D>;
   using T = typename D::T;
-  constexpr int U = kLogprobChunks;
   static_assert(kLogprobThreads <= 256 && kLogprobMaxCluster <= 8, "eight sums");
   extern __shared__ __align__(16) unsigned char top_raw[];
   __shared__ float red[3 * kLogprobThreads / 32];
@@ -610,11 +613,13 @@ template <typename D, bool ENT, bool TOP>
 cudaError_t run_logprob(LogprobArgs a, const DeviceInfo& dev, cudaStream_t s) {
   constexpr int GE = LogitChunk<D>::GE;
   const int chunks = a.V / GE + 1;
-  // Few rows: clusters share them, as long as the CTAs all fit at once and keep 128
-  // chunks each (64x131072 bf16 8.6 -> 6.7 us as 512 CTAs; 333x50001 as 666, which
-  // do not fit, 12.7 -> 16.1).
+  // Few rows: clusters share them, as long as the CTAs all fit at once and have a
+  // chunk for every other thread, or, more than one an SM, four for every thread (us,
+  // 64x131072 bf16 8.6 -> 6.7 as 512 CTAs; 333x50001 as 666, which do not fit, 12.7 ->
+  // 16.1; 150x50001 as 600 of three chunks a thread 8.9, as 300 of six 6.4).
   a.cl = 1;
-  while (a.cl < kLogprobMaxCluster && a.N * a.cl * 2 <= kLogprobPerSm * (int64_t)dev.sm_count && chunks / (a.cl * 2) >= 128)
+  while (a.cl < kLogprobMaxCluster && a.N * a.cl * 2 <= kLogprobPerSm * (int64_t)dev.sm_count &&
+         chunks / (a.cl * 2) >= (a.N * a.cl * 2 <= dev.sm_count ? kLogprobThreads / 2 : 4 * kLogprobThreads))
     a.cl *= 2;
   // Otherwise 16 chunks a thread, or two with alternatives, whose threads each keep
   // a candidate: what a row costs besides its logits is the same for each warp (us,
@@ -625,7 +630,11 @@ cudaError_t run_logprob(LogprobArgs a, const DeviceInfo& dev, cudaStream_t s) {
   while (a.tpr < kLogprobThreads && a.tpr * each < chunks) a.tpr *= 2;
   const int rows = kLogprobThreads / a.tpr;
   FirstLaunch first(kLogprobThreads, TOP ? top_bytes(rows) : 0, s, a.cl);
-  return first.launch((unsigned)(a.cl > 1 ? a.N * a.cl : (a.N + rows - 1) / rows), true, logprob_kernel<D, ENT, TOP>, a);
+  const int64_t ctas = a.cl > 1 ? a.N * a.cl : (a.N + rows - 1) / rows;
+  auto launch = [&](auto kern) { return first.launch((unsigned)ctas, true, kern, a); };
+  if (ctas <= 2 * (int64_t)dev.sm_count && a.cl <= 2) return launch(logprob_kernel<D, ENT, TOP, 6, 2>);
+  if (ctas <= 3 * (int64_t)dev.sm_count) return launch(logprob_kernel<D, ENT, TOP, 4, 3>);
+  return launch(logprob_kernel<D, ENT, TOP, 3, kLogprobPerSm>);
 }
 
 template <typename D>
