@@ -50,6 +50,7 @@ struct HeadArgs {
   int want;  // whether any dgamma is wanted
   // filled in by the launcher:
   int lanes;   // a head, a power of two
+  int pass;    // forward: stores that leave L2 first
   int its;        // units of a token: heads a group has to take
   int64_t each;   // units a warp, and how many warps have one more
   int64_t extra;
