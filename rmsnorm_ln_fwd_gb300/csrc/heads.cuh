@@ -11,14 +11,16 @@
 // one exchange.
 //
 // A few flops an element: the traffic bounds both.  16384 tokens of 32+8 heads of
-// 128, bf16, run forward in 60 us, 5.6 TB/s in and out, and stores without the
-// arithmetic in 59; the gradient of 8192 tokens in 46 us, 5.5 TB/s.
+// 128, bf16, run forward in 59 us, 5.7 TB/s in and out; the gradient of 8192 tokens in
+// 46 us, 5.5 TB/s.
 //
 // A head is a group of `lanes` lanes with 16 columns each, chosen so that both
 // members of a pair are in one lane: eight columns of each half (or sixteen
 // neighbours).  The norm is then a butterfly over the group and the rotation
-// needs no exchange.  A warp takes a token, or a part of its heads: its groups walk
-// them with the token's cos and sin in shared memory, read once a token.
+// needs no exchange.  A warp takes a block of tokens, one a group, and walks their
+// heads, the same head of each token at a time: a token's angles are read once, and
+// no group idles whatever the number of heads.  (With the groups on one token's heads,
+// us, forward and gradient: 16384 tokens of 5+1x128 15.9, 24.8; so 11.1, 20.0.)
 #pragma once
 
 #include <algorithm>
@@ -29,10 +31,9 @@
 
 namespace normk {
 
-// Two CTAs (kHeadPerSm) of eight warps an SM, up to 128 registers.  (us, 16384 tokens of 32+8
-// heads of 128 bf16 forward, and 8192 backward while the gradient still held its next
-// head in registers: 59.8, 51.8; five CTAs of four warps 59.9, 57; three of six 59.4,
-// 68; three of eight, 80 registers, 59.8, 69.)
+// Two CTAs (kHeadPerSm) of eight warps an SM.  (us, bf16, 16384 tokens of 32+8x128 and
+// 16+16x64 forward: two 59.5, 23.1; three 60.5, 23.0; the gradient at three an SM, 80
+// registers, spills.)
 constexpr int kHeadWarps = 8;
 constexpr int kHeadThreads = 32 * kHeadWarps;
 
@@ -218,16 +219,17 @@ struct HeadLane {
     if constexpr (PAIRS) return 2 * i + 1 < n0() + n1() ? c0 + 2 * i + 1 : -1;
     return i < n1() ? c1() + i : -1;
   }
-  // Every rotated pair turned by the angles in the lane's slot; the others stay,
+  // Every rotated pair turned by the lane's angles, four granules 512 bytes apart:
+  // cos of the first and last four pairs, sin of them; the other columns stay,
   // whatever they hold.  BACK: the other way.
   template <bool BACK>
-  __device__ __forceinline__ void turn(float2 (&a)[4], float2 (&b)[4], uint32_t slot) const {
+  __device__ __forceinline__ void turn(float2 (&a)[4], float2 (&b)[4], uint32_t angles) const {
     if (nr() == 8) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         float2 c[2], s[2];
-        lds_pairs(slot + 16 * k, c);
-        lds_pairs(slot + 32 + 16 * k, s);
+        lds_pairs(angles + 512 * k, c);
+        lds_pairs(angles + 1024 + 512 * k, s);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float2& x = BACK ? b[2 * k + i] : a[2 * k + i];
@@ -238,18 +240,44 @@ struct HeadLane {
         }
       }
     } else if (nr() > 0) {
+      float* x = reinterpret_cast<float*>(BACK ? b : a);
+      float* y = reinterpret_cast<float*>(BACK ? a : b);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float* x = reinterpret_cast<float*>(BACK ? b : a);
-        float* y = reinterpret_cast<float*>(BACK ? a : b);
+      for (int i = 0; i < 8; ++i) {
+        if (i < nr()) {
+          const uint32_t at = angles + i / 4 * 512 + i % 4 * 4;
+          const float c = __uint_as_float(lds_u32(at)), s = __uint_as_float(lds_u32(at + 1024));
+          const float u = x[i] * c - y[i] * s;
+          y[i] = fmaf(y[i], c, x[i] * s);
+          x[i] = u;
+        }
+      }
+    }
+  }
+  // The angles of a table row into the lane's granules: copies, where the tables take
+  // them (to be waited for), else loads.
+  __device__ __forceinline__ void fetch_angles(const HeadArgs& a, int64_t row, int unit, uint32_t to) const {
+    if (nr() == 0) return;
+    if (a.cvec) {
+      const float* c = reinterpret_cast<const float*>(a.cos) + row * a.ldcos + 8 * unit;
+      const float* s = reinterpret_cast<const float*>(a.sin) + row * a.ldsin + 8 * unit;
 #pragma unroll
-        for (int i = 2 * k; i < 2 * k + 2; ++i) {
-          if (i < nr()) {
-            const float c = __uint_as_float(lds_u32(slot + 4 * i)), s = __uint_as_float(lds_u32(slot + 32 + 4 * i));
-            const float u = x[i] * c - y[i] * s;
-            y[i] = fmaf(y[i], c, x[i] * s);
-            x[i] = u;
-          }
+      for (int k = 0; k < 2; ++k) {
+        if (4 * k < nr()) {
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to + 512 * k), "l"(c + 4 * k) : "memory");
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to + 1024 + 512 * k), "l"(s + 4 * k) : "memory");
+        }
+      }
+    } else {
+      const size_t es = a.c_f32 ? 4 : ES;
+      const void* c = reinterpret_cast<const unsigned char*>(a.cos) + (row * a.ldcos + 8 * unit) * es;
+      const void* s = reinterpret_cast<const unsigned char*>(a.sin) + (row * a.ldsin + 8 * unit) * es;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i < nr()) {
+          const uint32_t at = to + i / 4 * 512 + i % 4 * 4;
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(load_param<D>(c, i, a.c_f32)) : "memory");
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 1024), "f"(load_param<D>(s, i, a.c_f32)) : "memory");
         }
       }
     }
@@ -278,106 +306,29 @@ __device__ __forceinline__ void head_gamma(float* slots, const HeadArgs& a, cons
 struct HeadToken {
   unsigned b, t;
   __device__ __forceinline__ HeadToken(const HeadArgs& a, unsigned n) : b(a.B == 1 ? 0u : n / (unsigned)a.T), t(n - b * (unsigned)a.T) {}
-  __device__ __forceinline__ void step(const HeadArgs& a) {
-    if (++t == (unsigned)a.T) {
-      t = 0;
-      ++b;
-    }
-  }
 };
 
-// A warp's share of the work, in units of one head a group: the units of all
-// tokens, a.its each, are shared out evenly, whichever tokens they fall into.
+// A warp's share of the work, in units of one head of a block of tokens: the units
+// of all blocks, as many as heads each, are shared out evenly, whichever blocks they
+// fall into.
 struct HeadShare {
-  unsigned first;  // the token of the first one
-  int lo;          // and which of its units that is
+  unsigned block;  // of the first one
+  int lo, heads;   // which of its units that is
   int64_t left;    // units
-  __device__ __forceinline__ HeadShare(const HeadArgs& a, int warp) {
+  __device__ __forceinline__ HeadShare(const HeadArgs& a, int warp, int heads_) : heads(heads_) {
     const int64_t u = warp * a.each + min((int64_t)warp, a.extra);
     left = a.each + (warp < a.extra);
-    first = (unsigned)(u < (int64_t(1) << 31) ? (unsigned)u / (unsigned)a.its : u / a.its);
-    lo = (int)(u - (int64_t)first * a.its);
+    block = (unsigned)(u < (int64_t(1) << 31) ? (unsigned)u / (unsigned)heads : u / heads);
+    lo = (int)(u - (int64_t)block * heads);
   }
-  // Units [lo, hi) of the token at hand; false behind the last.
-  __device__ __forceinline__ bool take(const HeadArgs& a, int& from, int& to) {
+  // Units [from, to) of the block at hand; false behind the last.
+  __device__ __forceinline__ bool take(int& from, int& to) {
     if (left <= 0) return false;
     from = lo;
-    to = (int)min((int64_t)a.its, lo + left);
+    to = (int)min((int64_t)heads, lo + left);
     left -= to - from;
     lo = 0;
     return true;
-  }
-};
-
-// The angles of a warp's tokens: positions two tokens ahead and table rows one
-// ahead are in registers, the token's own angles in the warp's slots.
-template <typename D, int LANES>
-struct HeadAngles {
-  static constexpr int AHEAD = LANES == 16 ? 8 : 4;  // values of a table row a lane holds: 128 or 256
-  const HeadArgs& a;
-  float* slots;
-  int lane;
-  HeadToken ahead;  // the token whose position is to be fetched
-  int tokens;       // that are left from it on
-  int64_t pos;      // the position of the token after the next one
-  int64_t row;      // the next one's, and its table row
-  float v[AHEAD];
-  bool next_good;
-
-  __device__ __forceinline__ HeadAngles(const HeadArgs& a_, float* slots_, int lane_, const HeadToken& first, int tokens_)
-      : a(a_), slots(slots_), lane(lane_), ahead(first), tokens(tokens_), pos(0), row(0), next_good(true) {
-    if (!a.R) return;
-    fetch_position();
-    fetch_row();
-    fetch_position();
-  }
-  __device__ __forceinline__ void fetch_position() {
-    if (tokens-- <= 0) return;
-    pos = ahead.t;
-    if (a.positions) {
-      const int64_t i = ahead.b * a.pb + ahead.t * a.pt;
-      pos = a.pos64 ? reinterpret_cast<const long long*>(a.positions)[i]
-                    : (int64_t) reinterpret_cast<const int*>(a.positions)[i];
-    }
-    ahead.step(a);
-  }
-  // Value e of the row [cos | sin].
-  __device__ __forceinline__ float value(int e) const {
-    const int half = a.R / 2;
-    const void* t = e < half ? a.cos : a.sin;
-    const int64_t at = row * (e < half ? a.ldcos : a.ldsin) + (e < half ? e : e - half);
-    return a.c_f32 ? reinterpret_cast<const float*>(t)[at] : load_elem<D>(t, at);
-  }
-  __device__ __forceinline__ void put(int e, float x) const {
-    const int half = a.R / 2, i = e < half ? e : e - half;
-    slots[i / 8 * kHeadSlot + i % 8 + (e < half ? 0 : 8)] = x;
-  }
-  __device__ __forceinline__ void fetch_row() {
-    row = pos;
-    next_good = row >= 0 && row < a.table_rows;
-    if (!next_good) return;
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k)
-      if (lane + 32 * k < a.R) v[k] = value(lane + 32 * k);
-  }
-  // The next token's angles go into the slots, and those after it are asked for.
-  // Whether its position is in the table.
-  __device__ __forceinline__ bool turn_over() {
-    if (!a.R) return true;
-    const bool good = next_good;
-    __syncwarp();  // the lanes are through with the angles before
-    if (good) {
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k)
-        if (lane + 32 * k < a.R) put(lane + 32 * k, v[k]);
-      for (int e = lane + 32 * AHEAD; e < a.R; e += 32) put(e, value(e));
-    } else if (lane == 0) {
-      atomicOr(a.err, kErrBadPosition);
-    }
-    __syncwarp();
-    fetch_row();
-    fetch_position();
-    return good;
   }
 };
 
@@ -397,61 +348,146 @@ __device__ __forceinline__ T* head_at(const HeadView& q, const HeadView& k, cons
   return reinterpret_cast<T*>(first ? q.p : k.p) + at;
 }
 
-// The gradient's inputs on their way to a lane: x and dy of its columns.
-// RegisterRing holds one head.  CopyRing has copies of two in flight to shared
-// memory (half precision, where 16 or 8 bytes can be copied), which no register
-// pays for: bf16 8192x32+8x128 50.4 -> 45.6 us.  A slot is written again an
-// iteration after its values were used, with the head's sums, which all lanes
-// exchange, in between.
-template <typename Lane, typename T>
+// Heads on their way to a lane: of NT tensors, its columns.  RegisterRing holds one
+// head.  CopyRing has copies of SLOTS heads in flight to shared memory (half
+// precision, where 16 or 8 bytes can be copied), which no register pays for (gradient,
+// 8192x32+8x128 bf16 50.4 -> 45.6 us).  A slot is written again when its values have
+// been used, which the head's sums, exchanged by all lanes, tell.
+template <typename Lane, typename T, int NT>
 struct RegisterRing {
-  static constexpr int AHEAD = 1;
+  static constexpr bool COPIES = false;
+  static constexpr int SLOTS = 1;
   static constexpr int BYTES = 0;  // of shared memory a warp
-  uint32_t x[Lane::NW], y[Lane::NW];
+  uint32_t w[NT][Lane::NW];
   __device__ __forceinline__ RegisterRing(unsigned char*, int, int, int, int) {}
-  __device__ __forceinline__ void fetch(const Lane& me, bool on, const T* px, const T* py) {
+  __device__ __forceinline__ void fetch(const Lane& me, bool on, const T* (&p)[NT]) {
     if (!on) return;
-    me.load(px, x);
-    me.load(py, y);
-  }
-  __device__ __forceinline__ void take(uint32_t (&tx)[Lane::NW], uint32_t (&ty)[Lane::NW]) const {
 #pragma unroll
-    for (int j = 0; j < Lane::NW; ++j) {
-      tx[j] = x[j];
-      ty[j] = y[j];
-    }
+    for (int i = 0; i < NT; ++i) me.load(p[i], w[i]);
+  }
+  __device__ __forceinline__ void take(uint32_t (&to)[NT][Lane::NW]) const {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < Lane::NW; ++j) to[i][j] = w[i][j];
   }
 };
-template <typename Lane, typename T>
+template <typename Lane, typename T, int NT, int SLOTS_>
 struct CopyRing {
-  static constexpr int AHEAD = 2;
-  static constexpr int SLOTS = AHEAD + 1;
-  static constexpr int BYTES = SLOTS * 2048;
+  static constexpr bool COPIES = true;
+  static constexpr int SLOTS = SLOTS_;
+  static constexpr int BYTES = SLOTS * NT * 1024;
   uint32_t base;  // of the lane's granules
   int unit, lanes, cols;
   int in = 0, out = 0;
   __device__ __forceinline__ CopyRing(unsigned char* smem, int lane, int unit_, int lanes_, int cols_)
       : base(smem_u32(smem) + lane * Lane::kLaneBytes), unit(unit_), lanes(lanes_), cols(cols_) {}
-  // One group of copies a call, empty without a head.
-  __device__ __forceinline__ void fetch(const Lane& me, bool on, const T* px, const T* py) {
+  // One group of copies a call, with whatever was copied before it; empty without a
+  // head.
+  __device__ __forceinline__ void fetch(const Lane& me, bool on, const T* (&p)[NT]) {
     if (on) {
-      me.copy(px, unit, lanes, cols, base + in * 2048);
-      me.copy(py, unit, lanes, cols, base + in * 2048 + 1024);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) me.copy(p[i], unit, lanes, cols, base + (in * NT + i) * 1024);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     in = in + 1 == SLOTS ? 0 : in + 1;
   }
-  __device__ __forceinline__ void take(uint32_t (&tx)[Lane::NW], uint32_t (&ty)[Lane::NW]) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+  __device__ __forceinline__ void take(uint32_t (&to)[NT][Lane::NW]) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
     __syncwarp();  // every lane's copies are there
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      lds_words<4>(base + out * 2048 + j * Lane::kNext, tx + 4 * j);
-      lds_words<4>(base + out * 2048 + 1024 + j * Lane::kNext, ty + 4 * j);
-    }
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) lds_words<4>(base + (out * NT + i) * 1024 + j * Lane::kNext, to[i] + 4 * j);
     out = out + 1 == SLOTS ? 0 : out + 1;
   }
 };
+template <typename D, int CA, bool PAIRS, int LANES, int NT>
+struct HeadRing {
+  using Lane = HeadLane<D, CA, PAIRS, 16 * LANES>;
+  using T = typename D::T;
+  // Forward (us, 16384 tokens of 32+8x128 and 16+16x64): two slots 59.4, 26.0; three
+  // 59.5, 23.1; four 63.4, 22.4.  Backward two fill what shared memory two CTAs leave.
+  using Type = std::conditional_t<sizeof(T) == 2 && CA >= 4, CopyRing<Lane, T, NT, NT == 1 ? 3 : 2>, RegisterRing<Lane, T, NT>>;
+};
+
+// What runs ahead of a warp's work: the heads into the ring, and, with the first one
+// of each block, the angles of its tokens into one of a.bufs sets of the lanes'
+// granules.  The position of a group's next token is read a block before.
+template <typename D, typename Lane, typename Ring, typename I, int NT>
+struct HeadFeed {
+  using T = typename D::T;
+  static_assert(NT == 1 || NT == 2, "x, or x and dy");
+  const HeadArgs& a;
+  const Lane& me;
+  Ring& ring;
+  HeadShare share;
+  unsigned token;   // the group's in the block at hand
+  int groups, unit, hq;
+  uint32_t angles;  // the lane's first granule of the first set
+  int buf = 0;      // the set to be written next
+  unsigned good = 0;  // whether the tokens of each set have positions in the table
+  HeadPlace<I> x, dy;
+  int h = 0, end = 0;
+  bool on = false;
+  int64_t pos = 0;  // of the group's token in the next block
+
+  __device__ __forceinline__ HeadFeed(const HeadArgs& a_, const Lane& me_, Ring& ring_, const HeadShare& share_, int groups_,
+                                      int group, int unit_, int hq_, uint32_t angles_)
+      : a(a_), me(me_), ring(ring_), share(share_), token(share_.block * groups_ + group - groups_), groups(groups_),
+        unit(unit_), hq(hq_), angles(angles_), x(HeadToken(a_, 0), a_.side[0].x, a_.side[1].x, hq_), dy(x) {
+    if (a.R && share.left > 0) fetch_position(token + groups);
+#pragma unroll
+    for (int i = 0; i < Ring::SLOTS; ++i) fetch();
+  }
+  __device__ __forceinline__ void fetch_position(unsigned n) {
+    if (n >= a.N) return;
+    const HeadToken next(a, n);
+    pos = next.t;
+    if (a.positions) {
+      const int64_t i = next.b * a.pb + next.t * a.pt;
+      pos = a.pos64 ? reinterpret_cast<const long long*>(a.positions)[i]
+                    : (int64_t) reinterpret_cast<const int*>(a.positions)[i];
+    }
+  }
+  __device__ __forceinline__ void fetch() {
+    if (h >= end) {
+      if (!share.take(h, end)) {
+        h = end = 0;
+        on = false;
+      } else {
+        token += groups;
+        on = token < a.N;
+        if (on) {
+          const HeadToken n(a, token);
+          x = HeadPlace<I>(n, a.side[0].x, a.side[1].x, hq);
+          if (NT > 1) dy = HeadPlace<I>(n, a.side[0].dy, a.side[1].dy, hq);
+        }
+        if (a.R) {
+          const bool fits = pos >= 0 && pos < a.table_rows;
+          good = (good & ~(1u << buf)) | ((unsigned)fits << buf);
+          if (on && fits) me.fetch_angles(a, pos, unit, angles + buf * 2048);
+          if (on && !fits && unit == 0) atomicOr(a.err, kErrBadPosition);
+          if constexpr (!Ring::COPIES) asm volatile("cp.async.commit_group;" ::: "memory");
+          fetch_position(token + groups);
+        } else {
+          good = ~0u;
+        }
+        buf = buf + 1 == a.bufs ? 0 : buf + 1;
+      }
+    }
+    const T* p[NT];
+    p[0] = head_at<const T, I>(a.side[0].x, a.side[1].x, x, hq, h);
+    if constexpr (NT > 1) p[1] = head_at<const T, I>(a.side[0].dy, a.side[1].dy, dy, hq, h);
+    ring.fetch(me, on, p);
+    ++h;
+  }
+};
+// At the start of a block's work.
+template <typename Ring>
+__device__ __forceinline__ void angles_ready() {
+  if constexpr (!Ring::COPIES) asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
 
 // Sum over each `lanes` lanes; LANES: as a compile-time value, or 0.
 template <int K, int LANES>
@@ -459,196 +495,133 @@ __device__ __forceinline__ void lanes_sum(float (&v)[K], int lanes) {
   warp_sum_pow2<K>(v, LANES ? LANES : lanes);
 }
 
-// U heads of a group are in flight, over the ends of tokens, while as many are at
-// work.  LANES > 0: heads of 16 * LANES columns, all rotated.
-template <typename D, int CA, bool PAIRS, int U, int LANES, typename I>
+// LANES > 0: heads of 16 * LANES columns, all rotated.
+template <typename D, int CA, bool PAIRS, int LANES, typename I>
 __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_kernel(const HeadArgs a) {
   using Lane = HeadLane<D, CA, PAIRS, 16 * LANES>;
   using T = typename D::T;
-  extern __shared__ __align__(16) float slots[];  // gamma of both sides, each warp's angles
+  using Ring = typename HeadRing<D, CA, PAIRS, LANES, 1>::Type;
+  extern __shared__ __align__(16) unsigned char smem[];  // gamma of both sides, each warp's angles and ring
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int lanes = LANES ? LANES : a.lanes;
   const int groups = 32 / lanes, group = lane / lanes, unit = lane & (lanes - 1);
   const Lane me(unit, a.D, a.R);
   const float inv_d = 1.f / (float)a.D;
   const int hq = a.side[0].heads, heads = hq + a.side[1].heads;
-  const uint32_t gammas = smem_u32(slots + unit * kHeadSlot);
-  float* angles = slots + (2 + warp) * lanes * kHeadSlot;
-  const uint32_t angle = smem_u32(angles + unit * kHeadSlot);
+  float* slots = reinterpret_cast<float*>(smem);
+  unsigned char* at = smem + 2 * lanes * kHeadSlot * 4 + warp * (a.bufs * 2048 + Ring::BYTES);
+  const uint32_t angles = smem_u32(at) + lane * 16;
   pdl_launch_dependents();
   pdl_wait_primary();
-  HeadShare share(a, blockIdx.x * kHeadWarps + warp);
-  HeadToken token(a, share.first);
-  const int tokens = share.left > 0 ? (int)((share.lo + share.left + a.its - 1) / a.its) : 0;
-  HeadPlace<I> src(token, a.side[0].x, a.side[1].x, hq), dst(token, a.side[0].y, a.side[1].y, hq);
-  uint32_t next[U][Lane::NW];
-  auto fetch = [&](int h, int to) {
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (h + i * groups < to) me.load(head_at<T, I>(a.side[0].x, a.side[1].x, src, hq, h + i * groups), next[i]);
-  };
-  int lo, hi, from, to;
-  // the next token's units as heads [from, to), whose first ones are asked for
-  auto enter = [&] {
-    if (!share.take(a, lo, hi)) return false;
-    from = lo * groups + group;
-    to = min(hi * groups, heads);
-    src = HeadPlace<I>(token, a.side[0].x, a.side[1].x, hq);
-    dst = HeadPlace<I>(token, a.side[0].y, a.side[1].y, hq);
-    token.step(a);
-    fetch(from, to);
-    return true;
-  };
-  HeadAngles<D, LANES> way(a, angles, lane, token, tokens);
-  bool on = enter();
+  HeadShare work(a, blockIdx.x * kHeadWarps + warp, heads);
+  Ring ring(at + a.bufs * 2048, lane, unit, lanes, a.D);
+  HeadFeed<D, Lane, Ring, I, 1> feed(a, me, ring, work, groups, group, unit, hq, angles);
   for (int k = 0; k < 2; ++k)
     head_gamma<Lane, D>(slots + k * lanes * kHeadSlot, a, a.side[k].gamma, threadIdx.x, kHeadThreads);
   __syncthreads();
-  while (on) {
-    const bool good = way.turn_over();
-    const HeadPlace<I> here = dst;
-    const int end = to;
+  unsigned token = work.block * groups + group;
+  int lo, hi, buf = 0;
+  for (; work.take(lo, hi); token += groups, buf = buf + 1 == a.bufs ? 0 : buf + 1) {
+    const bool on = token < a.N;
+    const HeadPlace<I> dst(HeadToken(a, on ? token : 0), a.side[0].y, a.side[1].y, hq);
+    angles_ready<Ring>();
+    const bool good = feed.good >> buf & 1u;
 #pragma unroll 1
-    for (int h = from, more = 1; more; h += U * groups) {
-      uint32_t now[U][Lane::NW];
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-#pragma unroll
-        for (int j = 0; j < Lane::NW; ++j) now[i][j] = next[i][j];
-      more = h - group + U * groups < end;
-      if (more)
-        fetch(h + U * groups, end);
-      else
-        on = enter();
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int k = h + i * groups;
-        if (k - group >= end) break;  // the same for the whole warp
-        float2 p[4], q[4];
-        Lane::unpack(now[i], p, q);
-        float2 sum = splat2(0.f);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sum = fma2(q[j], q[j], fma2(p[j], p[j], sum));
-        float v[1] = {sum.x + sum.y};
-        lanes_sum<1, LANES>(v, lanes);
-        const float2 r = splat2(rsqrtf(fmaf(v[0], inv_d, a.eps)));
-        const uint32_t gamma = gammas + (k < hq ? 0 : lanes * kHeadSlot * 4);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float2 g[2];
-          lds_pairs(gamma + 16 * j, g);
-          p[2 * j] = mul2(mul2(p[2 * j], r), g[0]);
-          p[2 * j + 1] = mul2(mul2(p[2 * j + 1], r), g[1]);
-          lds_pairs(gamma + 32 + 16 * j, g);
-          q[2 * j] = mul2(mul2(q[2 * j], r), g[0]);
-          q[2 * j + 1] = mul2(mul2(q[2 * j + 1], r), g[1]);
-        }
-        if (good) {
-          me.template turn<false>(p, q, angle);
-          Lane::pack(p, q, now[i]);
-        } else {  // the token has no position: zeros
-#pragma unroll
-          for (int j = 0; j < Lane::NW; ++j) now[i][j] = 0u;
-        }
-        if (k < end) {
-          T* y = head_at<T, I>(a.side[0].y, a.side[1].y, here, hq, k);
-          if (a.pass)
-            me.template store<true>(y, now[i]);
-          else
-            me.store(y, now[i]);
-        }
+    for (int h = lo; h < hi; ++h) {
+      float2 p[4], q[4];
+      {
+        uint32_t w[1][Lane::NW];
+        ring.take(w);
+        Lane::unpack(w[0], p, q);
       }
+      if constexpr (!Ring::COPIES) feed.fetch();
+      float2 sum = splat2(0.f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum = fma2(q[j], q[j], fma2(p[j], p[j], sum));
+      float v[1] = {sum.x + sum.y};
+      lanes_sum<1, LANES>(v, lanes);
+      if constexpr (Ring::COPIES) feed.fetch();
+      const float2 r = splat2(rsqrtf(fmaf(v[0], inv_d, a.eps)));
+      const uint32_t gamma = smem_u32(slots + ((h < hq ? 0 : lanes) + unit) * kHeadSlot);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float2 g[2];
+        lds_pairs(gamma + 16 * j, g);
+        p[2 * j] = mul2(mul2(p[2 * j], r), g[0]);
+        p[2 * j + 1] = mul2(mul2(p[2 * j + 1], r), g[1]);
+        lds_pairs(gamma + 32 + 16 * j, g);
+        q[2 * j] = mul2(mul2(q[2 * j], r), g[0]);
+        q[2 * j + 1] = mul2(mul2(q[2 * j + 1], r), g[1]);
+      }
+      if (!on) continue;  // no lane exchanges anything below
+      uint32_t o[Lane::NW];
+      if (good) {
+        me.template turn<false>(p, q, angles + buf * 2048);
+        Lane::pack(p, q, o);
+      } else {  // the token has no position: zeros
+#pragma unroll
+        for (int j = 0; j < Lane::NW; ++j) o[j] = 0u;
+      }
+      T* y = head_at<T, I>(a.side[0].y, a.side[1].y, dst, hq, h);
+      if (a.pass)
+        me.template store<true>(y, o);
+      else
+        me.store(y, o);
     }
   }
 }
 
 // The gradient.  A lane sums dgamma of its columns, for either side, in granules of
-// its own in shared memory (in registers, with a change of sides at every token,
-// fp32 4096x32+8x128 47.5 -> 52.3 us); a CTA's sums become its partial row.  The
-// next heads of a group are in flight, over the ends of tokens, while one is at
-// work.
-template <typename D, int CA, bool PAIRS, int LANES>
-struct HeadGradRing {
-  using Lane = HeadLane<D, CA, PAIRS, 16 * LANES>;
-  using T = typename D::T;
-  static constexpr bool COPIES = sizeof(T) == 2 && CA >= 4;
-  using Type = std::conditional_t<COPIES, CopyRing<Lane, T>, RegisterRing<Lane, T>>;
-};
+// its own in shared memory (in registers, moved there at a change of sides, fp32
+// 4096x32+8x128 47.5 -> 52.3 us); a CTA's sums become its partial row.
 template <typename D, int CA, bool PAIRS, int LANES, typename I>
 __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_grad_kernel(const HeadArgs a) {
   using Lane = HeadLane<D, CA, PAIRS, 16 * LANES>;
   using T = typename D::T;
-  using Ring = typename HeadGradRing<D, CA, PAIRS, LANES>::Type;
-  extern __shared__ __align__(16) float slots[];  // gamma of both sides, each warp's angles, sums and ring
+  using Ring = typename HeadRing<D, CA, PAIRS, LANES, 2>::Type;
+  extern __shared__ __align__(16) unsigned char smem[];  // gamma of both sides, each warp's sums, then its angles and ring
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int lanes = LANES ? LANES : a.lanes;
   const int groups = 32 / lanes, group = lane / lanes, unit = lane & (lanes - 1);
   const Lane me(unit, a.D, a.R);
   const float inv_d = 1.f / (float)a.D;
   const int hq = a.side[0].heads, heads = hq + a.side[1].heads;
-  const uint32_t gammas = smem_u32(slots + unit * kHeadSlot);
-  float* angles = slots + (2 + warp) * lanes * kHeadSlot;
-  const uint32_t angle = smem_u32(angles + unit * kHeadSlot);
-  float4* sums = reinterpret_cast<float4*>(slots + (2 + kHeadWarps) * lanes * kHeadSlot);  // [warp][side][granule][lane]
+  float* slots = reinterpret_cast<float*>(smem);
+  float4* sums = reinterpret_cast<float4*>(slots + 2 * lanes * kHeadSlot);  // [warp][side][granule][lane]
   float4* mine = sums + warp * 256 + lane;
-  Ring ring(reinterpret_cast<unsigned char*>(sums + kHeadWarps * 256) + warp * Ring::BYTES, lane, unit, lanes, a.D);
+  unsigned char* at = reinterpret_cast<unsigned char*>(sums + kHeadWarps * 256) + warp * (a.bufs * 2048 + Ring::BYTES);
+  const uint32_t angles = smem_u32(at) + lane * 16;
   pdl_launch_dependents();
   pdl_wait_primary();
-  // the heads that are fetched, AHEAD units before those that are at work
-  HeadShare share(a, blockIdx.x * kHeadWarps + warp), work = share;
-  HeadToken token(a, share.first), ahead = token;
-  const int tokens = share.left > 0 ? (int)((share.lo + share.left + a.its - 1) / a.its) : 0;
-  HeadPlace<I> px(ahead, a.side[0].x, a.side[1].x, hq), py(ahead, a.side[0].dy, a.side[1].dy, hq);
-  int fk = 0, fend = 0;  // the next head to fetch (of group 0), and the end of the token's
-  bool first = true;
-  auto fetch = [&] {
-    if (fk >= fend) {
-      int lo, hi;
-      if (!share.take(a, lo, hi)) {
-        ring.fetch(me, false, nullptr, nullptr);
-        return;
-      }
-      if (!first) {
-        ahead.step(a);
-        px = HeadPlace<I>(ahead, a.side[0].x, a.side[1].x, hq);
-        py = HeadPlace<I>(ahead, a.side[0].dy, a.side[1].dy, hq);
-      }
-      first = false;
-      fk = lo * groups;
-      fend = min(hi * groups, heads);
-    }
-    const int k = fk + group;
-    ring.fetch(me, k < fend, head_at<T, I>(a.side[0].x, a.side[1].x, px, hq, k), head_at<T, I>(a.side[0].dy, a.side[1].dy, py, hq, k));
-    fk += groups;
-  };
-#pragma unroll
-  for (int i = 0; i < Ring::AHEAD; ++i) fetch();
-  HeadAngles<D, LANES> way(a, angles, lane, token, tokens);
+  HeadShare work(a, blockIdx.x * kHeadWarps + warp, heads);
+  Ring ring(at + a.bufs * 2048, lane, unit, lanes, a.D);
+  HeadFeed<D, Lane, Ring, I, 2> feed(a, me, ring, work, groups, group, unit, hq, angles);
   for (int k = 0; k < 2; ++k)
     head_gamma<Lane, D>(slots + k * lanes * kHeadSlot, a, a.side[k].gamma, threadIdx.x, kHeadThreads);
 #pragma unroll
   for (int j = 0; j < 8; ++j) mine[32 * j] = make_float4(0.f, 0.f, 0.f, 0.f);
   __syncthreads();
-  int lo, hi;
-  for (bool more = work.take(a, lo, hi); more; more = work.take(a, lo, hi)) {
-    const HeadPlace<I> dst(token, a.side[0].y, a.side[1].y, hq);
-    token.step(a);
-    const int end = min(hi * groups, heads);
-    const bool good = way.turn_over();
+  unsigned token = work.block * groups + group;
+  int lo, hi, buf = 0;
+  for (; work.take(lo, hi); token += groups, buf = buf + 1 == a.bufs ? 0 : buf + 1) {
+    const bool on = token < a.N;
+    const HeadPlace<I> dst(HeadToken(a, on ? token : 0), a.side[0].y, a.side[1].y, hq);
+    angles_ready<Ring>();
+    const bool good = feed.good >> buf & 1u;
 #pragma unroll 1
-    for (int k = lo * groups + group; k - group < end; k += groups) {
+    for (int h = lo; h < hi; ++h) {
       float2 p[4], q[4], u[4], v[4];
       {
-        uint32_t wx[Lane::NW], wy[Lane::NW];
-        ring.take(wx, wy);
-        Lane::unpack(wx, p, q);
-        Lane::unpack(wy, u, v);
+        uint32_t w[2][Lane::NW];
+        ring.take(w);
+        Lane::unpack(w[0], p, q);
+        Lane::unpack(w[1], u, v);
       }
-      fetch();
-      const int which = k < hq ? 0 : 1;
-      if (good) me.template turn<true>(u, v, angle);
+      if constexpr (!Ring::COPIES) feed.fetch();
+      const int side = h < hq ? 0 : 1;
+      if (good) me.template turn<true>(u, v, angles + buf * 2048);
       float2 sx = splat2(0.f), sw = splat2(0.f);
-      const uint32_t gamma = gammas + which * lanes * kHeadSlot * 4;
+      const uint32_t gamma = smem_u32(slots + (side * lanes + unit) * kHeadSlot);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         float2 g[2], e[2];
@@ -663,22 +636,23 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_grad_ker
       }
       float m[2] = {sx.x + sx.y, sw.x + sw.y};
       lanes_sum<2, LANES>(m, lanes);
-      if (k >= end) continue;  // no lane exchanges anything below
+      if constexpr (Ring::COPIES) feed.fetch();
+      if (!on) continue;  // no lane exchanges anything below
       uint32_t o[Lane::NW];
       if (good) {
         const float r = rsqrtf(fmaf(m[0], inv_d, a.eps));
         // dx = rstd (w - x rstd^2 mean(w x)); w is formed again rather than kept
         const float2 r2 = splat2(r), k2 = splat2(-(m[1] * inv_d) * r * r);
-        float4* at = mine + which * 128;
+        float4* sum = mine + side * 128;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float4 x = at[32 * j], y = at[32 * (2 + j)];
+          const float4 x = sum[32 * j], y = sum[32 * (2 + j)];
           const float2 x0 = fma2(u[2 * j], mul2(p[2 * j], r2), make_float2(x.x, x.y));
           const float2 x1 = fma2(u[2 * j + 1], mul2(p[2 * j + 1], r2), make_float2(x.z, x.w));
           const float2 y0 = fma2(v[2 * j], mul2(q[2 * j], r2), make_float2(y.x, y.y));
           const float2 y1 = fma2(v[2 * j + 1], mul2(q[2 * j + 1], r2), make_float2(y.z, y.w));
-          at[32 * j] = make_float4(x0.x, x0.y, x1.x, x1.y);
-          at[32 * (2 + j)] = make_float4(y0.x, y0.y, y1.x, y1.y);
+          sum[32 * j] = make_float4(x0.x, x0.y, x1.x, x1.y);
+          sum[32 * (2 + j)] = make_float4(y0.x, y0.y, y1.x, y1.y);
           float2 g[2], e[2];
           lds_pairs(gamma + 16 * j, g);
           lds_pairs(gamma + 32 + 16 * j, e);
@@ -694,7 +668,7 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_grad_ker
 #pragma unroll
         for (int j = 0; j < Lane::NW; ++j) o[j] = 0u;
       }
-      me.store(head_at<T, I>(a.side[0].y, a.side[1].y, dst, hq, k), o);
+      me.store(head_at<T, I>(a.side[0].y, a.side[1].y, dst, hq, h), o);
     }
   }
   if (!a.want) return;
@@ -775,10 +749,17 @@ int head_access(const HeadArgs& a, bool grad) {
 }
 
 // The kernel on as many CTAs as are resident, or fewer.  Its units are shared out
-// to the warps one by one: whole tokens would leave some warps with four and others
-// with three of 8192 (56 us for 51.8).
+// to the warps one by one: with whole tokens some warps had four and others three of
+// 8192 (gradient 56 us for 51.8).  `fixed` bytes of shared memory, `ring` bytes of
+// a warp's ring of `slots` heads.
 template <typename K>
-cudaError_t run_heads(K kern, HeadArgs& a, size_t smem, KernelMemo& memo, const DeviceInfo& dev, cudaStream_t s, int* ctas) {
+cudaError_t run_heads(K kern, HeadArgs& a, size_t fixed, int ring, int slots, KernelMemo& memo, const DeviceInfo& dev,
+                      cudaStream_t s, int* ctas) {
+  const int heads = a.side[0].heads + a.side[1].heads, groups = 32 / a.lanes;
+  // sets of angles: of the blocks that a feed of `slots` heads may have entered, and
+  // the one at work
+  a.bufs = a.R ? (slots + heads - 1) / heads + 1 : 1;
+  const size_t smem = fixed + 2 * a.lanes * kHeadSlot * sizeof(float) + (size_t)kHeadWarps * (a.bufs * 2048 + ring);
   if (smem > 48 * 1024) {
     const cudaError_t e = memo.allow_smem(kern, dev.max_smem_optin - 1024, dev);
     if (e != cudaSuccess) return e;
@@ -788,35 +769,35 @@ cudaError_t run_heads(K kern, HeadArgs& a, size_t smem, KernelMemo& memo, const 
     *n = std::min(*n, kHeadPerSm) * dev.sm_count;
     return e;
   });
-  const int groups = 32 / a.lanes;
-  a.its = (a.side[0].heads + a.side[1].heads + groups - 1) / groups;
-  const int64_t units = a.N * a.its;
+  const int64_t units = (a.N + groups - 1) / groups * heads;
   *ctas = (int)std::min<int64_t>((units + kHeadWarps - 1) / kHeadWarps, resident);
   a.each = units / ((int64_t)*ctas * kHeadWarps);
   a.extra = units % ((int64_t)*ctas * kHeadWarps);
+  const unsigned long long bits = (unsigned long long)reinterpret_cast<uintptr_t>(a.cos) |
+                                  (unsigned long long)reinterpret_cast<uintptr_t>(a.sin) |
+                                  (unsigned long long)((a.ldcos | a.ldsin) * 4) | (unsigned long long)(a.R / 2 * 4);
+  a.cvec = a.c_f32 && (bits & 15) == 0;
   FirstLaunch first(kHeadThreads, smem, s, 1);
   return first.launch((unsigned)*ctas, true, kern, a);
 }
 
 template <typename D, int CA, bool PAIRS, int LANES, typename I>
 cudaError_t run_head_rotary(HeadArgs a, const DeviceInfo& dev, cudaStream_t s) {
-  constexpr int U = sizeof(typename D::T) == 2 ? 2 : 1;  // 64 bytes of a lane
+  using Ring = typename HeadRing<D, CA, PAIRS, LANES, 1>::Type;
   // Heads that L2 will not hold until they are read again (a half of its 129 MB, the
   // inputs passing through the other) do not displace the inputs: bf16 32+8x128, 16384
   // tokens 59.8 -> 58.3 us, 16+16x64 25.3 -> 23.9.
   a.pass = a.N * (a.side[0].heads + a.side[1].heads) * a.D * (int64_t)sizeof(typename D::T) > 64000000;
   static KernelMemo memo;
   int ctas;
-  return run_heads(head_rotary_kernel<D, CA, PAIRS, U, LANES, I>, a, sizeof(float) * (2 + kHeadWarps) * a.lanes * kHeadSlot, memo,
-                   dev, s, &ctas);
+  return run_heads(head_rotary_kernel<D, CA, PAIRS, LANES, I>, a, 0, Ring::BYTES, Ring::SLOTS, memo, dev, s, &ctas);
 }
 
 template <typename D, int CA, bool PAIRS, int LANES, typename I>
 cudaError_t run_head_rotary_grad(HeadArgs a, const DeviceInfo& dev, cudaStream_t s, int* ctas) {
+  using Ring = typename HeadRing<D, CA, PAIRS, LANES, 2>::Type;
   static KernelMemo memo;
-  return run_heads(head_rotary_grad_kernel<D, CA, PAIRS, LANES, I>, a,
-                   sizeof(float) * (2 + kHeadWarps) * a.lanes * kHeadSlot +
-                       kHeadWarps * (4096 + HeadGradRing<D, CA, PAIRS, LANES>::Type::BYTES),
+  return run_heads(head_rotary_grad_kernel<D, CA, PAIRS, LANES, I>, a, kHeadWarps * 4096, Ring::BYTES, Ring::SLOTS,
                    memo, dev, s, ctas);
 }
 

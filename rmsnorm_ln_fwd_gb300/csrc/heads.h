@@ -51,7 +51,8 @@ struct HeadArgs {
   // filled in by the launcher:
   int lanes;   // a head, a power of two
   int pass;    // forward: stores that leave L2 first
-  int its;        // units of a token: heads a group has to take
+  int bufs;       // sets of angles a warp has
+  int cvec;       // cos and sin take copies of 16 bytes
   int64_t each;   // units a warp, and how many warps have one more
   int64_t extra;
 };

@@ -10,9 +10,9 @@ Tolerances, from the arithmetic (U = 2^-24, half an fp32 step):
   3 U more.  KF = 20 steps of U on the magnitudes of its two terms.
 * dx = rstd (w - x rstd^2 mean(w x)): w has 4 U on the magnitudes of u's terms,
   the sum 16 U more, rstd^2 26 U, products 4 U, rstd again 13 U: KB = 64.
-* dgamma, a sum over rows: u x rstd has 18 U a term.  Units of one head a lane
-  group are shared out evenly over the warps (2432 of them, or one unit each): a lane
-  adds at most rows/256 + 4.  Then the CTA adds up 8 warps of at most 32 groups, 256
+* dgamma, a sum over rows: u x rstd has 18 U a term.  Units, one head of as many
+  tokens as a warp has lane groups, are shared out evenly over the warps (2432 of
+  them, or one unit each): a lane adds at most rows/256 + 4.  Then the CTA adds up 8 warps of at most 32 groups, 256
   in a row, and the partial rows 19 + 16 and 4 levels: 300 in all.
 * a value stored in fewer bits: half a step, on top.
 """
@@ -387,6 +387,29 @@ def test_many_tokens(shape, dt):
     again = call_grad(c)
     for a, b in zip(g, again):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kind", ["plain", "interleaved", "unaligned table", "table of the rows' type"])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(1, 9001, 1, 0, 64, 64), (1, 9001, 1, 1, 16, 16), (3, 1501, 2, 0, 128, 64), (1, 5003, 5, 1, 128, 128),
+                                   (1, 1999, 8, 2, 192, 192), (2, 997, 3, 1, 192, 96), (1, 1201, 1, 0, 500, 250), (7, 643, 2, 1, 48, 0)])
+def test_few_heads_and_many_tokens(shape, dt, kind):
+    """Warps that take blocks of tokens, or parts of them, one after another, while the angles of the next ones arrive."""
+    R = shape[-1]
+    own = kind == "table of the rows' type" and dt != "f32"
+    c = make(*shape, dt, wdt="f32", layout="fused", positions="each", seed=sum(shape),
+             cdt=DT[dt] if own else torch.float32)
+    if R and kind == "unaligned table":
+        rows = c["cos"].shape[0]
+        both = torch.empty(rows, R + 1, device=DEV)
+        c["cos"], c["sin"] = both[:, 1:R // 2 + 1].copy_(c["cos"]), both[:, R // 2 + 1:].copy_(c["sin"])
+    if R:
+        c["pos"][-1, -2], c["pos"][0, 5] = -3, c["cos"].shape[0]
+    _lib.device_errors()
+    pairs = kind == "interleaved"
+    check(c, call(c, interleaved=pairs), 1e-5, pairs)
+    check_grad(c, call_grad(c, interleaved=pairs), 1e-5, pairs)
+    assert _lib.device_errors() == (_lib.NORM_DEVICE_ERR_BAD_POSITION if R else 0)
 
 
 def test_offsets_past_32_bits():
