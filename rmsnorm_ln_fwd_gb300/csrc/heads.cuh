@@ -38,7 +38,7 @@ constexpr int kHeadWarps = 8;
 constexpr int kHeadThreads = 32 * kHeadWarps;
 
 // A lane's 16 columns: [c0, c0 + n0) and [c1, c1 + n1), in halves [0, R/2) and
-// [R/2, R), or past R; with PAIRS neighbours.  CA columns an access.  As fp32,
+// [R/2, R), or in halves of the columns past R; with PAIRS neighbours.  CA columns an access.  As fp32,
 // pair i (of eight) is element i of `a` and of `b`.
 // FULL > 0: heads of FULL columns, all of them rotated, a power of two: what
 // follows from that is known at compile time.
@@ -58,9 +58,9 @@ struct HeadLane {
   __device__ __forceinline__ HeadLane(int unit, int cols, int R) {
     const int rot = R / 2, units = (rot + 7) / 8;
     if (PAIRS || unit >= units) {
-      c0 = PAIRS ? 16 * unit : R + 16 * (unit - units);
-      c1_ = c0 + 8;
-      n0_ = clamp8(cols - c0);
+      c0 = PAIRS ? 16 * unit : R + 8 * (unit - units);
+      c1_ = c0 + (PAIRS ? 8 : (cols - R + 15) / 16 * 8);
+      n0_ = clamp8(min(cols, PAIRS ? cols : R + (cols - R + 15) / 16 * 8) - c0);
       n1_ = clamp8(cols - c1_);
       nr_ = PAIRS ? clamp8(rot - 8 * unit) : 0;
     } else {
@@ -423,7 +423,7 @@ struct HeadFeed {
   Ring& ring;
   HeadShare share;
   unsigned token;   // the group's in the block at hand
-  int groups, unit, hq;
+  int groups, group, unit, hq;
   uint32_t angles;  // the lane's first granule of the first set
   int buf = 0;      // the set to be written next
   unsigned good = 0;  // whether the tokens of each set have positions in the table
@@ -433,9 +433,9 @@ struct HeadFeed {
   int64_t pos = 0;  // of the group's token in the next block
 
   __device__ __forceinline__ HeadFeed(const HeadArgs& a_, const Lane& me_, Ring& ring_, const HeadShare& share_, int groups_,
-                                      int group, int unit_, int hq_, uint32_t angles_)
-      : a(a_), me(me_), ring(ring_), share(share_), token(share_.block * groups_ + group - groups_), groups(groups_),
-        unit(unit_), hq(hq_), angles(angles_), x(HeadToken(a_, 0), a_.side[0].x, a_.side[1].x, hq_), dy(x) {
+                                      int group_, int unit_, int hq_, uint32_t angles_)
+      : a(a_), me(me_), ring(ring_), share(share_), token(share_.block * groups_ + group_ - groups_), groups(groups_),
+        group(group_), unit(unit_), hq(hq_), angles(angles_), x(HeadToken(a_, 0), a_.side[0].x, a_.side[1].x, hq_), dy(x) {
     if (a.R && share.left > 0) fetch_position(token + groups);
 #pragma unroll
     for (int i = 0; i < Ring::SLOTS; ++i) fetch();
@@ -457,7 +457,7 @@ struct HeadFeed {
         on = false;
       } else {
         token += groups;
-        on = token < a.N;
+        on = token < a.N && group < groups;
         if (on) {
           const HeadToken n(a, token);
           x = HeadPlace<I>(n, a.side[0].x, a.side[1].x, hq);
@@ -489,10 +489,27 @@ __device__ __forceinline__ void angles_ready() {
   if constexpr (!Ring::COPIES) asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Sum over each `lanes` lanes; LANES: as a compile-time value, or 0.
+// Sum over each `lanes` lanes; LANES: as a compile-time value, or 0.  No power of
+// two: a tree into the first one (behind each step, those below `off` hold sums of
+// all), which all read.
 template <int K, int LANES>
-__device__ __forceinline__ void lanes_sum(float (&v)[K], int lanes) {
-  warp_sum_pow2<K>(v, LANES ? LANES : lanes);
+__device__ __forceinline__ void lanes_sum(float (&v)[K], int lanes, int unit) {
+  if (LANES || (lanes & (lanes - 1)) == 0) {
+    warp_sum_pow2<K>(v, LANES ? LANES : lanes);
+    return;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    if (off < lanes) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const float other = __shfl_down_sync(0xffffffffu, v[k], off);
+        if (unit + off < lanes) v[k] += other;
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], (threadIdx.x & 31) - unit);
 }
 
 // LANES > 0: heads of 16 * LANES columns, all rotated.
@@ -504,7 +521,7 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_kernel(c
   extern __shared__ __align__(16) unsigned char smem[];  // gamma of both sides, each warp's angles and ring
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int lanes = LANES ? LANES : a.lanes;
-  const int groups = 32 / lanes, group = lane / lanes, unit = lane & (lanes - 1);
+  const int groups = 32 / lanes, group = lane / lanes, unit = lane - group * lanes;
   const Lane me(unit, a.D, a.R);
   const float inv_d = 1.f / (float)a.D;
   const int hq = a.side[0].heads, heads = hq + a.side[1].heads;
@@ -522,7 +539,7 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_kernel(c
   unsigned token = work.block * groups + group;
   int lo, hi, buf = 0;
   for (; work.take(lo, hi); token += groups, buf = buf + 1 == a.bufs ? 0 : buf + 1) {
-    const bool on = token < a.N;
+    const bool on = token < a.N && group < groups;
     const HeadPlace<I> dst(HeadToken(a, on ? token : 0), a.side[0].y, a.side[1].y, hq);
     angles_ready<Ring>();
     const bool good = feed.good >> buf & 1u;
@@ -539,7 +556,7 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_kernel(c
 #pragma unroll
       for (int j = 0; j < 4; ++j) sum = fma2(q[j], q[j], fma2(p[j], p[j], sum));
       float v[1] = {sum.x + sum.y};
-      lanes_sum<1, LANES>(v, lanes);
+      lanes_sum<1, LANES>(v, lanes, unit);
       if constexpr (Ring::COPIES) feed.fetch();
       const float2 r = splat2(rsqrtf(fmaf(v[0], inv_d, a.eps)));
       const uint32_t gamma = smem_u32(slots + ((h < hq ? 0 : lanes) + unit) * kHeadSlot);
@@ -582,7 +599,7 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_grad_ker
   extern __shared__ __align__(16) unsigned char smem[];  // gamma of both sides, each warp's sums, then its angles and ring
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int lanes = LANES ? LANES : a.lanes;
-  const int groups = 32 / lanes, group = lane / lanes, unit = lane & (lanes - 1);
+  const int groups = 32 / lanes, group = lane / lanes, unit = lane - group * lanes;
   const Lane me(unit, a.D, a.R);
   const float inv_d = 1.f / (float)a.D;
   const int hq = a.side[0].heads, heads = hq + a.side[1].heads;
@@ -604,7 +621,7 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_grad_ker
   unsigned token = work.block * groups + group;
   int lo, hi, buf = 0;
   for (; work.take(lo, hi); token += groups, buf = buf + 1 == a.bufs ? 0 : buf + 1) {
-    const bool on = token < a.N;
+    const bool on = token < a.N && group < groups;
     const HeadPlace<I> dst(HeadToken(a, on ? token : 0), a.side[0].y, a.side[1].y, hq);
     angles_ready<Ring>();
     const bool good = feed.good >> buf & 1u;
@@ -635,7 +652,7 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_grad_ker
         }
       }
       float m[2] = {sx.x + sx.y, sw.x + sw.y};
-      lanes_sum<2, LANES>(m, lanes);
+      lanes_sum<2, LANES>(m, lanes, unit);
       if constexpr (Ring::COPIES) feed.fetch();
       if (!on) continue;  // no lane exchanges anything below
       uint32_t o[Lane::NW];
@@ -722,12 +739,13 @@ __global__ void __launch_bounds__(32 * kHeadReduceWarps) head_gamma_reduce_kerne
     store_elem<D>(dg, i, total);
 }
 
-// Lanes a head takes: whole units of 16 columns, rounded to a power of two.
+// Lanes a head takes: whole units of 16 columns, rounded to a power of two unless
+// more heads fit into a warp without.
 inline int head_lanes(const HeadArgs& a) {
   const int units = a.interleaved || a.R == 0 ? (a.D + 15) / 16 : (a.R / 2 + 7) / 8 + (a.D - a.R + 15) / 16;
   int lanes = 1;
   while (lanes < units) lanes <<= 1;
-  return lanes;
+  return 32 / units > 32 / lanes ? units : lanes;
 }
 
 // Columns an access: eight (16 bytes of half precision, 32 of fp32), four or one,

@@ -49,7 +49,7 @@ struct HeadArgs {
   float* ws;
   int want;  // whether any dgamma is wanted
   // filled in by the launcher:
-  int lanes;   // a head, a power of two
+  int lanes;   // a head
   int pass;    // forward: stores that leave L2 first
   int bufs;       // sets of angles a warp has
   int cvec;       // cos and sin take copies of 16 bytes
