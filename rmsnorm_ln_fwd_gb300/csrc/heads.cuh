@@ -47,6 +47,13 @@ struct HeadLane {
   using T = typename D::T;
   static constexpr int ES = (int)sizeof(T);
   static constexpr int NW = 16 * ES / 4;  // packed words
+  static constexpr bool kFull = FULL > 0;
+  // Halves that no 16 bytes fit (R/2 = 10, 20): copied in the order of the columns, and
+  // stored in it by way of shared memory, where a lane's accesses are narrow (32+8 heads
+  // of 80 columns, bf16, 20 of them rotated, forward and gradient 162, 198 us with a
+  // lane's own accesses to the tensors, 41, 67 so; 112, 56 rotated: 33, 69; 34, 58).
+  static constexpr bool STAGED = !PAIRS && ES == 2 && (CA == 4 || CA == 2);
+  static constexpr bool ORDERED = PAIRS || STAGED;
   int c0, c1_, n0_, n1_;
   int nr_;  // rotated pairs
 
@@ -144,34 +151,91 @@ struct HeadLane {
   }
   // Copy n columns (of eight) into a 16-byte granule of shared memory; zeros for the
   // rest.
-  __device__ static __forceinline__ void copy_granule(const T* p, int n, uint32_t to) {
-    constexpr int B = CA * ES;
-    static_assert(ES == 2 && (B == 16 || B == 8), "copies of 16 or 8 bytes");
+  __device__ static __forceinline__ void copy_granule(const T* p, int n, uint32_t to, bool wide) {
+    static_assert(ES == 2, "copies of 16 or 8 bytes");
+    if (CA == 8 || (STAGED && wide)) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p), "r"(n > 0 ? 16 : 0) : "memory");
+    } else {
 #pragma unroll
-    for (int k = 0; k < 8 / CA; ++k) {
-      const T* from = k * CA < n ? p + k * CA : p;
-      if constexpr (B == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(k * CA < n ? 16 : 0) : "memory");
-      else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + k * B), "l"(from), "r"(k * CA < n ? 8 : 0) : "memory");
+      for (int k = 0; k < 2; ++k) {
+        const T* from = 4 * k < n ? p + 4 * k : p;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + k * 8), "l"(from), "r"(4 * k < n ? 8 : 0) : "memory");
+      }
     }
   }
   // Copy the group's part of a head into its lanes' granules: kLaneBytes a lane,
   // the second one of a lane kNext behind the first.  Neighbours are copied in the
   // order of the columns, to addresses in that order, each lane for others: a lane's
   // own two granules in turn, or addresses far apart, ask for each 32-byte sector
-  // twice (8192x32+8x128 70.8 us for 49.8).
-  static constexpr int kLaneBytes = PAIRS ? 32 : 16, kNext = PAIRS ? 16 : 512;
-  __device__ __forceinline__ void copy(const T* head, int unit, int lanes, int cols, uint32_t to) const {
-    if constexpr (PAIRS) {
+  // twice (8192x32+8x128 70.8 us for 49.8).  Halves in the order of the columns gain
+  // nothing (128 of which 64 are rotated 24.4 us for 23.8, gradient 41.2 for 38.9).
+  static constexpr int kLaneBytes = ORDERED ? 32 : 16, kNext = ORDERED ? 16 : 512;
+  __device__ __forceinline__ void copy(const T* head, int unit, int lanes, int cols, uint32_t to, bool wide) const {
+    if constexpr (ORDERED) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int g = unit + j * lanes, n = FULL ? 8 : clamp8(cols - 8 * g);
-        copy_granule(head + (n ? 8 * g : 0), n, to + (g - 2 * unit) * 16);
+        copy_granule(head + (n ? 8 * g : 0), n, to + (g - 2 * unit) * 16, wide);
       }
     } else {
-      copy_granule(head + (n0() ? c0 : 0), n0(), to);
-      copy_granule(head + (n1() ? c1() : 0), n1(), to + kNext);
+      copy_granule(head + (n0() ? c0 : 0), n0(), to, wide);
+      copy_granule(head + (n1() ? c1() : 0), n1(), to + kNext, wide);
+    }
+  }
+  // The lane's columns from its granules; STAGED: from the group's.
+  __device__ __forceinline__ void read(uint32_t from, int unit, uint32_t (&w)[NW]) const {
+    if constexpr (!STAGED) {
+      lds_words<4>(from, w);
+      lds_words<4>(from + kNext, w + 4);
+    } else {
+      read_half(from - unit * 32 + c0 * 2, n0(), w);
+      read_half(from - unit * 32 + c1() * 2, n1(), w + 4);
+    }
+  }
+  __device__ static __forceinline__ void read_half(uint32_t from, int n, uint32_t* w) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = 0u;
+#pragma unroll
+    for (int k = 0; k < 8 / CA; ++k)
+      if (k * CA < n) {
+        if constexpr (CA == 2)
+          w[k] = lds_u32(from + k * 4);
+        else
+          lds_words<CA / 2>(from + k * CA * 2, w + k * CA / 2);
+      }
+  }
+  __device__ static __forceinline__ void write_half(uint32_t to, int n, const uint32_t* w) {
+#pragma unroll
+    for (int k = 0; k < 8 / CA; ++k) {
+      if (k * CA < n) {
+        if constexpr (CA == 4)
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to + k * 8), "r"(w[2 * k]), "r"(w[2 * k + 1]) : "memory");
+        else
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + k * 4), "r"(w[k]) : "memory");
+      }
+    }
+  }
+  // Store by way of the lanes' granules at `at`: by all lanes of the warp, `on` those
+  // whose group has a head.  The next head's are written behind a barrier (of take).
+  __device__ __forceinline__ void store_staged(T* head, bool on, int unit, int lanes, int cols, uint32_t at, bool wide,
+                                               const uint32_t (&w)[NW]) const {
+    at -= unit * 32;
+    write_half(at + c0 * 2, n0(), w);
+    write_half(at + c1() * 2, n1(), w + 4);
+    __syncwarp();
+    if (!on) return;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int g = unit + j * lanes, n = clamp8(cols - 8 * g);
+      if (n <= 0) continue;
+      uint32_t v[4];
+      lds_words<4>(at + g * 16, v);
+      if (wide) {
+        st_vec(head + 8 * g, make_uint4(v[0], v[1], v[2], v[3]));
+      } else {
+        *reinterpret_cast<uint2*>(head + 8 * g) = make_uint2(v[0], v[1]);
+        if (n > 4) *reinterpret_cast<uint2*>(head + 8 * g + 4) = make_uint2(v[2], v[3]);
+      }
     }
   }
   template <bool PASS = false>
@@ -220,11 +284,11 @@ struct HeadLane {
     return i < n1() ? c1() + i : -1;
   }
   // Every rotated pair turned by the lane's angles, four granules 512 bytes apart:
-  // cos of the first and last four pairs, sin of them; the other columns stay,
-  // whatever they hold.  BACK: the other way.
+  // cos of the first and last four pairs, sin of them (0 past the last rotated pair);
+  // the other columns stay, whatever they hold.  BACK: the other way.
   template <bool BACK>
   __device__ __forceinline__ void turn(float2 (&a)[4], float2 (&b)[4], uint32_t angles) const {
-    if (nr() == 8) {
+    if (PAIRS ? nr() == 8 : nr() > 0) {  // halves have no columns beyond: zeros, and their angles too
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         float2 c[2], s[2];
@@ -239,7 +303,7 @@ struct HeadLane {
           x = u;
         }
       }
-    } else if (nr() > 0) {
+    } else if (PAIRS && nr() > 0) {
       float* x = reinterpret_cast<float*>(BACK ? b : a);
       float* y = reinterpret_cast<float*>(BACK ? a : b);
 #pragma unroll
@@ -357,15 +421,15 @@ template <typename Lane, typename T, int NT>
 struct RegisterRing {
   static constexpr bool COPIES = false;
   static constexpr int SLOTS = 1;
-  static constexpr int BYTES = 0;  // of shared memory a warp
+  static constexpr int BYTES = 0;
   uint32_t w[NT][Lane::NW];
-  __device__ __forceinline__ RegisterRing(unsigned char*, int, int, int, int) {}
+  __device__ __forceinline__ RegisterRing(unsigned char*, const HeadArgs&, int, int, int) {}
   __device__ __forceinline__ void fetch(const Lane& me, bool on, const T* (&p)[NT]) {
     if (!on) return;
 #pragma unroll
     for (int i = 0; i < NT; ++i) me.load(p[i], w[i]);
   }
-  __device__ __forceinline__ void take(uint32_t (&to)[NT][Lane::NW]) const {
+  __device__ __forceinline__ void take(const Lane&, uint32_t (&to)[NT][Lane::NW]) const {
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -376,29 +440,28 @@ template <typename Lane, typename T, int NT, int SLOTS_>
 struct CopyRing {
   static constexpr bool COPIES = true;
   static constexpr int SLOTS = SLOTS_;
-  static constexpr int BYTES = SLOTS * NT * 1024;
+  static constexpr int BYTES = SLOTS * NT * 1024;  // of shared memory a warp
   uint32_t base;  // of the lane's granules
   int unit, lanes, cols;
+  bool wide;
   int in = 0, out = 0;
-  __device__ __forceinline__ CopyRing(unsigned char* smem, int lane, int unit_, int lanes_, int cols_)
-      : base(smem_u32(smem) + lane * Lane::kLaneBytes), unit(unit_), lanes(lanes_), cols(cols_) {}
+  __device__ __forceinline__ CopyRing(unsigned char* smem, const HeadArgs& a, int lane, int unit_, int lanes_)
+      : base(smem_u32(smem) + lane * Lane::kLaneBytes), unit(unit_), lanes(lanes_), cols(a.D), wide(a.wide) {}
   // One group of copies a call, with whatever was copied before it; empty without a
   // head.
   __device__ __forceinline__ void fetch(const Lane& me, bool on, const T* (&p)[NT]) {
     if (on) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i) me.copy(p[i], unit, lanes, cols, base + (in * NT + i) * 1024);
+      for (int i = 0; i < NT; ++i) me.copy(p[i], unit, lanes, cols, base + (in * NT + i) * 1024, wide);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     in = in + 1 == SLOTS ? 0 : in + 1;
   }
-  __device__ __forceinline__ void take(uint32_t (&to)[NT][Lane::NW]) {
+  __device__ __forceinline__ void take(const Lane& me, uint32_t (&to)[NT][Lane::NW]) {
     asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
     __syncwarp();  // every lane's copies are there
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) lds_words<4>(base + (out * NT + i) * 1024 + j * Lane::kNext, to[i] + 4 * j);
+    for (int i = 0; i < NT; ++i) me.read(base + (out * NT + i) * 1024, unit, to[i]);
     out = out + 1 == SLOTS ? 0 : out + 1;
   }
 };
@@ -408,7 +471,7 @@ struct HeadRing {
   using T = typename D::T;
   // Forward (us, 16384 tokens of 32+8x128 and 16+16x64): two slots 59.4, 26.0; three
   // 59.5, 23.1; four 63.4, 22.4.  Backward two fill what shared memory two CTAs leave.
-  using Type = std::conditional_t<sizeof(T) == 2 && CA >= 4, CopyRing<Lane, T, NT, NT == 1 ? 3 : 2>, RegisterRing<Lane, T, NT>>;
+  using Type = std::conditional_t<sizeof(T) == 2 && CA >= 2, CopyRing<Lane, T, NT, NT == 1 ? 3 : 2>, RegisterRing<Lane, T, NT>>;
 };
 
 // What runs ahead of a warp's work: the heads into the ring, and, with the first one
@@ -436,6 +499,10 @@ struct HeadFeed {
                                       int group_, int unit_, int hq_, uint32_t angles_)
       : a(a_), me(me_), ring(ring_), share(share_), token(share_.block * groups_ + group_ - groups_), groups(groups_),
         group(group_), unit(unit_), hq(hq_), angles(angles_), x(HeadToken(a_, 0), a_.side[0].x, a_.side[1].x, hq_), dy(x) {
+    if constexpr (!Lane::kFull) {  // no angles for pairs that a lane does not have
+      for (int i = 0; i < 4 * a.bufs; ++i)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(angles + i * 512), "r"(0u) : "memory");
+    }
     if (a.R && share.left > 0) fetch_position(token + groups);
 #pragma unroll
     for (int i = 0; i < Ring::SLOTS; ++i) fetch();
@@ -494,22 +561,24 @@ __device__ __forceinline__ void angles_ready() {
 // all), which all read.
 template <int K, int LANES>
 __device__ __forceinline__ void lanes_sum(float (&v)[K], int lanes, int unit) {
-  if (LANES || (lanes & (lanes - 1)) == 0) {
-    warp_sum_pow2<K>(v, LANES ? LANES : lanes);
-    return;
-  }
+  if constexpr (LANES > 0) {
+    warp_sum_pow2<K>(v, LANES);
+  } else if ((lanes & (lanes - 1)) == 0) {
+    warp_sum_pow2<K>(v, lanes);
+  } else {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    if (off < lanes) {
+    for (int off = 16; off > 0; off >>= 1) {
+      if (off < lanes) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const float other = __shfl_down_sync(0xffffffffu, v[k], off);
-        if (unit + off < lanes) v[k] += other;
+        for (int k = 0; k < K; ++k) {
+          const float other = __shfl_down_sync(0xffffffffu, v[k], off);
+          if (unit + off < lanes) v[k] += other;
+        }
       }
     }
-  }
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], (threadIdx.x & 31) - unit);
+    for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], (threadIdx.x & 31) - unit);
+  }
 }
 
 // LANES > 0: heads of 16 * LANES columns, all rotated.
@@ -522,16 +591,17 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_kernel(c
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int lanes = LANES ? LANES : a.lanes;
   const int groups = 32 / lanes, group = lane / lanes, unit = lane - group * lanes;
-  const Lane me(unit, a.D, a.R);
+  const Lane me(group < groups ? unit : kHeadMaxCols, a.D, a.R);  // no columns for a lane too many
   const float inv_d = 1.f / (float)a.D;
   const int hq = a.side[0].heads, heads = hq + a.side[1].heads;
   float* slots = reinterpret_cast<float*>(smem);
-  unsigned char* at = smem + 2 * lanes * kHeadSlot * 4 + warp * (a.bufs * 2048 + Ring::BYTES);
+  unsigned char* at = smem + 2 * lanes * kHeadSlot * 4 + warp * (a.bufs * 2048 + Ring::BYTES + (Lane::STAGED ? 1024 : 0));
   const uint32_t angles = smem_u32(at) + lane * 16;
   pdl_launch_dependents();
   pdl_wait_primary();
   HeadShare work(a, blockIdx.x * kHeadWarps + warp, heads);
-  Ring ring(at + a.bufs * 2048, lane, unit, lanes, a.D);
+  Ring ring(at + a.bufs * 2048, a, lane, unit, lanes);
+  const uint32_t stage = smem_u32(at + a.bufs * 2048 + Ring::BYTES) + lane * 32;
   HeadFeed<D, Lane, Ring, I, 1> feed(a, me, ring, work, groups, group, unit, hq, angles);
   for (int k = 0; k < 2; ++k)
     head_gamma<Lane, D>(slots + k * lanes * kHeadSlot, a, a.side[k].gamma, threadIdx.x, kHeadThreads);
@@ -542,13 +612,13 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_kernel(c
     const bool on = token < a.N && group < groups;
     const HeadPlace<I> dst(HeadToken(a, on ? token : 0), a.side[0].y, a.side[1].y, hq);
     angles_ready<Ring>();
-    const bool good = feed.good >> buf & 1u;
+    const bool good = on && (feed.good >> buf & 1u);
 #pragma unroll 1
     for (int h = lo; h < hi; ++h) {
       float2 p[4], q[4];
       {
         uint32_t w[1][Lane::NW];
-        ring.take(w);
+        ring.take(me, w);
         Lane::unpack(w[0], p, q);
       }
       if constexpr (!Ring::COPIES) feed.fetch();
@@ -570,7 +640,7 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_kernel(c
         q[2 * j] = mul2(mul2(q[2 * j], r), g[0]);
         q[2 * j + 1] = mul2(mul2(q[2 * j + 1], r), g[1]);
       }
-      if (!on) continue;  // no lane exchanges anything below
+      if (!Lane::STAGED && !on) continue;  // no lane exchanges anything below
       uint32_t o[Lane::NW];
       if (good) {
         me.template turn<false>(p, q, angles + buf * 2048);
@@ -580,7 +650,9 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_kernel(c
         for (int j = 0; j < Lane::NW; ++j) o[j] = 0u;
       }
       T* y = head_at<T, I>(a.side[0].y, a.side[1].y, dst, hq, h);
-      if (a.pass)
+      if constexpr (Lane::STAGED)
+        me.store_staged(y, on, unit, lanes, a.D, stage, a.wide, o);
+      else if (a.pass)
         me.template store<true>(y, o);
       else
         me.store(y, o);
@@ -600,18 +672,19 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_grad_ker
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int lanes = LANES ? LANES : a.lanes;
   const int groups = 32 / lanes, group = lane / lanes, unit = lane - group * lanes;
-  const Lane me(unit, a.D, a.R);
+  const Lane me(group < groups ? unit : kHeadMaxCols, a.D, a.R);  // no columns for a lane too many
   const float inv_d = 1.f / (float)a.D;
   const int hq = a.side[0].heads, heads = hq + a.side[1].heads;
   float* slots = reinterpret_cast<float*>(smem);
   float4* sums = reinterpret_cast<float4*>(slots + 2 * lanes * kHeadSlot);  // [warp][side][granule][lane]
   float4* mine = sums + warp * 256 + lane;
-  unsigned char* at = reinterpret_cast<unsigned char*>(sums + kHeadWarps * 256) + warp * (a.bufs * 2048 + Ring::BYTES);
+  unsigned char* at = reinterpret_cast<unsigned char*>(sums + kHeadWarps * 256) + warp * (a.bufs * 2048 + Ring::BYTES + (Lane::STAGED ? 1024 : 0));
   const uint32_t angles = smem_u32(at) + lane * 16;
   pdl_launch_dependents();
   pdl_wait_primary();
   HeadShare work(a, blockIdx.x * kHeadWarps + warp, heads);
-  Ring ring(at + a.bufs * 2048, lane, unit, lanes, a.D);
+  Ring ring(at + a.bufs * 2048, a, lane, unit, lanes);
+  const uint32_t stage = smem_u32(at + a.bufs * 2048 + Ring::BYTES) + lane * 32;
   HeadFeed<D, Lane, Ring, I, 2> feed(a, me, ring, work, groups, group, unit, hq, angles);
   for (int k = 0; k < 2; ++k)
     head_gamma<Lane, D>(slots + k * lanes * kHeadSlot, a, a.side[k].gamma, threadIdx.x, kHeadThreads);
@@ -624,13 +697,13 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_grad_ker
     const bool on = token < a.N && group < groups;
     const HeadPlace<I> dst(HeadToken(a, on ? token : 0), a.side[0].y, a.side[1].y, hq);
     angles_ready<Ring>();
-    const bool good = feed.good >> buf & 1u;
+    const bool good = on && (feed.good >> buf & 1u);
 #pragma unroll 1
     for (int h = lo; h < hi; ++h) {
       float2 p[4], q[4], u[4], v[4];
       {
         uint32_t w[2][Lane::NW];
-        ring.take(w);
+        ring.take(me, w);
         Lane::unpack(w[0], p, q);
         Lane::unpack(w[1], u, v);
       }
@@ -654,7 +727,7 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_grad_ker
       float m[2] = {sx.x + sx.y, sw.x + sw.y};
       lanes_sum<2, LANES>(m, lanes, unit);
       if constexpr (Ring::COPIES) feed.fetch();
-      if (!on) continue;  // no lane exchanges anything below
+      if (!Lane::STAGED && !on) continue;  // no lane exchanges anything below
       uint32_t o[Lane::NW];
       if (good) {
         const float r = rsqrtf(fmaf(m[0], inv_d, a.eps));
@@ -685,7 +758,11 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_grad_ker
 #pragma unroll
         for (int j = 0; j < Lane::NW; ++j) o[j] = 0u;
       }
-      me.store(head_at<T, I>(a.side[0].y, a.side[1].y, dst, hq, h), o);
+      T* dx = head_at<T, I>(a.side[0].y, a.side[1].y, dst, hq, h);
+      if constexpr (Lane::STAGED)
+        me.store_staged(dx, on, unit, lanes, a.D, stage, a.wide, o);
+      else
+        me.store(dx, o);
     }
   }
   if (!a.want) return;
@@ -748,13 +825,14 @@ inline int head_lanes(const HeadArgs& a) {
   return 32 / units > 32 / lanes ? units : lanes;
 }
 
-// Columns an access: eight (16 bytes of half precision, 32 of fp32), four or one,
-// whichever divides every column that an access starts at, and fits every tensor.
+// Columns an access: eight (16 bytes of half precision, 32 of fp32), four, two (of
+// half precision, in halves) or one, whichever divides every column that a lane's
+// start at.  Eight and one, and four of fp32 or of neighbours, are the accesses to
+// the tensors too, which they have to fit; else a.wide has them 16 or 8 bytes.
 template <typename D>
-int head_access(const HeadArgs& a, bool grad) {
+int head_access(HeadArgs& a, bool grad) {
   constexpr int ES = (int)sizeof(typename D::T);
   unsigned long long bits = (unsigned long long)a.D * ES;
-  bits |= (unsigned long long)(a.interleaved || a.R == 0 ? 0 : a.R / 2) * ES;
   for (const HeadSide& s : a.side) {
     if (!s.heads) continue;
     for (const HeadView* v : {&s.x, &s.y, &s.dy}) {
@@ -763,7 +841,11 @@ int head_access(const HeadArgs& a, bool grad) {
       bits |= (unsigned long long)((v->sb | v->st | v->sh) * ES);
     }
   }
-  return (bits & (8 * ES - 1)) == 0 ? 8 : (bits & (4 * ES - 1)) == 0 ? 4 : 1;
+  const int fit = (bits & (8 * ES - 1)) == 0 ? 8 : (bits & (4 * ES - 1)) == 0 ? 4 : 1;
+  a.wide = fit == 8;
+  const int half = a.interleaved ? 0 : a.R / 2;
+  const int cols = half % 8 == 0 ? 8 : half % 4 == 0 ? 4 : half % 2 == 0 && ES == 2 ? 2 : 1;
+  return fit == 1 ? 1 : cols < fit ? cols : fit;
 }
 
 // The kernel on as many CTAs as are resident, or fewer.  Its units are shared out
@@ -801,6 +883,7 @@ cudaError_t run_heads(K kern, HeadArgs& a, size_t fixed, int ring, int slots, Ke
 
 template <typename D, int CA, bool PAIRS, int LANES, typename I>
 cudaError_t run_head_rotary(HeadArgs a, const DeviceInfo& dev, cudaStream_t s) {
+  using Lane = HeadLane<D, CA, PAIRS, 16 * LANES>;
   using Ring = typename HeadRing<D, CA, PAIRS, LANES, 1>::Type;
   // Heads that L2 will not hold until they are read again (a half of its 129 MB, the
   // inputs passing through the other) do not displace the inputs: bf16 32+8x128, 16384
@@ -808,15 +891,17 @@ cudaError_t run_head_rotary(HeadArgs a, const DeviceInfo& dev, cudaStream_t s) {
   a.pass = a.N * (a.side[0].heads + a.side[1].heads) * a.D * (int64_t)sizeof(typename D::T) > 64000000;
   static KernelMemo memo;
   int ctas;
-  return run_heads(head_rotary_kernel<D, CA, PAIRS, LANES, I>, a, 0, Ring::BYTES, Ring::SLOTS, memo, dev, s, &ctas);
+  return run_heads(head_rotary_kernel<D, CA, PAIRS, LANES, I>, a, 0, Ring::BYTES + Lane::STAGED * 1024, Ring::SLOTS, memo, dev, s,
+                   &ctas);
 }
 
 template <typename D, int CA, bool PAIRS, int LANES, typename I>
 cudaError_t run_head_rotary_grad(HeadArgs a, const DeviceInfo& dev, cudaStream_t s, int* ctas) {
+  using Lane = HeadLane<D, CA, PAIRS, 16 * LANES>;
   using Ring = typename HeadRing<D, CA, PAIRS, LANES, 2>::Type;
   static KernelMemo memo;
-  return run_heads(head_rotary_grad_kernel<D, CA, PAIRS, LANES, I>, a, kHeadWarps * 4096, Ring::BYTES, Ring::SLOTS,
-                   memo, dev, s, ctas);
+  return run_heads(head_rotary_grad_kernel<D, CA, PAIRS, LANES, I>, a, kHeadWarps * 4096,
+                   Ring::BYTES + Lane::STAGED * 1024, Ring::SLOTS, memo, dev, s, ctas);
 }
 
 // Whether every tensor has fewer than 2^31 elements from its first to its last.
@@ -834,14 +919,17 @@ inline bool head_offsets_fit(const HeadArgs& a, bool grad) {
 // f(columns an access, whether pairs are neighbours, lanes a head of 64, 128 or 256
 // rotated columns or 0, an offset's type) as compile-time values.
 template <typename D, typename F>
-cudaError_t head_variants(const HeadArgs& a, bool grad, F&& f) {
+cudaError_t head_variants(HeadArgs& a, bool grad, F&& f) {
   const int access = head_access<D>(a, grad);
   auto with = [&](auto ca, auto l, auto off) {
-    return a.interleaved && a.R ? f(ca, std::integral_constant<bool, true>{}, l, off)
-                                : f(ca, std::integral_constant<bool, false>{}, l, off);
+    if constexpr (ca != 2) {
+      if (a.interleaved && a.R) return f(ca, std::integral_constant<bool, true>{}, l, off);
+    }
+    return f(ca, std::integral_constant<bool, false>{}, l, off);
   };
   const std::integral_constant<int, 8> eight;
   const std::integral_constant<int, 4> four;
+  const std::integral_constant<int, 2> two;
   const std::integral_constant<int, 1> one;
   const std::integral_constant<int, 0> any;
   if (!head_offsets_fit(a, grad)) return access == 8 ? with(eight, any, int64_t{}) : with(one, any, int64_t{});
@@ -849,6 +937,9 @@ cudaError_t head_variants(const HeadArgs& a, bool grad, F&& f) {
     if (a.D == 64) return with(eight, std::integral_constant<int, 4>{}, uint32_t{});
     if (a.D == 128) return with(eight, std::integral_constant<int, 8>{}, uint32_t{});
     if (a.D == 256) return with(eight, std::integral_constant<int, 16>{}, uint32_t{});
+  }
+  if constexpr (sizeof(typename D::T) == 2) {
+    if (access == 2) return with(two, any, uint32_t{});
   }
   return access == 8 ? with(eight, any, uint32_t{}) : access == 4 ? with(four, any, uint32_t{}) : with(one, any, uint32_t{});
 }

@@ -50,6 +50,7 @@ struct HeadArgs {
   int want;  // whether any dgamma is wanted
   // filled in by the launcher:
   int lanes;   // a head
+  bool wide;   // every head starts at 16 bytes (of fp32, 32)
   int pass;    // forward: stores that leave L2 first
   int bufs;       // sets of angles a warp has
   int cvec;       // cos and sin take copies of 16 bytes

@@ -412,6 +412,51 @@ def test_few_heads_and_many_tokens(shape, dt, kind):
     assert _lib.device_errors() == (_lib.NORM_DEVICE_ERR_BAD_POSITION if R else 0)
 
 
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("D,R", [(80, 20), (84, 84), (64, 12), (20, 20), (36, 4), (16, 4), (80, 32), (100, 100), (256, 252), (160, 160),
+                                 (144, 144), (40, 40), (72, 8), (60, 20), (68, 10), (24, 0), (88, 48), (476, 476), (44, 36)])
+def test_columns_of_every_access_and_lanes_of_every_number(D, R, dt):
+    """Halves that start at any multiple, lanes a head that are no power of two, at addresses of 16 and of 8 bytes."""
+    c = make(3, 59, 3, 2, D, R, dt, wdt="f32", positions="each", seed=D + R)
+    if R:
+        c["pos"][1, 17] = -1
+    want, grads = call(c), call_grad(c)
+    check(c, want, 1e-5, False)
+    check_grad(c, grads, 1e-5, False)
+    for off in (8 // c["q"].element_size(), 1):
+
+        def shift(t):
+            flat = torch.full((t.numel() + 32,), 3.0, device=DEV, dtype=t.dtype)
+            v = flat[off:off + t.numel()].view(t.shape)
+            return v.copy_(t)
+
+        d = {**c, **{n: shift(c[n]) for n in ("q", "k", "dyq", "dyk")}}
+        q, k = torch.full_like(shift(c["q"]), 5.0), shift(torch.full_like(c["k"], 5.0))
+        got = call(d, q_out=q, k_out=k)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        base = k._base
+        assert bool((base[:off] == 3.0).all()) and bool((base[off + k.numel():] == 3.0).all())
+        for a, b in zip(call_grad(d, dk=k), grads):
+            assert torch.equal(a, b)
+        assert bool((base[:off] == 3.0).all()) and bool((base[off + k.numel():] == 3.0).all())
+    _lib.device_errors()
+
+
+def test_an_infinite_column_beside_narrow_halves():
+    """A column that is not rotated, in the same lane or the next one, and whatever a table's other columns hold."""
+    for D, R in ((80, 20), (80, 40), (64, 32)):
+        c = make(1, 6, 4, 2, D, R, "bf16", seed=D)
+        want = call(c)
+        c["q"][0, 3, 0, R + 1] = float("inf")
+        got = call(c)
+        assert torch.equal(got[0][0, 3, 1:], want[0][0, 3, 1:]) and torch.equal(got[1], want[1])
+        assert bool(got[0][0, 3, 0, R + 1].isnan()) and int(got[0][0, 3, 0].isnan().sum()) == 1
+        wide = torch.full((2, c["cos"].shape[0], R), float("nan"), device=DEV)
+        wide[:, :, :R // 2] = torch.stack([c["cos"], c["sin"]])
+        got = call({**c, "cos": wide[0, :, :R // 2], "sin": wide[1, :, :R // 2]})
+        assert torch.equal(got[0][0, 4], want[0][0, 4]) and torch.equal(got[1], want[1])
+
+
 def test_offsets_past_32_bits():
     """Heads past 2^31 elements: repeated tokens have the bits of the first."""
     free = torch.cuda.mem_get_info()[0]
