@@ -24,11 +24,9 @@ namespace normk {
 // 128 threads 198, 14.7, 83).  The kernel comes in three shapes of chunks that a
 // thread has in flight and CTAs an SM, by how many CTAs there are: 3 and 4 where they
 // fill the GPU, 4 and 3 (80 registers) where three an SM hold them all, 6 and 2 where
-// two do, except in clusters of more than two, which two an SM may not hold.  (us, as
-// 3 and 4; 4 and 3; 6 and 2: 4096x131072 159; 169; 184, 333x50001 12.8; 11.1; 16.3,
-// 150x50001 in clusters of two 9.2; 7.0; 6.4, 2000x4096 7.2; 6.2; 5.3, 32x131072 with
-// 20 alternatives in clusters of eight 11.5; 10.3; 12.8.  Four chunks and four CTAs,
-// 64 registers, 159, 13.5; two 167, 12.5.)
+// two do.  (us, as 3 and 4; 4 and 3; 6 and 2: 4096x131072 159; 169; 184, 333x50001
+// 12.8; 11.1; 16.3, 150x50001 in clusters of two 9.2; 7.0; 6.4, 2000x4096 7.2; 6.2; 5.3.
+// Four chunks and four CTAs, 64 registers, 159, 13.5; two 167, 12.5.)
 constexpr int kLogprobThreads = 256;  // of a CTA
 constexpr int kLogprobPerSm = 4;      // CTAs
 constexpr int kLogprobMaxCluster = 8;
@@ -613,14 +611,44 @@ template <typename D, bool ENT, bool TOP>
 cudaError_t run_logprob(LogprobArgs a, const DeviceInfo& dev, cudaStream_t s) {
   constexpr int GE = LogitChunk<D>::GE;
   const int chunks = a.V / GE + 1;
-  // Few rows: clusters share them, as long as the CTAs all fit at once and have a
-  // chunk for every other thread, or, more than one an SM, four for every thread (us,
-  // 64x131072 bf16 8.6 -> 6.7 as 512 CTAs; 333x50001 as 666, which do not fit, 12.7 ->
-  // 16.1; 150x50001 as 600 of three chunks a thread 8.9, as 300 of six 6.4).
+  // Few rows: clusters share them, the largest of which all fit at once on the GPU
+  // (which the runtime knows: three clusters of eight an SM leave SMs unused), two CTAs
+  // an SM before three and four.  Those of two, four and eight have at least half a
+  // chunk a thread, one and two; the larger ones at more than two CTAs an SM, and any
+  // with alternatives, which its CTAs have to merge, four.  Those of eight that merge
+  // leave a quarter of the places free: as long as an earlier call's merge, they find
+  // none (32x131072 with 20 alternatives, call after call, 13.4 us for 10.6 in clusters
+  // of four).  (us, bf16, in order of the list below, then without a cluster; * does not
+  // fit: 24x131072 5.2, 5.6, 6.0, 6.3, 6.6, 7.6, 8.4, 9.4, 11.4; with 20 alternatives 9.7,
+  // 10.7, 10.1, 10.5, 10.6, 12.1, 13.1, 14.1, 16.3; 57x131072 9.7*, 10.0*, 7.5, 7.9,
+  // 9.1, 9.2, 8.7, 10.9, 12.2; 112x131072 17.2*, 14.9*, 13.5*, 12.5*, 10.3, 10.7, 11.5,
+  // 14.3, 14.5; 128x32000 13.2*, 10.5*, 7.7*, 7.8*, 5.9, 5.3, 6.1, 7.0, 7.5; 32x32000
+  // with 20 alternatives 11.8*, 9.1, 7.4, 7.7, 7.6, 7.2, 7.1, 7.3, 6.9.)
+  struct Plan {
+    int cl, per_sm;
+  };
+  constexpr Plan plans[] = {{8, 2}, {8, 3}, {4, 2}, {4, 3}, {4, 4}, {2, 2}, {2, 3}, {2, 4}};
+  constexpr int count = sizeof(plans) / sizeof(plans[0]);
+  static KernelMemo memo[count];
+  auto with_kernel = [&](int per_sm, auto&& f) {
+    return per_sm == 2 ? f(logprob_kernel<D, ENT, TOP, 6, 2>)
+                       : per_sm == 3 ? f(logprob_kernel<D, ENT, TOP, 4, 3>) : f(logprob_kernel<D, ENT, TOP, 3, kLogprobPerSm>);
+  };
   a.cl = 1;
-  while (a.cl < kLogprobMaxCluster && a.N * a.cl * 2 <= kLogprobPerSm * (int64_t)dev.sm_count &&
-         chunks / (a.cl * 2) >= (a.N * a.cl * 2 <= dev.sm_count ? kLogprobThreads / 2 : 4 * kLogprobThreads))
-    a.cl *= 2;
+  int per_sm = 0;
+  for (int i = 0; i < count && a.cl == 1; ++i) {
+    const int cl = plans[i].cl, per = plans[i].per_sm;
+    if (a.N * cl > per * (int64_t)dev.sm_count || (TOP && cl == 8 && per > 2)) continue;
+    if (chunks / cl < (TOP || (cl > 2 && per > 2) ? 4 * kLogprobThreads : cl * kLogprobThreads / 4)) continue;
+    FirstLaunch shape(kLogprobThreads, TOP ? top_bytes(1) : 0, s, cl);
+    shape.cfg.gridDim.x = (unsigned)cl;
+    const int fit = memo[i].resident(kLogprobThreads, shape.cfg.dynamicSmemBytes, dev, [&](int* n) {
+      return with_kernel(per, [&](auto kern) { return cudaOccupancyMaxActiveClusters(n, kern, &shape.cfg); });
+    });
+    if (a.N > (TOP && cl == 8 ? fit * 3 / 4 : fit)) continue;
+    a.cl = cl;
+    per_sm = per;
+  }
   // Otherwise 16 chunks a thread, or two with alternatives, whose threads each keep
   // a candidate: what a row costs besides its logits is the same for each warp (us,
   // 16384x4096 bf16 with 16, 8, 4 chunks a thread 27.6, 33, 51; 1024x2000 with 20
@@ -631,10 +659,8 @@ cudaError_t run_logprob(LogprobArgs a, const DeviceInfo& dev, cudaStream_t s) {
   const int rows = kLogprobThreads / a.tpr;
   FirstLaunch first(kLogprobThreads, TOP ? top_bytes(rows) : 0, s, a.cl);
   const int64_t ctas = a.cl > 1 ? a.N * a.cl : (a.N + rows - 1) / rows;
-  auto launch = [&](auto kern) { return first.launch((unsigned)ctas, true, kern, a); };
-  if (ctas <= 2 * (int64_t)dev.sm_count && a.cl <= 2) return launch(logprob_kernel<D, ENT, TOP, 6, 2>);
-  if (ctas <= 3 * (int64_t)dev.sm_count) return launch(logprob_kernel<D, ENT, TOP, 4, 3>);
-  return launch(logprob_kernel<D, ENT, TOP, 3, kLogprobPerSm>);
+  if (per_sm == 0) per_sm = ctas <= 2 * (int64_t)dev.sm_count ? 2 : ctas <= 3 * (int64_t)dev.sm_count ? 3 : kLogprobPerSm;
+  return with_kernel(per_sm, [&](auto kern) { return first.launch((unsigned)ctas, true, kern, a); });
 }
 
 template <typename D>

@@ -154,6 +154,21 @@ def test_forward_and_gradient(N, V, dt):
     check_grad(z, tokens, scale, got, out[3], out[1], dlp, dent, dlse, -100)
 
 
+@pytest.mark.parametrize("N,V,top", [(2, 18000, 0), (3, 70000, 0), (44, 70000, 0), (60, 70000, 0), (90, 70001, 0), (130, 70000, 0), (100, 9000, 0),
+                                     (170, 9001, 0), (250, 9000, 0), (12, 140000, 20), (30, 140000, 5), (60, 70000, 20), (90, 70000, 3),
+                                     (120, 70001, 32), (130, 40000, 20), (200, 40000, 20), (260, 40000, 20), (310, 9000, 20)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_rows_shared_in_every_way(N, V, top, dt):
+    """By two, four and eight CTAs, two to four of them an SM, as the number of rows has it."""
+    V = V // 2 + 1 if dt == "f32" else V
+    z, tokens = make(N, V, dt, seed=N + V, banned=0.05, ignore=-100)
+    z[N // 2, : V - 3] = -INF
+    out = nl.token_logprobs(z, tokens, top=top, ignore_index=-100)
+    check(z, tokens, 1.0, out, top, -100)
+    for a, b in zip(nl.token_logprobs(z, tokens, top=top, ignore_index=-100), out):
+        assert (a is None and b is None) or torch.equal(a, b)
+
+
 @pytest.mark.parametrize("dt", list(DT))
 def test_each_gradient_alone(dt):
     z, tokens = make(9, 3001, dt, seed=1)
