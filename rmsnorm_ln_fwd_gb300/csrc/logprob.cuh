@@ -216,9 +216,11 @@ struct RowSums {
 // Shared memory of a row's alternatives.  512 candidates: a row that is constant,
 // or masked with one value, has 16 columns of one thread for each alternative.
 constexpr int kTopCandidates = 512;
+constexpr int kTopOneGroup = 24;  // alternatives that one group of threads a lane does for
 struct __align__(16) TopShared {
   unsigned long long key[kTopCandidates];
   unsigned long long best[kMaxTop];
+  unsigned long long tau;
   int listed, found;
   unsigned char list[kLogprobThreads];
 };
@@ -229,11 +231,14 @@ __host__ __device__ constexpr int top_bytes(int rows) { return rows * (int)sizeo
 // are fewer).  Each thread comes with its largest logit and the chunk it met it
 // in first.  A key at that chunk's last column is no larger than the key of the
 // logit itself, so at least `top` logits reach tau, the top-th largest of those
-// over 32 groups of threads (the same lane of each warp); all that do are in the
-// chunks of threads whose own key does.  Only those chunks are read again: a 12th of
-// the row for 20 of 256 threads, most of them still in L2.  (us, 1x131072 bf16 with 20
-// of them 8.4, without 4.1; 1024x131072 64; 47; ranks among 128 groups by reads of
-// shared memory 10.3 and 65.)
+// over 32 groups of threads (the same lane of each warp) or, of more than 24, over 64
+// (the same lane of each other warp); all that do are in the chunks of threads whose
+// own key does.  Only those chunks are read again: a 12th of the row for 20 of 256
+// threads, most of them still in L2.  The first warp finds tau and lists the threads;
+// what all warps do between a row's two reads costs the others their issue slots.
+// (us, bf16: 1x131072 with 20 of them 7.6, without 3.5; 1024x131072 62; 45; with 32 of
+// them 66, 93 by 32 groups; with 20 56 for 62 by 64, but 512x4096 6.5 for 6.0.  Every
+// warp finding tau: 4096x32000 with one 69 for 66, 512x4096 6.2 for 5.3.)
 template <typename D>
 __device__ __forceinline__ void row_top(const RowGroup& g, TopShared& sh, unsigned long long* lanes, const typename D::T* z,
                                         int a0, int V, int first, int last, int top, float mx, int mi) {
@@ -242,32 +247,56 @@ __device__ __forceinline__ void row_top(const RowGroup& g, TopShared& sh, unsign
   const float none = __int_as_float(0xff800000);
   const unsigned long long mine = mx > none ? top_key(mx, mi * L::GE - a0 + L::GE - 1) : 0ull;
   if (g.t < kMaxTop) sh.best[g.t] = 0ull;
-  if (g.t == 0) sh.listed = sh.found = 0;
-  unsigned long long most = mine;
-  if (g.n > 32) lanes[g.t] = mine;
+  if (g.t == 0) sh.found = 0;
+  lanes[g.t] = mine;
   g.sync();
-  if (g.n > 32) {
+  if (g.t < 32) {
+    constexpr int W = kLogprobThreads / 32;
+    unsigned long long k[W], most[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < kLogprobThreads / 32; ++i) {
-      const unsigned long long o = 32 * i < g.n ? lanes[32 * i + lane] : 0ull;
-      most = o > most ? o : most;
+    for (int i = 0; i < W; ++i) {
+      k[i] = 32 * i < g.n ? lanes[32 * i + lane] : 0ull;
+      most[i & 1] = k[i] > most[i & 1] ? k[i] : most[i & 1];
+    }
+    unsigned long long tau = 1ull;  // fewer groups than alternatives have a logit at all: any will do
+    if (top <= kTopOneGroup || g.n == 32) {
+      const unsigned long long v = most[0] > most[1] ? most[0] : most[1];
+      int rank = 0;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) rank += __shfl_sync(0xffffffffu, v, i) > v;
+      const unsigned at = __ballot_sync(0xffffffffu, rank == top - 1 && v != 0);
+      if (at) tau = __shfl_sync(0xffffffffu, v, __ffs(at) - 1);
+    } else {
+      int rank[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const unsigned long long x = __shfl_sync(0xffffffffu, most[0], i), y = __shfl_sync(0xffffffffu, most[1], i);
+        rank[0] += (x > most[0]) + (y > most[0]);
+        rank[1] += (x > most[1]) + (y > most[1]);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const unsigned at = __ballot_sync(0xffffffffu, rank[j] == top - 1 && most[j] != 0);
+        if (at) tau = __shfl_sync(0xffffffffu, most[j], __ffs(at) - 1);
+      }
+    }
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const unsigned in = __ballot_sync(0xffffffffu, k[i] >= tau);
+      if (k[i] >= tau) sh.list[n + __popc(in & ((1u << lane) - 1u))] = (unsigned char)(32 * i + lane);
+      n += __popc(in);
+    }
+    if (lane == 0) {
+      sh.listed = n;
+      sh.tau = tau;
     }
   }
-  int rank = 0;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) rank += __shfl_sync(0xffffffffu, most, i) > most;
-  const unsigned at = __ballot_sync(0xffffffffu, rank == top - 1 && most != 0);
-  // fewer groups than alternatives have a logit at all: any logit will do
-  const unsigned long long tau = at ? __shfl_sync(0xffffffffu, most, __ffs(at) - 1) : 1ull;
-  const unsigned in = __ballot_sync(0xffffffffu, mine >= tau);
-  int slot = 0;
-  if (lane == 0 && in) slot = atomicAdd(&sh.listed, __popc(in));
-  slot = __shfl_sync(0xffffffffu, slot, 0) + __popc(in & ((1u << lane) - 1u));
-  if (mine >= tau) sh.list[slot] = (unsigned char)g.t;
   g.sync();
+  const unsigned long long tau = sh.tau;
   const int each = (last - first + g.n - 1) / g.n;  // chunks a thread
   const int pairs = sh.listed * each;
-  const float least = at ? key_value(tau) : none;
+  const float least = tau > 1ull ? key_value(tau) : none;
   for (int p = g.t; p < pairs; p += g.n) {
     const int i = first + sh.list[p / each] + (p % each) * g.n;
     if (i >= last) continue;
@@ -649,13 +678,19 @@ cudaError_t run_logprob(LogprobArgs a, const DeviceInfo& dev, cudaStream_t s) {
     a.cl = cl;
     per_sm = per;
   }
-  // Otherwise 16 chunks a thread, or two with alternatives, whose threads each keep
-  // a candidate: what a row costs besides its logits is the same for each warp (us,
-  // 16384x4096 bf16 with 16, 8, 4 chunks a thread 27.6, 33, 51; 1024x2000 with 20
-  // alternatives 9.8 with four, 8.4 with two).
-  constexpr int each = TOP ? 2 : 16;
+  // Otherwise as many threads as leave each three chunks, or, where one wave of CTAs
+  // does not hold that many, fewer, with up to 16: what a row costs besides its logits
+  // is the same for each warp.  (us, bf16, three and 16 chunks a thread: 320x4096 2.9,
+  // 3.8; 640x8192 4.65, 5.4; 16384x4096 with 16, 8, 4 27.6, 33, 51.  With 20
+  // alternatives, as this has it, and two chunks: 4096x4096 20.3, 39; 2048x8192 16.9,
+  // 24; 512x4096 6.0, 6.4.)  More than 24 alternatives take two warps, which have a
+  // thread for each (8192x1000 with 32 31.9 for 66, with 20 25.8 for 21.1).
   a.tpr = a.cl > 1 ? kLogprobThreads : 32;
-  while (a.tpr < kLogprobThreads && a.tpr * each < chunks) a.tpr *= 2;
+  const int least = TOP && a.top > kTopOneGroup && chunks > 32 ? 64 : 32;
+  while (a.tpr < kLogprobThreads && (a.tpr < least || a.tpr * 3 < chunks)) a.tpr *= 2;
+  while (a.cl == 1 && a.tpr > least && chunks <= 16 * (a.tpr / 2) &&
+         a.N * a.tpr > (int64_t)kLogprobPerSm * dev.sm_count * kLogprobThreads)
+    a.tpr /= 2;
   const int rows = kLogprobThreads / a.tpr;
   FirstLaunch first(kLogprobThreads, TOP ? top_bytes(rows) : 0, s, a.cl);
   const int64_t ctas = a.cl > 1 ? a.N * a.cl : (a.N + rows - 1) / rows;
