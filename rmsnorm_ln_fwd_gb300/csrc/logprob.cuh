@@ -22,11 +22,12 @@ namespace normk {
 
 // 256 threads a CTA (us, 4096x131072, 333x50001 and 16384x4096 bf16: 159, 13, 28;
 // 128 threads 198, 14.7, 83).  The kernel comes in three shapes of chunks that a
-// thread has in flight and CTAs an SM, by how many CTAs there are: 3 and 4 where they
-// fill the GPU, 4 and 3 (80 registers) where three an SM hold them all, 6 and 2 where
-// two do.  (us, as 3 and 4; 4 and 3; 6 and 2: 4096x131072 159; 169; 184, 333x50001
-// 12.8; 11.1; 16.3, 150x50001 in clusters of two 9.2; 7.0; 6.4, 2000x4096 7.2; 6.2; 5.3.
-// Four chunks and four CTAs, 64 registers, 159, 13.5; two 167, 12.5.)
+// thread has in flight and CTAs an SM, by how many CTAs there are: 6 and 2 where two
+// an SM hold them all, 4 and 3 (80 registers) where three take as many waves as four,
+// else 3 and 4.  (us, as 3 and 4; 4 and 3; 6 and 2: 4096x131072 159; 169; 184,
+// 640x131072 37.8; 34.2; 40, 333x50001 12.8; 11.1; 16.3, 150x50001 in clusters of two
+// 9.2; 7.0; 6.4, 2000x4096 7.2; 6.2; 5.3.  Four chunks and four CTAs, 64 registers, 159,
+// 13.5; two 167, 12.5.)
 constexpr int kLogprobThreads = 256;  // of a CTA
 constexpr int kLogprobPerSm = 4;      // CTAs
 constexpr int kLogprobMaxCluster = 8;
@@ -694,7 +695,11 @@ cudaError_t run_logprob(LogprobArgs a, const DeviceInfo& dev, cudaStream_t s) {
   const int rows = kLogprobThreads / a.tpr;
   FirstLaunch first(kLogprobThreads, TOP ? top_bytes(rows) : 0, s, a.cl);
   const int64_t ctas = a.cl > 1 ? a.N * a.cl : (a.N + rows - 1) / rows;
-  if (per_sm == 0) per_sm = ctas <= 2 * (int64_t)dev.sm_count ? 2 : ctas <= 3 * (int64_t)dev.sm_count ? 3 : kLogprobPerSm;
+  if (per_sm == 0) {
+    // the fewest waves, in the fewest CTAs an SM
+    auto waves = [&](int per) { return (ctas + per * (int64_t)dev.sm_count - 1) / (per * (int64_t)dev.sm_count); };
+    per_sm = waves(2) == 1 ? 2 : waves(3) == waves(kLogprobPerSm) ? 3 : kLogprobPerSm;
+  }
   return with_kernel(per_sm, [&](auto kern) { return first.launch((unsigned)ctas, true, kern, a); });
 }
 
