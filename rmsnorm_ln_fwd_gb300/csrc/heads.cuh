@@ -767,13 +767,17 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadPerSm) head_rotary_grad_ker
   }
   if (!a.want) return;
   __syncthreads();
-  // column by column, over warps and groups in a fixed order
+  // column by column, over groups and warps in a fixed order
   for (int i = threadIdx.x; i < 2 * lanes * 16; i += kHeadThreads) {
     const int k = i / (lanes * 16), l = i / 16 % lanes, e = i % 16;
     float sum = 0.f;
-    for (int w = 0; w < kHeadWarps; ++w)
-      for (int g = 0; g < groups; ++g)
-        sum += reinterpret_cast<const float*>(sums + (w * 2 + k) * 128 + e / 4 * 32 + g * lanes + l)[e % 4];
+    for (int g = 0; g < groups; ++g) {
+      float v[kHeadWarps];  // all in flight: 517 tokens of 9+3x96 8.6 -> 8.1 us
+#pragma unroll
+      for (int w = 0; w < kHeadWarps; ++w)
+        v[w] = reinterpret_cast<const float*>(sums + (w * 2 + k) * 128 + e / 4 * 32 + g * lanes + l)[e % 4];
+      sum += tree_sum<kHeadWarps>(v);
+    }
     const Lane that(l, a.D, a.R);
     const int col = e < 8 ? that.col_a(e) : that.col_b(e - 8);
     if (col >= 0) a.ws[((int64_t)blockIdx.x * 2 + k) * a.D + col] = sum;

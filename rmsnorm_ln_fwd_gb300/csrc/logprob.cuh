@@ -70,16 +70,21 @@ struct LogitChunk {
         ld_stream32(row + col, w);
       return;
     }
+    // A part of one: whole words (a chunk starts at 32 bytes) and a half at either end
+    // (by elements, us: 16384x602 bf16 16.6 for 13.7).
 #pragma unroll
-    for (int k = 0; k < 8; ++k) w[k] = kMasked;
-#pragma unroll
-    for (int e = 0; e < GE; ++e) {
-      if (col + e >= 0 && col + e < V) {
-        if constexpr (ES == 4) {
-          w[e] = Chunk<D, ES, 4>::ldg32(row + col + e);
-        } else {
-          const uint32_t v = Chunk<D, ES, 4>::ldg16(row + col + e);
-          w[e / 2] = e & 1 ? __byte_perm(w[e / 2], v, 0x5410) : __byte_perm(v, w[e / 2], 0x7610);
+    for (int k = 0; k < 8; ++k) {
+      w[k] = kMasked;
+      if constexpr (ES == 4) {
+        if ((unsigned)(col + k) < (unsigned)V) w[k] = Chunk<D, ES, 4>::ldg32(row + col + k);
+      } else {
+        const int c = col + 2 * k;
+        const bool lo = (unsigned)c < (unsigned)V, hi = (unsigned)(c + 1) < (unsigned)V;
+        if (lo && hi) {
+          w[k] = Chunk<D, ES, 4>::ldg32(row + c);
+        } else if (lo || hi) {
+          const uint32_t v = Chunk<D, ES, 4>::ldg16(row + c + (lo ? 0 : 1));
+          w[k] = lo ? __byte_perm(v, kMasked, 0x5410) : __byte_perm(kMasked, v, 0x5410);
         }
       }
     }

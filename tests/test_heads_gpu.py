@@ -12,8 +12,9 @@ Tolerances, from the arithmetic (U = 2^-24, half an fp32 step):
   the sum 16 U more, rstd^2 26 U, products 4 U, rstd again 13 U: KB = 64.
 * dgamma, a sum over rows: u x rstd has 18 U a term.  Units, one head of as many
   tokens as a warp has lane groups, are shared out evenly over the warps (2432 of
-  them, or one unit each): a lane adds at most rows/256 + 4.  Then the CTA adds up 8 warps of at most 32 groups, 256
-  in a row, and the partial rows 19 + 16 and 4 levels: 300 in all.
+  them, or one unit each): a lane adds at most rows/256 + 4.  Then the CTA adds up
+  8 warps of at most 32 groups, 256 in a row, and the partial rows 19 + 16 and 4
+  levels: 300 in all.
 * a value stored in fewer bits: half a step, on top.
 """
 
