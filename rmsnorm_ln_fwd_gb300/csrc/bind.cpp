@@ -480,17 +480,20 @@ bool rotation_of(const Opt& cos, const Opt& sin, const Opt& positions, bool inte
 }
 
 // Outputs shaped as q and k.  Small ones (a decode step's, where a call is host
-// time) share an allocation; large ones are kept or freed one by one.
+// time) share an allocation, with the gammas' gradients if there are any; large ones
+// are kept or freed one by one.
 bool small(const Tensor& q, const Tensor& k) {
   return (q.numel() + k.numel()) * (int64_t)q.element_size() <= (int64_t(1) << 20);
 }
-void new_pair(const Tensor& q, const Tensor& k, Tensor (&out)[2]) {
-  Parts parts;
-  const int64_t at_q = parts.add(q.numel(), q.scalar_type()), at_k = parts.add(k.numel(), k.scalar_type());
-  parts.allocate(q);
-  out[0] = parts.get(at_q, q.sizes(), q.scalar_type());
-  out[1] = parts.get(at_k, k.sizes(), k.scalar_type());
-}
+struct PairPlaces {
+  int64_t q, k;
+  PairPlaces(Parts& parts, const Tensor& tq, const Tensor& tk)
+      : q(parts.add(tq.numel(), tq.scalar_type())), k(parts.add(tk.numel(), tk.scalar_type())) {}
+  void get(const Parts& parts, const Tensor& tq, const Tensor& tk, Tensor (&out)[2]) const {
+    out[0] = parts.get(q, tq.sizes(), tq.scalar_type());
+    out[1] = parts.get(k, tk.sizes(), tk.scalar_type());
+  }
+};
 
 py::tuple head_rms_rotary_(const Tensor& q, const Opt& k, const Opt& gamma_q, const Opt& gamma_k, const Opt& cos,
                            const Opt& sin, const Opt& positions, double eps, bool interleaved, const Opt& q_out,
@@ -507,7 +510,12 @@ py::tuple head_rms_rotary_(const Tensor& q, const Opt& k, const Opt& gamma_q, co
   const bool turned = rotation_of(cos, sin, positions, interleaved, q, qh, &rot);
   const c10::cuda::CUDAGuard guard(q.device());
   Tensor fresh[2];
-  if (!q_out && k && !k_out && small(q, *k)) new_pair(q, *k, fresh);
+  if (!q_out && k && !k_out && small(q, *k)) {
+    Parts parts;
+    const PairPlaces at(parts, q, *k);
+    parts.allocate(q);
+    at.get(parts, q, *k, fresh);
+  }
   const Tensor qo = q_out ? *q_out : fresh[0].defined() ? fresh[0] : new_like(q);
   const HeadsOf qoh = q_out ? heads_like(qo, q, qh.H, "q_out") : heads_view(qo, "q_out");
   Tensor ko;
@@ -545,24 +553,26 @@ py::tuple head_rms_rotary_grad_(const Tensor& dyq, const Opt& dyk, const Tensor&
   norm_rotation rot;
   const bool turned = rotation_of(cos, sin, positions, interleaved, q, qh, &rot);
   const c10::cuda::CUDAGuard guard(q.device());
-  Tensor fresh[2];
-  if (!dq && k && !dk && small(q, *k)) new_pair(q, *k, fresh);
+  Tensor fresh[2], dgq, dgk, ws;
+  size_t wsb = 0;
+  Parts parts;
+  std::optional<PairPlaces> pair;
+  if (!dq && k && !dk && small(q, *k)) pair.emplace(parts, q, *k);
+  const int64_t at_q = need_param_grads ? parts.add(qh.D, wt) : 0, at_k = need_param_grads && k ? parts.add(qh.D, wt) : 0;
+  if (pair || need_param_grads) parts.allocate(q);
+  if (pair) pair->get(parts, q, *k, fresh);
+  if (need_param_grads) {
+    dgq = parts.get(at_q, {qh.D}, wt);
+    if (k) dgk = parts.get(at_k, {qh.D}, wt);
+    ws = workspace_of(workspace, head_rms_rotary_workspace_bytes(qh.D, q.get_device()), q, &wsb);
+  }
   const Tensor qo = dq ? *dq : fresh[0].defined() ? fresh[0] : new_like(q);
   const HeadsOf qoh = dq ? heads_like(qo, q, qh.H, "dq") : heads_view(qo, "dq");
-  Tensor ko, dgq, dgk, ws;
+  Tensor ko;
   HeadsOf koh;
   if (k) {
     ko = dk ? *dk : fresh[1].defined() ? fresh[1] : new_like(*k);
     koh = dk ? heads_like(ko, q, kh.H, "dk") : heads_view(ko, "dk");
-  }
-  size_t wsb = 0;
-  if (need_param_grads) {
-    Parts parts;
-    const int64_t at_q = parts.add(qh.D, wt), at_k = parts.add(k ? qh.D : 0, wt);
-    parts.allocate(q);
-    dgq = parts.get(at_q, {qh.D}, wt);
-    if (k) dgk = parts.get(at_k, {qh.D}, wt);
-    ws = workspace_of(workspace, head_rms_rotary_workspace_bytes(qh.D, q.get_device()), q, &wsb);
   }
   auto ptr = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
   check("head_rms_rotary_grad",
