@@ -230,7 +230,7 @@ struct __align__(16) TopShared {
   int listed, found;
   unsigned char list[kLogprobThreads];
 };
-// Followed by each warp's largest keys, one a lane.
+// Followed by each thread's largest key.
 __host__ __device__ constexpr int top_bytes(int rows) { return rows * (int)sizeof(TopShared) + 8 * kLogprobThreads; }
 
 // The first `top` keys of the chunks [first, last) into sh.best (0 where there
