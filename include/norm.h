@@ -427,7 +427,8 @@ typedef struct {
  * gamma_q, gamma_k [D] or NULL (ones).  rotation: NULL for the norm alone.
  * q_out, k_out: outputs of distinct elements.  Each may be exactly its input (in
  *   place); otherwise they are clear of the inputs and of each other.  Parts of
- *   one fused tensor count as clear where their columns are.
+ *   one fused tensor count as clear where their columns are: queries behind keys,
+ *   or a head's query and key side by side.
  * A token whose position is outside the table gives heads of zeros and raises
  * NORM_DEVICE_ERR_BAD_POSITION.
  */

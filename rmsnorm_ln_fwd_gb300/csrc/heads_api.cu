@@ -76,7 +76,9 @@ bool same(const Heads& a, const Heads& b) {
 // element: their ranges are apart, or they are parts of one period, as the queries
 // and keys of a fused projection are: both repeat at multiples of it, and the
 // columns that they take of it are apart.  The period is a token, or a batch (in
-// either order, whichever is inside the other).
+// either order, whichever is inside the other), or the least stride of all, where a
+// head's query and key are side by side.  Or both have the same strides, and within
+// the room of a token, whichever that is, their columns are apart.
 bool apart(const Heads& a, const Heads& b) {
   if (!overlap(a.span(), b.span())) return true;
   const intptr_t bytes = (intptr_t)(reinterpret_cast<uintptr_t>(b.v.p) - reinterpret_cast<uintptr_t>(a.v.p));
@@ -87,6 +89,13 @@ bool apart(const Heads& a, const Heads& b) {
     const int64_t r = ((delta % period) + period) % period;
     return wa <= period && r >= wa && r + wb <= period;
   };
+  const int64_t strides[] = {a.v.sh, a.v.st, a.v.sb, b.v.sh, b.v.st, b.v.sb};
+  int64_t least = INT64_MAX;
+  for (int64_t s : strides)
+    if (s > 0) least = std::min(least, s);
+  if (least < INT64_MAX && std::all_of(strides, strides + 6, [&](int64_t s) { return s % least == 0; }) &&
+      within(least, a.D, b.D))
+    return true;
   // inner and outer strides of the dims of more than one
   struct Outer {
     int64_t inner, n_inner, outer;  // outer: 0 with one such dim
@@ -99,8 +108,13 @@ bool apart(const Heads& a, const Heads& b) {
   const int64_t wa = (a.H - 1) * a.v.sh + a.D, wb = (b.H - 1) * b.v.sh + b.D;
   if (oa.inner > 0 && oa.inner == ob.inner && oa.outer % oa.inner == 0 && ob.outer % ob.inner == 0 && within(oa.inner, wa, wb))
     return true;
-  return oa.outer > 0 && oa.outer == ob.outer &&
-         within(oa.outer, (oa.n_inner - 1) * oa.inner + wa, (ob.n_inner - 1) * ob.inner + wb);
+  if (oa.outer > 0 && oa.outer == ob.outer &&
+      within(oa.outer, (oa.n_inner - 1) * oa.inner + wa, (ob.n_inner - 1) * ob.inner + wb))
+    return true;
+  // rooms from the first column of either to the last
+  const int64_t room = std::max(wa, delta + wb) - std::min<int64_t>(0, delta);
+  return a.v.sb == b.v.sb && a.v.st == b.v.st && (delta >= wa || -delta >= wb) && room <= oa.inner &&
+         (oa.outer == 0 || (oa.n_inner - 1) * oa.inner + room <= oa.outer);
 }
 
 size_t index_size(norm_itype t) { return t == NORM_I64 ? 8 : 4; }

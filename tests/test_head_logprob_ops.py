@@ -238,6 +238,70 @@ def test_rotary_grad_refusals(lib):
     assert _rgrad(lib, T=0, dgq=None, dgk=None) == OK
 
 
+def test_parts_of_heads_side_by_side(lib):
+    # (B, T, heads, 3, D): a head's query, key and value beside one another; ws=None shows that all else is accepted
+    f = dict(sb=3 * 4 * 192, st=4 * 192, sh=192)
+
+    def parts(p):
+        return _heads(p, **f), _heads(p + 2 * 64, **f)
+
+    def ask(**kw):
+        x, dy, dx = parts(M), parts(5 * M), parts(3 * M)
+        a = dict(q=x[0], k=x[1], dyq=dy[0], dyk=dy[1], dq=dx[0], dk=dx[1], ws=None)
+        return _rgrad(lib, **{**a, **kw})
+
+    assert ask() == WORKSPACE
+    dy = parts(5 * M)
+    assert ask(dq=dy[0], dk=dy[1]) == WORKSPACE  # in place
+    assert ask(dk=_heads(3 * M + 2 * 128, **f)) == WORKSPACE
+    assert ask(hk=1, dk=_heads(3 * M + 2 * 128, f["sb"], f["st"], 0)) == WORKSPACE  # one key head beside the first query's
+    # (B, T, 4 + 4 heads) with room behind each sequence that is no multiple of a token's
+    g = dict(sb=3 * 512 + 24, st=512, sh=64)
+    assert ask(dq=_heads(3 * M, **g), dk=_heads(3 * M + 2 * 256, **g)) == WORKSPACE
+    assert ask(dq=_heads(3 * M, **g), dk=_heads(3 * M + 2 * 255, **g)) == INVALID
+    for name, kw in dict(
+            early=dict(dk=_heads(3 * M + 2 * 63, **f)), late=dict(dk=_heads(3 * M + 2 * 129, **f)),
+            crossed=dict(dq=dy[1], dk=dy[0]), halfway=dict(dk=_heads(3 * M + 2 * 64 + 1, **f)),
+            other_period=dict(dk=_heads(3 * M + 2 * 64, f["sb"], f["st"], 128)),
+            other_tokens=dict(dk=_heads(3 * M + 2 * 64, f["sb"] + 64, f["st"], 192))).items():
+        assert ask(**kw) == INVALID, name
+
+
+def test_parts_are_taken_only_where_no_element_is_shared(lib):
+    """Gradients of queries and keys in one buffer, in random layouts, against the elements that they have; ws=None shows that
+    all else is accepted."""
+    r = np.random.default_rng(5)
+    taken = 0
+    for _ in range(20000):
+        B, T, hq, hk, D = (int(v) for v in (*r.integers(1, 4, 2), *r.integers(1, 4, 2), r.choice([1, 2, 4])))
+
+        def layout(heads):
+            sizes = {"sb": B, "st": T, "sh": heads}
+            at, out = int(r.choice([D, D, 2 * D, 3 * D, D + 1])), {}
+            for name in r.permutation(["sb", "st", "sh"]):
+                out[name] = at
+                at = at * sizes[name] + int(r.choice([0, 0, 0, D, 1]))
+            return out
+
+        fq = layout(max(hq, hk) if r.random() < 0.5 else hq + hk)
+        fk = fq if r.random() < 0.7 else layout(hk)
+        off = int(r.integers(0, 1 + max(fq.values())) if r.random() < 0.3 else r.integers(0, 8) * D)
+
+        def elements(f, heads, at):
+            i = np.indices((B, T, heads, D)).reshape(4, -1)
+            return set((i[0] * f["sb"] + i[1] * f["st"] + i[2] * f["sh"] + i[3] + at).tolist())
+
+        eq, ek = elements(fq, hq, 0), elements(fk, hk, off)
+        if len(eq) < B * T * hq * D or len(ek) < B * T * hk * D:
+            continue
+        got = _rgrad(lib, hq=hq, hk=hk, B=B, T=T, D=D, rot=None, xd=F32, wd=F32, ws=None, dq=_heads(3 * M, **fq),
+                     dk=_heads(3 * M + 4 * off, **fk))
+        assert got in (INVALID, WORKSPACE)
+        assert got == INVALID or not eq & ek, (B, T, hq, hk, D, fq, fk, off)
+        taken += got == WORKSPACE
+    assert taken > 3000
+
+
 def _lp(lib, **kw):
     a = dict(z=M, ld=64, tok=2 * M, it=I64, scale=1.0, ignore=-100, lp=3 * M, ent=4 * M, lse=5 * M, st=6 * M, tlp=7 * M,
              tid=8 * M, top=5, N=4, V=64, dt=BF16)

@@ -235,6 +235,31 @@ def test_in_place_on_a_fused_projection(order):
         call(c, q_out=q, k_out=base[:, :, hq - 1:hq - 1 + hk])
 
 
+@pytest.mark.parametrize("D,R,dt", [(64, 64, "bf16"), (80, 20, "f16"), (48, 0, "f32")])
+def test_in_place_where_a_heads_query_key_and_value_are_side_by_side(D, R, dt):
+    """(B, T, heads, 3, D), forward in place, and the gradients as parts of such a tensor."""
+    B, T, H = 2, 13, 5
+    base, grads = (rnd((B, T, H, 3, D), s, DT[dt]) for s in (50, 51))
+    q, k, v = (base[:, :, :, i] for i in range(3))
+    c = dict(q=q, k=k, gq=rnd((D,), 52, DT[dt], 1.0, 0.2), gk=rnd((D,), 53, DT[dt], 1.0, 0.2), cos=None, sin=None, pos=None,
+             dyq=grads[:, :, :, 0], dyk=grads[:, :, :, 1])
+    if R:
+        c["cos"], c["sin"] = tables(64, R)
+    want, dwant, v, dv = call(c), call_grad(c), v.clone(), grads[:, :, :, 2].clone()
+    check(c, want, 1e-5, False)
+    into = torch.full_like(base, 3.0)
+    got = call_grad(c, dq=into[:, :, :, 0], dk=into[:, :, :, 1])
+    for a, b in zip(got, dwant):
+        assert torch.equal(a, b)
+    assert bool((into[:, :, :, 2] == 3.0).all())
+    call_grad(c, dq=c["dyq"], dk=c["dyk"])
+    assert torch.equal(c["dyq"], dwant[0]) and torch.equal(c["dyk"], dwant[1]) and torch.equal(grads[:, :, :, 2], dv)
+    call(c, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(base[:, :, :, 2], v)
+    with pytest.raises(nl.NormError):  # a query's last column
+        call(c, q_out=q, k_out=base.view(B, T, H, 3 * D)[..., D - 1:2 * D - 1])
+
+
 def test_outputs_in_other_layouts_and_margins():
     c = make(2, 11, 4, 2, 64, 32, "bf16", layout="fused", seed=5)
     want = call(c)
