@@ -60,11 +60,11 @@ struct Rows {
   int64_t N = 0, H = 0, ld = 0;
 };
 
-// The rows of a tensor on any device.
-Rows row_view(const Tensor& t, const char* what) {
+// The rows of a tensor on any device; returns whether one row stride reaches them all.
+bool row_layout(const Tensor& t, const char* what, Rows* out) {
   const int64_t d = t.dim();
   if (d < 1) value_error(std::string(what) + " must have at least one dim");
-  Rows r;
+  Rows& r = *out;
   r.p = t.data_ptr();
   r.H = t.size(d - 1);
   if (r.H > 1 && t.stride(d - 1) != 1) value_error(std::string(what) + ": the last dim must be contiguous");
@@ -87,19 +87,28 @@ Rows row_view(const Tensor& t, const char* what) {
     }
     reach *= n;
   }
-  if (r.N > 1 && !flat) value_error(std::string(what) + ": leading dims do not flatten to one row stride");
   r.ld = r.N > 1 ? ld : std::max<int64_t>(r.H, 1);
+  return r.N <= 1 || flat;
+}
+
+Rows row_view(const Tensor& t, const char* what) {
+  Rows r;
+  if (!row_layout(t, what, &r)) value_error(std::string(what) + ": leading dims do not flatten to one row stride");
   return r;
 }
 
 Rows rows(const Tensor& t, const char* what) { return row_view(cuda_tensor(t, what), what); }
 
-// A tensor that matches the rows of `ref`.
-Rows like(const Tensor& t, const Tensor& ref, const Rows& of, const char* what) {
-  const Rows r = rows(t, what);
+void same_rows(const Tensor& t, const Rows& r, const Tensor& ref, const Rows& of, const char* what) {
   if (r.N != of.N || r.H != of.H || t.scalar_type() != ref.scalar_type() || t.device() != ref.device())
     value_error(std::string(what) + " must match the rows, width, dtype (" + name_of(ref.scalar_type()) + ") and device (" +
                 ref.device().str() + ") of the input");
+}
+
+// A tensor that matches the rows of `ref`.
+Rows like(const Tensor& t, const Tensor& ref, const Rows& of, const char* what) {
+  const Rows r = rows(t, what);
+  same_rows(t, r, ref, of, what);
   return r;
 }
 
@@ -303,11 +312,11 @@ py::tuple sandwich_rms_grad_(const Opt& dy, const Tensor& x, const Opt& h, const
   return py::make_tuple(obj(odx), obj(odr), obj(dgpost), obj(dgate), obj(dgpre));
 }
 
-norm_itype tokens_of(const Tensor& tokens, const Tensor& ref) {
+norm_itype tokens_of(const Tensor& tokens, const Tensor& ref, bool contiguous = true) {
   cuda_tensor(tokens, "tokens");
   const at::ScalarType t = tokens.scalar_type();
   if (t != at::kInt && t != at::kLong) type_error("tokens: dtype " + name_of(t) + " not supported (int32 or int64)");
-  if (!tokens.is_contiguous()) value_error("tokens must be contiguous");
+  if (contiguous && !tokens.is_contiguous()) value_error("tokens must be contiguous");
   if (tokens.device() != ref.device())
     value_error("tokens are on " + tokens.device().str() + ", the rows on " + ref.device().str());
   return t == at::kLong ? NORM_I64 : NORM_I32;
@@ -586,21 +595,124 @@ py::tuple head_rms_rotary_grad_(const Tensor& dyq, const Opt& dyk, const Tensor&
 
 constexpr int64_t kNoToken = INT64_MIN;
 
-// The token of each row, of the leading dims' number.
-const void* row_tokens(const Opt& tokens, const Tensor& logits, int64_t N, norm_itype* type) {
-  if (!tokens) return nullptr;
-  *type = tokens_of(*tokens, logits);
-  if (tokens->numel() != N)
-    value_error(std::to_string(N) + " rows of logits, but " + std::to_string(tokens->numel()) + " tokens");
-  return tokens->data_ptr();
+// The dims [result, n) of a tensor that one stride reaches; that stride, or `stride` where it is given.
+int64_t flat_from(const Tensor& t, int64_t n, int64_t stride) {
+  bool seen = stride != 0;
+  int64_t reach = stride;
+  for (int64_t i = n - 1; i >= 0; --i) {
+    if (t.size(i) == 1) continue;
+    if (seen && t.stride(i) != reach) return i + 1;
+    reach = t.size(i) * (seen ? reach : t.stride(i));
+    seen = true;
+  }
+  return 0;
+}
+
+// Rows of logits with their tokens and their gradient as runs that one row stride
+// each reaches and whose tokens are neighbours: one run where the leading dims allow
+// it, else, as for logits[:, :-1] with tokens[:, 1:], one for each index of the outer
+// dims, each a call of the library.
+struct Runs {
+  int64_t N = 0, ld = 0, ldo = 0;  // of a run
+  int64_t token_size = 8;
+  struct At {
+    int64_t z, tok, out;  // elements from each tensor's first
+  };
+  c10::SmallVector<At, 1> at;
+};
+
+Runs runs_of(const Tensor& logits, const Opt& tokens, const Opt& out) {
+  Runs r;
+  Rows z, o;
+  bool flat = row_layout(logits, "logits", &z);
+  if (out) flat &= row_layout(*out, "out", &o);
+  if (tokens) {
+    r.token_size = tokens->element_size();
+    if (tokens->numel() != z.N)
+      value_error(std::to_string(z.N) + " rows of logits, but " + std::to_string(tokens->numel()) + " tokens");
+  }
+  const bool strided = tokens && !tokens->is_contiguous();
+  if (flat && !strided) {
+    r.N = z.N;
+    r.ld = z.ld;
+    r.ldo = o.ld;
+    r.at.push_back({0, 0, 0});
+    return r;
+  }
+  if (out && out->sizes() != logits.sizes()) value_error("out must have the logits' dims");
+  const int64_t lead = logits.dim() - 1;
+  const at::IntArrayRef dims = logits.sizes().slice(0, lead);
+  int64_t from = flat_from(logits, lead, 0);
+  if (out) from = std::max(from, flat_from(*out, lead, 0));
+  if (strided) {
+    if (tokens->sizes() != dims) value_error("tokens must be contiguous or of the logits' leading dims");
+    from = std::max(from, flat_from(*tokens, lead, 1));
+  }
+  int64_t runs = 1, inner = 0;  // the innermost dim of several rows in a run
+  r.N = 1;
+  for (int64_t i = 0; i < lead; ++i) {
+    (i < from ? runs : r.N) *= dims[i];
+    if (i >= from && dims[i] > 1) inner = i;
+  }
+  // (a run of one row: tokens that are not neighbours at all)
+  if (r.N == 1 && strided) value_error("tokens must be contiguous along the last of the rows' dims");
+  r.ld = r.N > 1 ? logits.stride(inner) : std::max<int64_t>(z.H, 1);
+  if (out) r.ldo = r.N > 1 ? out->stride(inner) : std::max<int64_t>(z.H, 1);
+  for (int64_t k = 0; k < runs; ++k) {
+    Runs::At a{0, strided ? 0 : k * r.N, 0};
+    for (int64_t i = from - 1, left = k; i >= 0; left /= dims[i], --i) {
+      const int64_t at = left % dims[i];
+      a.z += at * logits.stride(i);
+      if (strided) a.tok += at * tokens->stride(i);
+      if (out) a.out += at * out->stride(i);
+    }
+    r.at.push_back(a);
+  }
+  return r;
+}
+
+void* bytes_on(const void* p, int64_t bytes) { return p ? (char*)p + bytes : nullptr; }
+
+// Where a gradient of several runs is written: the rows are distinct, and either the
+// logits themselves or clear of them and of the other inputs.  (The library sees one
+// run at a time.)
+bool out_is_clear(const Tensor& out, const Tensor& logits, std::initializer_list<const Opt*> others) {
+  struct Range {
+    uintptr_t lo, hi;
+  };
+  auto range = [](const Tensor& t) {
+    int64_t last = 0;
+    for (int64_t i = 0; i < t.dim(); ++i) last += (t.size(i) - 1) * t.stride(i);
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(t.data_ptr());
+    return Range{lo, lo + (uintptr_t)(last + 1) * t.element_size()};
+  };
+  const Range o = range(out);
+  auto meets = [&](const Tensor& t) {
+    const Range r = range(t);
+    return o.lo < r.hi && r.lo < o.hi;
+  };
+  std::vector<std::pair<int64_t, int64_t>> dims;
+  for (int64_t i = 0; i < out.dim(); ++i)
+    if (out.size(i) > 1) dims.emplace_back(out.stride(i), out.size(i));
+  std::sort(dims.begin(), dims.end());
+  int64_t reach = 1;
+  for (const auto& [stride, n] : dims) {
+    if (stride < reach) return false;
+    reach += (n - 1) * stride;
+  }
+  if (meets(logits) && !(out.data_ptr() == logits.data_ptr() && out.strides() == logits.strides())) return false;
+  for (const Opt* t : others)
+    if (*t && meets(**t)) return false;
+  return true;
 }
 
 py::tuple token_logprobs_(const Tensor& logits, const Opt& tokens, double scale, int64_t top, std::optional<int64_t> ignore,
                           bool entropy) {
-  const Rows zr = rows(logits, "logits");
+  Rows zr;
+  row_layout(cuda_tensor(logits, "logits"), "logits", &zr);
   const norm_dtype xc = code(logits.scalar_type(), "logits");
-  norm_itype it = NORM_I64;
-  const void* tp = row_tokens(tokens, logits, zr.N, &it);
+  const norm_itype it = tokens ? tokens_of(*tokens, logits, false) : NORM_I64;
+  const Runs runs = runs_of(logits, tokens, std::nullopt);
   if (top < 0 || top > NORM_MAX_TOP)
     value_error("top must be 0 to " + std::to_string(NORM_MAX_TOP) + ", not " + std::to_string(top));
   const c10::cuda::CUDAGuard guard(logits.device());
@@ -622,19 +734,28 @@ py::tuple token_logprobs_(const Tensor& logits, const Opt& tokens, double scale,
     tid = parts.get(a_tid, more, at::kLong);
   }
   auto ptr = [](const Tensor& t) { return t.defined() ? t.data_ptr<float>() : nullptr; };
-  check("token_logprobs", token_logprobs(zr.p, zr.ld, tp, it, (float)scale, ignore.value_or(kNoToken), ptr(lp), ptr(en),
-                                         ptr(lse), ptr(st), ptr(tlp), top ? tid.data_ptr<int64_t>() : nullptr, top, zr.N,
-                                         zr.H, xc, stream_of(logits)));
+  float* const p[] = {ptr(lp), ptr(en), ptr(lse), ptr(st), ptr(tlp)};
+  int64_t* const ids = top ? tid.data_ptr<int64_t>() : nullptr;
+  const void* const tp = tokens ? tokens->data_ptr() : nullptr;
+  int64_t row = 0;
+  for (const Runs::At& at : runs.at) {
+    auto on = [&](float* q, int64_t n) { return q ? q + row * n : nullptr; };
+    check("token_logprobs",
+          token_logprobs(bytes_on(zr.p, at.z * logits.element_size()), runs.ld, bytes_on(tp, at.tok * runs.token_size), it,
+                         (float)scale, ignore.value_or(kNoToken), on(p[0], 1), on(p[1], 1), on(p[2], 1), on(p[3], 2),
+                         on(p[4], top), ids ? ids + row * top : nullptr, top, runs.N, zr.H, xc, stream_of(logits)));
+    row += runs.N;
+  }
   return py::make_tuple(obj(lp), obj(en), obj(lse), obj(st), obj(tlp), obj(tid));
 }
 
 py::object token_logprobs_grad_(const Opt& dlogprob, const Tensor& logits, const Opt& tokens, const Tensor& row_stats,
                                 const Opt& entropy, const Opt& dentropy, const Opt& dlse, double scale,
                                 std::optional<int64_t> ignore, const Opt& out) {
-  const Rows zr = rows(logits, "logits");
+  Rows zr;
+  row_layout(cuda_tensor(logits, "logits"), "logits", &zr);
   const norm_dtype xc = code(logits.scalar_type(), "logits");
-  norm_itype it = NORM_I64;
-  const void* tp = row_tokens(tokens, logits, zr.N, &it);
+  const norm_itype it = tokens ? tokens_of(*tokens, logits, false) : NORM_I64;
   if (dlogprob && !tokens) value_error("dlogprob needs tokens");
   if (dentropy && !entropy) value_error("dentropy needs entropy");
   if (!dlogprob && !dentropy && !dlse) value_error("dlogprob, dentropy and dlse are all None: no gradient arrives");
@@ -645,10 +766,26 @@ py::object token_logprobs_grad_(const Opt& dlogprob, const Tensor& logits, const
   const float* st = stats(Opt(row_stats), 2 * zr.N, "stats", logits);
   const c10::cuda::CUDAGuard guard(logits.device());
   const Tensor dz = out ? *out : new_like(logits);
-  const Rows dr = out ? like(dz, logits, zr, "out") : Rows{dz.data_ptr(), zr.N, zr.H, std::max<int64_t>(zr.H, 1)};
-  check("token_logprobs_grad",
-        token_logprobs_grad(dlp, zr.p, zr.ld, tp, it, st, en, den, dl, (float)scale, ignore.value_or(kNoToken), dr.p, dr.ld,
-                            zr.N, zr.H, xc, stream_of(logits)));
+  if (out) {
+    Rows o;
+    row_layout(cuda_tensor(dz, "out"), "out", &o);
+    same_rows(dz, o, logits, zr, "out");
+  }
+  const Runs runs = runs_of(logits, tokens, dz);
+  const Opt all_stats(row_stats);
+  if (runs.at.size() > 1 && !out_is_clear(dz, logits, {&tokens, &dlogprob, &all_stats, &entropy, &dentropy, &dlse}))
+    check("token_logprobs_grad", NORM_ERR_INVALID_VALUE);
+  const void* const tp = tokens ? tokens->data_ptr() : nullptr;
+  int64_t row = 0;
+  for (const Runs::At& at : runs.at) {
+    auto on = [&](const float* q, int64_t n) { return q ? q + row * n : nullptr; };
+    check("token_logprobs_grad",
+          token_logprobs_grad(on(dlp, 1), bytes_on(zr.p, at.z * logits.element_size()), runs.ld,
+                              bytes_on(tp, at.tok * runs.token_size), it, on(st, 2), on(en, 1), on(den, 1), on(dl, 1),
+                              (float)scale, ignore.value_or(kNoToken), bytes_on(dz.data_ptr(), at.out * dz.element_size()),
+                              runs.ldo, runs.N, zr.H, xc, stream_of(logits)));
+    row += runs.N;
+  }
   return obj(dz);
 }
 
@@ -674,6 +811,12 @@ PYBIND11_MODULE(_bind, m) {
   });
   m.def("head_rms_rotary", &head_rms_rotary_);
   m.def("head_rms_rotary_grad", &head_rms_rotary_grad_);
+  m.def("token_runs", [](const Tensor& logits, const Opt& tokens, const Opt& out) {  // of tensors on any device, for tests
+    const Runs r = runs_of(logits, tokens, out);
+    py::list at;
+    for (const Runs::At& a : r.at) at.append(py::make_tuple(a.z, a.tok, a.out));
+    return py::make_tuple(r.N, r.ld, at);
+  });
   m.def("token_logprobs", &token_logprobs_);
   m.def("token_logprobs_grad", &token_logprobs_grad_);
 }

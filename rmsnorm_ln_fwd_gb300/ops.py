@@ -429,7 +429,10 @@ def token_logprobs(logits, tokens=None, scale: float = 1.0, *, top: int = 0, ign
     """Log probabilities of ``tokens`` under softmax(scale * logits), one a row,
     with the rows' entropy and their ``top`` most probable tokens.
 
-    ``tokens`` are int32 or int64 of the leading dims' shape (or None).  A row
+    ``tokens`` are int32 or int64 of the leading dims' shape (or None), neighbours
+    along the last of these.  Rows that one stride reaches, with contiguous tokens,
+    are one launch; parts of sequences, as ``logits[:, :-1]`` with
+    ``tokens[:, 1:]``, are one for each sequence.  A row
     whose token is ``ignore_index`` has log probability 0; so has one whose token
     is outside the vocabulary, which sets NORM_DEVICE_ERR_BAD_TOKEN.  Returns
     (logprob, entropy, lse, stats, top_logprobs, top_ids): lse is the log of the
@@ -445,7 +448,9 @@ def token_logprobs_grad(dlogprob, logits, tokens, stats, entropy=None, dentropy=
     """Gradient of the logits from those of token_logprobs' log probabilities,
     entropies and lse (float32, one a row, contiguous; None for zeros).
 
-    ``stats`` and, with ``dentropy``, ``entropy`` are the forward's.  ``out`` may be
-    ``logits`` itself.  The alternatives have no gradient."""
+    ``stats`` and, with ``dentropy``, ``entropy`` are the forward's; logits and
+    tokens as there.  ``out`` may be ``logits`` itself, or a tensor clear of it and
+    of the other inputs; a fresh one is contiguous.  The alternatives have no
+    gradient."""
     return _lib.bind().token_logprobs_grad(dlogprob, logits, tokens, stats, entropy, dentropy, dlse, scale, ignore_index,
                                            out)

@@ -357,6 +357,30 @@ def test_heads_view_of_strided_tensors(lib):
             view(bad)
 
 
+def test_runs_of_rows_and_their_tokens(lib):
+    """Rows that no single stride reaches, and tokens of a slice, as runs (first row, first token), rows a run and row stride."""
+    runs = _lib.bind().token_runs
+    z, t = torch.empty(3, 5, 7), torch.arange(15).view(3, 5)
+    assert runs(z, None, None) == (15, 7, [(0, 0, 0)])
+    assert runs(z, t, None) == (15, 7, [(0, 0, 0)])
+    assert runs(z[:, :-1], t[:, 1:], None) == (4, 7, [(0, 0, 0), (35, 5, 0), (70, 10, 0)])  # tokens from their own first one
+    assert runs(z[:, :-1], t[:, 1:].reshape(-1), None) == (4, 7, [(0, 0, 0), (35, 4, 0), (70, 8, 0)])
+    assert runs(z[:, :-1], t[:, 1:].contiguous(), None) == (4, 7, [(0, 0, 0), (35, 4, 0), (70, 8, 0)])
+    assert runs(z[:, :4].contiguous(), t[:, 1:], None) == (4, 7, [(0, 0, 0), (28, 5, 0), (56, 10, 0)])
+    assert runs(z[:, :1], t[:, :1].contiguous(), None) == (3, 35, [(0, 0, 0)])
+    assert runs(z.transpose(0, 1), t.t().contiguous(), None) == (3, 35, [(7 * i, 3 * i, 0) for i in range(5)])
+    assert runs(z, t, torch.empty(3, 9, 8)[:, 2:7, 1:]) == (5, 7, [(0, 0, 0), (35, 5, 72), (70, 10, 144)])
+    w = torch.empty(2, 3, 5, 7)
+    assert runs(w[:, :, 1:], None, None) == (4, 7, [(35 * i, 4 * i, 0) for i in range(6)])
+    assert runs(w[:, :2], None, None) == (10, 7, [(0, 0, 0), (105, 10, 0)])
+    assert runs(w[:, :0], torch.empty(2, 0, 5, dtype=torch.long), None)[0] == 0
+    assert runs(z[0, 0], t[0, 0], None) == (1, 7, [(0, 0, 0)])
+    assert runs(z[:1].expand(3, 5, 7), t, None) == (5, 7, [(0, 0, 0), (0, 5, 0), (0, 10, 0)])
+    for tokens in (t.t(), t[:, ::2], t[:2, 1:]):  # of other dims than the rows', or no neighbours
+        with pytest.raises(ValueError):
+            runs(z, tokens, None)
+
+
 def test_host_tensors_are_refused(lib):
     x, c = torch.zeros(3, 2, 8), torch.zeros(4, 4)
     with pytest.raises(ValueError, match="CUDA"):

@@ -209,6 +209,86 @@ def test_leading_dims_and_strides():
         assert torch.equal(mine[keep], whole[keep])
 
 
+def sequences(B, T, V, dt, seed):
+    z = rnd((B, T, V), seed, DT[dt], std=2.0)
+    return z, torch.tensor(np.random.default_rng(seed).integers(0, V, (B, T)), device=DEV)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("B,T,V", [(3, 9, 1001), (2, 2, 40000), (5, 33, 64)])
+def test_each_tokens_logits_with_the_next_token(B, T, V, dt):
+    """logits[:, :-1] and tokens[:, 1:], which no one stride reaches: the log probabilities, and the gradient into a fresh
+    tensor, into a part of another and in place."""
+    whole, tokens = sequences(B, T, V, dt, 40)
+    tokens[0, 1], tokens[-1, -1] = -100, -100
+    z, t = whole[:, :-1], tokens[:, 1:]
+    n = B * (T - 1)
+    d = [g.view(B, T - 1) for g in grads_in(n, 41)]
+    out = nl.token_logprobs(z, t, 0.9, top=5, ignore_index=-100)
+    assert out[0].shape == (B, T - 1) and out[3].shape == (B, T - 1, 2) and out[5].shape == (B, T - 1, 5)
+    check(z, t, 0.9, out, 5, -100)
+    check(z, t, 0.9, nl.token_logprobs(z, t.int().contiguous(), 0.9, ignore_index=-100), 0, -100)
+    check(z.contiguous(), t, 0.9, nl.token_logprobs(z.contiguous(), t, 0.9, ignore_index=-100), 0, -100)
+    check(z, None, 0.9, nl.token_logprobs(z, None, 0.9, entropy=False), 0, None, False)
+    args = (z, t, out[3], out[1], d[1], d[2], 0.9)
+    fresh = nl.token_logprobs_grad(d[0], *args, ignore_index=-100)
+    assert fresh.is_contiguous() and fresh.shape == z.shape
+    check_grad(z, t, 0.9, fresh, out[3], out[1], *d, -100)
+    base = torch.full((B, T + 1, V + 3), 5.0, device=DEV, dtype=DT[dt])
+    into = base[:, 1:-1, 2:-1]
+    nl.token_logprobs_grad(d[0], *args, ignore_index=-100, out=into)
+    assert torch.equal(into, fresh)
+    into.fill_(5.0)
+    assert bool((base == 5.0).all())
+    last = whole[:, -1].clone()
+    nl.token_logprobs_grad(d[0], *args, ignore_index=-100, out=z)
+    assert torch.equal(z, fresh) and torch.equal(whole[:, -1], last)
+
+
+def test_rows_of_other_orders_and_shared_ones():
+    whole, tokens = sequences(4, 6, 777, "bf16", 42)
+    for z, t in ((whole.transpose(0, 1), tokens.t().contiguous()), (whole[::2, 1:4], tokens[::2, 1:4]),
+                 (whole[:1].expand(4, 6, 777), tokens), (whole.view(2, 2, 6, 777)[:, :, ::3], tokens.view(2, 2, 6)[:, :, ::3].contiguous())):
+        out = nl.token_logprobs(z, t, top=3)
+        check(z, t, 1.0, out, 3)
+        d = [g.view(t.shape) for g in grads_in(t.numel(), 43)]
+        got = nl.token_logprobs_grad(d[0], z, t, out[3], out[1], d[1], d[2])
+        check_grad(z, t, 1.0, got, out[3], out[1], *d)
+
+
+def test_runs_of_rows_bad_tokens_and_refusals():
+    whole, tokens = sequences(3, 5, 300, "f32", 44)
+    z, t = whole[:, :-1], tokens[:, 1:]
+    t[2, 1] = 300
+    _lib.device_errors()
+    out = nl.token_logprobs(z, t)
+    torch.cuda.synchronize()
+    assert _lib.device_errors() == _lib.NORM_DEVICE_ERR_BAD_TOKEN and out[0][2, 1] == 0
+    check(z, t, 1.0, out)
+    one = torch.ones(3, 4, device=DEV)
+    before, stats = whole.clone(), out[3]
+
+    def bad(err, z, t, out, stats=stats, n=3):
+        with pytest.raises(err):
+            nl.token_logprobs_grad(one[:n], z, t[:n], stats[:n], out=out)
+        assert torch.equal(whole, before)
+
+    bad(nl.NormError, whole[:-1, :-1], t, whole[1:, :-1], n=2)          # the next sequence's logits
+    bad(nl.NormError, whole[:1, :-1].expand(3, 4, 300), t, whole[:1, :-1].expand(3, 4, 300))
+    bad(nl.NormError, z, t, torch.empty(1, 4, 300, device=DEV).expand(3, 4, 300))
+    bad(nl.NormError, z, t, whole[:, 1:])
+    bad(nl.NormError, z, t, torch.empty(9000, device=DEV).as_strided((3, 4, 300), (600, 300, 1)))
+    bad(ValueError, z, t, torch.empty(3, 4, 299, device=DEV))
+    bad(ValueError, z, tokens[:, ::2], None)
+    room = torch.zeros(3, 5, 300, device=DEV)                           # statistics inside the gradient's second sequence
+    room[1, 0, :24] = stats.flatten()
+    bad(nl.NormError, z, t, room[:, :-1], room[1, 0, :24].view(3, 4, 2))
+    with pytest.raises(ValueError):
+        nl.token_logprobs(z, t[:, :3])
+    with pytest.raises(ValueError):
+        nl.token_logprobs(z, tokens.t()[1:])
+
+
 @pytest.mark.parametrize("dt", list(DT))
 @pytest.mark.parametrize("V", [40, 5000, 70001])
 def test_masked_rows(V, dt):
