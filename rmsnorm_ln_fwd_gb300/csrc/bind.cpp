@@ -189,7 +189,10 @@ Tensor new_like(const Tensor& x) { return at::empty(x.sizes(), x.options().requi
 Tensor new_vec(int64_t n, const Tensor& ref, at::ScalarType t) { return at::empty({n}, ref.options().dtype(t).requires_grad(false)); }
 
 // Small outputs of one call as parts of one allocation (which costs 1.2 us of host
-// time, a part 0.2): first the sizes, then the tensors.
+// time, a part 0.2): first the sizes, then the tensors.  Who keeps one keeps them all,
+// so that larger ones are allocated one by one.
+constexpr int64_t kSharedBytes = int64_t(1) << 20;
+
 class Parts {
  public:
   // Reserve a tensor of `n` elements; returns its place.
@@ -198,6 +201,7 @@ class Parts {
     bytes_ += (n * (int64_t)c10::elementSize(t) + 255) / 256 * 256;
     return at;
   }
+  int64_t bytes() const { return bytes_; }
   void allocate(const Tensor& ref) {
     base_ = at::empty({std::max<int64_t>(bytes_, 1)}, ref.options().dtype(at::kByte).requires_grad(false));
   }
@@ -492,7 +496,7 @@ bool rotation_of(const Opt& cos, const Opt& sin, const Opt& positions, bool inte
 // time) share an allocation, with the gammas' gradients if there are any; large ones
 // are kept or freed one by one.
 bool small(const Tensor& q, const Tensor& k) {
-  return (q.numel() + k.numel()) * (int64_t)q.element_size() <= (int64_t(1) << 20);
+  return (q.numel() + k.numel()) * (int64_t)q.element_size() <= kSharedBytes;
 }
 struct PairPlaces {
   int64_t q, k;
@@ -723,15 +727,19 @@ py::tuple token_logprobs_(const Tensor& logits, const Opt& tokens, double scale,
   const int64_t a_st = parts.add(2 * zr.N, at::kFloat), a_lse = parts.add(zr.N, at::kFloat);
   const int64_t a_lp = tokens ? parts.add(zr.N, at::kFloat) : 0, a_en = entropy ? parts.add(zr.N, at::kFloat) : 0;
   const int64_t a_tlp = parts.add(zr.N * top, at::kFloat), a_tid = parts.add(zr.N * top, at::kLong);
-  parts.allocate(logits);
+  const bool shared = parts.bytes() <= kSharedBytes;
+  if (shared) parts.allocate(logits);
+  auto output = [&](int64_t place, at::IntArrayRef sizes, at::ScalarType t) {
+    return shared ? parts.get(place, sizes, t) : at::empty(sizes, logits.options().dtype(t).requires_grad(false));
+  };
   Tensor lp, en, tlp, tid;
-  const Tensor lse = parts.get(a_lse, lead, at::kFloat), st = parts.get(a_st, more, at::kFloat);
-  if (tokens) lp = parts.get(a_lp, lead, at::kFloat);
-  if (entropy) en = parts.get(a_en, lead, at::kFloat);
+  const Tensor lse = output(a_lse, lead, at::kFloat), st = output(a_st, more, at::kFloat);
+  if (tokens) lp = output(a_lp, lead, at::kFloat);
+  if (entropy) en = output(a_en, lead, at::kFloat);
   if (top) {
     more.back() = top;
-    tlp = parts.get(a_tlp, more, at::kFloat);
-    tid = parts.get(a_tid, more, at::kLong);
+    tlp = output(a_tlp, more, at::kFloat);
+    tid = output(a_tid, more, at::kLong);
   }
   auto ptr = [](const Tensor& t) { return t.defined() ? t.data_ptr<float>() : nullptr; };
   float* const p[] = {ptr(lp), ptr(en), ptr(lse), ptr(st), ptr(tlp)};

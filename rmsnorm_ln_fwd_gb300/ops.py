@@ -406,8 +406,8 @@ def head_rms_rotary(q, k=None, gamma_q=None, gamma_k=None, cos=None, sin=None, p
     ``positions`` are int32 or int64, (T,) or (B, T); None: 0, 1, ... in each
     sequence.  A position outside the table gives zeros and sets
     NORM_DEVICE_ERR_BAD_POSITION in the device error word.  ``q_out`` and ``k_out``
-    may be fresh (default, contiguous), ``q`` and ``k`` themselves, or any clear
-    tensor.  Returns (q_out, k_out)."""
+    may be fresh (default, contiguous; of up to 1 MB together in one allocation),
+    ``q`` and ``k`` themselves, or any clear tensor.  Returns (q_out, k_out)."""
     return _lib.bind().head_rms_rotary(q, k, gamma_q, gamma_k, cos, sin, positions, eps, interleaved, q_out, k_out)
 
 
@@ -439,7 +439,8 @@ def token_logprobs(logits, tokens=None, scale: float = 1.0, *, top: int = 0, ign
     sum of exp(scale * logits), stats (..., 2) what token_logprobs_grad needs, the
     alternatives (..., top) in descending order, equal logits by id, int64; -1
     where fewer tokens are left than asked for (logits of -inf are not listed).
-    None stands for what was not asked for."""
+    None stands for what was not asked for.  Outputs of up to 1 MB in all share an
+    allocation: to keep one of them alone, clone it."""
     return _lib.bind().token_logprobs(logits, tokens, scale, top, ignore_index, entropy)
 
 

@@ -443,6 +443,16 @@ def test_offsets_past_32_bits():
     assert bool((got == got[:1]).all())
 
 
+def test_outputs_of_many_rows_keep_nothing_else():
+    """A kept log probability must not hold the alternatives of all rows."""
+    z, tokens = make(3000, 64, "bf16", seed=25)
+    out = nl.token_logprobs(z, tokens, top=32)
+    assert sum(t.numel() * t.element_size() for t in out) > 1 << 20
+    for t in out:
+        assert t.untyped_storage().nbytes() == t.numel() * t.element_size() and t.storage_offset() == 0
+    check(z, tokens, 1.0, out, 32)
+
+
 def test_repeated_calls_have_the_same_bits():
     z, tokens = make(37, 50001, "bf16", seed=19)
     first = nl.token_logprobs(z, tokens, top=20)
