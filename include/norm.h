@@ -475,8 +475,8 @@ norm_status head_rms_rotary_grad(const norm_heads* dyq, const norm_heads* q, int
  *   lse = a m + l,  stats = (m, l), kept apart for token_logprobs_grad,
  *   and the `top` most probable tokens, larger logits first and equal ones by id.
  * logits [N x ldl] in `dtype`.  tokens [N], contiguous, or NULL (no logprob).  A
- *   row whose token is ignore_index has logprob 0.  A token outside [0, V) has so
- *   too and raises NORM_DEVICE_ERR_BAD_TOKEN.
+ *   row whose token is ignore_index (NORM_NO_IGNORE: none is) has logprob 0.  A
+ *   token outside [0, V) has so too and raises NORM_DEVICE_ERR_BAD_TOKEN.
  * logprob [N] (with tokens), entropy [N], lse [N], stats [N x 2, 8-byte aligned]:
  *   fp32; entropy, lse and stats may be NULL.  top_logprobs fp32, top_ids int64
  *   [N x top]; top is at most NORM_MAX_TOP, 0 for none (then both NULL).
@@ -487,6 +487,7 @@ norm_status head_rms_rotary_grad(const norm_heads* dyq, const norm_heads* q, int
  * N is at most 2^28.
  */
 #define NORM_MAX_TOP 32
+#define NORM_NO_IGNORE INT64_MIN
 norm_status token_logprobs(const void* logits, int64_t ldl, const void* tokens, norm_itype token_type, float scale,
                            int64_t ignore_index, float* logprob, float* entropy, float* lse, float* stats,
                            float* top_logprobs, int64_t* top_ids, int64_t top, int64_t N, int64_t V, norm_dtype dtype,

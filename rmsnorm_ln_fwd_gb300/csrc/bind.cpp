@@ -597,8 +597,6 @@ py::tuple head_rms_rotary_grad_(const Tensor& dyq, const Opt& dyk, const Tensor&
 
 // ------------------------------------------------------ log probabilities
 
-constexpr int64_t kNoToken = INT64_MIN;
-
 // The dims [result, n) of a tensor that one stride reaches; that stride, or `stride` where it is given.
 int64_t flat_from(const Tensor& t, int64_t n, int64_t stride) {
   bool seen = stride != 0;
@@ -750,7 +748,7 @@ py::tuple token_logprobs_(const Tensor& logits, const Opt& tokens, double scale,
     auto on = [&](float* q, int64_t n) { return q ? q + row * n : nullptr; };
     check("token_logprobs",
           token_logprobs(bytes_on(zr.p, at.z * logits.element_size()), runs.ld, bytes_on(tp, at.tok * runs.token_size), it,
-                         (float)scale, ignore.value_or(kNoToken), on(p[0], 1), on(p[1], 1), on(p[2], 1), on(p[3], 2),
+                         (float)scale, ignore.value_or(NORM_NO_IGNORE), on(p[0], 1), on(p[1], 1), on(p[2], 1), on(p[3], 2),
                          on(p[4], top), ids ? ids + row * top : nullptr, top, runs.N, zr.H, xc, stream_of(logits)));
     row += runs.N;
   }
@@ -790,7 +788,7 @@ py::object token_logprobs_grad_(const Opt& dlogprob, const Tensor& logits, const
     check("token_logprobs_grad",
           token_logprobs_grad(on(dlp, 1), bytes_on(zr.p, at.z * logits.element_size()), runs.ld,
                               bytes_on(tp, at.tok * runs.token_size), it, on(st, 2), on(en, 1), on(den, 1), on(dl, 1),
-                              (float)scale, ignore.value_or(kNoToken), bytes_on(dz.data_ptr(), at.out * dz.element_size()),
+                              (float)scale, ignore.value_or(NORM_NO_IGNORE), bytes_on(dz.data_ptr(), at.out * dz.element_size()),
                               runs.ldo, runs.N, zr.H, xc, stream_of(logits)));
     row += runs.N;
   }

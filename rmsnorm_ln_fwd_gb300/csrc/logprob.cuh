@@ -37,6 +37,9 @@ constexpr float kLowest = -3.402823466e38f;
 // with one must stay finite.
 constexpr float kFarDown = -1e4f;
 
+// Whether a row has no token.
+__device__ __forceinline__ bool ignored(int64_t token, int64_t ignore) { return token == ignore && ignore != NORM_NO_IGNORE; }
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -531,7 +534,7 @@ __global__ void __launch_bounds__(kLogprobThreads, PER_SM) logprob_kernel(const 
     if (a.lse) a.lse[row] = r.mx == none ? log_sum : fmaf(a.scale, r.mx, log_sum);
     // log 2 turns the sums of exponents of two into those of e
     if (ENT && a.entropy) a.entropy[row] = r.s == 0.f ? 0.f : log_sum - 0.6931471805599453f * (r.u / r.s);
-    if (a.logprob && !has && tok != a.ignore) atomicOr(a.err, kErrBadToken);
+    if (a.logprob && !has && !ignored(tok, a.ignore)) atomicOr(a.err, kErrBadToken);
     if (a.logprob) a.logprob[row] = !has ? 0.f : r.s == 0.f ? none : fmaf(a.scale, zt - r.mx, -log_sum);
   }
   if constexpr (TOP) {
@@ -586,7 +589,7 @@ __global__ void __launch_bounds__(kLogprobGradThreads, 8) logprob_grad_kernel(co
     if (a.dlogprob) {
       const int64_t tok = a.tok64 ? reinterpret_cast<const long long*>(a.tokens)[row]
                                   : (int64_t) reinterpret_cast<const int*>(a.tokens)[row];
-      if (tok != a.ignore) {
+      if (!ignored(tok, a.ignore)) {
         if (tok >= 0 && tok < a.V) {
           token = (int)tok;
           dlp = a.dlogprob[row];

@@ -19,7 +19,7 @@ struct LogprobArgs {
   int64_t ldz;
   const void* tokens;  // may be null: no log probabilities
   int tok64;
-  int64_t ignore;   // a token that stands for none
+  int64_t ignore;   // a token that stands for none, or NORM_NO_IGNORE
   float scale;
   float* logprob;
   float* entropy;    // may be null

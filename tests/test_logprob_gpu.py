@@ -403,6 +403,26 @@ def test_tokens_outside_the_vocabulary():
     assert _lib.device_errors() == 0 and out[0][1] == 0
 
 
+def test_the_least_token_is_no_ignored_one():
+    """Without ignore_index every token outside the vocabulary is an error, the least of its type too."""
+    z, tokens = make(5, 300, "f32", seed=23)
+    d = grads_in(5, 24)
+    for t in (tokens, tokens.int()):
+        t[2] = torch.iinfo(t.dtype).min
+        _lib.device_errors()
+        out = nl.token_logprobs(z, t)
+        torch.cuda.synchronize()
+        assert _lib.device_errors() == _lib.NORM_DEVICE_ERR_BAD_TOKEN
+        check(z, t, 1.0, out)
+        got = nl.token_logprobs_grad(d[0], z, t, out[3], out[1], d[1], d[2])
+        torch.cuda.synchronize()
+        assert _lib.device_errors() == _lib.NORM_DEVICE_ERR_BAD_TOKEN
+        check_grad(z, t, 1.0, got, out[3], out[1], *d)
+        nl.token_logprobs(z, t, ignore_index=int(torch.iinfo(torch.int32).min))
+        torch.cuda.synchronize()
+        assert _lib.device_errors() == (_lib.NORM_DEVICE_ERR_BAD_TOKEN if t.dtype == torch.long else 0)
+
+
 @pytest.mark.parametrize("scale", [1e-30, 1e-3, 30.0, 1e4])
 def test_scales(scale):
     z, tokens = make(5, 4001, "f32", seed=13)
