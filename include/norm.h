@@ -422,8 +422,9 @@ typedef struct {
  *   y_a = n_a * cos - n_b * sin,  y_b = n_b * cos + n_a * sin  for each rotated
  *   pair (a, b),  y_j = n_j for the other columns; all in fp32, rounded once.
  * q [B, T, q_heads, D], k [B, T, k_heads, D]: either may have no heads (and is
- *   then NULL).  D is at most 512, or 496 where part of a head is rotated in
- *   halves; at most 65535 heads a side and 2^31 - 1 tokens.
+ *   then NULL).  D is at most 512; where a part of a head is rotated in halves,
+ *   ceil(columns / 16) + ceil((D - columns) / 16) is at most 32 as well (always so
+ *   up to D = 496).  At most 65535 heads a side and 2^31 - 1 tokens.
  * gamma_q, gamma_k [D] or NULL (ones).  rotation: NULL for the norm alone.
  * q_out, k_out: outputs of distinct elements.  Each may be exactly its input (in
  *   place); otherwise they are clear of the inputs and of each other.  Parts of

@@ -393,6 +393,16 @@ def test_host_tensors_are_refused(lib):
         nl.token_logprobs_grad(None, torch.zeros(3, 8), None, torch.zeros(3, 2))
 
 
+def test_columns_of_a_head_that_is_partly_rotated_in_halves(lib):
+    for D in (1, 2, 63, 64, 495, 496, 497, 500, 511, 512, 513):
+        for R in range(2, D + 1, 2):
+            for pairs in (0, 1):
+                ok = D <= 512 and (pairs or -(-R // 16) + -(-(D - R) // 16) <= 32)
+                assert ok or D > 496
+                got = _rotary(lib, D=D, T=0, rot=_rotation(columns=R, cos_stride=R // 2, sin_stride=R // 2, interleaved=pairs))
+                assert got == (OK if ok else INVALID), (D, R, pairs)
+
+
 def test_workspace_size_needs_a_width(lib):
     assert lib.head_rms_rotary_workspace_bytes(0, 0) == 0
     assert lib.head_rms_rotary_workspace_bytes(513, 0) == 0
