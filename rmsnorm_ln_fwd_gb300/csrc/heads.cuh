@@ -78,7 +78,9 @@ struct HeadLane {
   }
   __device__ static __forceinline__ int clamp8(int n) { return n < 0 ? 0 : n > 8 ? 8 : n; }
 
+  // (Half precision by whole accesses is copied to shared memory.)
   __device__ static __forceinline__ void load_half(const T* p, int n, uint32_t* w) {
+    static_assert(ES == 4 || CA == 1, "see HeadRing");
     if constexpr (CA * ES == 32) {
       if (n > 0) {
         ld_stream32(p, *reinterpret_cast<uint32_t(*)[8]>(w));
@@ -94,13 +96,6 @@ struct HeadLane {
         w[4 * k + 1] = u.y;
         w[4 * k + 2] = u.z;
         w[4 * k + 3] = u.w;
-      }
-    } else if constexpr (CA * ES == 8) {
-#pragma unroll
-      for (int k = 0; k < 8 / CA; ++k) {
-        w[2 * k] = w[2 * k + 1] = 0u;
-        if (k * CA < n)
-          asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[2 * k]), "=r"(w[2 * k + 1]) : "l"(p + k * CA));
       }
     } else if constexpr (ES == 4) {
 #pragma unroll
