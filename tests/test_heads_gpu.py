@@ -504,6 +504,36 @@ def test_offsets_past_32_bits():
     assert torch.allclose(dg.float(), T * d1.float(), rtol=2 * 2.0 ** -8, atol=T * 2.0 ** -8 * float(d1.float().abs().mean()))
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("hq,hk,D,R,off", [(3, 2, 128, 128, 0), (3, 1, 80, 40, 0), (2, 2, 80, 20, 4), (2, 1, 33, 10, 0), (1, 0, 64, 64, 1)])
+def test_sequences_more_than_32_bits_apart(hq, hk, D, R, off, interleaved):
+    """Two sequences 2^31 elements apart, queries and keys, in every width of access: the bits of near ones."""
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GB")
+    B, T, dt = 2, 21, torch.bfloat16
+    c = make(B, T, hq, hk, D, R, "bf16", positions="each", seed=60)
+    row = (hq + hk) * D + 16
+
+    def far():
+        base = torch.empty(2 ** 31 + T * row + 16, device=DEV, dtype=dt)
+        part = lambda H, at: base.as_strided((B, T, H, D), (2 ** 31, row, D, 1), off + at) if H else None
+        return part(hq, 0), part(hk, hq * D)
+
+    want, grads = call(c, interleaved=interleaved), call_grad(c, interleaved=interleaved)
+    check(c, want, 1e-5, interleaved)
+    d = dict(c)
+    d["q"], d["k"] = far()
+    d["dyq"], d["dyk"] = far()
+    for n in ("q", "k", "dyq", "dyk"):
+        if c[n] is not None:
+            d[n].copy_(c[n])
+    got = call_grad(d, interleaved=interleaved, dq=d["dyq"], dk=d["dyk"])
+    check_grad(c, got, 1e-5, interleaved)
+    assert torch.equal(got[0], grads[0]) and (not hk or torch.equal(got[1], grads[1]))
+    got = call(d, interleaved=interleaved, q_out=d["q"], k_out=d["k"])
+    assert torch.equal(got[0], want[0]) and (not hk or torch.equal(got[1], want[1]))
+
+
 def test_capture_and_replay_with_new_inputs():
     c = make(2, 64, 8, 2, 128, 128, "bf16", layout="fused", positions="each", seed=14)
     other = make(2, 64, 8, 2, 128, 128, "bf16", layout="fused", positions="each", seed=15)

@@ -376,6 +376,24 @@ def test_more_candidates_than_fit(dt):
         assert torch.equal(out[5], torch.sort(z.float(), dim=1, descending=True, stable=True)[1][:, :top])
 
 
+@pytest.mark.parametrize("dt", list(DT))
+def test_more_candidates_than_fit_in_some_parts_of_a_row(dt):
+    """Rows shared by clusters of eight CTAs of 1536 chunks: in two of the CTAs the largest logits are in the chunks of a dozen
+    of the 256 threads, which find them one after another, in the others they are not."""
+    GE = 32 // torch.finfo(DT[dt]).bits * 8
+    part = 256 * 6
+    V = 8 * part * GE
+    z = rnd((3, V), 9, DT[dt])
+    chunk = torch.arange(V, device=DEV) // GE
+    few = (chunk % 256 >= 36) & (chunk % 256 < 48)
+    z[:, few & ((chunk // part == 1) | (chunk // part == 6))] += 60.0
+    z[1, chunk // part == 3] += 50.0
+    z[2] = torch.where(few, 9.0, z[2])  # equal ones, in all of them
+    for top in (20, 32):
+        out = nl.token_logprobs(z, top=top)
+        check(z, None, 1.0, out, top)
+
+
 def test_more_alternatives_than_tokens():
     z = rnd((3, 4), 10, torch.float32)
     out = nl.token_logprobs(z, top=9)
