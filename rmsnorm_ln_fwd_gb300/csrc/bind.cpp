@@ -648,6 +648,8 @@ Runs runs_of(const Tensor& logits, const Opt& tokens, const Opt& out) {
   if (out) from = std::max(from, flat_from(*out, lead, 0));
   if (strided) {
     if (tokens->sizes() != dims) value_error("tokens must be contiguous or of the logits' leading dims");
+    if (dims[lead - 1] > 1 && tokens->stride(lead - 1) != 1)
+      value_error("tokens must be contiguous along the last of the rows' dims");
     from = std::max(from, flat_from(*tokens, lead, 1));
   }
   int64_t runs = 1, inner = 0;  // the innermost dim of several rows in a run
@@ -656,8 +658,6 @@ Runs runs_of(const Tensor& logits, const Opt& tokens, const Opt& out) {
     (i < from ? runs : r.N) *= dims[i];
     if (i >= from && dims[i] > 1) inner = i;
   }
-  // (a run of one row: tokens that are not neighbours at all)
-  if (r.N == 1 && strided) value_error("tokens must be contiguous along the last of the rows' dims");
   r.ld = r.N > 1 ? logits.stride(inner) : std::max<int64_t>(z.H, 1);
   if (out) r.ldo = r.N > 1 ? out->stride(inner) : std::max<int64_t>(z.H, 1);
   for (int64_t k = 0; k < runs; ++k) {

@@ -368,6 +368,7 @@ def test_runs_of_rows_and_their_tokens(lib):
     assert runs(z[:, :-1], t[:, 1:].contiguous(), None) == (4, 7, [(0, 0, 0), (35, 4, 0), (70, 8, 0)])
     assert runs(z[:, :4].contiguous(), t[:, 1:], None) == (4, 7, [(0, 0, 0), (28, 5, 0), (56, 10, 0)])
     assert runs(z[:, :1], t[:, :1].contiguous(), None) == (3, 35, [(0, 0, 0)])
+    assert runs(z[:, :1], t[:, 1:2], None) == (1, 7, [(0, 0, 0), (35, 5, 0), (70, 10, 0)])  # a token of each sequence
     assert runs(z.transpose(0, 1), t.t().contiguous(), None) == (3, 35, [(7 * i, 3 * i, 0) for i in range(5)])
     assert runs(z, t, torch.empty(3, 9, 8)[:, 2:7, 1:]) == (5, 7, [(0, 0, 0), (35, 5, 72), (70, 10, 144)])
     w = torch.empty(2, 3, 5, 7)
