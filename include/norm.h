@@ -484,7 +484,8 @@ norm_status head_rms_rotary_grad(const norm_heads* dyq, const norm_heads* q, int
  * A logit of -inf has probability 0 and is no alternative: where fewer than `top`
  *   are left, the rest is id -1 with log probability -inf (NaN is none either).
  *   A row that is -inf throughout has logprob, lse and stats of -inf and entropy
- *   0.  A row with a NaN or +inf has NaN in all but its maximum and its ids.
+ *   0.  A row with a NaN or +inf has NaN in all but its maximum and its ids (and
+ *   the logprob of 0 of a row without a token, the -inf of an id -1).
  * N is at most 2^28.
  */
 #define NORM_MAX_TOP 32

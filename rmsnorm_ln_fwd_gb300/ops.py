@@ -451,7 +451,9 @@ def token_logprobs_grad(dlogprob, logits, tokens, stats, entropy=None, dentropy=
 
     ``stats`` and, with ``dentropy``, ``entropy`` are the forward's; logits and
     tokens as there.  ``out`` may be ``logits`` itself, or a tensor clear of it and
-    of the other inputs; a fresh one is contiguous.  The alternatives have no
-    gradient."""
+    of the other inputs; a fresh one is contiguous.  An ``out`` whose rows are not
+    as the logits' against 32 bytes is written several times more slowly: for
+    logits of a padded odd vocabulary pass one of their row stride.  The
+    alternatives have no gradient."""
     return _lib.bind().token_logprobs_grad(dlogprob, logits, tokens, stats, entropy, dentropy, dlse, scale, ignore_index,
                                            out)

@@ -256,6 +256,30 @@ def test_rows_of_other_orders_and_shared_ones():
         check_grad(z, t, 1.0, got, out[3], out[1], *d)
 
 
+def test_runs_of_rows_captured_and_replayed():
+    whole, tokens = sequences(3, 7, 1001, "bf16", 45)
+    other, more = sequences(3, 7, 1001, "bf16", 46)
+    d = [g.view(3, 6) for g in grads_in(18, 47)]
+
+    def both(whole, tokens):
+        z, t = whole[:, :-1], tokens[:, 1:]
+        out = nl.token_logprobs(z, t, top=4)
+        return [*out, nl.token_logprobs_grad(d[0], z, t, out[3], out[1], d[1], d[2])]
+
+    want = both(other, more)
+    both(whole, tokens)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both(whole, tokens)
+    whole.copy_(other)
+    tokens.copy_(more)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 def test_runs_of_rows_bad_tokens_and_refusals():
     whole, tokens = sequences(3, 5, 300, "f32", 44)
     z, t = whole[:, :-1], tokens[:, 1:]
