@@ -554,8 +554,9 @@ __global__ void __launch_bounds__(kLogprobThreads, PER_SM) logprob_kernel(const 
 // logits and gradient have the same lead, so that aligned chunks of the one are
 // aligned in the other; else the gradient is stored by elements (4096x50257 bf16 of row
 // stride 50304 into contiguous rows 1026 us, into rows of that stride 120).  (us,
-// 4096x131072 bf16, 333x50001 bf16: 128 threads and three chunks 309, 12.2; two 333, 12.9; four 315, 12.1; 256 and three 313, 12.5; two 342,
-// 13.6; one 382, 14.5; 512 and two 349, 15.4.)
+// 4096x131072 bf16, 333x50001 bf16: 128 threads and three chunks 309, 12.2; two 333,
+// 12.9; four 315, 12.1; 256 and three 313, 12.5; two 342, 13.6; one 382, 14.5; 512 and
+// two 349, 15.4.)
 constexpr int kLogprobGradThreads = 128;
 constexpr int kLogprobGradU = 3;
 template <typename D, bool ENT, bool SAME>
